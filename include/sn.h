@@ -280,6 +280,136 @@ sn_status sn_energy_forces_static(const sn_model *model, const sn_system *sys, c
  * (SN_OK or the first error a kernel flagged) and clear it. */
 sn_status sn_read_status(void *ws, void *stream);
 
+/* ---------------------------------------------------------------- context operators
+ *
+ * Conditioning of the bead features on the states of a sequence encoder,
+ * before or between the interactions: a group norm with an activation over
+ * the rows of each replica, and cross attention of the beads to the states
+ * (another number of rows) with a learned relative position bias.  Both have
+ * a forward and a backward pass.  They are extensions of this library; the
+ * pages do not describe them.
+ *
+ * Both take ragged rows as sn_system does: the rows of segment b are
+ * [ptr[b], ptr[b+1]), ptr[0] = 0, non-decreasing, ptr[B] = the row count, no
+ * segment longer than the stated maximum.  Segments may be empty.  The
+ * arrays lie on the device; a kernel that finds one inconsistent flags
+ * SN_ERR_INVALID in the status words of the workspace (sn_read_status) and
+ * skips the segment, so nothing is read or written out of range.
+ * Strides are in elements; the last index of every tensor is contiguous.
+ * Any stride and element-aligned pointer is accepted (rows that are
+ * 16-byte aligned with strides of 16 bytes load faster).  Outputs are
+ * contiguous and are written for every row of every consistent segment.
+ * The workspace begins with 256 bytes of status words, which the caller
+ * zeroes once, before its first use.  Results do not depend on timing:
+ * repeated calls give identical bits.  No call synchronises. */
+
+/* Element type of the row tensors; everything is accumulated in fp32. */
+#define SN_F32 0
+#define SN_BF16 1
+
+/* Activations of the group norm. */
+#define SN_ACT_NONE 0
+#define SN_ACT_SSP 1   /* ln(e^z/2 + 1/2), the model's shifted softplus */
+#define SN_ACT_SILU 2  /* z / (1 + e^-z) */
+
+/* Largest head size and largest number of position buckets. */
+#define SN_MAX_HEAD_DIM 128
+#define SN_MAX_BUCKETS 64
+/* Largest thresholds[n_buckets-2] - thresholds[0]. */
+#define SN_MAX_BUCKET_SPAN 2046
+
+/* Cross attention.  For query row i and key row j of the same segment, and
+ * head h (sharing key/value head h / (n_heads / n_kv_heads)):
+ *     rel  = k_pos[j] - q_pos[i]              (saturating)
+ *     s    = scale q_ih . k_jh + bias[h][bucket(rel)],
+ *     bucket(rel) = number of thresholds <= rel
+ *     p    = exp(s) / sum over the kept keys of exp(s)
+ *     o_ih = sum over the kept keys of p v_jh
+ * A row without a kept key gives o = 0 and lse = -inf, and zero gradients.
+ * Keys that are not kept are never multiplied in: whatever they hold (NaN
+ * and infinities too) does not reach an output, and their gradients are 0. */
+typedef struct sn_cross_attention {
+    int32_t n_segments;          /* B >= 1 */
+    int32_t n_q, n_k;            /* rows of all segments, >= 0 */
+    int32_t max_q, max_k;        /* rows of the longest segment */
+    const int32_t *q_ptr;        /* device [B+1] */
+    const int32_t *k_ptr;        /* device [B+1] */
+    int32_t n_heads;             /* H, a multiple of n_kv_heads */
+    int32_t n_kv_heads;
+    int32_t head_dim;            /* D, 1 .. SN_MAX_HEAD_DIM */
+    int32_t dtype;               /* SN_F32 or SN_BF16: q, k, v, o and their gradients */
+    float scale;                 /* finite */
+    const void *q;               /* device [n_q][H][D] */
+    const void *k, *v;           /* device [n_k][n_kv_heads][D] */
+    int64_t q_stride, q_head_stride;
+    int64_t k_stride, k_head_stride;
+    int64_t v_stride, v_head_stride;
+    const uint8_t *keep;         /* device [n_k], 0 = the key is absent; or NULL: every key is kept */
+    const float *bias;           /* device [H][n_buckets], contiguous; or NULL: none */
+    int32_t n_buckets;           /* 1 .. SN_MAX_BUCKETS (with bias) */
+    const int32_t *thresholds;   /* host [n_buckets-1], non-decreasing (with bias) */
+    const int32_t *q_pos;        /* device [n_q], or NULL: the row's index in its segment */
+    const int32_t *k_pos;        /* device [n_k], or NULL: the same */
+} sn_cross_attention;
+
+/* Thresholds of the usual logarithmic buckets (host only): n_buckets (even,
+ * >= 4) / 2 buckets for rel <= 0 by the distance -rel and as many for
+ * rel > 0 by rel - 1; of each half, the nearer half hold one distance each,
+ * the others grow by equal ratios up to max_distance, from where the last is
+ * open.  Writes n_buckets - 1 values.  SN_ERR_INVALID on an odd or
+ * out-of-range count or max_distance <= n_buckets / 4. */
+sn_status sn_relative_thresholds(int32_t n_buckets, int32_t max_distance, int32_t *thresholds);
+
+/* Bytes of workspace of both calls below (host; sizes only, no pointer of
+ * `op` is read).  0 for a descriptor that they would refuse for its sizes. */
+size_t sn_cross_attention_workspace_bytes(const sn_cross_attention *op);
+
+/* o [n_q][H][D] (op->dtype).  For the backward pass (each may be NULL):
+ * o_acc [n_q][H][D], the same rows in fp32 before they are rounded;
+ * lse [n_q][H], the logarithm of the sum of exp(s). */
+sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *o_acc, float *lse, void *ws,
+                                     size_t ws_bytes, void *stream);
+
+/* Gradients of the forward's o from its own o_acc and lse and d_o
+ * [n_q][H][D]: dq [n_q][H][D], dk and dv [n_k][n_kv_heads][D] (op->dtype;
+ * shared heads summed), dbias [H][n_buckets] (fp32, NULL without bias).
+ * d_o holds finite values. */
+sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float *o_acc, const float *lse,
+                                      const void *d_o, int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk,
+                                      void *dv, float *dbias, void *ws, size_t ws_bytes, void *stream);
+
+/* Group norm with an activation, channels last: channel c belongs to group
+ * c / (n_channels / n_groups); over the rows of a segment and the channels
+ * of a group
+ *     xh = (x - mean) / sqrt(var + eps),  y = act(gamma_c xh + beta_c). */
+typedef struct sn_group_norm {
+    int32_t n_segments;          /* B >= 1 */
+    int32_t n_rows, max_rows;    /* rows of all segments, of the longest segment */
+    const int32_t *row_ptr;      /* device [B+1] */
+    int32_t n_channels;          /* C, a multiple of n_groups, at most 65536 */
+    int32_t n_groups;
+    int32_t activation;          /* SN_ACT_* */
+    int32_t dtype;               /* SN_F32 or SN_BF16: x, y and their gradients */
+    float eps;                   /* > 0 */
+    const void *x;               /* device [n_rows][C] */
+    int64_t x_stride;
+    const float *gamma, *beta;   /* device [C], or NULL: 1 and 0 */
+} sn_group_norm;
+
+/* Bytes of workspace of both calls below (host; sizes only). */
+size_t sn_group_norm_workspace_bytes(const sn_group_norm *op);
+
+/* y [n_rows][C] (op->dtype).  For the backward pass (each may be NULL):
+ * mean, rstd [B][n_groups] (an empty segment: 0 and 1 / sqrt(eps)). */
+sn_status sn_group_norm_forward(const sn_group_norm *op, void *y, float *mean, float *rstd, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* dx [n_rows][C] (op->dtype), dgamma and dbeta [C] (fp32, each may be NULL)
+ * from the forward's mean and rstd and dy [n_rows][C]. */
+sn_status sn_group_norm_backward(const sn_group_norm *op, const float *mean, const float *rstd, const void *dy,
+                                 int64_t dy_stride, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                                 void *stream);
+
 /* ---------------------------------------------------------------- timing */
 
 /* Per-kernel timing with HIP events recorded around every launch on the

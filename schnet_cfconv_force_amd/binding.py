@@ -25,12 +25,23 @@ SN_ERR_WORKSPACE = -6
 SN_ERR_ROW = -7
 SN_MAX_ROW = 2048
 SN_MD_GRAPH = 1
+SN_F32 = 0
+SN_BF16 = 1
+SN_ACT_NONE = 0
+SN_ACT_SSP = 1
+SN_ACT_SILU = 2
+SN_MAX_HEAD_DIM = 128
+SN_MAX_BUCKETS = 64
+SN_MAX_BUCKET_SPAN = 2046
 
 EXPORTED = (
     "sn_param_count", "sn_param_offsets", "sn_quantize_filter_weights", "sn_workspace_bytes",
     "sn_status_string", "sn_version", "sn_build_csr_neighbors", "sn_energy_forces", "sn_verlet_step",
     "sn_filter_forward", "sn_read_status", "sn_profile_enable", "sn_profile_classes", "sn_profile_name",
     "sn_profile_collect", "sn_energy_forces_static",
+    "sn_relative_thresholds", "sn_cross_attention_workspace_bytes", "sn_cross_attention_forward",
+    "sn_cross_attention_backward", "sn_group_norm_workspace_bytes", "sn_group_norm_forward",
+    "sn_group_norm_backward",
 )
 SN_STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -48,6 +59,28 @@ class SnModel(ctypes.Structure):
                 ("rbf_gamma", ctypes.c_float), ("filter_format", ctypes.c_int32),
                 ("params", ctypes.c_void_p), ("qweights", ctypes.c_void_p), ("qscales", ctypes.c_void_p),
                 ("filter_math", ctypes.c_int32)]
+
+
+class SnCrossAttention(ctypes.Structure):
+    _fields_ = [("n_segments", ctypes.c_int32), ("n_q", ctypes.c_int32), ("n_k", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_k", ctypes.c_int32),
+                ("q_ptr", ctypes.c_void_p), ("k_ptr", ctypes.c_void_p),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("keep", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("n_buckets", ctypes.c_int32),
+                ("thresholds", ctypes.c_void_p), ("q_pos", ctypes.c_void_p), ("k_pos", ctypes.c_void_p)]
+
+
+class SnGroupNorm(ctypes.Structure):
+    _fields_ = [("n_segments", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("row_ptr", ctypes.c_void_p), ("n_channels", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
 
 
 class SnError(RuntimeError):
@@ -88,6 +121,13 @@ def lib() -> ctypes.CDLL:
         "sn_profile_classes": (i32, []),
         "sn_profile_name": (ctypes.c_char_p, [i32]),
         "sn_profile_collect": (i32, [ctypes.POINTER(ctypes.c_double), P64]),
+        "sn_relative_thresholds": (i32, [i32, i32, vp]),
+        "sn_cross_attention_workspace_bytes": (sz, [vp]),
+        "sn_cross_attention_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
+        "sn_cross_attention_backward": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
+        "sn_group_norm_workspace_bytes": (sz, [vp]),
+        "sn_group_norm_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
+        "sn_group_norm_backward": (i32, [vp, vp, vp, vp, i64, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -331,6 +371,246 @@ def filter_forward(model: Model, interaction: int, d, ws, phi=None, stream=None)
 
 def read_status(ws, stream=None) -> int:
     return int(lib().sn_read_status(ws.data_ptr(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ context operators
+
+_ACTIVATIONS = {"none": SN_ACT_NONE, "ssp": SN_ACT_SSP, "silu": SN_ACT_SILU}
+
+
+def _row_type(dtype) -> int:
+    torch = _torch()
+    if dtype == torch.float32:
+        return SN_F32
+    if dtype == torch.bfloat16:
+        return SN_BF16
+    raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, not {dtype}")
+
+
+def _ragged(ptr, name: str):
+    """Checked host copy of a segment pointer array and its longest segment."""
+    ptr = np.asarray(ptr, np.int64).ravel()
+    if ptr.size < 2 or ptr[0] != 0 or np.any(np.diff(ptr) < 0) or ptr[-1] > np.iinfo(np.int32).max:
+        raise ValueError(f"{name} must be a non-decreasing array of B + 1 >= 2 row offsets that begins with 0")
+    return ptr.astype(np.int32), int(np.diff(ptr).max())
+
+
+def _rows(t, name: str, shape, dtype, device):
+    """Check a row tensor (its last index contiguous); returns its address."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or (t.stride(-1) != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on {device} whose last index is contiguous, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _flat(t, name: str, shape, dtypes, device):
+    """Check an optional contiguous tensor; returns its address or None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor {tuple(shape)} on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _launch_stream(plan, stream, *outputs) -> int:
+    """The raw stream of a call; outputs allocated on the current stream are tied to an explicit one."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.current_stream(plan.device).cuda_stream
+    for t in outputs:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _zeroed_workspace(plan):
+    torch = _torch()
+    ws = torch.empty(plan.workspace_bytes + 256, dtype=torch.uint8, device=plan.device)
+    ws = ws[(-ws.data_ptr()) % 256:][:plan.workspace_bytes]
+    ws[:256].zero_()      # the status words
+    return ws
+
+
+def relative_thresholds(n_buckets: int = 32, max_distance: int = 128) -> np.ndarray:
+    """sn_relative_thresholds: int32 [n_buckets - 1]; bucket(rel) = number of thresholds <= rel."""
+    out = np.zeros(max(int(n_buckets) - 1, 1), np.int32)
+    _check(lib().sn_relative_thresholds(int(n_buckets), int(max_distance), out.ctypes.data), "sn_relative_thresholds")
+    return out
+
+
+class CrossAttention:
+    """Segment pointers, head layout and position buckets of a cross attention (sn_cross_attention).
+
+    q_ptr, k_ptr: host row offsets [B + 1] of the query and the key/value segments.
+    thresholds: int32 [n_buckets - 1] (see relative_thresholds), needed where a bias is given.
+    scale: default 1 / sqrt(head_dim)."""
+
+    def __init__(self, q_ptr, k_ptr, n_heads: int, n_kv_heads: int, head_dim: int, dtype=None, scale=None,
+                 thresholds=None, device="cuda"):
+        torch = _torch()
+        self.dtype = torch.float32 if dtype is None else dtype
+        code = _row_type(self.dtype)
+        qp, max_q = _ragged(q_ptr, "q_ptr")
+        kp, max_k = _ragged(k_ptr, "k_ptr")
+        if qp.size != kp.size:
+            raise ValueError(f"q_ptr has {qp.size - 1} segments, k_ptr {kp.size - 1}")
+        self.thresholds = None if thresholds is None else np.ascontiguousarray(thresholds, np.int32).ravel()
+        self.n_buckets = 0 if self.thresholds is None else self.thresholds.size + 1
+        self.q_ptr = torch.from_numpy(qp).to(device)
+        self.k_ptr = torch.from_numpy(kp).to(device)
+        self.device = self.q_ptr.device
+        self.n_q, self.n_k = int(qp[-1]), int(kp[-1])
+        self.n_heads, self.n_kv_heads, self.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
+        self.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
+        # sizes are checked with the bias slot set, so that the bucket count is checked too
+        self.c = SnCrossAttention(qp.size - 1, self.n_q, self.n_k, max_q, max_k, _ptr(self.q_ptr), _ptr(self.k_ptr),
+                                  self.n_heads, self.n_kv_heads, self.head_dim, code, self.scale)
+        self.c.n_buckets = self.n_buckets
+        self.c.thresholds = None if self.thresholds is None else self.thresholds.ctypes.data
+        self.c.bias = 16 if self.n_buckets else None
+        self.workspace_bytes = int(lib().sn_cross_attention_workspace_bytes(ctypes.byref(self.c)))
+        self.c.bias = None
+        if self.workspace_bytes == 0:
+            raise SnError(SN_ERR_INVALID, "sn_cross_attention")
+        self.q_shape = torch.Size((self.n_q, self.n_heads, self.head_dim))
+        self.k_shape = torch.Size((self.n_k, self.n_kv_heads, self.head_dim))
+
+    def _bind(self, q, k, v, bias, q_pos, k_pos, keep):
+        torch = _torch()
+        op = SnCrossAttention.from_buffer_copy(self.c)    # calls from several threads do not share it
+        op.q = _rows(q, "q", self.q_shape, self.dtype, self.device)
+        op.k = _rows(k, "k", self.k_shape, self.dtype, self.device)
+        op.v = _rows(v, "v", self.k_shape, self.dtype, self.device)
+        op.q_stride, op.q_head_stride, _ = q.stride()
+        op.k_stride, op.k_head_stride, _ = k.stride()
+        op.v_stride, op.v_head_stride, _ = v.stride()
+        if bias is not None:
+            if not self.n_buckets:
+                raise ValueError("a bias needs the plan's thresholds")
+            op.bias = _flat(bias, "bias", (self.n_heads, self.n_buckets), (torch.float32,), self.device)
+        if q_pos is not None:
+            op.q_pos = _flat(q_pos, "q_pos", (self.n_q,), (torch.int32,), self.device)
+        if k_pos is not None:
+            op.k_pos = _flat(k_pos, "k_pos", (self.n_k,), (torch.int32,), self.device)
+        if keep is not None:
+            op.keep = _flat(keep, "keep", (self.n_k,), (torch.bool, torch.uint8), self.device)
+        return op
+
+
+def cross_attention_workspace(plan: CrossAttention):
+    """A workspace (status words zeroed) for the plan's calls; calls that share one must be ordered on a stream."""
+    return _zeroed_workspace(plan)
+
+
+def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=None, k_pos=None, keep=None,
+                            save: bool = False, stream=None):
+    """sn_cross_attention_forward -> o [n_q, H, D]; with save=True -> (o, saved), saved = (o_acc, lse) for the
+    backward pass.  q [n_q, H, D], k and v [n_k, Hkv, D]; bias float32 [H, n_buckets]; q_pos [n_q] and k_pos
+    [n_k] int32 (default: the index in the segment); keep bool [n_k], False: the key is absent."""
+    torch = _torch()
+    op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
+    o = torch.empty(plan.q_shape, dtype=plan.dtype, device=plan.device)
+    acc = lse = None
+    if save:
+        lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device)
+        # fp32 rows are their own unrounded rows
+        acc = o if plan.dtype == torch.float32 else torch.empty(plan.q_shape, dtype=torch.float32, device=plan.device)
+    st = lib().sn_cross_attention_forward(ctypes.byref(op), o.data_ptr(), None if acc is o else _ptr(acc), _ptr(lse),
+                                          ws.data_ptr(), ws.numel(), _launch_stream(plan, stream, o, acc, lse))
+    _check(st, "sn_cross_attention_forward")
+    return (o, (acc, lse)) if save else o
+
+
+def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias=None, q_pos=None, k_pos=None,
+                             keep=None, stream=None):
+    """sn_cross_attention_backward -> (dq, dk, dv, dbias) from the forward's `saved` and the gradient d_o of o;
+    dbias is None without a bias.  The other arguments are the forward's."""
+    torch = _torch()
+    op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
+    acc, lse = saved
+    g = _rows(d_o, "d_o", plan.q_shape, plan.dtype, plan.device)
+    dq = torch.empty(plan.q_shape, dtype=plan.dtype, device=plan.device)
+    dk = torch.empty(plan.k_shape, dtype=plan.dtype, device=plan.device)
+    dv = torch.empty(plan.k_shape, dtype=plan.dtype, device=plan.device)
+    dbias = None if bias is None else torch.empty((plan.n_heads, plan.n_buckets), dtype=torch.float32,
+                                                  device=plan.device)
+    st = lib().sn_cross_attention_backward(
+        ctypes.byref(op), _flat(acc, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
+        _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), g, d_o.stride(0), d_o.stride(1),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(),
+        _launch_stream(plan, stream, dq, dk, dv, dbias))
+    _check(st, "sn_cross_attention_backward")
+    return dq, dk, dv, dbias
+
+
+class GroupNorm:
+    """Segment pointers, groups and activation of a group norm (sn_group_norm); row_ptr: host row offsets [B + 1]."""
+
+    def __init__(self, row_ptr, n_channels: int, n_groups: int, activation: str = "none", eps: float = 1e-5,
+                 dtype=None, device="cuda"):
+        torch = _torch()
+        self.dtype = torch.float32 if dtype is None else dtype
+        code = _row_type(self.dtype)
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation must be one of {tuple(_ACTIVATIONS)}, not {activation!r}")
+        rp, longest = _ragged(row_ptr, "row_ptr")
+        self.row_ptr = torch.from_numpy(rp).to(device)
+        self.device = self.row_ptr.device
+        self.n_segments, self.n_rows = rp.size - 1, int(rp[-1])
+        self.n_channels, self.n_groups = int(n_channels), int(n_groups)
+        self.c = SnGroupNorm(self.n_segments, self.n_rows, longest, _ptr(self.row_ptr), self.n_channels,
+                             self.n_groups, _ACTIVATIONS[activation], code, float(eps))
+        self.workspace_bytes = int(lib().sn_group_norm_workspace_bytes(ctypes.byref(self.c)))
+        if self.workspace_bytes == 0:
+            raise SnError(SN_ERR_INVALID, "sn_group_norm")
+        self.shape = torch.Size((self.n_rows, self.n_channels))
+
+    def _bind(self, x, gamma, beta):
+        torch = _torch()
+        op = SnGroupNorm.from_buffer_copy(self.c)
+        op.x = _rows(x, "x", self.shape, self.dtype, self.device)
+        op.x_stride = x.stride(0)
+        op.gamma = _flat(gamma, "gamma", (self.n_channels,), (torch.float32,), self.device)
+        op.beta = _flat(beta, "beta", (self.n_channels,), (torch.float32,), self.device)
+        return op
+
+
+def group_norm_workspace(plan: GroupNorm):
+    """A workspace (status words zeroed) for the plan's calls; calls that share one must be ordered on a stream."""
+    return _zeroed_workspace(plan)
+
+
+def group_norm_forward(plan: GroupNorm, x, gamma, beta, ws, save: bool = False, stream=None):
+    """sn_group_norm_forward -> y [n_rows, C]; with save=True -> (y, saved), saved = (mean, rstd) [B, n_groups].
+    gamma, beta: float32 [C], or None for 1 and 0."""
+    torch = _torch()
+    op = plan._bind(x, gamma, beta)
+    y = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    mean = rstd = None
+    if save:
+        mean, rstd = torch.empty((2, plan.n_segments, plan.n_groups), dtype=torch.float32, device=plan.device)
+    st = lib().sn_group_norm_forward(ctypes.byref(op), y.data_ptr(), _ptr(mean), _ptr(rstd), ws.data_ptr(),
+                                     ws.numel(), _launch_stream(plan, stream, y, mean, rstd))
+    _check(st, "sn_group_norm_forward")
+    return (y, (mean, rstd)) if save else y
+
+
+def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=None):
+    """sn_group_norm_backward -> (dx, dgamma, dbeta) from the forward's `saved` and the gradient dy of y."""
+    torch = _torch()
+    op = plan._bind(x, gamma, beta)
+    g = _rows(dy, "dy", plan.shape, plan.dtype, plan.device)
+    stats = (plan.n_segments, plan.n_groups)
+    dx = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    dgamma, dbeta = torch.empty((2, plan.n_channels), dtype=torch.float32, device=plan.device)
+    st = lib().sn_group_norm_backward(
+        ctypes.byref(op), _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
+        _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), g, dy.stride(0), dx.data_ptr(),
+        dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel(),
+        _launch_stream(plan, stream, dx, dgamma, dbeta))
+    _check(st, "sn_group_norm_backward")
+    return dx, dgamma, dbeta
 
 
 # ------------------------------------------------------------------ timing

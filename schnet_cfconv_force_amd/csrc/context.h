@@ -1,0 +1,77 @@
+// Shared declarations of the context operators (cross attention with a
+// relative position bias; group norm with an activation).
+#pragma once
+
+#include <hip/hip_bf16.h>
+
+#include "sn_internal.h"
+
+namespace sn {
+
+// --------------------------------------------------------------- element types
+
+typedef __bf16 bf16;
+
+__device__ inline float to_f32(float v) { return v; }
+__device__ inline float to_f32(bf16 v) { return (float)v; }
+// the output's own type, rounded to nearest even once
+template <typename T>
+__device__ inline T from_f32(float v) { return (T)v; }
+
+// --------------------------------------------------------------- ragged rows
+
+// Rows of segment b: start and length, or length 0 where the pointer array
+// contradicts the sizes that the host was given (flagged in the status word).
+__device__ inline void segment_rows(const int32_t *ptr, int b, int n_segments, int n_rows, int max_rows, int *status,
+                                    int &start, int &len) {
+    const int s = ptr[b], e = ptr[b + 1];
+    start = s;
+    len = e - s;
+    if (s < 0 || e < s || e > n_rows || e - s > max_rows || (b == 0 && s != 0) ||
+        (b == n_segments - 1 && e != n_rows)) {
+        len = 0;
+        start = 0;
+        if (threadIdx.x == 0) flag_status(status, SN_ERR_INVALID);
+    }
+}
+
+// --------------------------------------------------------------- attention
+
+struct AttnArgs {
+    int B, n_q, n_k, max_q, max_k;
+    const int32_t *q_ptr, *k_ptr;
+    int H, Hkv, G, D;
+    float scale;
+    const void *q, *k, *v, *d_o;
+    int64_t qs, qh, ks, kh, vs, vh, gs, gh;   // row and head strides (g: d_o)
+    const uint8_t *keep;
+    const float *bias;
+    int nb;                                   // buckets (0: no bias)
+    const int32_t *q_pos, *k_pos;
+    int *status;
+    int32_t thr[SN_MAX_BUCKETS - 1];
+};
+
+size_t attn_workspace(const sn_cross_attention &op);
+sn_status attn_forward(const AttnArgs &a, int dtype, void *o, float *o_acc, float *lse, char *ws, hipStream_t s);
+sn_status attn_backward(const AttnArgs &a, int dtype, const float *o_acc, const float *lse, void *dq, void *dk,
+                        void *dv, float *dbias, char *ws, hipStream_t s);
+
+// --------------------------------------------------------------- group norm
+
+struct NormArgs {
+    int B, n_rows, max_rows, C, groups, width, act;
+    float eps;
+    const int32_t *ptr;
+    const void *x, *dy;
+    int64_t xs, dys;
+    const float *gamma, *beta;
+    int *status;
+};
+
+size_t norm_workspace(const sn_group_norm &op);
+sn_status norm_forward(const NormArgs &a, int dtype, void *y, float *mean, float *rstd, char *ws, hipStream_t s);
+sn_status norm_backward(const NormArgs &a, int dtype, const float *mean, const float *rstd, void *dx, float *dgamma,
+                        float *dbeta, char *ws, hipStream_t s);
+
+}  // namespace sn

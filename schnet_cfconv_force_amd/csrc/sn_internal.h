@@ -116,6 +116,7 @@ __device__ inline int xcd_block(int n) {
 enum KernelClass {
     K_NB_GRID = 0, K_NB_BIN, K_NB_SCAN, K_NB_COUNT, K_NB_FILL, K_NB_REV,
     K_PAIRS, K_MLP, K_FILTER_FWD, K_CFCONV, K_FILTER_BWD, K_FORCES, K_VERLET, K_KINETIC, K_PACK,
+    K_ATTN_FWD, K_ATTN_BWD, K_NORM_FWD, K_NORM_BWD,
     K_NUM_CLASSES
 };
 
