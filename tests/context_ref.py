@@ -4,15 +4,15 @@ Tolerances.  u = 2^-24 is half a unit of fp32.  A score is an inner product of a
 an exponential and a normalisation: 128 u of the sum of the magnitudes covers their roundings while the scores
 stay within about 8; larger ones amplify an error of s in exp(s), so the factor grows with max |s| / 8.  Every
 output is a sum; its error is taken relative to the same sum over magnitudes (`abs` below), so cancellation
-needs no allowance of its own.  bf16 tensors add the rounding of the output (2^-9 of its value, half a unit)
-and of one 16-bit operand of the last product (2^-9 of the magnitudes).
+needs no allowance of its own.  bf16 keeps 8 significant bits: half a unit is 2^-8.  bf16 tensors add the rounding
+of the output (2^-8 of its value) and of one 16-bit operand of the last product (2^-8 of the magnitudes).
 """
 import math
 
 import numpy as np
 import torch
 
-U32, U16 = 2.0 ** -24, 2.0 ** -9
+U32, U16 = 2.0 ** -24, 2.0 ** -8
 
 
 def bucket(rel, thresholds):
