@@ -364,19 +364,18 @@ sn_status sn_relative_thresholds(int32_t n_buckets, int32_t max_distance, int32_
  * `op` is read).  0 for a descriptor that they would refuse for its sizes. */
 size_t sn_cross_attention_workspace_bytes(const sn_cross_attention *op);
 
-/* o [n_q][H][D] (op->dtype).  For the backward pass (each may be NULL):
- * o_acc [n_q][H][D], the same rows in fp32 before they are rounded;
+/* o [n_q][H][D] (op->dtype); for the backward pass (may be NULL)
  * lse [n_q][H], the logarithm of the sum of exp(s). */
-sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *o_acc, float *lse, void *ws,
-                                     size_t ws_bytes, void *stream);
+sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *lse, void *ws, size_t ws_bytes,
+                                     void *stream);
 
-/* Gradients of the forward's o from its own o_acc and lse and d_o
+/* Gradients of the forward's o from that o, its lse and d_o
  * [n_q][H][D]: dq [n_q][H][D], dk and dv [n_k][n_kv_heads][D] (op->dtype;
  * shared heads summed), dbias [H][n_buckets] (fp32, NULL without bias).
  * d_o holds finite values. */
-sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float *o_acc, const float *lse,
-                                      const void *d_o, int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk,
-                                      void *dv, float *dbias, void *ws, size_t ws_bytes, void *stream);
+sn_status sn_cross_attention_backward(const sn_cross_attention *op, const void *o, const float *lse, const void *d_o,
+                                      int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk, void *dv,
+                                      float *dbias, void *ws, size_t ws_bytes, void *stream);
 
 /* Group norm with an activation, channels last: channel c belongs to group
  * c / (n_channels / n_groups); over the rows of a segment and the channels

@@ -123,7 +123,7 @@ def lib() -> ctypes.CDLL:
         "sn_profile_collect": (i32, [ctypes.POINTER(ctypes.c_double), P64]),
         "sn_relative_thresholds": (i32, [i32, i32, vp]),
         "sn_cross_attention_workspace_bytes": (sz, [vp]),
-        "sn_cross_attention_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
+        "sn_cross_attention_forward": (i32, [vp, vp, vp, vp, sz, vp]),
         "sn_cross_attention_backward": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
         "sn_group_norm_workspace_bytes": (sz, [vp]),
         "sn_group_norm_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
@@ -505,21 +505,17 @@ def cross_attention_workspace(plan: CrossAttention):
 
 def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=None, k_pos=None, keep=None,
                             save: bool = False, stream=None):
-    """sn_cross_attention_forward -> o [n_q, H, D]; with save=True -> (o, saved), saved = (o_acc, lse) for the
+    """sn_cross_attention_forward -> o [n_q, H, D]; with save=True -> (o, saved), saved = (o, lse) for the
     backward pass.  q [n_q, H, D], k and v [n_k, Hkv, D]; bias float32 [H, n_buckets]; q_pos [n_q] and k_pos
     [n_k] int32 (default: the index in the segment); keep bool [n_k], False: the key is absent."""
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
     o = torch.empty(plan.q_shape, dtype=plan.dtype, device=plan.device)
-    acc = lse = None
-    if save:
-        lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device)
-        # fp32 rows are their own unrounded rows
-        acc = o if plan.dtype == torch.float32 else torch.empty(plan.q_shape, dtype=torch.float32, device=plan.device)
-    st = lib().sn_cross_attention_forward(ctypes.byref(op), o.data_ptr(), None if acc is o else _ptr(acc), _ptr(lse),
-                                          ws.data_ptr(), ws.numel(), _launch_stream(plan, stream, o, acc, lse))
+    lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device) if save else None
+    st = lib().sn_cross_attention_forward(ctypes.byref(op), o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
+                                          _launch_stream(plan, stream, o, lse))
     _check(st, "sn_cross_attention_forward")
-    return (o, (acc, lse)) if save else o
+    return (o, (o, lse)) if save else o
 
 
 def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias=None, q_pos=None, k_pos=None,
@@ -528,7 +524,7 @@ def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias
     dbias is None without a bias.  The other arguments are the forward's."""
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
-    acc, lse = saved
+    o, lse = saved
     g = _rows(d_o, "d_o", plan.q_shape, plan.dtype, plan.device)
     dq = torch.empty(plan.q_shape, dtype=plan.dtype, device=plan.device)
     dk = torch.empty(plan.k_shape, dtype=plan.dtype, device=plan.device)
@@ -536,7 +532,7 @@ def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias
     dbias = None if bias is None else torch.empty((plan.n_heads, plan.n_buckets), dtype=torch.float32,
                                                   device=plan.device)
     st = lib().sn_cross_attention_backward(
-        ctypes.byref(op), _flat(acc, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
+        ctypes.byref(op), _flat(o, "saved[0]", plan.q_shape, (plan.dtype,), plan.device),
         _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), g, d_o.stride(0), d_o.stride(1),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(),
         _launch_stream(plan, stream, dq, dk, dv, dbias))

@@ -1,0 +1,314 @@
+// Tiles, products and position buckets shared by the attention kernels.
+//
+// Every product runs on v_mfma_f32_32x32x16_bf16.  bf16 rows enter as they
+// are (one plane); an fp32 row is held as three bf16 planes, x = x0 + x1 + x2
+// (8 + 8 + 8 bits: the residuals are exact, so the sum is x to 2^-24), and a
+// product of two of them is the six plane products of weight 2^-16 or more.
+// Six bf16 products cost 6/16 of one fp32 matrix instruction of that size.
+//
+// Layout of one 32x32x16 product (64 lanes): A fragment of lane l = row l%32,
+// k = 8(l/32) + j; B fragment = column l%32, k = 8(l/32) + j; accumulator of
+// lane l = column l%32, rows 8(r/4) + 4(l/32) + r%4.  The sums over k may run
+// in any order if both operands agree on it: a finished 32x32 score tile
+// (its rows the next product's k) is used as the B operand as it lies in the
+// registers, with slot j of half h standing for k = 8(j/4) + 4h + j%4, and
+// frag_cols() reads the A operand in that order.
+#pragma once
+
+#include "context.h"
+
+namespace sn {
+
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kAttnThreads = 256;   // four wavefronts
+constexpr int kLutMax = 2048;       // entries of a position table (SN_MAX_BUCKET_SPAN + 2)
+
+template <int NP>
+struct RowOf { using T = float; };
+template <>
+struct RowOf<1> { using T = bf16; };
+
+// Eight consecutive elements of a row as NP planes.
+template <int NP>
+struct Frag { bf16x8 p[NP]; };
+
+template <int NP>
+__device__ inline Frag<NP> split8f(const float (&x)[8]) {
+    Frag<NP> f;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        float r[2] = {x[j], x[j + 1]};
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const bf16x2 h = __builtin_convertvector((floatx2{r[0], r[1]}), bf16x2);
+            f.p[n][j] = h[0];
+            f.p[n][j + 1] = h[1];
+            r[0] -= (float)h[0];
+            r[1] -= (float)h[1];
+        }
+    }
+    return f;
+}
+
+template <int NP>
+__device__ inline floatx16 mma(const Frag<NP> &a, const Frag<NP> &b, floatx16 c) {
+    if constexpr (NP == 3) {   // the small terms first
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
+    }
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
+}
+
+// Ends a chain of products whose sums vector instructions read next: the
+// hardware does not hold such a read back until the last product is through
+// (11 wait states for eight passes), and where a branch lies between, the
+// compiler (ROCm 7.2) was seen to count the waits along its longer side only,
+// so that the last registers were read early.  Here they pass through this
+// block, in the chain's own straight line.
+__device__ inline void settle(floatx16 &x) { asm volatile("s_nop 7\n\ts_nop 3" : "+v"(x)); }
+
+// --------------------------------------------------------------- tiles in LDS
+
+// A tile row holds DP elements in chunks of eight (16 bytes); chunk c of row
+// r lies at position c ^ swizzle(r).  Sixteen rows read at one chunk, and
+// four rows from a multiple of four read over four chunks, each touch every
+// bank once.
+template <int DP>
+__device__ inline int swizzle(int row) {
+    if constexpr (DP == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+    if constexpr (DP == 64) return ((row & 2) << 1) | ((row >> 2) & 3);
+    return (row >> 2) & 3;
+}
+template <int DP>
+__device__ inline int tile_at(int row, int chunk) {
+    return row * DP + ((chunk ^ swizzle<DP>(row)) << 3);
+}
+
+// Rows row0 .. row0 + 31, elements 16 s + 8 (l/32) ..: an A operand whose
+// rows are tile rows.  Planes lie `plane` elements apart.
+template <int NP, int DP>
+__device__ inline Frag<NP> frag_rows(const bf16 *tile, int plane, int row0, int s, int lane) {
+    Frag<NP> f;
+    const int at = tile_at<DP>(row0 + (lane & 31), 2 * s + (lane >> 5));
+#pragma unroll
+    for (int n = 0; n < NP; ++n) f.p[n] = *reinterpret_cast<const bf16x8 *>(tile + n * plane + at);
+    return f;
+}
+
+// Elements 32 e .. 32 e + 31 as rows, tile rows row0 .. row0 + 15 as k in the
+// order of a score tile's registers: the transposing LDS read hands lane i
+// of sixteen the column i of the 4 x 16 block that the sixteen lanes address.
+template <int NP, int DP>
+__device__ inline Frag<NP> frag_cols(const bf16 *tile, int plane, int row0, int e, int lane) {
+    Frag<NP> f;
+    const int i = lane & 15, row = row0 + 4 * (lane >> 5) + (i >> 2);
+    const int d = 32 * e + (lane & 16) + 4 * (i & 3);
+    typedef __attribute__((address_space(3))) short4v *lds4;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4)(tile + n * plane + tile_at<DP>(row, d >> 3) + (d & 7)));
+        short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4)(tile + n * plane + tile_at<DP>(row + 8, d >> 3) + (d & 7)));
+        const bf16x4 a = __builtin_bit_cast(bf16x4, lo), b = __builtin_bit_cast(bf16x4, hi);
+        f.p[n] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return f;
+}
+
+// Eight elements at `p` (elements d .. d + 7 of a row of D; zero beyond D),
+// as loaded.  vec: the row and its strides are 16-byte aligned and D is a
+// multiple of eight.
+template <int NP>
+struct Raw8 {
+    float4 v[NP == 1 ? 1 : 2];
+};
+template <int NP>
+__device__ inline Raw8<NP> raw_zero() {
+    Raw8<NP> r;
+    r.v[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (NP == 3) r.v[1] = r.v[0];
+    return r;
+}
+template <int NP>
+__device__ inline Raw8<NP> load8(const typename RowOf<NP>::T *p, int d, int D, bool vec) {
+    Raw8<NP> r = raw_zero<NP>();
+    if (d >= D) return r;
+    if (vec) {
+        r.v[0] = *reinterpret_cast<const float4 *>(p);
+        if constexpr (NP == 3) r.v[1] = *reinterpret_cast<const float4 *>(p + 4);
+    } else if constexpr (NP == 1) {
+        bf16x8 t;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = d + j < D ? p[j] : (bf16)0.0f;
+        r.v[0] = __builtin_bit_cast(float4, t);
+    } else {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = d + j < D ? p[j] : 0.0f;
+        r.v[0] = make_float4(t[0], t[1], t[2], t[3]);
+        r.v[1] = make_float4(t[4], t[5], t[6], t[7]);
+    }
+    return r;
+}
+template <int NP>
+__device__ inline Frag<NP> to_frag(const Raw8<NP> &r) {
+    if constexpr (NP == 1) {
+        Frag<1> f;
+        f.p[0] = __builtin_bit_cast(bf16x8, r.v[0]);
+        return f;
+    } else {
+        const float x[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+        return split8f<NP>(x);
+    }
+}
+
+// One tile of R rows on its way from global memory to LDS, by NT threads:
+// load() issues the reads into registers, store() splits and writes them.
+template <int NP, int DP, int R, int NT>
+struct TileMove {
+    static constexpr int CH = DP / 8, IT = (R * CH + NT - 1) / NT;
+    Raw8<NP> raw[IT];
+    uint8_t kept[IT];
+    // rows row0 .. row0 + R - 1 of base (element rows `stride` apart), those
+    // from `n` on zero; keep (may be null): rows with keep[row] = 0 are zero
+    // (cleared by store(): nothing here waits for a load)
+    __device__ inline void load(const typename RowOf<NP>::T *base, int64_t stride, int row0, int n, int D, bool vec,
+                                int tid, const uint8_t *keep) {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int c = tid + it * NT, row = row0 + c / CH, d = (c % CH) * 8;
+            raw[it] = raw_zero<NP>();
+            kept[it] = 1;
+            if (row < n && (IT * NT == R * CH || c < R * CH)) {
+                raw[it] = load8<NP>(base + (int64_t)row * stride + d, d, D, vec);
+                if (keep) kept[it] = keep[row];
+            }
+        }
+    }
+    __device__ inline void store(bf16 *tile, int tid) const {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int c = tid + it * NT;
+            if (IT * NT != R * CH && c >= R * CH) continue;
+            const Frag<NP> f = to_frag<NP>(kept[it] ? raw[it] : raw_zero<NP>());
+            const int at = tile_at<DP>(c / CH, c % CH);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8 *>(tile + n * R * DP + at) = f.p[n];
+        }
+    }
+};
+
+// --------------------------------------------------------------- wavefront sums
+
+// Smallest value over the 64 lanes, in every lane (DPP row shifts and row
+// broadcasts: no LDS traffic).
+__device__ inline int wave_min(int v) {
+    v = min(v, __builtin_amdgcn_update_dpp(v, v, 0x111, 0xf, 0xf, false));
+    v = min(v, __builtin_amdgcn_update_dpp(v, v, 0x112, 0xf, 0xf, false));
+    v = min(v, __builtin_amdgcn_update_dpp(v, v, 0x114, 0xf, 0xf, false));
+    v = min(v, __builtin_amdgcn_update_dpp(v, v, 0x118, 0xf, 0xf, false));
+    v = min(v, __builtin_amdgcn_update_dpp(v, v, 0x142, 0xf, 0xf, false));
+    v = min(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xf, 0xf, false));
+    return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ inline int wave_max(int v) { return ~wave_min(~v); }
+
+// The value of the lane's other half (lane ^ 32).
+__device__ inline float half_swap(float v) { return __shfl_xor(v, 32, 64); }
+
+// A value that is the same in every lane, in scalar registers.
+__device__ inline uint64_t uniform64(uint64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | lo;
+}
+
+// --------------------------------------------------------------- positions
+
+__device__ inline int bucket_of(const AttnArgs &a, int rel) {
+    int n = 0;
+    for (int t = 0; t + 1 < a.nb; ++t) n += rel >= a.thr[t];
+    return n;
+}
+// Entry of the position table for one offset: the table holds every offset
+// from below the first threshold to the last one, its ends stand for all
+// beyond.
+__device__ inline int lut_index(const AttnArgs &a, int rel) {
+    return min(max(rel, a.lut_base), a.lut_base + (a.lut_n - 1)) - a.lut_base;
+}
+__device__ inline int offset_of(int k_pos, int q_pos) { return __builtin_elementwise_sub_sat(k_pos, q_pos); }
+
+// --------------------------------------------------------------- rows of a block
+
+// The queries of a segment and the heads of a subgroup (gs heads of one
+// key/value head) form one list of rows, r = query gs + head: a query's
+// heads read the same keys, so few queries still fill a tile.
+struct RowBlock {
+    int b, hk, sub, split, tile;   // segment, key/value head, subgroup, key split, row tile
+    int q0, nq, k0, nk;            // the segment's rows
+    int h0, gs;                    // first head, heads of the subgroup
+};
+
+// The block's place in the batch; false where there is nothing to do.
+// Row tiles are the fastest index and xcd_block() keeps neighbours on one
+// XCD, so the tiles that read the same keys share an L2.
+__device__ inline bool locate(const AttnArgs &a, RowBlock &w) {
+    const int n = a.B * a.Hkv * a.subs * a.splits * a.row_tiles;
+    int i = xcd_block(n);
+    if (i < 0) return false;
+    w.tile = i % a.row_tiles; i /= a.row_tiles;
+    w.split = i % a.splits; i /= a.splits;
+    w.sub = i % a.subs; i /= a.subs;
+    w.hk = i % a.Hkv;
+    w.b = i / a.Hkv;
+    w.h0 = w.hk * a.G + w.sub * a.Gs;
+    w.gs = min(a.Gs, a.G - w.sub * a.Gs);
+    segment_rows(a.q_ptr, w.b, a.B, a.n_q, a.max_q, a.status, w.q0, w.nq);
+    segment_rows(a.k_ptr, w.b, a.B, a.n_k, a.max_k, a.status, w.k0, w.nk);
+    return true;
+}
+
+// Key positions and the kept keys of a tile, by one wavefront (lane = key).
+template <int KT>
+struct KeyInfo {
+    int pos[KT];
+    int lo, hi;
+    uint64_t mask;
+};
+struct KeyLoad {
+    int pos;
+    bool ok;
+    __device__ inline void load(const AttnArgs &a, const RowBlock &w, int key0, int KT, int lane) {
+        const int j = key0 + lane;
+        ok = lane < KT && j < w.nk;
+        pos = j;
+        if (ok) {
+            if (a.k_pos) pos = a.k_pos[w.k0 + j];
+            if (a.keep) ok = a.keep[w.k0 + j] != 0;
+        }
+    }
+    template <int KT>
+    __device__ inline void store(KeyInfo<KT> &k, int lane) const {
+        const uint64_t mask = __ballot(ok);
+        const int lo = wave_min(ok ? pos : 0x7fffffff), hi = wave_max(ok ? pos : (int)0x80000000);
+        if (lane < KT) k.pos[lane] = pos;
+        if (lane == 0) {
+            k.lo = lo;
+            k.hi = hi;
+            k.mask = mask;
+        }
+    }
+};
+
+}  // namespace sn

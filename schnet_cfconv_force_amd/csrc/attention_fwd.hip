@@ -1,0 +1,442 @@
+// Cross attention with a learned relative position bias, forward.
+//
+//   s_ij = scale q_i.k_j + bias[bucket(k_pos_j - q_pos_i)],  o_i = sum_j softmax_j(s_ij) v_j
+//
+// One pass over the keys with the running maximum m, sum l and unnormalised
+// row O: a tile's p = 2^(s log2e - m) joins as O += p v, l += sum p, and when
+// m rises by more than 8 both are scaled by 2^(m_old - m_new) (a smaller
+// rise is left in p, which stays below 2^8).
+//
+// A wavefront owns 32 rows.  It computes S^T = K Q^T, so a lane holds one
+// row's scores: the maximum and sum are register operations and one exchange
+// with the lane's other half, m and l are one register each, and the score
+// tile is the B operand of O^T += V^T P^T as it lies.
+#include <algorithm>
+
+#include "attention.h"
+
+namespace sn {
+namespace {
+
+struct FwdOut {
+    void *o;
+    float *lse;
+    float *part_o;      // [split][n_q H][D] unnormalised rows (splits > 1)
+    float2 *part_ml;    // [split][n_q H] their maximum (log2) and sum
+};
+
+// Position table of the subgroup's heads, in log2 units.
+__device__ inline void fill_lut(const AttnArgs &a, const RowBlock &w, float *lut) {
+    for (int e = threadIdx.x; e < a.lut_n; e += blockDim.x) {
+        const int bk = bucket_of(a, a.lut_base + e);
+        for (int g = 0; g < w.gs; ++g) lut[g * a.lut_n + e] = a.bias[(int64_t)(w.h0 + g) * a.nb + bk] * kLog2e;
+    }
+}
+
+// What a wavefront keeps of its 32 rows (a lane: row lane % 32).
+template <int NP, int DP>
+struct RowState {
+    Frag<NP> q[DP / 16];
+    floatx16 o[DP / 32];
+    float m, l;
+    int row, g, pos;        // query row (-1: none), head of the subgroup, position
+    int pos_lo, pos_hi;     // of the wavefront's rows
+    float c;                // |scale| log2e; the sign of the scale is in q
+
+    __device__ inline void init(const AttnArgs &a, const RowBlock &w, int r0, int lane) {
+        using T = typename RowOf<NP>::T;
+        const int r = r0 + (lane & 31), qi = r / w.gs;
+        g = r % w.gs;
+        row = qi < w.nq ? w.q0 + qi : -1;
+        pos = 0;
+        const bool neg = a.scale < 0.0f;
+        c = fabsf(a.scale) * kLog2e;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+            const int d = 16 * s + 8 * (lane >> 5);
+            Raw8<NP> raw = raw_zero<NP>();
+            if (row >= 0)
+                raw = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + g) * a.qh + d, d, a.D, a.vec & 1);
+            q[s] = to_frag<NP>(raw);
+            if (neg)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) q[s].p[n] = -q[s].p[n];
+        }
+        if (row >= 0) pos = a.q_pos ? a.q_pos[row] : qi;
+        pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff);
+        pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[e][i] = 0.0f;
+    }
+
+    // One tile of KT keys (KT / 32 score tiles).  mask: the kept keys;
+    // key_pos: their positions in LDS, between lo and hi.
+    template <int KT>
+    __device__ inline void step(const AttnArgs &a, const bf16 *kt, const bf16 *vt, uint64_t mask, const int *key_pos,
+                                int key_lo, int key_hi, const float *lut, int lane) {
+        constexpr int NS = KT / 32;
+        const int lo = __builtin_amdgcn_readfirstlane(key_lo), hi = __builtin_amdgcn_readfirstlane(key_hi);
+        const int half = lane >> 5;
+        floatx16 s[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                s[u] = mma<NP>(frag_rows<NP, DP>(kt, KT * DP, 32 * u, k, lane), q[k], s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < NS; ++u) settle(s[u]);
+        float add = 0.0f;
+        bool table = false;
+        if (a.nb) {
+            // every offset of the tile in one bucket: one bias for all of it
+            const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
+            add = lut[g * a.lut_n + first];
+            table = first != last;
+        }
+        if (table) {
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int at = lut_index(a, offset_of(key_pos[32 * u + 8 * (i / 4) + 4 * half + i % 4], pos));
+                    s[u][i] = fmaf(s[u][i], c, lut[g * a.lut_n + at]);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[u][i] = fmaf(s[u][i], c, add);
+        }
+        if (mask != (KT == 64 ? ~0ull : 0xffffffffull)) {
+            const uint64_t mine = mask >> (4 * half);
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!((mine >> (32 * u + 8 * (i / 4) + i % 4)) & 1)) s[u][i] = -INFINITY;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
+        mx = fmaxf(mx, half_swap(mx));
+        if (__any(mx > m + 8.0f)) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);   // both -inf: nothing to scale
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[e][i] *= f;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;   // a row without a key so far: p = 2^-inf = 0
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[u][i] = __builtin_amdgcn_exp2f(s[u][i] - base);
+                l += s[u][i];
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = s[u][8 * t + j];
+                // bf16 rows: p is rounded to 8 bits here, at most 2^-8 of each
+                // term of O, as much as rounding o itself costs
+                const Frag<NP> p = split8f<NP>(x);
+#pragma unroll
+                for (int e = 0; e < DP / 32; ++e)
+                    o[e] = mma<NP>(frag_cols<NP, DP>(vt, KT * DP, 32 * u + 16 * t, e, lane), p, o[e]);
+            }
+        }
+    }
+};
+
+// One finished row: O / l, or the partial row of a key split.
+template <int NP>
+__device__ inline void write_row4(const AttnArgs &a, const FwdOut &out, int split, int64_t at, int d, floatx4 v,
+                                  float inv) {
+    using T = typename RowOf<NP>::T;
+    if (a.splits > 1) {
+        float *p = out.part_o + ((int64_t)split * a.n_q * a.H + at) * a.D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d + i < a.D) p[d + i] = v[i];
+        return;
+    }
+    T *o = (T *)out.o + at * a.D;
+    v *= inv;
+    if (a.D % 4 == 0) {   // rows are then aligned for four elements
+        if (d >= a.D) return;
+        if constexpr (NP == 1)
+            *reinterpret_cast<bf16x4 *>(o + d) = __builtin_convertvector(v, bf16x4);
+        else
+            *reinterpret_cast<floatx4 *>(o + d) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (d + i < a.D) o[d + i] = (T)v[i];
+}
+
+__device__ inline void write_stats(const AttnArgs &a, const FwdOut &out, int split, int64_t at, float m, float l) {
+    if (a.splits > 1)
+        out.part_ml[(int64_t)split * a.n_q * a.H + at] = make_float2(m, l);
+    else if (out.lse)
+        out.lse[at] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Many rows: each wavefront owns 32 of the block's 128 rows and all of them
+// read the same key tiles, staged in LDS while the tile before is computed.
+template <int NP, int DP, int KT>
+__global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
+    using T = typename RowOf<NP>::T;
+    constexpr int kTile = NP * KT * DP;
+    __shared__ bf16 tiles[2][2][kTile];   // [buffer][K, V]
+    __shared__ KeyInfo<KT> info[2];
+    __shared__ float lut[kLutMax];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    RowBlock w;
+    if (!locate(a, w)) return;
+    if (w.tile * 128 >= w.nq * w.gs) return;
+    if (a.nb) fill_lut(a, w, lut);
+    const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
+    const uint8_t *keep = a.keep ? a.keep + w.k0 : nullptr;
+    const int n_tiles = (w.nk + KT - 1) / KT, per = (n_tiles + a.splits - 1) / a.splits;
+    const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
+
+    RowState<NP, DP> st;
+    st.init(a, w, w.tile * 128 + wave * 32, lane);
+    const bool active = __any(st.row >= 0);
+    TileMove<NP, DP, KT, kAttnThreads> mk, mv;
+    KeyLoad kl;
+    auto load = [&](int t) {
+        mk.load(K, a.ks, t * KT, w.nk, a.D, a.vec & 2, tid, keep);
+        mv.load(V, a.vs, t * KT, w.nk, a.D, a.vec & 4, tid, keep);
+        if (wave == 0) kl.load(a, w, t * KT, KT, lane);
+    };
+    auto store = [&](int buf) {
+        mk.store(tiles[buf][0], tid);
+        mv.store(tiles[buf][1], tid);
+        if (wave == 0) kl.store(info[buf], lane);
+    };
+    if (t0 < t1) {
+        load(t0);
+        store(0);
+    }
+    __syncthreads();
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
+        if (t + 1 < t1) load(t + 1);
+        const KeyInfo<KT> &ki = info[buf];
+        const uint64_t mask = uniform64(ki.mask);
+        if (active && mask)
+            st.template step<KT>(a, tiles[buf][0], tiles[buf][1], mask, ki.pos, ki.lo, ki.hi, lut, lane);
+        if (t + 1 < t1) store(buf ^ 1);
+        __syncthreads();
+    }
+    if (st.row < 0) return;
+    const float l = st.l + half_swap(st.l), inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int64_t at = (int64_t)st.row * a.H + w.h0 + st.g;
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            write_row4<NP>(a, out, w.split, at, 32 * e + 8 * i + 4 * (lane >> 5),
+                           floatx4{st.o[e][4 * i], st.o[e][4 * i + 1], st.o[e][4 * i + 2], st.o[e][4 * i + 3]}, inv);
+    if (lane < 32) write_stats(a, out, w.split, at, st.m, l);
+}
+
+// Few rows (at most 32 of a key/value head's subgroup): every wavefront
+// holds all of them and takes every NW-th tile of 32 keys, with tiles of its
+// own in LDS, so no wavefront waits for another until the rows are joined at
+// the end.  The keys and values are read once, and that is what bounds it.
+template <int NP, int DP, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut out) {
+    using T = typename RowOf<NP>::T;
+    constexpr int kTile = NP * 32 * DP;
+    constexpr int kJoin = DP * 33 * 2;   // O^T of all rows in fp32, as bf16 elements
+    constexpr int kLds = 2 * NW * kTile > kJoin ? 2 * NW * kTile : kJoin;
+    __shared__ __align__(16) bf16 lds[kLds];
+    __shared__ KeyInfo<32> info[NW];
+    __shared__ float lut[kLutMax];
+    __shared__ float wave_m[NW][32], wave_l[NW][32];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    RowBlock w;
+    if (!locate(a, w)) return;
+    if (w.tile * 32 >= w.nq * w.gs) return;
+    const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
+    const uint8_t *keep = a.keep ? a.keep + w.k0 : nullptr;
+    const int n_tiles = (w.nk + 31) / 32, per = (n_tiles + a.splits - 1) / a.splits;
+    const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
+    bf16 *kt = lds + 2 * wave * kTile, *vt = kt + kTile;
+
+    TileMove<NP, DP, 32, 64> mk, mv;
+    KeyLoad kl;
+    auto load = [&](int t) {
+        mk.load(K, a.ks, t * 32, w.nk, a.D, a.vec & 2, lane, keep);
+        mv.load(V, a.vs, t * 32, w.nk, a.D, a.vec & 4, lane, keep);
+        kl.load(a, w, t * 32, 32, lane);
+    };
+    int t = t0 + wave;
+    if (t < t1) load(t);
+    if (a.nb) fill_lut(a, w, lut);
+    RowState<NP, DP> st;
+    st.init(a, w, w.tile * 32, lane);
+    __syncthreads();
+    for (; t < t1; t += NW) {
+        mk.store(kt, lane);
+        mv.store(vt, lane);
+        kl.store(info[wave], lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (t + NW < t1) load(t + NW);
+        const KeyInfo<32> &ki = info[wave];
+        const uint64_t mask = uniform64(ki.mask);
+        if (mask) st.template step<32>(a, kt, vt, mask, ki.pos, ki.lo, ki.hi, lut, lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    // join the wavefronts' rows, in their order
+    const float lw = st.l + half_swap(st.l);
+    if (lane < 32) {
+        wave_m[wave][lane] = st.m;
+        wave_l[wave][lane] = lw;
+    }
+    __syncthreads();
+    float m = -INFINITY, l = 0.0f;
+    for (int v = 0; v < NW; ++v) m = fmaxf(m, wave_m[v][lane & 31]);
+    for (int v = 0; v < NW; ++v)
+        if (wave_l[v][lane & 31] > 0.0f || wave_l[v][lane & 31] != wave_l[v][lane & 31])
+            l += wave_l[v][lane & 31] * __builtin_amdgcn_exp2f(wave_m[v][lane & 31] - m);
+    const float f = st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m);
+    float *rows = reinterpret_cast<float *>(lds);   // [DP][33]
+    for (int v = 0; v < NW; ++v) {
+        if (wave == v)
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float &x = rows[(32 * e + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)];
+                    x = v == 0 ? st.o[e][i] * f : fmaf(st.o[e][i], f, x);
+                }
+        __syncthreads();
+    }
+    if (tid < 32 && st.row >= 0) {
+        wave_l[0][lane] = l > 0.0f ? 1.0f / l : 0.0f;
+        write_stats(a, out, w.split, (int64_t)st.row * a.H + w.h0 + st.g, m, l);
+    }
+    __syncthreads();
+    const int n = min(32, w.nq * w.gs - w.tile * 32);
+    for (int i = tid; i < n * (DP / 4); i += 64 * NW) {
+        const int r = i / (DP / 4), d = (i % (DP / 4)) * 4, rr = w.tile * 32 + r;
+        const int64_t at = (int64_t)(w.q0 + rr / w.gs) * a.H + w.h0 + rr % w.gs;
+        write_row4<NP>(a, out, w.split, at, d,
+                       floatx4{rows[d * 33 + r], rows[(d + 1) * 33 + r], rows[(d + 2) * 33 + r], rows[(d + 3) * 33 + r]},
+                       wave_l[0][r]);
+    }
+}
+
+// Join the key splits of a row: one wavefront per row and head.
+template <int NP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, FwdOut out) {
+    using T = typename RowOf<NP>::T;
+    const int64_t rows = (int64_t)a.n_q * a.H, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (at >= rows) return;
+    float m = -INFINITY, l = 0.0f;
+    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, out.part_ml[k * rows + at].x);
+    float acc[2] = {0.0f, 0.0f};
+    for (int k = 0; k < a.splits; ++k) {
+        const float2 p = out.part_ml[k * rows + at];
+        if (p.x == -INFINITY) continue;   // no key in this split: its row was not computed
+        const float f = __builtin_amdgcn_exp2f(p.x - m);
+        l = fmaf(p.y, f, l);
+        for (int u = 0; u < 2; ++u)
+            if (lane + 64 * u < a.D) acc[u] = fmaf(out.part_o[(k * rows + at) * a.D + lane + 64 * u], f, acc[u]);
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    for (int u = 0; u < 2; ++u) {
+        const int d = lane + 64 * u;
+        if (d >= a.D) continue;
+        ((T *)out.o)[at * a.D + d] = (T)(acc[u] * inv);
+    }
+    if (lane == 0 && out.lse) out.lse[at] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// How the rows are cut: few rows or many, row tiles, key splits.
+struct FwdPlan {
+    bool few;
+    int Gs, subs, row_tiles, splits;
+};
+
+FwdPlan fwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
+    FwdPlan p;
+    p.Gs = std::max(1, std::min({8, G, kLutMax / std::max(1, lut_n)}));
+    p.subs = (G + p.Gs - 1) / p.Gs;
+    p.few = (int64_t)max_q * p.Gs <= 32;
+    p.row_tiles = std::max<int64_t>(1, ((int64_t)max_q * p.Gs + (p.few ? 31 : 127)) / (p.few ? 32 : 128));
+    const int64_t blocks = (int64_t)B * Hkv * p.subs * p.row_tiles;
+    const int64_t want = p.few ? 1024 : 512, least = p.few ? 512 : 256;   // keys that a split is worth
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(want / blocks, max_k / least));
+    return p;
+}
+
+template <int NP, int DP>
+sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
+    const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
+    constexpr int NW = NP == 3 && DP == 128 ? 2 : 4;
+    if (few)
+        attn_few_kernel<NP, DP, NW><<<grid, 64 * NW, 0, s>>>(a, out);
+    else
+        attn_rows_kernel<NP, DP, NP == 1 ? 64 : 32><<<grid, kAttnThreads, 0, s>>>(a, out);
+    SN_TRY(launch_status());
+    if (a.splits > 1) {
+        attn_join_kernel<NP><<<(int)(((int64_t)a.n_q * a.H + 3) / 4), 256, 0, s>>>(a, out);
+        SN_TRY(launch_status());
+    }
+    return SN_OK;
+}
+
+template <int NP>
+sn_status launch_dim(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
+    if (a.D <= 32) return launch<NP, 32>(a, out, few, s);
+    if (a.D <= 64) return launch<NP, 64>(a, out, few, s);
+    return launch<NP, 128>(a, out, few, s);
+}
+
+}  // namespace
+
+size_t attn_forward_workspace(const sn_cross_attention &op) {
+    // the thresholds, which are not read here, decide how many heads share a table
+    size_t splits = 1;
+    for (int heads = 1; heads <= 8; ++heads)
+        splits = std::max<size_t>(splits, fwd_plan(op.n_segments, op.n_kv_heads, op.n_heads / op.n_kv_heads, op.max_q,
+                                                   op.max_k, kLutMax / heads).splits);
+    if (splits == 1) return kWsBase;
+    const size_t rows = (size_t)op.n_q * op.n_heads;
+    return kWsBase + align256(rows * splits * sizeof(float2)) + align256(rows * splits * op.head_dim * sizeof(float));
+}
+
+sn_status attn_forward(AttnArgs a, int dtype, void *o, float *lse, char *ws, hipStream_t s) {
+    ProfScope prof(K_ATTN_FWD, s);
+    const FwdPlan p = fwd_plan(a.B, a.Hkv, a.G, a.max_q, a.max_k, a.lut_n);
+    a.Gs = p.Gs; a.subs = p.subs; a.row_tiles = p.row_tiles; a.splits = p.splits;
+    const size_t rows = (size_t)a.n_q * a.H;
+    FwdOut out{o, lse, nullptr, nullptr};
+    if (p.splits > 1) {
+        out.part_ml = reinterpret_cast<float2 *>(ws + kWsBase);
+        out.part_o = reinterpret_cast<float *>(ws + kWsBase + align256(rows * p.splits * sizeof(float2)));
+    }
+    return dtype == SN_F32 ? launch_dim<3>(a, out, p.few, s) : launch_dim<1>(a, out, p.few, s);
+}
+
+}  // namespace sn

@@ -49,13 +49,19 @@ struct AttnArgs {
     int nb;                                   // buckets (0: no bias)
     const int32_t *q_pos, *k_pos;
     int *status;
+    // derived
+    int vec;                                  // 1: q, 2: k, 4: v, 8: d_o rows are 16-byte aligned (and D % 8 = 0)
+    int Gs, subs;                             // heads of a row block's subgroup, subgroups of a key/value head
+    int row_tiles, splits;                    // row tiles of the longest segment, key splits
+    int lut_base, lut_n;                      // first offset and length of the position table
     int32_t thr[SN_MAX_BUCKETS - 1];
 };
 
-size_t attn_workspace(const sn_cross_attention &op);
-sn_status attn_forward(const AttnArgs &a, int dtype, void *o, float *o_acc, float *lse, char *ws, hipStream_t s);
-sn_status attn_backward(const AttnArgs &a, int dtype, const float *o_acc, const float *lse, void *dq, void *dk,
-                        void *dv, float *dbias, char *ws, hipStream_t s);
+size_t attn_forward_workspace(const sn_cross_attention &op);
+size_t attn_backward_workspace(const sn_cross_attention &op);
+sn_status attn_forward(AttnArgs a, int dtype, void *o, float *lse, char *ws, hipStream_t s);
+sn_status attn_backward(AttnArgs a, int dtype, const void *o, const float *lse, void *dq, void *dk, void *dv,
+                        float *dbias, char *ws, hipStream_t s);
 
 // --------------------------------------------------------------- group norm
 

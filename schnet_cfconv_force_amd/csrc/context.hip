@@ -1,5 +1,6 @@
 // C-ABI entry points of the context operators: argument checks and argument
 // packing.  The kernels are in attention.hip and norm.hip.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -52,6 +53,17 @@ sn_status check_attn(const sn_cross_attention *op) {
     return SN_OK;
 }
 
+size_t attn_workspace(const sn_cross_attention &op) {
+    return std::max(attn_forward_workspace(op), attn_backward_workspace(op));
+}
+
+// Whether every row of a tensor can be read 16 bytes at a time.
+bool rows_aligned(const sn_cross_attention &op, const void *p, int64_t stride, int64_t head_stride) {
+    const int64_t per = op.dtype == SN_F32 ? 4 : 8;
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % per == 0 && head_stride % per == 0 &&
+           op.head_dim % 8 == 0;
+}
+
 AttnArgs attn_args(const sn_cross_attention &op, void *ws) {
     AttnArgs a{};
     a.B = op.n_segments;
@@ -70,6 +82,15 @@ AttnArgs attn_args(const sn_cross_attention &op, void *ws) {
     a.q_pos = op.q_pos; a.k_pos = op.k_pos;
     a.status = reinterpret_cast<int *>(ws);
     for (int i = 0; i + 1 < a.nb; ++i) a.thr[i] = op.thresholds[i];
+    if (a.nb > 1) {   // from one below the first threshold (if there is one below) to the last
+        a.lut_base = a.thr[0] == INT32_MIN ? INT32_MIN : a.thr[0] - 1;
+        a.lut_n = (int)((int64_t)a.thr[a.nb - 2] - a.lut_base + 1);
+    } else {
+        a.lut_n = a.nb;
+    }
+    a.vec = (rows_aligned(op, op.q, op.q_stride, op.q_head_stride) ? 1 : 0) |
+            (rows_aligned(op, op.k, op.k_stride, op.k_head_stride) ? 2 : 0) |
+            (rows_aligned(op, op.v, op.v_stride, op.v_head_stride) ? 4 : 0);
     return a;
 }
 
@@ -130,32 +151,33 @@ size_t sn_cross_attention_workspace_bytes(const sn_cross_attention *op) {
     return check_attn_sizes(op) == SN_OK ? attn_workspace(*op) : 0;
 }
 
-sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *o_acc, float *lse, void *ws,
-                                     size_t ws_bytes, void *stream) {
+sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *lse, void *ws, size_t ws_bytes,
+                                     void *stream) {
     SN_TRY(check_attn(op));
     SN_TRY(check_ctx_ws(ws, ws_bytes, attn_workspace(*op)));
     if (op->n_q == 0) return SN_OK;
     if (!o || !aligned_for(o, op->dtype)) return SN_ERR_INVALID;
-    return attn_forward(attn_args(*op, ws), op->dtype, o, o_acc, lse, static_cast<char *>(ws),
+    return attn_forward(attn_args(*op, ws), op->dtype, o, lse, static_cast<char *>(ws),
                         reinterpret_cast<hipStream_t>(stream));
 }
 
-sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float *o_acc, const float *lse,
-                                      const void *d_o, int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk,
-                                      void *dv, float *dbias, void *ws, size_t ws_bytes, void *stream) {
+sn_status sn_cross_attention_backward(const sn_cross_attention *op, const void *o, const float *lse, const void *d_o,
+                                      int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk, void *dv,
+                                      float *dbias, void *ws, size_t ws_bytes, void *stream) {
     SN_TRY(check_attn(op));
     SN_TRY(check_ctx_ws(ws, ws_bytes, attn_workspace(*op)));
-    if (op->n_q > 0 && (!o_acc || !lse || !d_o || !dq)) return SN_ERR_INVALID;
+    if (op->n_q > 0 && (!o || !lse || !d_o || !dq)) return SN_ERR_INVALID;
     if (op->n_k > 0 && (!dk || !dv)) return SN_ERR_INVALID;
     if (op->bias && !dbias) return SN_ERR_INVALID;
-    if (!aligned_for(d_o, op->dtype) || !aligned_for(dq, op->dtype) || !aligned_for(dk, op->dtype) ||
+    if (!aligned_for(o, op->dtype) || !aligned_for(d_o, op->dtype) || !aligned_for(dq, op->dtype) || !aligned_for(dk, op->dtype) ||
         !aligned_for(dv, op->dtype))
         return SN_ERR_INVALID;
     AttnArgs a = attn_args(*op, ws);
     a.d_o = d_o;
     a.gs = d_o_stride;
     a.gh = d_o_head_stride;
-    return attn_backward(a, op->dtype, o_acc, lse, dq, dk, dv, op->bias ? dbias : nullptr, static_cast<char *>(ws),
+    if (rows_aligned(*op, d_o, d_o_stride, d_o_head_stride)) a.vec |= 8;
+    return attn_backward(a, op->dtype, o, lse, dq, dk, dv, op->bias ? dbias : nullptr, static_cast<char *>(ws),
                          reinterpret_cast<hipStream_t>(stream));
 }
 

@@ -114,10 +114,10 @@ def test_attention_entry_points_refuse_before_any_gpu_work():
         return d
 
     def forward(d, o=256, ws=256, ws_bytes=1 << 40):
-        return lib.sn_cross_attention_forward(None if d is None else ctypes.byref(d), o, None, None, ws, ws_bytes, None)
+        return lib.sn_cross_attention_forward(None if d is None else ctypes.byref(d), o, None, ws, ws_bytes, None)
 
-    def backward(d, acc=256, lse=256, d_o=256, dq=256, dk=256, dv=256, dbias=256, ws=256, ws_bytes=1 << 40):
-        return lib.sn_cross_attention_backward(ctypes.byref(d), acc, lse, d_o, 128, 32, dq, dk, dv, dbias, ws, ws_bytes,
+    def backward(d, o=256, lse=256, d_o=256, dq=256, dk=256, dv=256, dbias=256, ws=256, ws_bytes=1 << 40):
+        return lib.sn_cross_attention_backward(ctypes.byref(d), o, lse, d_o, 128, 32, dq, dk, dv, dbias, ws, ws_bytes,
                                                None)
 
     assert forward(None) == sn.SN_ERR_INVALID
@@ -140,7 +140,7 @@ def test_attention_entry_points_refuse_before_any_gpu_work():
         assert forward(d, ws=ws, ws_bytes=size) == sn.SN_ERR_WORKSPACE
         assert backward(d, ws=ws, ws_bytes=size) == sn.SN_ERR_WORKSPACE
     assert forward(d, o=None) == sn.SN_ERR_INVALID and forward(d, o=257) == sn.SN_ERR_INVALID
-    for name in ("acc", "lse", "d_o", "dq", "dk", "dv", "dbias"):
+    for name in ("o", "lse", "d_o", "dq", "dk", "dv", "dbias"):
         assert backward(d, **{name: None}) == sn.SN_ERR_INVALID, name
     assert forward(desc(n_q=0, max_q=0), o=None) == sn.SN_OK          # no query rows: nothing to do
 
