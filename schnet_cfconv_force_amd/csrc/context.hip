@@ -102,8 +102,10 @@ sn_status check_norm_sizes(const sn_group_norm *op) {
         return SN_ERR_INVALID;
     if (op->dtype != SN_F32 && op->dtype != SN_BF16) return SN_ERR_INVALID;
     if (op->activation < SN_ACT_NONE || op->activation > SN_ACT_SILU) return SN_ERR_INVALID;
-    // blocks are counted in 32 bits
-    if ((int64_t)op->n_segments * op->n_channels > INT32_MAX / 64) return SN_ERR_INVALID;
+    // blocks are counted in 32 bits: at most one for 2048 elements of every segment's longest, one for each of
+    // its channels and 512 more
+    const double blocks = (double)op->max_rows * op->n_channels / 2048 + op->n_channels + 512;
+    if (blocks * op->n_segments > INT32_MAX) return SN_ERR_INVALID;
     return SN_OK;
 }
 

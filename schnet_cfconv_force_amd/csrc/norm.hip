@@ -1,15 +1,31 @@
 // Group norm with an activation over the rows of each segment, channels
-// last, forward and backward: one block per segment and group.
+// last, forward and backward.
 //
 //   xh = (x - mean) rstd, z = gamma xh + beta, y = act(z)
 //   dz = dy act'(z), dbeta = sum dz, dgamma = sum dz xh,
 //   dx = rstd (dz gamma - mean(dz gamma) - xh mean(dz gamma xh))
+//
+// A block owns a slab: some rows of a segment times a run of channels (whole
+// groups, or a piece of one that is wider than the block).  A thread owns one
+// vector of channels of the slab and every RP-th row, so per-channel
+// quantities are registers.  Where the longest segment's slab fits a block's
+// registers, one launch does everything and x (and dy) is read once.  Longer
+// segments are cut into chunks of rows: one launch leaves each chunk's
+// statistics, the next joins them and reads the rows again.
+//
+// The mean is subtracted before squaring (in the chunk by its own mean, in
+// the join by n_c (mean_c - mean)^2), so a large common offset costs no
+// digits of the variance.  All sums are fp32 in a block and fp64 in a join,
+// each in one order.
+#include <algorithm>
+
 #include "context.h"
 
 namespace sn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kMaxGroups = kThreads / 32;   // groups of a slab: 32 lanes join each
 
 __device__ inline float act_fwd(float z, int act) {
     if (act == SN_ACT_SSP) return ssp(z);
@@ -25,133 +41,731 @@ __device__ inline float act_grad(float z, int act) {
     return 1.0f;
 }
 
-__device__ inline float block_sum(float v, float *red) {
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < kThreads / 64; ++w) s += red[w];
-    return s;
+// V consecutive elements of a row, as they lie in memory.
+template <typename T, int V>
+struct Vec {
+    typedef T type __attribute__((ext_vector_type(V)));
+    type v;
+};
+template <typename T>
+struct Vec<T, 1> {
+    struct type {
+        T x;
+        __device__ inline T &operator[](int) { return x; }
+        __device__ inline T operator[](int) const { return x; }
+    };
+    type v;
+};
+template <typename T, int V>
+__device__ inline Vec<T, V> load_vec(const T *p) {
+    Vec<T, V> r;
+    r.v = *reinterpret_cast<const typename Vec<T, V>::type *>(p);
+    return r;
+}
+template <typename T, int V>
+__device__ inline void store_vec(T *p, const float (&x)[V]) {
+    typename Vec<T, V>::type t;
+#pragma unroll
+    for (int j = 0; j < V; ++j) t[j] = (T)x[j];
+    *reinterpret_cast<typename Vec<T, V>::type *>(p) = t;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void fwd_kernel(NormArgs a, T *y, float *mean, float *rstd) {
-    __shared__ float red[kThreads / 64];
-    const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+// How rows and channels are cut (host).
+struct NormCut {
+    int V;          // channels of a vector
+    int gs;         // groups of a slab (1 where a slab is a piece of a group)
+    int piece;      // channels of a piece; 0: slabs hold whole groups
+    int slabs;      // slabs of a row
+    int chunks;     // chunks of the longest segment (1: fused)
+    int chunk_rows;
+    int it;         // vectors that a thread holds of a chunk
+};
+
+// A block's slab.
+struct Slab {
+    int b, slab, chunk;
+    int r0, n;          // the segment's rows
+    int first, rows;    // the chunk's rows, relative to r0
+    int c0, cs;         // first channel, channels
+    int g0, gs;         // first group, groups
+    int piece, pieces;  // piece of the group
+    int cv, rp;         // vectors of a slab row, rows per pass
+    int col, row;       // this thread's vector (-1: none) and first row
+    int group;          // its group within the slab
+    int wv;             // vectors of one of the slab's groups
+};
+
+__device__ inline bool locate(const NormArgs &a, const NormCut &k, int block, Slab &s) {
+    s.chunk = block % k.chunks;
+    s.slab = block / k.chunks % k.slabs;
+    s.b = block / k.chunks / k.slabs;
+    segment_rows(a.ptr, s.b, a.B, a.n_rows, a.max_rows, a.status, s.r0, s.n);
+    s.first = s.chunk * k.chunk_rows;
+    s.rows = min(k.chunk_rows, s.n - s.first);
+    if (k.piece) {
+        s.pieces = k.slabs / a.groups;
+        s.piece = s.slab % s.pieces;
+        s.g0 = s.slab / s.pieces;
+        s.gs = 1;
+        s.c0 = s.g0 * a.width + s.piece * k.piece;
+        s.cs = min(k.piece, a.width - s.piece * k.piece);
+    } else {
+        s.pieces = 1;
+        s.piece = 0;
+        s.g0 = s.slab * k.gs;
+        s.gs = min(k.gs, a.groups - s.g0);
+        s.c0 = s.g0 * a.width;
+        s.cs = s.gs * a.width;
+    }
+    s.cv = s.cs / k.V;
+    s.rp = kThreads / s.cv;
+    s.wv = s.cv / s.gs;
+    const int t = threadIdx.x;
+    s.row = t / s.cv;
+    s.col = s.row < s.rp ? t % s.cv : -1;
+    s.group = s.col < 0 ? 0 : s.col / s.wv;
+    return s.rows > 0;
+}
+
+// Elements of one group in chunk c (piece p) of a segment of n rows.
+__device__ inline int64_t part_count(const NormArgs &a, const NormCut &k, int n, int c, int p) {
+    const int rows = min(k.chunk_rows, n - c * k.chunk_rows);
+    const int width = k.piece ? min(k.piece, a.width - p * k.piece) : a.width;
+    return (int64_t)max(rows, 0) * width;
+}
+
+template <typename F>
+__device__ inline F half_wave_sum(F v) {
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor(v, o, 32);
+    return v;
+}
+
+// Sums of every thread's v over the threads of its group; out[group].
+// Thirty-two lanes add a group's threads in strides, then one another.
+__device__ inline void group_sums(const Slab &s, float v, float *buf, float *out) {
+    __syncthreads();
+    buf[threadIdx.x] = v;
+    __syncthreads();
+    const int g = threadIdx.x >> 5, l = threadIdx.x & 31;
+    float sum = 0.0f;
+    if (g < s.gs)
+        for (int i = l; i < s.rp * s.wv; i += 32) sum += buf[i / s.wv * s.cv + g * s.wv + i % s.wv];
+    sum = half_wave_sum(sum);
+    if (g < s.gs && l == 0) out[g] = sum;
+    __syncthreads();
+}
+
+template <int V>
+__device__ inline void load_affine(const NormArgs &a, const Slab &s, float (&ga)[V], float (&be)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        ga[j] = 1.0f;
+        be[j] = 0.0f;
+        if (s.col >= 0) {
+            const int c = s.c0 + s.col * V + j;
+            if (a.gamma) ga[j] = a.gamma[c];
+            if (a.beta) be[j] = a.beta[c];
+        }
+    }
+}
+
+// The chunk's mean and sum of squared differences from it, per group, from
+// the vectors held in registers.
+template <typename T, int V, int IT>
+__device__ inline void chunk_stats(const NormArgs &a, const NormCut &k, const Slab &s, const Vec<T, V> (&x)[IT],
+                                   float *buf, float *mean, float *m2) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        if (s.col >= 0 && s.row + i * s.rp < s.rows)
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += to_f32(x[i].v[j]);
+    group_sums(s, sum, buf, mean);
+    const float cnt = (float)s.rows * (s.wv * V);
+    if (threadIdx.x < s.gs) mean[threadIdx.x] /= cnt;
+    __syncthreads();
+    const float mu = mean[s.group];
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        if (s.col >= 0 && s.row + i * s.rp < s.rows)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = to_f32(x[i].v[j]) - mu;
+                sum = fmaf(d, d, sum);
+            }
+    group_sums(s, sum, buf, m2);
+}
+
+template <typename T, int V, int IT>
+__device__ inline void load_rows(const NormCut &k, const Slab &s, const T *base, int64_t stride, Vec<T, V> (&x)[IT]) {
+    const T *p = base + (int64_t)(s.r0 + s.first) * stride + s.c0 + s.col * V;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[i].v[j] = (T)0.0f;
+        const int r = s.row + i * s.rp;
+        if (s.col >= 0 && r < s.rows) x[i] = load_vec<T, V>(p + r * stride);
+    }
+}
+
+template <typename T, int V>
+__device__ inline void write_y(const NormArgs &a, const Vec<T, V> &x, float mu, float r, const float (&ga)[V],
+                               const float (&be)[V], T *p) {
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = act_fwd(fmaf((to_f32(x.v[j]) - mu) * r, ga[j], be[j]), a.act);
+    store_vec<T, V>(p, y);
+}
+
+// ------------------------------------------------------------------ forward
+
+// The whole segment in registers: statistics and output in one pass.
+template <typename T, int V, int IT>
+__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut k, T *y, float *mean, float *rstd) {
+    __shared__ float buf[kThreads], mu[kMaxGroups], m2[kMaxGroups];
+    Slab s;
+    const bool any = locate(a, k, blockIdx.x, s);
+    if (!any) {   // an empty segment
+        if (threadIdx.x < s.gs) {
+            if (mean) mean[s.b * a.groups + s.g0 + threadIdx.x] = 0.0f;
+            if (rstd) rstd[s.b * a.groups + s.g0 + threadIdx.x] = 1.0f / sqrtf(a.eps);
+        }
+        return;
+    }
+    Vec<T, V> x[IT];
+    load_rows<T, V, IT>(k, s, (const T *)a.x, a.xs, x);
+    float ga[V], be[V];
+    load_affine<V>(a, s, ga, be);
+    chunk_stats<T, V, IT>(a, k, s, x, buf, mu, m2);
+    const float cnt = (float)s.rows * a.width;
+    if (threadIdx.x < s.gs) {
+        const int at = s.b * a.groups + s.g0 + threadIdx.x;
+        if (mean) mean[at] = mu[threadIdx.x];
+        if (rstd) rstd[at] = 1.0f / sqrtf(m2[threadIdx.x] / cnt + a.eps);
+    }
+    if (s.col < 0) return;
+    const float m = mu[s.group], r = 1.0f / sqrtf(m2[s.group] / cnt + a.eps);
+    T *p = y + (int64_t)s.r0 * a.C + s.c0 + s.col * V;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int row = s.row + i * s.rp;
+        if (row < s.rows) write_y<T, V>(a, x[i], m, r, ga, be, p + (int64_t)row * a.C);
+    }
+}
+
+// part [b][group][chunk pieces + piece]: the chunk's {mean, sum of squared
+// differences} of each group
+template <typename T, int V, int IT>
+__global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a, NormCut k, float2 *part) {
+    __shared__ float buf[kThreads], mu[kMaxGroups], m2[kMaxGroups];
+    Slab s;
+    if (!locate(a, k, blockIdx.x, s)) return;
+    Vec<T, V> x[IT];
+    load_rows<T, V, IT>(k, s, (const T *)a.x, a.xs, x);
+    chunk_stats<T, V, IT>(a, k, s, x, buf, mu, m2);
+    if (threadIdx.x < s.gs)
+        part[((int64_t)s.b * a.groups + s.g0 + threadIdx.x) * k.chunks * s.pieces + s.chunk * s.pieces + s.piece] =
+            make_float2(mu[threadIdx.x], m2[threadIdx.x]);
+}
+
+// Joins the chunks' statistics and writes this chunk's rows.
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCut k, const float2 *part, T *y,
+                                                              float *mean, float *rstd) {
+    __shared__ float mu[kMaxGroups], rs[kMaxGroups];
+    Slab s;
+    const bool any = locate(a, k, gridDim.x - 1 - blockIdx.x, s);   // the rows read last are the likeliest in a cache
+    if (!any && s.chunk > 0) return;
+    const int g = threadIdx.x >> 5, l = threadIdx.x & 31;
+    if (g < s.gs) {
+        const int n = (s.n + k.chunk_rows - 1) / k.chunk_rows * s.pieces;
+        const float2 *p = part + ((int64_t)s.b * a.groups + s.g0 + g) * k.chunks * s.pieces;
+        const double cnt = (double)s.n * a.width;
+        double sum = 0.0;
+        for (int i = l; i < n; i += 32) sum += (double)part_count(a, k, s.n, i / s.pieces, i % s.pieces) * p[i].x;
+        const double m = s.n ? half_wave_sum(sum) / cnt : 0.0;
+        sum = 0.0;
+        for (int i = l; i < n; i += 32) {
+            const double d = p[i].x - m;
+            sum += p[i].y + (double)part_count(a, k, s.n, i / s.pieces, i % s.pieces) * d * d;
+        }
+        const double var = s.n ? half_wave_sum(sum) / cnt : 0.0;
+        if (l == 0) {
+            mu[g] = (float)m;
+            rs[g] = 1.0f / sqrtf((float)var + a.eps);
+            if (s.chunk == 0 && s.piece == 0) {
+                if (mean) mean[s.b * a.groups + s.g0 + g] = mu[g];
+                if (rstd) rstd[s.b * a.groups + s.g0 + g] = rs[g];
+            }
+        }
+    }
+    __syncthreads();
+    if (s.col < 0 || !any) return;
+    float ga[V], be[V];
+    load_affine<V>(a, s, ga, be);
+    const float m = mu[s.group], r = rs[s.group];
+    const int64_t base = s.r0 + s.first;
+    const T *px = (const T *)a.x + base * a.xs + s.c0 + s.col * V;
+    T *py = y + base * a.C + s.c0 + s.col * V;
+#pragma unroll 4
+    for (int row = s.row; row < s.rows; row += s.rp)
+        write_y<T, V>(a, load_vec<T, V>(px + row * a.xs), m, r, ga, be, py + (int64_t)row * a.C);
+}
+
+// ------------------------------------------------------------------ backward
+
+// dz and xh of one vector.
+template <typename T, int V>
+__device__ inline void dz_xh(const NormArgs &a, const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r,
+                             const float (&ga)[V], const float (&be)[V], float (&dz)[V], float (&xh)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        xh[j] = (to_f32(x.v[j]) - mu) * r;
+        dz[j] = to_f32(dy.v[j]) * act_grad(fmaf(xh[j], ga[j], be[j]), a.act);
+    }
+}
+template <typename T, int V>
+__device__ inline void write_dx(const NormArgs &a, const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r, float m1,
+                                float m2, const float (&ga)[V], const float (&be)[V], T *p) {
+    float dz[V], xh[V];
+    dz_xh<T, V>(a, x, dy, mu, r, ga, be, dz, xh);
+#pragma unroll
+    for (int j = 0; j < V; ++j) dz[j] = r * (dz[j] * ga[j] - m1 - xh[j] * m2);
+    store_vec<T, V>(p, dz);
+}
+
+// Sums over the block's rows of every channel's two values: threads write
+// theirs to buf [2][rp][cs], then kThreads / cs threads per channel add the
+// rows in strides into buf's head, then one thread the rest.  out [2][cs].
+template <int V>
+__device__ inline void channel_sums(const Slab &s, const float (&sx)[V], const float (&sz)[V], float *buf, float *join,
+                                    float *out) {
+    const int t = threadIdx.x;
+    if (s.col >= 0)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            buf[s.row * s.cs + s.col * V + j] = sx[j];
+            buf[(s.rp + s.row) * s.cs + s.col * V + j] = sz[j];
+        }
+    __syncthreads();
+    const int parts = max(1, min(kThreads / s.cs, s.rp));
+    for (int i = t; i < parts * s.cs; i += kThreads) {
+        const int c = i % s.cs, q = i / s.cs;
+        float x = 0.0f, z = 0.0f;
+        for (int r = q; r < s.rp; r += parts) {
+            x += buf[r * s.cs + c];
+            z += buf[(s.rp + r) * s.cs + c];
+        }
+        if (parts == 1) {
+            out[c] = x;
+            out[s.cs + c] = z;
+        } else {
+            join[q * s.cs + c] = x;
+            join[(parts + q) * s.cs + c] = z;
+        }
+    }
+    __syncthreads();
+    if (parts > 1) {
+        for (int c = t; c < s.cs; c += kThreads) {
+            float x = 0.0f, z = 0.0f;
+            for (int q = 0; q < parts; ++q) {
+                x += join[q * s.cs + c];
+                z += join[(parts + q) * s.cs + c];
+            }
+            out[c] = x;
+            out[s.cs + c] = z;
+        }
+        __syncthreads();
+    }
+}
+
+template <int V>
+struct ChannelLds {
+    float buf[2 * kThreads * V];
+    float join[2 * kThreads];
+    float out[2 * kThreads * V];
+};
+
+// The whole segment in registers.  seg [b][2][C]: its sums of dz xh and dz.
+template <typename T, int V, int IT>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut k, const float *mean,
+                                                            const float *rstd, T *dx, float *seg) {
+    __shared__ ChannelLds<V> lds;
+    __shared__ float gm[2][kMaxGroups];
+    Slab s;
+    const bool any = locate(a, k, blockIdx.x, s);
+    if (!any) {
+        for (int c = threadIdx.x; c < s.cs; c += kThreads) {
+            seg[(int64_t)s.b * 2 * a.C + s.c0 + c] = 0.0f;
+            seg[((int64_t)s.b * 2 + 1) * a.C + s.c0 + c] = 0.0f;
+        }
+        return;
+    }
+    Vec<T, V> x[IT], dy[IT];
+    load_rows<T, V, IT>(k, s, (const T *)a.x, a.xs, x);
+    load_rows<T, V, IT>(k, s, (const T *)a.dy, a.dys, dy);
+    float ga[V], be[V], sx[V], sz[V];
+    load_affine<V>(a, s, ga, be);
+    const float mu = mean[s.b * a.groups + s.g0 + s.group], r = rstd[s.b * a.groups + s.g0 + s.group];
+#pragma unroll
+    for (int j = 0; j < V; ++j) sx[j] = sz[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        if (s.row + i * s.rp < s.rows) {
+            float dz[V], xh[V];
+            dz_xh<T, V>(a, x[i], dy[i], mu, r, ga, be, dz, xh);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                sx[j] = fmaf(dz[j], xh[j], sx[j]);
+                sz[j] += dz[j];
+            }
+        }
+    channel_sums<V>(s, sx, sz, lds.buf, lds.join, lds.out);
+    for (int c = threadIdx.x; c < s.cs; c += kThreads) {
+        seg[(int64_t)s.b * 2 * a.C + s.c0 + c] = lds.out[c];
+        seg[((int64_t)s.b * 2 + 1) * a.C + s.c0 + c] = lds.out[s.cs + c];
+    }
+    const int g = threadIdx.x >> 5, l = threadIdx.x & 31;
+    if (g < s.gs) {
+        float m1 = 0.0f, m2 = 0.0f;
+        for (int c = g * a.width + l; c < (g + 1) * a.width; c += 32) {
+            const float w = a.gamma ? a.gamma[s.c0 + c] : 1.0f;
+            m2 = fmaf(w, lds.out[c], m2);
+            m1 = fmaf(w, lds.out[s.cs + c], m1);
+        }
+        m1 = half_wave_sum(m1);
+        m2 = half_wave_sum(m2);
+        if (l == 0) {
+            const float cnt = (float)s.rows * a.width;
+            gm[0][g] = m1 / cnt;
+            gm[1][g] = m2 / cnt;
+        }
+    }
+    __syncthreads();
+    if (s.col < 0) return;
+    T *p = dx + (int64_t)s.r0 * a.C + s.c0 + s.col * V;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int row = s.row + i * s.rp;
+        if (row < s.rows)
+            write_dx<T, V>(a, x[i], dy[i], mu, r, gm[0][s.group], gm[1][s.group], ga, be, p + (int64_t)row * a.C);
+    }
+}
+
+// part [b][chunk][2][C]: the chunk's sums of dz xh and dz
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, NormCut k, const float *mean,
+                                                                 const float *rstd, float *part) {
+    __shared__ ChannelLds<V> lds;
+    Slab s;
+    if (!locate(a, k, blockIdx.x, s)) return;
+    float ga[V], be[V], sx[V], sz[V];
+    load_affine<V>(a, s, ga, be);
+#pragma unroll
+    for (int j = 0; j < V; ++j) sx[j] = sz[j] = 0.0f;
+    const float mu = mean[s.b * a.groups + s.g0 + s.group], r = rstd[s.b * a.groups + s.g0 + s.group];
+    if (s.col >= 0) {
+        const int64_t base = s.r0 + s.first;
+        const T *px = (const T *)a.x + base * a.xs + s.c0 + s.col * V;
+        const T *pg = (const T *)a.dy + base * a.dys + s.c0 + s.col * V;
+#pragma unroll 4
+        for (int row = s.row; row < s.rows; row += s.rp) {
+            float dz[V], xh[V];
+            dz_xh<T, V>(a, load_vec<T, V>(px + row * a.xs), load_vec<T, V>(pg + row * a.dys), mu, r, ga, be, dz, xh);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                sx[j] = fmaf(dz[j], xh[j], sx[j]);
+                sz[j] += dz[j];
+            }
+        }
+    }
+    channel_sums<V>(s, sx, sz, lds.buf, lds.join, lds.out);
+    float *p = part + ((int64_t)s.b * k.chunks + s.chunk) * 2 * a.C + s.c0;
+    for (int c = threadIdx.x; c < s.cs; c += kThreads) {
+        p[c] = lds.out[c];
+        p[a.C + c] = lds.out[s.cs + c];
+    }
+}
+
+// Joins the chunks of a segment, one block per segment and group: seg
+// [b][2][C] and the group's means of dz gamma and dz gamma xh.
+__global__ __launch_bounds__(256) void norm_bwd_join_kernel(NormArgs a, NormCut k, const float *part, float *seg,
+                                                            float2 *gmean) {
+    __shared__ double red[2][256];
+    const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups, t = threadIdx.x;
     int r0, n;
     segment_rows(a.ptr, b, a.B, a.n_rows, a.max_rows, a.status, r0, n);
-    const T *x = (const T *)a.x + r0 * a.xs + g * a.width;
-    const int64_t cnt = (int64_t)n * a.width;
-    float s = 0.0f;
-    for (int64_t i = threadIdx.x; i < cnt; i += kThreads) s += to_f32(x[i / a.width * a.xs + i % a.width]);
-    const float mu = cnt ? block_sum(s, red) / (float)cnt : 0.0f;
-    s = 0.0f;
-    for (int64_t i = threadIdx.x; i < cnt; i += kThreads) {
-        const float d = to_f32(x[i / a.width * a.xs + i % a.width]) - mu;
-        s = fmaf(d, d, s);
-    }
-    const float var = cnt ? block_sum(s, red) / (float)cnt : 0.0f;
-    const float r = 1.0f / sqrtf(var + a.eps);
-    for (int64_t i = threadIdx.x; i < cnt; i += kThreads) {
-        const int c = g * a.width + (int)(i % a.width);
-        const float xh = (to_f32(x[i / a.width * a.xs + i % a.width]) - mu) * r;
-        const float z = fmaf(xh, a.gamma ? a.gamma[c] : 1.0f, a.beta ? a.beta[c] : 0.0f);
-        y[(r0 + i / a.width) * a.C + c] = from_f32<T>(act_fwd(z, a.act));
-    }
-    if (threadIdx.x == 0) {
-        if (mean) mean[blockIdx.x] = mu;
-        if (rstd) rstd[blockIdx.x] = r;
-    }
-}
-
-// part [B][2][C]: the sums over the segment's rows of dz xh and dz
-template <typename T>
-__global__ __launch_bounds__(kThreads) void bwd_kernel(NormArgs a, const float *mean, const float *rstd, T *dx,
-                                                       float *part) {
-    __shared__ float red[kThreads / 64];
-    const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
-    int r0, n;
-    segment_rows(a.ptr, b, a.B, a.n_rows, a.max_rows, a.status, r0, n);
-    const float mu = mean[blockIdx.x], r = rstd[blockIdx.x];
-    const T *x = (const T *)a.x, *dy = (const T *)a.dy;
-    float m1 = 0.0f, m2 = 0.0f;
-    for (int c = g * a.width; c < (g + 1) * a.width; ++c) {
-        const float ga = a.gamma ? a.gamma[c] : 1.0f, be = a.beta ? a.beta[c] : 0.0f;
-        float sx = 0.0f, sz = 0.0f;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const float xh = (to_f32(x[(int64_t)(r0 + i) * a.xs + c]) - mu) * r;
-            const float dz = to_f32(dy[(int64_t)(r0 + i) * a.dys + c]) * act_grad(fmaf(xh, ga, be), a.act);
-            sx = fmaf(dz, xh, sx);
-            sz += dz;
+    const int chunks = (n + k.chunk_rows - 1) / k.chunk_rows;
+    // 256 / w threads share a channel's chunks; wider groups go in rounds
+    const int w = min(a.width, 256), share = 256 / w;
+    double m1 = 0.0, m2 = 0.0;
+    for (int c0 = 0; c0 < a.width; c0 += w) {
+        const int c = c0 + t % w, q = t / w;
+        double x = 0.0, z = 0.0;
+        if (c < a.width && q < share)
+            for (int i = q; i < chunks; i += share) {
+                const float *p = part + ((int64_t)b * k.chunks + i) * 2 * a.C + g * a.width + c;
+                x += p[0];
+                z += p[a.C];
+            }
+        __syncthreads();
+        red[0][t] = x;
+        red[1][t] = z;
+        __syncthreads();
+        if (t < w && c < a.width) {
+            for (int i = 1; i < share; ++i) {
+                x += red[0][i * w + t];
+                z += red[1][i * w + t];
+            }
+            seg[(int64_t)b * 2 * a.C + g * a.width + c] = (float)x;
+            seg[((int64_t)b * 2 + 1) * a.C + g * a.width + c] = (float)z;
+            const double ga = a.gamma ? a.gamma[g * a.width + c] : 1.0f;
+            m2 += ga * x;
+            m1 += ga * z;
         }
-        sx = block_sum(sx, red);
-        sz = block_sum(sz, red);
-        if (threadIdx.x == 0) {
-            part[((int64_t)b * 2) * a.C + c] = sx;
-            part[((int64_t)b * 2 + 1) * a.C + c] = sz;
+    }
+    __syncthreads();
+    red[0][t] = m1;
+    red[1][t] = m2;
+    __syncthreads();
+    for (int o = 128; o > 0; o >>= 1) {
+        if (t < o) {
+            red[0][t] += red[0][t + o];
+            red[1][t] += red[1][t + o];
         }
-        m1 = fmaf(sz, ga, m1);
-        m2 = fmaf(sx, ga, m2);
+        __syncthreads();
     }
-    const float inv = n ? 1.0f / ((float)n * a.width) : 0.0f;
-    m1 *= inv;
-    m2 *= inv;
-    for (int64_t i = threadIdx.x; i < (int64_t)n * a.width; i += kThreads) {
-        const int c = g * a.width + (int)(i % a.width);
-        const int64_t row = r0 + i / a.width;
-        const float ga = a.gamma ? a.gamma[c] : 1.0f, be = a.beta ? a.beta[c] : 0.0f;
-        const float xh = (to_f32(x[row * a.xs + c]) - mu) * r;
-        const float dz = to_f32(dy[row * a.dys + c]) * act_grad(fmaf(xh, ga, be), a.act);
-        dx[row * a.C + c] = from_f32<T>(r * (dz * ga - m1 - xh * m2));
-    }
+    const double cnt = n ? (double)n * a.width : 1.0;
+    if (t == 0) gmean[blockIdx.x] = make_float2((float)(red[0][0] / cnt), (float)(red[1][0] / cnt));
 }
 
-__global__ __launch_bounds__(64) void param_kernel(int B, int C, const float *part, float *dgamma, float *dbeta) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    if (c >= C) return;
-    double sx = 0.0, sz = 0.0;
-    for (int b = 0; b < B; ++b) {
-        sx += part[((int64_t)b * 2) * C + c];
-        sz += part[((int64_t)b * 2 + 1) * C + c];
+// dgamma and dbeta of 64 channels: the segments' sums, in their order.
+__device__ inline void param_sums(int block, const NormArgs &a, const float *seg, float *dgamma, float *dbeta,
+                                  double (*red)[64]) {
+    const int t = threadIdx.x, c = block * 64 + (t & 63), q = t >> 6;
+    double x = 0.0, z = 0.0;
+    if (c < a.C)
+        for (int b = q; b < a.B; b += kThreads / 64) {
+            x += seg[(int64_t)b * 2 * a.C + c];
+            z += seg[((int64_t)b * 2 + 1) * a.C + c];
+        }
+    red[2 * q][t & 63] = x;
+    red[2 * q + 1][t & 63] = z;
+    __syncthreads();
+    if (q != 0 || c >= a.C) return;
+    for (int i = 1; i < kThreads / 64; ++i) {
+        x += red[2 * i][t];
+        z += red[2 * i + 1][t];
     }
-    if (dgamma) dgamma[c] = (float)sx;
-    if (dbeta) dbeta[c] = (float)sz;
+    if (dgamma) dgamma[c] = (float)x;
+    if (dbeta) dbeta[c] = (float)z;
 }
 
-template <typename T>
-sn_status backward_t(const NormArgs &a, const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta,
-                     char *ws, hipStream_t s) {
-    ProfScope prof(K_NORM_BWD, s);
-    float *part = reinterpret_cast<float *>(ws + kWsBase);
-    bwd_kernel<T><<<a.B * a.groups, kThreads, 0, s>>>(a, mean, rstd, (T *)dx, part);
+__global__ __launch_bounds__(kThreads) void norm_param_kernel(NormArgs a, const float *seg, float *dgamma,
+                                                              float *dbeta) {
+    __shared__ double red[kThreads / 32][64];
+    param_sums(blockIdx.x, a, seg, dgamma, dbeta, red);
+}
+
+// dx of a chunk's rows; the first `params` blocks sum dgamma and dbeta
+// instead (one launch less).
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, NormCut k, const float *mean,
+                                                                  const float *rstd, const float2 *gmean, T *dx,
+                                                                  const float *seg, float *dgamma, float *dbeta,
+                                                                  int params) {
+    __shared__ double red[kThreads / 32][64];
+    if ((int)blockIdx.x < params) {
+        param_sums(blockIdx.x, a, seg, dgamma, dbeta, red);
+        return;
+    }
+    Slab s;
+    if (!locate(a, k, gridDim.x - 1 - blockIdx.x, s) || s.col < 0) return;
+    float ga[V], be[V];
+    load_affine<V>(a, s, ga, be);
+    const int at = s.b * a.groups + s.g0 + s.group;
+    const float mu = mean[at], r = rstd[at];
+    const float2 m = gmean[at];
+    const int64_t base = s.r0 + s.first;
+    const T *px = (const T *)a.x + base * a.xs + s.c0 + s.col * V;
+    const T *pg = (const T *)a.dy + base * a.dys + s.c0 + s.col * V;
+    T *pd = dx + base * a.C + s.c0 + s.col * V;
+#pragma unroll 4
+    for (int row = s.row; row < s.rows; row += s.rp)
+        write_dx<T, V>(a, load_vec<T, V>(px + row * a.xs), load_vec<T, V>(pg + row * a.dys), mu, r, m.x, m.y, ga, be,
+                       pd + (int64_t)row * a.C);
+}
+
+// ------------------------------------------------------------------ launches
+
+constexpr int kHold = 16;        // vectors that a thread of a fused launch can hold
+constexpr int kHoldStats = 8;    // of a chunk
+constexpr int kWantBlocks = 512; // two for every CU
+
+// V: the widest vector that divides a group and suits every tensor.
+NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V) {
+    NormCut k{};
+    const int width = C / groups;
+    k.V = V;
+    const int wv = width / V;
+    auto whole = [&](int bytes) {   // groups of a slab of about that many bytes a row
+        const int want = std::max(1, (bytes + width * es - 1) / (width * es));
+        return std::max(1, std::min({want, kMaxGroups, groups, kThreads / std::max(1, wv)}));
+    };
+    auto rows_held = [&](int gs, int it) { return kThreads / (gs * wv) * it; };
+    if (wv <= kThreads) {
+        // one launch: full 128-byte lines where the segment still fits
+        for (int bytes = 128; bytes >= 16; bytes /= 2) {
+            const int gs = whole(bytes);
+            if (rows_held(gs, kHold) < max_rows) continue;
+            k.gs = gs;
+            k.slabs = (groups + gs - 1) / gs;
+            k.chunks = 1;
+            k.chunk_rows = std::max(1, max_rows);
+            k.it = rows_held(gs, 4) >= max_rows ? 4 : kHold;
+            return k;
+        }
+        k.gs = whole(256);
+        k.slabs = (groups + k.gs - 1) / k.gs;
+    } else {
+        k.gs = 1;
+        k.piece = kThreads * V;
+        k.slabs = groups * ((width + k.piece - 1) / k.piece);
+    }
+    const int cv = k.piece ? kThreads : k.gs * wv, rp = kThreads / cv;
+    const int64_t blocks = (int64_t)B * k.slabs;
+    const int least = (max_rows + rp * kHoldStats - 1) / (rp * kHoldStats);
+    const int want = (int)std::min<int64_t>((max_rows + rp - 1) / rp, (kWantBlocks + blocks - 1) / blocks);
+    k.chunks = std::max(1, std::max(least, want));
+    k.chunk_rows = (std::max(1, max_rows) + k.chunks - 1) / k.chunks;
+    k.chunk_rows = (k.chunk_rows + rp - 1) / rp * rp;
+    k.chunks = std::max(1, (max_rows + k.chunk_rows - 1) / k.chunk_rows);
+    k.it = kHoldStats;
+    return k;
+}
+
+// The widest vector for a tensor's rows.
+int vector_of(int V, const void *p, int64_t stride, int es) {
+    while (V > 1 && (reinterpret_cast<uintptr_t>(p) % (V * es) != 0 || stride % V != 0)) V /= 2;
+    return V;
+}
+
+struct NormLayout {
+    size_t seg, gmean, part, total;
+};
+NormLayout norm_layout(const NormCut &k, int64_t B, int64_t C, int64_t groups) {
+    NormLayout L;
+    size_t o = kWsBase;
+    auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
+    L.seg = take(B * 2 * C * sizeof(float));
+    L.gmean = take(B * groups * sizeof(float2));
+    const int64_t pieces = k.piece ? k.slabs / groups : 1;
+    L.part = take(k.chunks > 1 || k.piece ? std::max(B * groups * k.chunks * pieces * (int64_t)sizeof(float2),
+                                                     B * k.chunks * 2 * C * (int64_t)sizeof(float))
+                                          : 0);
+    L.total = o;
+    return L;
+}
+
+bool fused(const NormCut &k) { return k.chunks == 1 && !k.piece; }
+
+template <typename T, int V>
+sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
+    const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V);
+    const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
+    const int grid = a.B * k.slabs * k.chunks;
+    if (fused(k)) {
+        if (k.it == 4)
+            norm_fwd_kernel<T, V, 4><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
+        else
+            norm_fwd_kernel<T, V, kHold><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
+        return launch_status();
+    }
+    float2 *part = reinterpret_cast<float2 *>(ws + L.part);
+    norm_stats_kernel<T, V, kHoldStats><<<grid, kThreads, 0, s>>>(a, k, part);
     SN_TRY(launch_status());
-    if (dgamma || dbeta) {
-        param_kernel<<<(a.C + 63) / 64, 64, 0, s>>>(a.B, a.C, part, dgamma, dbeta);
+    norm_apply_kernel<T, V><<<grid, kThreads, 0, s>>>(a, k, part, (T *)y, mean, rstd);
+    return launch_status();
+}
+
+template <typename T, int V>
+sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta,
+                     char *ws, hipStream_t s) {
+    const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V);
+    const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
+    const int grid = a.B * k.slabs * k.chunks, params = dgamma || dbeta ? (a.C + 63) / 64 : 0;
+    float *seg = reinterpret_cast<float *>(ws + L.seg), *part = reinterpret_cast<float *>(ws + L.part);
+    float2 *gmean = reinterpret_cast<float2 *>(ws + L.gmean);
+    if (fused(k)) {
+        if (k.it == 4)
+            norm_bwd_kernel<T, V, 4><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
+        else
+            norm_bwd_kernel<T, V, kHold><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
         SN_TRY(launch_status());
+        if (params) norm_param_kernel<<<params, kThreads, 0, s>>>(a, seg, dgamma, dbeta);
+        return launch_status();
     }
-    return SN_OK;
+    norm_bwd_sums_kernel<T, V><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, part);
+    SN_TRY(launch_status());
+    norm_bwd_join_kernel<<<a.B * a.groups, 256, 0, s>>>(a, k, part, seg, gmean);
+    SN_TRY(launch_status());
+    norm_bwd_apply_kernel<T, V><<<grid + params, kThreads, 0, s>>>(a, k, mean, rstd, gmean, (T *)dx, seg, dgamma,
+                                                                  dbeta, params);
+    return launch_status();
+}
+
+template <typename T>
+int widest(const NormArgs &a, const void *out, bool backward) {
+    int V = 16 / sizeof(T);
+    while (V > 1 && a.width % V != 0) V /= 2;
+    V = vector_of(V, a.x, a.xs, sizeof(T));
+    V = vector_of(V, out, a.C, sizeof(T));
+    if (backward) V = vector_of(V, a.dy, a.dys, sizeof(T));
+    return V;
 }
 
 }  // namespace
 
 size_t norm_workspace(const sn_group_norm &op) {
-    return kWsBase + (size_t)op.n_segments * 2 * op.n_channels * sizeof(float);
+    const int es = op.dtype == SN_F32 ? 4 : 2, width = op.n_channels / op.n_groups;
+    size_t need = kWsBase;
+    for (int V = 16 / es; V >= 1; V /= 2)   // which one depends on the tensors
+        if (width % V == 0)
+            need = std::max(need, norm_layout(norm_cut(op.n_segments, op.max_rows, op.n_channels, op.n_groups, es, V),
+                                              op.n_segments, op.n_channels, op.n_groups).total);
+    return need;
 }
 
 sn_status norm_forward(const NormArgs &a, int dtype, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
     ProfScope prof(K_NORM_FWD, s);
-    if (dtype == SN_F32)
-        fwd_kernel<float><<<a.B * a.groups, kThreads, 0, s>>>(a, (float *)y, mean, rstd);
-    else
-        fwd_kernel<bf16><<<a.B * a.groups, kThreads, 0, s>>>(a, (bf16 *)y, mean, rstd);
-    return launch_status();
+    if (dtype == SN_F32) {
+        const int V = widest<float>(a, y, false);
+        return V == 4   ? forward_v<float, 4>(a, y, mean, rstd, ws, s)
+               : V == 2 ? forward_v<float, 2>(a, y, mean, rstd, ws, s)
+                        : forward_v<float, 1>(a, y, mean, rstd, ws, s);
+    }
+    const int V = widest<bf16>(a, y, false);
+    return V == 8   ? forward_v<bf16, 8>(a, y, mean, rstd, ws, s)
+           : V == 4 ? forward_v<bf16, 4>(a, y, mean, rstd, ws, s)
+           : V == 2 ? forward_v<bf16, 2>(a, y, mean, rstd, ws, s)
+                    : forward_v<bf16, 1>(a, y, mean, rstd, ws, s);
 }
 
 sn_status norm_backward(const NormArgs &a, int dtype, const float *mean, const float *rstd, void *dx, float *dgamma,
                         float *dbeta, char *ws, hipStream_t s) {
-    return dtype == SN_F32 ? backward_t<float>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
-                           : backward_t<bf16>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
+    ProfScope prof(K_NORM_BWD, s);
+    if (dtype == SN_F32) {
+        const int V = widest<float>(a, dx, true);
+        return V == 4   ? backward_v<float, 4>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
+               : V == 2 ? backward_v<float, 2>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
+                        : backward_v<float, 1>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
+    }
+    const int V = widest<bf16>(a, dx, true);
+    return V == 8   ? backward_v<bf16, 8>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
+           : V == 4 ? backward_v<bf16, 4>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
+           : V == 2 ? backward_v<bf16, 2>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
+                    : backward_v<bf16, 1>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
 }
 
 }  // namespace sn
