@@ -174,34 +174,60 @@ __device__ inline Frag<NP> to_frag(const Raw8<NP> &r) {
 }
 
 // One tile of R rows on its way from global memory to LDS, by NT threads:
-// load() issues the reads into registers, store() splits and writes them.
-template <int NP, int DP, int R, int NT>
+// load() issues the reads into registers, store() splits and writes them, so
+// nothing waits for memory between the two.
+//
+// FAST: 16-byte aligned rows within 2^31 bytes of the tile's first.  They
+// are read through a buffer descriptor that ends with the tile's last valid
+// row: what lies beyond, and elements from D on (sent out of range), come
+// back as zeros without a branch or a 64-bit address per read.
+template <int NP, int DP, int R, int NT, bool FAST>
 struct TileMove {
+    using T = typename RowOf<NP>::T;
     static constexpr int CH = DP / 8, IT = (R * CH + NT - 1) / NT;
+    static constexpr bool kExact = IT * NT == R * CH;
     Raw8<NP> raw[IT];
-    uint8_t kept[IT];
-    // rows row0 .. row0 + R - 1 of base (element rows `stride` apart), those
-    // from `n` on zero; keep (may be null): rows with keep[row] = 0 are zero
-    // (cleared by store(): nothing here waits for a load)
-    __device__ inline void load(const typename RowOf<NP>::T *base, int64_t stride, int row0, int n, int D, bool vec,
-                                int tid, const uint8_t *keep) {
+    uint32_t off, step;
+    __device__ inline void init(int64_t stride, int D, int tid) {
+        if constexpr (FAST) {
+            const int c = tid % CH;
+            off = (kExact || tid < R * CH) && 8 * c < D ? (uint32_t)((tid / CH) * stride + 8 * c) * sizeof(T) : 0x80000000u;
+            step = (uint32_t)(NT / CH * stride) * sizeof(T);
+        }
+    }
+    // tile rows 0 .. R - 1 at base, `stride` apart, those from `rows` on zero
+    __device__ inline void load(const T *base, int64_t stride, int rows, int D, int tid) {
+        if constexpr (FAST) {
+            const int n = min(rows, R);
+            const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<T *>(base), 0, n > 0 ? (int)(((n - 1) * stride + D) * sizeof(T)) : 0, 0x00020000);
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int c = tid + it * NT, row = row0 + c / CH, d = (c % CH) * 8;
-            raw[it] = raw_zero<NP>();
-            kept[it] = 1;
-            if (row < n && (IT * NT == R * CH || c < R * CH)) {
-                raw[it] = load8<NP>(base + (int64_t)row * stride + d, d, D, vec);
-                if (keep) kept[it] = keep[row];
+            for (int it = 0; it < IT; ++it) {
+                const uint32_t at = off + it * step;
+                raw[it].v[0] = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
+                if constexpr (NP == 3)
+                    raw[it].v[1] = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + 16, 0, 0));
+            }
+        } else {
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int c = tid + it * NT, row = c / CH, d = (c % CH) * 8;
+                raw[it] = raw_zero<NP>();
+                if (row < rows && row < R) raw[it] = load8<NP>(base + row * stride + d, d, D, false);
             }
         }
     }
-    __device__ inline void store(bf16 *tile, int tid) const {
+    // partial: rows whose bit in `kept` is clear become zero
+    __device__ inline void store(bf16 *tile, int tid, bool partial, uint64_t kept) {
+        if (partial)
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+                if (!((kept >> ((tid + it * NT) / CH & 63)) & 1)) raw[it] = raw_zero<NP>();
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
             const int c = tid + it * NT;
-            if (IT * NT != R * CH && c >= R * CH) continue;
-            const Frag<NP> f = to_frag<NP>(kept[it] ? raw[it] : raw_zero<NP>());
+            if (!kExact && c >= R * CH) continue;
+            const Frag<NP> f = to_frag<NP>(raw[it]);
             const int at = tile_at<DP>(c / CH, c % CH);
 #pragma unroll
             for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8 *>(tile + n * R * DP + at) = f.p[n];
@@ -228,11 +254,7 @@ __device__ inline int wave_max(int v) { return ~wave_min(~v); }
 __device__ inline float half_swap(float v) { return __shfl_xor(v, 32, 64); }
 
 // A value that is the same in every lane, in scalar registers.
-__device__ inline uint64_t uniform64(uint64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
-    return (uint64_t)hi << 32 | lo;
-}
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // --------------------------------------------------------------- positions
 
@@ -279,36 +301,45 @@ __device__ inline bool locate(const AttnArgs &a, RowBlock &w) {
     return true;
 }
 
-// Key positions and the kept keys of a tile, by one wavefront (lane = key).
+// Position table of the subgroup's heads, in log2 units.
+__device__ inline void fill_lut(const AttnArgs &a, const RowBlock &w, float *lut) {
+    for (int e = threadIdx.x; e < a.lut_n; e += blockDim.x) {
+        const int bk = bucket_of(a, a.lut_base + e);
+        for (int g = 0; g < w.gs; ++g) lut[g * a.lut_n + e] = a.bias[(int64_t)(w.h0 + g) * a.nb + bk] * kLog2e;
+    }
+}
+
+// The kept keys of a tile, by every wavefront (lane = key), and their
+// positions, which one wavefront leaves in LDS for all.
 template <int KT>
 struct KeyInfo {
     int pos[KT];
-    int lo, hi;
-    uint64_t mask;
+    int lo, hi;     // of the kept keys
 };
+template <int KT>
 struct KeyLoad {
     int pos;
-    bool ok;
-    __device__ inline void load(const AttnArgs &a, const RowBlock &w, int key0, int KT, int lane) {
+    uint8_t kept;
+    __device__ inline void load(const AttnArgs &a, const RowBlock &w, int key0, bool positions, int lane) {
         const int j = key0 + lane;
-        ok = lane < KT && j < w.nk;
+        const bool in = lane < KT && j < w.nk;
+        kept = in;
         pos = j;
-        if (ok) {
-            if (a.k_pos) pos = a.k_pos[w.k0 + j];
-            if (a.keep) ok = a.keep[w.k0 + j] != 0;
-        }
+        if (positions && a.k_pos && in) pos = a.k_pos[w.k0 + j];
+        if (a.keep && in) kept = a.keep[w.k0 + j];
     }
-    template <int KT>
+    __device__ inline uint64_t mask() const { return __ballot(kept != 0); }
     __device__ inline void store(KeyInfo<KT> &k, int lane) const {
-        const uint64_t mask = __ballot(ok);
+        const bool ok = kept != 0;
         const int lo = wave_min(ok ? pos : 0x7fffffff), hi = wave_max(ok ? pos : (int)0x80000000);
         if (lane < KT) k.pos[lane] = pos;
         if (lane == 0) {
             k.lo = lo;
             k.hi = hi;
-            k.mask = mask;
         }
     }
 };
+template <int KT>
+__device__ inline bool is_partial(uint64_t mask) { return mask != (KT == 64 ? ~0ull : 0xffffffffull); }
 
 }  // namespace sn

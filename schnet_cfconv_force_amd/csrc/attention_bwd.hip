@@ -11,8 +11,8 @@
 //
 // delta starts as dO_i.o_i from the rounded o.  What that (and the forward's
 // 16-bit p) leaves is exactly what the row's dS fails to sum to zero by:
-// e_i = sum_j dS_ij.  The bias sums are corrected by it, dbias -= e_i times
-// the row's sum of p over the bucket, and the second pass takes delta + e.
+// e_i = sum_j dS_ij, as sum_j p_ij = 1.  The second pass takes delta + e; the
+// bias sums, which are fp32 whatever the rows are, are taken there.
 #include <algorithm>
 
 #include "attention.h"
@@ -32,17 +32,11 @@ struct BwdArgs {
     const float *lse;
     void *dq, *dk, *dv;
     float2 *row;        // [n_q H] {lse log2e - 24 (+inf: no key), delta}
-    float *part_bias;   // [Hkv subs][B row_tiles][Gs nb]
+    float *part_bias;   // [Hkv][B key_tiles splits][G nb]
     float *part_kv;     // [split][n_k Hkv][2][D] (splits > 1)
 };
 
-// LDS of the dq kernel: tiles, then the position table {bias log2e, bucket},
-// then the bias sums {dS, p} [wavefront][bucket][row].
 constexpr int kDqKeys = 32;
-template <int NP, int DP>
-constexpr int dq_buffers() { return NP == 3 && DP == 128 ? 1 : 2; }   // 160 KB of LDS
-template <int NP, int DP>
-constexpr size_t dq_tile_bytes() { return size_t(dq_buffers<NP, DP>()) * 2 * NP * kDqKeys * DP * sizeof(bf16); }
 
 template <typename T>
 __device__ inline void write4(T *row, int d, int D, floatx4 v) {
@@ -59,35 +53,18 @@ __device__ inline void write4(T *row, int d, int D, floatx4 v) {
         if (d + i < D) row[d + i] = (T)v[i];
 }
 
-template <int NP, int DP>
+template <int NP, int DP, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
-    constexpr int kBuf = dq_buffers<NP, DP>(), kTile = NP * kDqKeys * DP;
-    extern __shared__ __align__(16) char lds_bytes[];
-    bf16 *tiles = reinterpret_cast<bf16 *>(lds_bytes);   // [buffer][K, V]
-    float2 *lut = reinterpret_cast<float2 *>(lds_bytes + dq_tile_bytes<NP, DP>());
-    float *sums = reinterpret_cast<float *>(lut + a.Gs * a.lut_n);
+    constexpr int kTile = NP * kDqKeys * DP;
+    __shared__ __align__(16) bf16 tiles[2][2][kTile];   // [buffer][K, V]
     __shared__ KeyInfo<kDqKeys> info[2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+    __shared__ float lut[kLutMax];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5;
     RowBlock w;
     if (!locate(a, w)) return;
-    float *part = a.nb ? g.part_bias + ((int64_t)(w.hk * a.subs + w.sub) * a.B * a.row_tiles +
-                                        (w.b * a.row_tiles + w.tile)) * (a.Gs * a.nb)
-                       : nullptr;
-    if (w.tile * 128 >= w.nq * w.gs) {
-        for (int i = tid; a.nb && i < a.Gs * a.nb; i += kAttnThreads) part[i] = 0.0f;
-        return;
-    }
-    if (a.nb) {
-        for (int e = tid; e < a.lut_n; e += kAttnThreads) {
-            const int bk = bucket_of(a, a.lut_base + e);
-            for (int h = 0; h < w.gs; ++h)
-                lut[h * a.lut_n + e] = make_float2(a.bias[(int64_t)(w.h0 + h) * a.nb + bk] * kLog2e, __int_as_float(bk));
-        }
-        for (int i = tid; i < 4 * a.nb * 64; i += kAttnThreads) sums[i] = 0.0f;
-    }
-    // the lane's column of its wavefront's sums: {dS, p} of bucket b at mine + 64 b
-    float *mine = sums + wave * a.nb * 64 + (lane & 31) * 2;
+    if (w.tile * 128 >= w.nq * w.gs) return;
+    if (a.nb) fill_lut(a, w, lut);
 
     const int r = w.tile * 128 + wave * 32 + (lane & 31), qi = r / w.gs, hg = r % w.gs;
     const int row = qi < w.nq ? w.q0 + qi : -1;
@@ -101,9 +78,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
         const int d = 16 * s + 8 * half;
         Raw8<NP> rq = raw_zero<NP>(), rg = rq, ro = rq;
         if (row >= 0) {
-            rq = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + hg) * a.qh + d, d, a.D, a.vec & 1);
-            rg = load8<NP>((const T *)a.d_o + row * a.gs + (w.h0 + hg) * a.gh + d, d, a.D, a.vec & 8);
-            ro = load8<NP>((const T *)g.o + at * a.D + d, d, a.D, a.vec & 16);
+            rq = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + hg) * a.qh + d, d, a.D, FAST);
+            rg = load8<NP>((const T *)a.d_o + row * a.gs + (w.h0 + hg) * a.gh + d, d, a.D, FAST);
+            ro = load8<NP>((const T *)g.o + at * a.D + d, d, a.D, FAST);
         }
         q[s] = to_frag<NP>(rq);
         dO[s] = to_frag<NP>(rg);
@@ -132,47 +109,40 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
     const int pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff), pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
 
     const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
-    const uint8_t *keep = a.keep ? a.keep + w.k0 : nullptr;
     const int n_tiles = (w.nk + kDqKeys - 1) / kDqKeys;
-    TileMove<NP, DP, kDqKeys, kAttnThreads> mk, mv;
-    KeyLoad kl;
+    TileMove<NP, DP, kDqKeys, kAttnThreads, FAST> mk, mv;
+    KeyLoad<kDqKeys> kl;
+    mk.init(a.ks, a.D, tid);
+    mv.init(a.vs, a.D, tid);
     auto load = [&](int t) {
-        mk.load(K, a.ks, t * kDqKeys, w.nk, a.D, a.vec & 2, tid, keep);
-        mv.load(V, a.vs, t * kDqKeys, w.nk, a.D, a.vec & 4, tid, keep);
-        if (wave == 0) kl.load(a, w, t * kDqKeys, kDqKeys, lane);
+        mk.load(K + t * kDqKeys * a.ks, a.ks, w.nk - t * kDqKeys, a.D, tid);
+        mv.load(V + t * kDqKeys * a.vs, a.vs, w.nk - t * kDqKeys, a.D, tid);
+        kl.load(a, w, t * kDqKeys, a.nb && wave == 0, lane);
     };
     auto store = [&](int buf) {
-        mk.store(tiles + 2 * buf * kTile, tid);
-        mv.store(tiles + (2 * buf + 1) * kTile, tid);
-        if (wave == 0) kl.store(info[buf], lane);
+        const uint64_t mask = kl.mask();
+        mk.store(tiles[buf][0], tid, a.keep && is_partial<kDqKeys>(mask), mask);
+        mv.store(tiles[buf][1], tid, a.keep && is_partial<kDqKeys>(mask), mask);
+        if (a.nb && wave == 0) kl.store(info[buf], lane);
+        return mask;
     };
     floatx16 dq[DP / 32];
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[e][i] = 0.0f;
-    float row_ds = 0.0f;                        // sum of the row's dS (this half's keys)
-    float run_ds = 0.0f, run_p = 0.0f;          // of the tiles since the bucket last changed
-    int run_bucket = -1;
-    auto flush = [&]() {
-        // the halves of a row add in turn: one order
-        if (half == 0) { atomicAdd(mine + 64 * run_bucket, run_ds); atomicAdd(mine + 64 * run_bucket + 1, run_p); }
-        __builtin_amdgcn_wave_barrier();
-        if (half == 1) { atomicAdd(mine + 64 * run_bucket, run_ds); atomicAdd(mine + 64 * run_bucket + 1, run_p); }
-        __builtin_amdgcn_wave_barrier();
-        run_ds = run_p = 0.0f;
-    };
+    float row_ds = 0.0f;    // sum of the row's dS (this half's keys)
+    uint64_t mask = 0;
     if (n_tiles > 0) {
         load(0);
-        store(0);
+        mask = store(0);
     }
     __syncthreads();
     for (int t = 0; t < n_tiles; ++t) {
-        const int buf = kBuf == 2 ? t & 1 : 0;
+        const int buf = t & 1;
         if (t + 1 < n_tiles) load(t + 1);
-        const bf16 *kt = tiles + 2 * buf * kTile, *vt = kt + kTile;
+        const bf16 *kt = tiles[buf][0], *vt = tiles[buf][1];
         const KeyInfo<kDqKeys> &ki = info[buf];
-        const uint32_t mask = (uint32_t)uniform64(ki.mask);
         if (active && mask) {
             floatx16 s, dp;
 #pragma unroll
@@ -183,63 +153,33 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
             for (int k = 0; k < DP / 16; ++k) dp = mma<NP>(frag_rows<NP, DP>(vt, kDqKeys * DP, 0, k, lane), dO[k], dp);
             settle(s);
             settle(dp);
-            float add = 0.0f;
-            int bucket = -1;
-            bool table = false;
+            float mul = c, less = -L;
             if (a.nb) {
-                const int lo = __builtin_amdgcn_readfirstlane(ki.lo), hi = __builtin_amdgcn_readfirstlane(ki.hi);
+                const int lo = uniform(ki.lo), hi = uniform(ki.hi);
                 const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
-                const float2 entry = lut[hg * a.lut_n + first];
-                add = entry.x;
-                bucket = __builtin_amdgcn_readfirstlane(__float_as_int(entry.y));
-                table = first != last;
-            }
-            const uint32_t keys = mask >> (4 * half);
-            if (!table) {
-                float sum_ds = 0.0f, sum_p = 0.0f;
+                if (first == last) {
+                    less += lut[hg * a.lut_n + first];
+                } else {
+                    mul = 1.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, add) - L);
-                    if (mask != 0xffffffffu && !((keys >> (8 * (i / 4) + i % 4)) & 1)) p = 0.0f;
-                    const float ds = p * (dp[i] - delta);
-                    s[i] = ds;
-                    sum_ds += ds;
-                    sum_p += p;
-                }
-                row_ds += sum_ds;
-                if (a.nb) {
-                    if (bucket != run_bucket) {
-                        if (run_bucket >= 0) flush();
-                        run_bucket = bucket;
+                    for (int i = 0; i < 16; ++i) {
+                        const int e = lut_index(a, offset_of(ki.pos[8 * (i / 4) + 4 * half + i % 4], pos));
+                        s[i] = fmaf(s[i], c, lut[hg * a.lut_n + e]);
                     }
-                    run_ds += sum_ds;
-                    run_p += sum_p;
-                }
-            } else {
-                int bk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int e = lut_index(a, offset_of(ki.pos[8 * (i / 4) + 4 * half + i % 4], pos));
-                    const float2 entry = lut[hg * a.lut_n + e];
-                    bk[i] = __float_as_int(entry.y);
-                    float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, entry.x) - L);
-                    if (!((keys >> (8 * (i / 4) + i % 4)) & 1)) p = 0.0f;
-                    const float ds = p * (dp[i] - delta);
-                    s[i] = ds;
-                    dp[i] = p;
-                    row_ds += ds;
-                }
-#pragma unroll
-                for (int turn = 0; turn < 2; ++turn) {
-                    if (half == turn)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            atomicAdd(mine + 64 * bk[i], s[i]);
-                            atomicAdd(mine + 64 * bk[i] + 1, dp[i]);
-                        }
-                    __builtin_amdgcn_wave_barrier();
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], mul, less)) * (dp[i] - delta);
+            }
+            if (is_partial<kDqKeys>(mask)) {
+                const uint32_t keys = (uint32_t)mask >> (4 * half);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!((keys >> (8 * (i / 4) + i % 4)) & 1)) s[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) row_ds += s[i];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float x[8];
@@ -253,8 +193,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
                     dq[e] = mma<NP>(frag_cols<NP, DP>(kt, kDqKeys * DP, 16 * u, e, lane), ds, dq[e]);
             }
         }
-        if constexpr (kBuf == 1) __syncthreads();
-        if (t + 1 < n_tiles) store(kBuf == 2 ? buf ^ 1 : 0);
+        if (t + 1 < n_tiles) mask = store(buf ^ 1);
         __syncthreads();
     }
     // the row's sum of dS in units of p (sum_j p_ij is 2^24 by construction)
@@ -270,41 +209,23 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
                               (a.scale * kUnlift));
         if (half == 0) g.row[at] = make_float2(L, delta + err);
     }
-    if (!a.nb) return;
-    if (run_bucket >= 0) flush();
-    // err per row, then every (head, bucket) sums its rows in order
-    __syncthreads();
-    float *errs = reinterpret_cast<float *>(tiles);
-    if (half == 0) errs[wave * 32 + lane] = row >= 0 ? err : 0.0f;
-    __syncthreads();
-    for (int i = tid; i < a.Gs * a.nb; i += kAttnThreads) {
-        const int h = i / a.nb, b = i % a.nb;
-        float sum = 0.0f;
-        for (int k = 0; k < 128; ++k) {
-            if ((w.tile * 128 + k) % w.gs != h) continue;
-            const float *x = sums + ((k >> 5) * a.nb + b) * 64 + (k & 31) * 2;
-            sum += x[0] - errs[k] * x[1];
-        }
-        part[i] = sum;
-    }
 }
 
-// dbias[h][b]: the row blocks' sums, in their order.  One block per subgroup
-// and 64 of its (head, bucket) pairs; four wavefronts take every fourth.
-__global__ __launch_bounds__(256) void attn_dbias_kernel(AttnArgs a, const float *part, float *dbias) {
-    __shared__ double red[4][64];
-    const int cols = a.Gs * a.nb, group = blockIdx.y, hk = group / a.subs, sub = group % a.subs;
-    const int i = blockIdx.x * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6, n = a.B * a.row_tiles;
+// dbias[h][b]: the key blocks' sums, in their order.  One block per 64 of a
+// key/value head's (head, bucket) pairs; its wavefronts take every sixteenth.
+__global__ __launch_bounds__(1024) void attn_dbias_kernel(AttnArgs a, const float *part, float *dbias) {
+    __shared__ double red[16][64];
+    const int cols = a.G * a.nb, hk = blockIdx.y, n = a.B * a.row_tiles * a.splits;
+    const int i = blockIdx.x * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6;
     double s = 0.0;
     if (i < cols)
-        for (int k = wave; k < n; k += 4) s += part[((int64_t)group * n + k) * cols + i];
+#pragma unroll 4
+        for (int k = wave; k < n; k += 16) s += part[((int64_t)hk * n + k) * cols + i];
     red[wave][threadIdx.x & 63] = s;
     __syncthreads();
     if (wave != 0 || i >= cols) return;
-    const int h = i / a.nb;
-    if (sub * a.Gs + h >= a.G) return;
-    s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
-    dbias[(int64_t)(hk * a.G + sub * a.Gs + h) * a.nb + i % a.nb] = (float)(s * kUnlift);
+    for (int k = 1; k < 16; ++k) s += red[k][threadIdx.x];
+    dbias[(int64_t)hk * cols + i] = (float)(s * kUnlift);
 }
 
 // What the rows of a tile need beside q and dO.
@@ -314,15 +235,30 @@ struct RowInfo {
     int lo, hi;
 };
 
+// LDS beyond the tiles: the position table {bias, bucket} of one head and,
+// per wavefront, the bias sums [bucket][column] of the head.  A lane adds to
+// a column of its own (its key and half), so the sums need no order but the
+// lane's; where 160 KB of LDS leave only half the columns, the halves of a
+// wavefront take turns.
 template <int NP, int DP>
+constexpr int bias_columns() { return NP == 3 && DP == 128 ? 32 : 64; }
+template <int NP, int DP>
+size_t dkv_lds(const AttnArgs &a) {
+    return a.nb ? (size_t)a.lut_n * sizeof(float2) + (size_t)4 * a.nb * bias_columns<NP, DP>() * sizeof(float) : 0;
+}
+
+template <int NP, int DP, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void attn_dkv_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
     constexpr int kRows = 32, kTile = NP * kRows * DP;
     __shared__ __align__(16) bf16 tiles[2][2][kTile];   // [buffer][q, dO]
+    constexpr int kCols = bias_columns<NP, DP>();
     __shared__ RowInfo info[2];
-    __shared__ float lut[kLutMax];
-    __shared__ uint8_t lut_bucket[kLutMax];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+    extern __shared__ __align__(16) char lds_bytes[];
+    float2 *lut = reinterpret_cast<float2 *>(lds_bytes);
+    float *sums = reinterpret_cast<float *>(lut + a.lut_n);
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5;
+    float *mine = sums + wave * a.nb * kCols + lane % kCols;   // the lane's column
     const int n_blocks = a.B * a.Hkv * a.splits * a.row_tiles;
     int i0 = xcd_block(n_blocks);
     if (i0 < 0) return;
@@ -332,20 +268,25 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     int q0, nq, k0, nk;
     segment_rows(a.q_ptr, b, a.B, a.n_q, a.max_q, a.status, q0, nq);
     segment_rows(a.k_ptr, b, a.B, a.n_k, a.max_k, a.status, k0, nk);
-    if (key_tile * 128 >= nk) return;
+    float *part = a.nb ? g.part_bias + (((int64_t)hk * a.B + b) * a.row_tiles * a.splits + key_tile * a.splits + split) * a.G * a.nb
+                       : nullptr;
+    if (key_tile * 128 >= nk) {
+        for (int i = tid; a.nb && i < a.G * a.nb; i += kAttnThreads) part[i] = 0.0f;
+        return;
+    }
     const int j = key_tile * 128 + wave * 32 + (lane & 31);
     const bool have = j < nk, kept = have && (!a.keep || a.keep[k0 + j]);
     const bool active = __any(kept);
     if (a.nb)
-        for (int e = tid; e < a.lut_n; e += kAttnThreads) lut_bucket[e] = (uint8_t)bucket_of(a, a.lut_base + e);
+        for (int e = tid; e < a.lut_n; e += kAttnThreads) lut[e].y = __int_as_float(bucket_of(a, a.lut_base + e));
     Frag<NP> k[DP / 16], v[DP / 16];
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
         const int d = 16 * s + 8 * half;
         Raw8<NP> rk = raw_zero<NP>(), rv = rk;
         if (kept) {
-            rk = load8<NP>((const T *)a.k + (int64_t)(k0 + j) * a.ks + hk * a.kh + d, d, a.D, a.vec & 2);
-            rv = load8<NP>((const T *)a.v + (int64_t)(k0 + j) * a.vs + hk * a.vh + d, d, a.D, a.vec & 4);
+            rk = load8<NP>((const T *)a.k + (int64_t)(k0 + j) * a.ks + hk * a.kh + d, d, a.D, FAST);
+            rv = load8<NP>((const T *)a.v + (int64_t)(k0 + j) * a.vs + hk * a.vh + d, d, a.D, FAST);
         }
         k[s] = to_frag<NP>(rk);
         v[s] = to_frag<NP>(rv);
@@ -360,13 +301,15 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     // the rows of all heads that share these keys, head by head
     const int per_head = (nq + kRows - 1) / kRows, n_tiles = per_head * a.G, per = (n_tiles + a.splits - 1) / a.splits;
     const int t0 = split * per, t1 = min(n_tiles, t0 + per);
-    TileMove<NP, DP, kRows, kAttnThreads> mq, mg;
+    TileMove<NP, DP, kRows, kAttnThreads, FAST> mq, mg;
+    mq.init(a.qs, a.D, tid);
+    mg.init(a.gs, a.D, tid);
     float2 ri;
     int ri_pos;
     auto load = [&](int t) {
         const int h = hk * a.G + t / per_head, r0 = t % per_head * kRows;
-        mq.load((const T *)a.q + q0 * a.qs + h * a.qh, a.qs, r0, nq, a.D, a.vec & 1, tid, nullptr);
-        mg.load((const T *)a.d_o + q0 * a.gs + h * a.gh, a.gs, r0, nq, a.D, a.vec & 8, tid, nullptr);
+        mq.load((const T *)a.q + (q0 + r0) * a.qs + h * a.qh, a.qs, nq - r0, a.D, tid);
+        mg.load((const T *)a.d_o + (q0 + r0) * a.gs + h * a.gh, a.gs, nq - r0, a.D, tid);
         if (tid < kRows) {
             const int row = r0 + tid;
             ri = make_float2(INFINITY, 0.0f);
@@ -378,8 +321,8 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         }
     };
     auto store = [&](int t, int buf) {
-        mq.store(tiles[buf][0], tid);
-        mg.store(tiles[buf][1], tid);
+        mq.store(tiles[buf][0], tid, false, 0);
+        mg.store(tiles[buf][1], tid, false, 0);
         if (wave == 0) {
             const bool in = lane < kRows && t % per_head * kRows + lane < nq;
             const int lo = wave_min(in ? ri_pos : 0x7fffffff), hi = wave_max(in ? ri_pos : (int)0x80000000);
@@ -399,7 +342,37 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[e][i] = dv[e][i] = 0.0f;
-    int head = -1;
+    float run_ds = 0.0f;        // of the tiles since the bucket last changed
+    int run_bucket = -1, head = -1;
+    auto flush = [&]() {
+        if (run_bucket < 0) return;
+        if (kCols == 64 || half == 0) atomicAdd(mine + run_bucket * kCols, run_ds);
+        if (kCols != 64) {
+            __builtin_amdgcn_wave_barrier();
+            if (half == 1) atomicAdd(mine + run_bucket * kCols, run_ds);
+        }
+        run_ds = 0.0f;
+        run_bucket = -1;
+    };
+    // the head's sums are complete: every bucket adds its columns in order
+    auto finish_head = [&]() {
+        flush();
+        __syncthreads();
+        for (int i = tid; i < a.nb * 4; i += kAttnThreads) {
+            const int wv = i / a.nb, bk = i % a.nb;
+            float s = 0.0f;
+            for (int k = 0; k < kCols; ++k) s += sums[(wv * a.nb + bk) * kCols + (k + bk) % kCols];
+            sums[(wv * a.nb + bk) * kCols] = s;
+        }
+        __syncthreads();
+        for (int bk = tid; bk < a.nb; bk += kAttnThreads)
+            part[head * a.nb + bk] = (sums[bk * kCols] + sums[(a.nb + bk) * kCols]) +
+                                     (sums[(2 * a.nb + bk) * kCols] + sums[(3 * a.nb + bk) * kCols]);
+        __syncthreads();
+    };
+    if (a.nb)   // heads that this split does not reach
+        for (int i = tid; i < a.G * a.nb; i += kAttnThreads)
+            if (t0 >= t1 || i / a.nb < t0 / per_head || i / a.nb > (t1 - 1) / per_head) part[i] = 0.0f;
     if (t0 < t1) {
         load(t0);
         store(t0, 0);
@@ -409,9 +382,11 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         const int buf = (t - t0) & 1;
         if (t + 1 < t1) load(t + 1);
         if (a.nb && t / per_head != head) {   // every wavefront is past the last use of the table (barrier below)
+            if (head >= 0) finish_head();
             head = t / per_head;
             for (int e = tid; e < a.lut_n; e += kAttnThreads)
-                lut[e] = a.bias[(int64_t)(hk * a.G + head) * a.nb + lut_bucket[e]] * kLog2e;
+                lut[e].x = a.bias[(int64_t)(hk * a.G + head) * a.nb + __float_as_int(lut[e].y)] * kLog2e;
+            for (int i = tid; i < 4 * a.nb * kCols; i += kAttnThreads) sums[i] = 0.0f;
             __syncthreads();
         }
         const bf16 *qt = tiles[buf][0], *gt = tiles[buf][1];
@@ -426,22 +401,52 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             for (int e = 0; e < DP / 16; ++e) dp = mma<NP>(frag_rows<NP, DP>(gt, kRows * DP, 0, e, lane), v[e], dp);
             settle(s);
             settle(dp);
-            float add = 0.0f;
+            float mul = c, add = 0.0f;
+            int bk[16], bucket = -1;
             bool table = false;
             if (a.nb) {
-                const int lo = __builtin_amdgcn_readfirstlane(ri_t.lo), hi = __builtin_amdgcn_readfirstlane(ri_t.hi);
+                const int lo = uniform(ri_t.lo), hi = uniform(ri_t.hi);
                 const int first = lut_index(a, offset_of(pos_lo, hi)), last = lut_index(a, offset_of(pos_hi, lo));
-                add = lut[first];
                 table = first != last;
+                if (!table) {
+                    add = lut[first].x;
+                    bucket = uniform(__float_as_int(lut[first].y));
+                } else {
+                    mul = 1.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 e = lut[lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))];
+                        s[i] = fmaf(s[i], c, e.x);
+                        bk[i] = __float_as_int(e.y);
+                    }
+                }
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int row = 8 * (i / 4) + 4 * half + i % 4;
-                float x = add;
-                if (table) x = lut[lut_index(a, offset_of(pos, ri_t.pos[row]))];
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, x) - ri_t.L[row]);
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], mul, add - ri_t.L[row]));
                 s[i] = p;
                 dp[i] = p * (dp[i] - ri_t.delta[row]);
+            }
+            if (a.nb) {
+                if (!table) {
+                    if (bucket != run_bucket) flush();
+                    run_bucket = bucket;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) run_ds += kept ? dp[i] : 0.0f;
+                } else if (kCols == 64) {
+                    if (kept)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) atomicAdd(mine + bk[i] * kCols, dp[i]);
+                } else {
+#pragma unroll
+                    for (int turn = 0; turn < 2; ++turn) {
+                        if (kept && half == turn)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) atomicAdd(mine + bk[i] * kCols, dp[i]);
+                        __builtin_amdgcn_wave_barrier();
+                    }
+                }
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -462,6 +467,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         if (t + 1 < t1) store(t + 1, buf ^ 1);
         __syncthreads();
     }
+    if (a.nb && head >= 0) finish_head();
     if (!have) return;
     const int64_t at = (int64_t)(k0 + j) * a.Hkv + hk;
     const float fk = kept ? a.scale * kUnlift : 0.0f, fv = kept ? kUnlift : 0.0f;
@@ -524,13 +530,13 @@ BwdLayout bwd_layout(const BwdPlan &p, int B, int Hkv, int H, int64_t n_q, int64
     size_t o = kWsBase;
     auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
     L.row = take(n_q * H * sizeof(float2));
-    L.bias = take((size_t)Hkv * p.subs * B * p.row_tiles * p.Gs * nb * sizeof(float));
+    L.bias = take((size_t)H * B * p.key_tiles * p.splits * nb * sizeof(float));
     L.kv = take(p.splits > 1 ? (size_t)p.splits * n_k * Hkv * 2 * D * sizeof(float) : 0);
     L.total = o;
     return L;
 }
 
-template <int NP, int DP>
+template <int NP, int DP, bool FAST>
 sn_status launch(const AttnArgs &a0, const BwdArgs &g, const BwdPlan &p, hipStream_t s) {
     using T = typename RowOf<NP>::T;
     AttnArgs a = a0;
@@ -538,14 +544,14 @@ sn_status launch(const AttnArgs &a0, const BwdArgs &g, const BwdPlan &p, hipStre
     if (a.n_q) {
         a.row_tiles = p.row_tiles;
         a.splits = 1;
-        const size_t lds = dq_tile_bytes<NP, DP>() + (a.nb ? (size_t)a.Gs * a.lut_n * sizeof(float2) + 4 * a.nb * 256 : 0);
-        attn_dq_kernel<NP, DP><<<xcd_grid(a.B * a.Hkv * a.subs * a.row_tiles), kAttnThreads, lds, s>>>(a, g);
+        attn_dq_kernel<NP, DP, FAST><<<xcd_grid(a.B * a.Hkv * a.subs * a.row_tiles), kAttnThreads, 0, s>>>(a, g);
         SN_TRY(launch_status());
     }
     if (a.n_k) {
         a.row_tiles = p.key_tiles;
         a.splits = p.splits;
-        attn_dkv_kernel<NP, DP><<<xcd_grid(a.B * a.Hkv * a.splits * a.row_tiles), kAttnThreads, 0, s>>>(a, g);
+        attn_dkv_kernel<NP, DP, FAST><<<xcd_grid(a.B * a.Hkv * a.splits * a.row_tiles), kAttnThreads,
+                                        dkv_lds<NP, DP>(a), s>>>(a, g);
         SN_TRY(launch_status());
         if (a.splits > 1) {
             const int64_t n = (int64_t)a.n_k * a.Hkv * 2 * a.D;
@@ -556,11 +562,11 @@ sn_status launch(const AttnArgs &a0, const BwdArgs &g, const BwdPlan &p, hipStre
     return SN_OK;
 }
 
-template <int NP>
+template <int NP, bool FAST>
 sn_status launch_dim(const AttnArgs &a, const BwdArgs &g, const BwdPlan &p, hipStream_t s) {
-    if (a.D <= 32) return launch<NP, 32>(a, g, p, s);
-    if (a.D <= 64) return launch<NP, 64>(a, g, p, s);
-    return launch<NP, 128>(a, g, p, s);
+    if (a.D <= 32) return launch<NP, 32, FAST>(a, g, p, s);
+    if (a.D <= 64) return launch<NP, 64, FAST>(a, g, p, s);
+    return launch<NP, 128, FAST>(a, g, p, s);
 }
 
 __global__ void fill_zero_kernel(float *x, int n) {
@@ -587,14 +593,16 @@ sn_status attn_backward(AttnArgs a, int dtype, const void *o, const float *lse, 
     ProfScope prof(K_ATTN_BWD, s);
     const BwdPlan p = bwd_plan(a.B, a.Hkv, a.G, a.max_q, a.max_k, a.lut_n);
     const BwdLayout L = bwd_layout(p, a.B, a.Hkv, a.H, a.n_q, a.n_k, a.D, a.nb);
-    if (a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) a.vec |= 16;
     BwdArgs g{o, lse, dq, dk, dv, reinterpret_cast<float2 *>(ws + L.row), reinterpret_cast<float *>(ws + L.bias),
               reinterpret_cast<float *>(ws + L.kv)};
-    SN_TRY(dtype == SN_F32 ? launch_dim<3>(a, g, p, s) : launch_dim<1>(a, g, p, s));
+    if (a.fast)
+        SN_TRY((dtype == SN_F32 ? launch_dim<3, true>(a, g, p, s) : launch_dim<1, true>(a, g, p, s)));
+    else
+        SN_TRY((dtype == SN_F32 ? launch_dim<3, false>(a, g, p, s) : launch_dim<1, false>(a, g, p, s)));
     if (!dbias) return SN_OK;
-    if (a.n_q) {
-        a.Gs = p.Gs; a.subs = p.subs; a.row_tiles = p.row_tiles;
-        attn_dbias_kernel<<<dim3((a.Gs * a.nb + 63) / 64, a.Hkv * a.subs), 256, 0, s>>>(a, g.part_bias, dbias);
+    if (a.n_k) {
+        a.row_tiles = p.key_tiles; a.splits = p.splits;
+        attn_dbias_kernel<<<dim3((a.G * a.nb + 63) / 64, a.Hkv), 1024, 0, s>>>(a, g.part_bias, dbias);
     } else {
         fill_zero_kernel<<<(a.H * a.nb + 255) / 256, 256, 0, s>>>(dbias, a.H * a.nb);
     }

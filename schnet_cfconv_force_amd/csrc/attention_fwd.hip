@@ -25,16 +25,8 @@ struct FwdOut {
     float2 *part_ml;    // [split][n_q H] their maximum (log2) and sum
 };
 
-// Position table of the subgroup's heads, in log2 units.
-__device__ inline void fill_lut(const AttnArgs &a, const RowBlock &w, float *lut) {
-    for (int e = threadIdx.x; e < a.lut_n; e += blockDim.x) {
-        const int bk = bucket_of(a, a.lut_base + e);
-        for (int g = 0; g < w.gs; ++g) lut[g * a.lut_n + e] = a.bias[(int64_t)(w.h0 + g) * a.nb + bk] * kLog2e;
-    }
-}
-
 // What a wavefront keeps of its 32 rows (a lane: row lane % 32).
-template <int NP, int DP>
+template <int NP, int DP, bool FAST>
 struct RowState {
     Frag<NP> q[DP / 16];
     floatx16 o[DP / 32];
@@ -56,7 +48,7 @@ struct RowState {
             const int d = 16 * s + 8 * (lane >> 5);
             Raw8<NP> raw = raw_zero<NP>();
             if (row >= 0)
-                raw = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + g) * a.qh + d, d, a.D, a.vec & 1);
+                raw = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + g) * a.qh + d, d, a.D, FAST);
             q[s] = to_frag<NP>(raw);
             if (neg)
 #pragma unroll
@@ -73,13 +65,12 @@ struct RowState {
             for (int i = 0; i < 16; ++i) o[e][i] = 0.0f;
     }
 
-    // One tile of KT keys (KT / 32 score tiles).  mask: the kept keys;
-    // key_pos: their positions in LDS, between lo and hi.
+    // One tile of KT keys (KT / 32 score tiles).  mask: the kept keys; ki:
+    // their positions (used with a bias).
     template <int KT>
-    __device__ inline void step(const AttnArgs &a, const bf16 *kt, const bf16 *vt, uint64_t mask, const int *key_pos,
-                                int key_lo, int key_hi, const float *lut, int lane) {
+    __device__ inline void step(const AttnArgs &a, const bf16 *kt, const bf16 *vt, uint64_t mask, const KeyInfo<KT> &ki,
+                                const float *lut, int lane) {
         constexpr int NS = KT / 32;
-        const int lo = __builtin_amdgcn_readfirstlane(key_lo), hi = __builtin_amdgcn_readfirstlane(key_hi);
         const int half = lane >> 5;
         floatx16 s[NS];
 #pragma unroll
@@ -92,29 +83,26 @@ struct RowState {
         }
 #pragma unroll
         for (int u = 0; u < NS; ++u) settle(s[u]);
-        float add = 0.0f;
-        bool table = false;
+        // x = s c + add, in log2 units: one bias for a tile whose offsets all
+        // fall in one bucket, else c is folded in here, element by element
+        float mul = c, add = 0.0f;
         if (a.nb) {
-            // every offset of the tile in one bucket: one bias for all of it
+            const int lo = uniform(ki.lo), hi = uniform(ki.hi);
             const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
-            add = lut[g * a.lut_n + first];
-            table = first != last;
+            if (first == last) {
+                add = lut[g * a.lut_n + first];
+            } else {
+                mul = 1.0f;
+#pragma unroll
+                for (int u = 0; u < NS; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int at = lut_index(a, offset_of(ki.pos[32 * u + 8 * (i / 4) + 4 * half + i % 4], pos));
+                        s[u][i] = fmaf(s[u][i], c, lut[g * a.lut_n + at]);
+                    }
+            }
         }
-        if (table) {
-#pragma unroll
-            for (int u = 0; u < NS; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int at = lut_index(a, offset_of(key_pos[32 * u + 8 * (i / 4) + 4 * half + i % 4], pos));
-                    s[u][i] = fmaf(s[u][i], c, lut[g * a.lut_n + at]);
-                }
-        } else {
-#pragma unroll
-            for (int u = 0; u < NS; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[u][i] = fmaf(s[u][i], c, add);
-        }
-        if (mask != (KT == 64 ? ~0ull : 0xffffffffull)) {
+        if (is_partial<KT>(mask)) {
             const uint64_t mine = mask >> (4 * half);
 #pragma unroll
             for (int u = 0; u < NS; ++u)
@@ -128,6 +116,7 @@ struct RowState {
 #pragma unroll
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
         mx = fmaxf(mx, half_swap(mx));
+        mx = mx == -INFINITY ? mx : fmaf(mx, mul, add);   // no key, whatever the scale
         if (__any(mx > m + 8.0f)) {
             const float mn = fmaxf(m, mx);
             const float f = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);   // both -inf: nothing to scale
@@ -138,12 +127,15 @@ struct RowState {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[e][i] *= f;
         }
-        const float base = m == -INFINITY ? 0.0f : m;   // a row without a key so far: p = 2^-inf = 0
+        // p = 2^(x - m); a row without a key so far: 2^-inf = 0.  An absent
+        // key must stay at -inf: a zero multiplier would make it NaN
+        const float less = add - (m == -INFINITY ? 0.0f : m);
+        mul = mul == 0.0f ? 1e-38f : mul;
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[u][i] = __builtin_amdgcn_exp2f(s[u][i] - base);
+                s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], mul, less));
                 l += s[u][i];
             }
 #pragma unroll
@@ -198,51 +190,52 @@ __device__ inline void write_stats(const AttnArgs &a, const FwdOut &out, int spl
 
 // Many rows: each wavefront owns 32 of the block's 128 rows and all of them
 // read the same key tiles, staged in LDS while the tile before is computed.
-template <int NP, int DP, int KT>
+template <int NP, int DP, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * KT * DP;
-    __shared__ bf16 tiles[2][2][kTile];   // [buffer][K, V]
+    __shared__ __align__(16) bf16 tiles[2][2][kTile];   // [buffer][K, V]
     __shared__ KeyInfo<KT> info[2];
     __shared__ float lut[kLutMax];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     RowBlock w;
     if (!locate(a, w)) return;
     if (w.tile * 128 >= w.nq * w.gs) return;
     if (a.nb) fill_lut(a, w, lut);
     const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
-    const uint8_t *keep = a.keep ? a.keep + w.k0 : nullptr;
     const int n_tiles = (w.nk + KT - 1) / KT, per = (n_tiles + a.splits - 1) / a.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
 
-    RowState<NP, DP> st;
+    RowState<NP, DP, FAST> st;
     st.init(a, w, w.tile * 128 + wave * 32, lane);
     const bool active = __any(st.row >= 0);
-    TileMove<NP, DP, KT, kAttnThreads> mk, mv;
-    KeyLoad kl;
+    TileMove<NP, DP, KT, kAttnThreads, FAST> mk, mv;
+    KeyLoad<KT> kl;
+    mk.init(a.ks, a.D, tid);
+    mv.init(a.vs, a.D, tid);
     auto load = [&](int t) {
-        mk.load(K, a.ks, t * KT, w.nk, a.D, a.vec & 2, tid, keep);
-        mv.load(V, a.vs, t * KT, w.nk, a.D, a.vec & 4, tid, keep);
-        if (wave == 0) kl.load(a, w, t * KT, KT, lane);
+        mk.load(K + t * KT * a.ks, a.ks, w.nk - t * KT, a.D, tid);
+        mv.load(V + t * KT * a.vs, a.vs, w.nk - t * KT, a.D, tid);
+        kl.load(a, w, t * KT, a.nb && wave == 0, lane);
     };
     auto store = [&](int buf) {
-        mk.store(tiles[buf][0], tid);
-        mv.store(tiles[buf][1], tid);
-        if (wave == 0) kl.store(info[buf], lane);
+        const uint64_t mask = kl.mask();
+        mk.store(tiles[buf][0], tid, a.keep && is_partial<KT>(mask), mask);
+        mv.store(tiles[buf][1], tid, a.keep && is_partial<KT>(mask), mask);
+        if (a.nb && wave == 0) kl.store(info[buf], lane);
+        return mask;
     };
+    uint64_t mask = 0;
     if (t0 < t1) {
         load(t0);
-        store(0);
+        mask = store(0);
     }
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1;
         if (t + 1 < t1) load(t + 1);
-        const KeyInfo<KT> &ki = info[buf];
-        const uint64_t mask = uniform64(ki.mask);
-        if (active && mask)
-            st.template step<KT>(a, tiles[buf][0], tiles[buf][1], mask, ki.pos, ki.lo, ki.hi, lut, lane);
-        if (t + 1 < t1) store(buf ^ 1);
+        if (active && mask) st.template step<KT>(a, tiles[buf][0], tiles[buf][1], mask, info[buf], lut, lane);
+        if (t + 1 < t1) mask = store(buf ^ 1);
         __syncthreads();
     }
     if (st.row < 0) return;
@@ -261,7 +254,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kerne
 // holds all of them and takes every NW-th tile of 32 keys, with tiles of its
 // own in LDS, so no wavefront waits for another until the rows are joined at
 // the end.  The keys and values are read once, and that is what bounds it.
-template <int NP, int DP, int NW>
+template <int NP, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * 32 * DP;
@@ -271,38 +264,38 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     __shared__ KeyInfo<32> info[NW];
     __shared__ float lut[kLutMax];
     __shared__ float wave_m[NW][32], wave_l[NW][32];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     RowBlock w;
     if (!locate(a, w)) return;
     if (w.tile * 32 >= w.nq * w.gs) return;
     const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
-    const uint8_t *keep = a.keep ? a.keep + w.k0 : nullptr;
     const int n_tiles = (w.nk + 31) / 32, per = (n_tiles + a.splits - 1) / a.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
     bf16 *kt = lds + 2 * wave * kTile, *vt = kt + kTile;
 
-    TileMove<NP, DP, 32, 64> mk, mv;
-    KeyLoad kl;
+    TileMove<NP, DP, 32, 64, FAST> mk, mv;
+    KeyLoad<32> kl;
+    mk.init(a.ks, a.D, lane);
+    mv.init(a.vs, a.D, lane);
     auto load = [&](int t) {
-        mk.load(K, a.ks, t * 32, w.nk, a.D, a.vec & 2, lane, keep);
-        mv.load(V, a.vs, t * 32, w.nk, a.D, a.vec & 4, lane, keep);
-        kl.load(a, w, t * 32, 32, lane);
+        mk.load(K + t * 32 * a.ks, a.ks, w.nk - t * 32, a.D, lane);
+        mv.load(V + t * 32 * a.vs, a.vs, w.nk - t * 32, a.D, lane);
+        kl.load(a, w, t * 32, a.nb, lane);
     };
     int t = t0 + wave;
     if (t < t1) load(t);
     if (a.nb) fill_lut(a, w, lut);
-    RowState<NP, DP> st;
+    RowState<NP, DP, FAST> st;
     st.init(a, w, w.tile * 32, lane);
     __syncthreads();
     for (; t < t1; t += NW) {
-        mk.store(kt, lane);
-        mv.store(vt, lane);
-        kl.store(info[wave], lane);
+        const uint64_t mask = kl.mask();
+        mk.store(kt, lane, a.keep && is_partial<32>(mask), mask);
+        mv.store(vt, lane, a.keep && is_partial<32>(mask), mask);
+        if (a.nb) kl.store(info[wave], lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (t + NW < t1) load(t + NW);
-        const KeyInfo<32> &ki = info[wave];
-        const uint64_t mask = uniform64(ki.mask);
-        if (mask) st.template step<32>(a, kt, vt, mask, ki.pos, ki.lo, ki.hi, lut, lane);
+        if (mask) st.template step<32>(a, kt, vt, mask, info[wave], lut, lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     // join the wavefronts' rows, in their order
@@ -390,14 +383,14 @@ FwdPlan fwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
     return p;
 }
 
-template <int NP, int DP>
+template <int NP, int DP, bool FAST>
 sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
     const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
     constexpr int NW = NP == 3 && DP == 128 ? 2 : 4;
     if (few)
-        attn_few_kernel<NP, DP, NW><<<grid, 64 * NW, 0, s>>>(a, out);
+        attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, 0, s>>>(a, out);
     else
-        attn_rows_kernel<NP, DP, NP == 1 ? 64 : 32><<<grid, kAttnThreads, 0, s>>>(a, out);
+        attn_rows_kernel<NP, DP, NP == 1 ? 64 : 32, FAST><<<grid, kAttnThreads, 0, s>>>(a, out);
     SN_TRY(launch_status());
     if (a.splits > 1) {
         attn_join_kernel<NP><<<(int)(((int64_t)a.n_q * a.H + 3) / 4), 256, 0, s>>>(a, out);
@@ -406,11 +399,11 @@ sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) 
     return SN_OK;
 }
 
-template <int NP>
+template <int NP, bool FAST>
 sn_status launch_dim(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
-    if (a.D <= 32) return launch<NP, 32>(a, out, few, s);
-    if (a.D <= 64) return launch<NP, 64>(a, out, few, s);
-    return launch<NP, 128>(a, out, few, s);
+    if (a.D <= 32) return launch<NP, 32, FAST>(a, out, few, s);
+    if (a.D <= 64) return launch<NP, 64, FAST>(a, out, few, s);
+    return launch<NP, 128, FAST>(a, out, few, s);
 }
 
 }  // namespace
@@ -436,7 +429,9 @@ sn_status attn_forward(AttnArgs a, int dtype, void *o, float *lse, char *ws, hip
         out.part_ml = reinterpret_cast<float2 *>(ws + kWsBase);
         out.part_o = reinterpret_cast<float *>(ws + kWsBase + align256(rows * p.splits * sizeof(float2)));
     }
-    return dtype == SN_F32 ? launch_dim<3>(a, out, p.few, s) : launch_dim<1>(a, out, p.few, s);
+    if (a.fast)
+        return dtype == SN_F32 ? launch_dim<3, true>(a, out, p.few, s) : launch_dim<1, true>(a, out, p.few, s);
+    return dtype == SN_F32 ? launch_dim<3, false>(a, out, p.few, s) : launch_dim<1, false>(a, out, p.few, s);
 }
 
 }  // namespace sn

@@ -50,7 +50,7 @@ struct AttnArgs {
     const int32_t *q_pos, *k_pos;
     int *status;
     // derived
-    int vec;                                  // 1: q, 2: k, 4: v, 8: d_o rows are 16-byte aligned (and D % 8 = 0)
+    int fast;                                 // every tensor's rows suit 16-byte reads at 31-bit offsets in a tile
     int Gs, subs;                             // heads of a row block's subgroup, subgroups of a key/value head
     int row_tiles, splits;                    // row tiles of the longest segment, key splits
     int lut_base, lut_n;                      // first offset and length of the position table

@@ -57,11 +57,12 @@ size_t attn_workspace(const sn_cross_attention &op) {
     return std::max(attn_forward_workspace(op), attn_backward_workspace(op));
 }
 
-// Whether every row of a tensor can be read 16 bytes at a time.
-bool rows_aligned(const sn_cross_attention &op, const void *p, int64_t stride, int64_t head_stride) {
+// Whether a tensor's rows can be read 16 bytes at a time, and 64 of them
+// from one base with 31-bit byte offsets.
+bool rows_fast(const sn_cross_attention &op, const void *p, int64_t stride, int64_t head_stride) {
     const int64_t per = op.dtype == SN_F32 ? 4 : 8;
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % per == 0 && head_stride % per == 0 &&
-           op.head_dim % 8 == 0;
+           op.head_dim % 8 == 0 && stride >= 0 && stride < (1ll << 24) / (op.dtype == SN_F32 ? 4 : 2);
 }
 
 AttnArgs attn_args(const sn_cross_attention &op, void *ws) {
@@ -88,9 +89,8 @@ AttnArgs attn_args(const sn_cross_attention &op, void *ws) {
     } else {
         a.lut_n = a.nb;
     }
-    a.vec = (rows_aligned(op, op.q, op.q_stride, op.q_head_stride) ? 1 : 0) |
-            (rows_aligned(op, op.k, op.k_stride, op.k_head_stride) ? 2 : 0) |
-            (rows_aligned(op, op.v, op.v_stride, op.v_head_stride) ? 4 : 0);
+    a.fast = rows_fast(op, op.q, op.q_stride, op.q_head_stride) && rows_fast(op, op.k, op.k_stride, op.k_head_stride) &&
+             rows_fast(op, op.v, op.v_stride, op.v_head_stride);
     return a;
 }
 
@@ -178,7 +178,7 @@ sn_status sn_cross_attention_backward(const sn_cross_attention *op, const void *
     a.d_o = d_o;
     a.gs = d_o_stride;
     a.gh = d_o_head_stride;
-    if (rows_aligned(*op, d_o, d_o_stride, d_o_head_stride)) a.vec |= 8;
+    a.fast = a.fast && rows_fast(*op, d_o, d_o_stride, d_o_head_stride) && (reinterpret_cast<uintptr_t>(o) & 15) == 0;
     return attn_backward(a, op->dtype, o, lse, dq, dk, dv, op->bias ? dbias : nullptr, static_cast<char *>(ws),
                          reinterpret_cast<hipStream_t>(stream));
 }
