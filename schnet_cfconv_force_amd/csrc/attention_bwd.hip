@@ -233,32 +233,51 @@ struct RowInfo {
     float L[32], delta[32];
     int pos[32];
     int lo, hi;
+    int run;        // the positions are pos[0], pos[0] + 1, ...
 };
 
-// LDS beyond the tiles: the position table {bias, bucket} of one head and,
-// per wavefront, the bias sums [bucket][column] of the head.  A lane adds to
-// a column of its own (its key and half), so the sums need no order but the
-// lane's; where 160 KB of LDS leave only half the columns, the halves of a
-// wavefront take turns.
-template <int NP, int DP>
-constexpr int bias_columns() { return NP == 3 && DP == 128 ? 32 : 64; }
-template <int NP, int DP>
-size_t dkv_lds(const AttnArgs &a) {
-    return a.nb ? (size_t)a.lut_n * sizeof(float2) + (size_t)4 * a.nb * bias_columns<NP, DP>() * sizeof(float) : 0;
+// The bias sums of a tile whose offsets span several buckets.  LDS float
+// atomics take about 150 clocks each (16 per tile and wavefront doubled the
+// kernel), so where the positions on both sides run without gaps, the tile's
+// dS goes through LDS in a skewed layout instead: a lane reads one diagonal
+// (one offset), sums it and adds it to its entry of a table of offsets.
+// Other positions add to columns of their own [bucket][column], the halves
+// of a wavefront in turn.  Both are one order; the buckets are summed when
+// the head is done.
+constexpr int kRunLut = 512;                    // longest position table that takes the diagonals
+constexpr int kSkewRow = 17, kSkewRows = 62;    // [key + 15][row of 16], zeros around the 32 keys
+constexpr int kRunPad = 64;                     // offsets beyond the table that a tile can reach
+struct BiasLds {
+    int lut, sums, skew, run, total;            // in floats
+};
+__host__ __device__ inline BiasLds bias_lds(int lut_n, int nb) {
+    BiasLds l;
+    l.lut = 0;                                  // {bias log2e, bucket} of one head
+    l.sums = 2 * lut_n;                         // [wavefront][bucket][32]
+    l.skew = l.sums + 4 * 32 * nb;              // [wavefront][kSkewRows][kSkewRow]
+    l.run = l.skew + (lut_n <= kRunLut ? 4 * kSkewRows * kSkewRow : 0);   // [wavefront][lut_n + 2 kRunPad]
+    l.total = l.run + (lut_n <= kRunLut ? 4 * (lut_n + 2 * kRunPad) : 0);
+    return l;
 }
+template <int NP, int DP>
+constexpr int dkv_buffers() { return NP == 3 && DP == 128 ? 1 : 2; }   // 160 KB of LDS
 
 template <int NP, int DP, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void attn_dkv_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
     constexpr int kRows = 32, kTile = NP * kRows * DP;
-    __shared__ __align__(16) bf16 tiles[2][2][kTile];   // [buffer][q, dO]
-    constexpr int kCols = bias_columns<NP, DP>();
-    __shared__ RowInfo info[2];
-    extern __shared__ __align__(16) char lds_bytes[];
-    float2 *lut = reinterpret_cast<float2 *>(lds_bytes);
-    float *sums = reinterpret_cast<float *>(lut + a.lut_n);
+    constexpr int kBuf = dkv_buffers<NP, DP>();
+    __shared__ __align__(16) bf16 tiles[kBuf][2][kTile];   // [buffer][q, dO]
+    __shared__ RowInfo info[kBuf];
+    extern __shared__ __align__(16) float bias_mem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5;
-    float *mine = sums + wave * a.nb * kCols + lane % kCols;   // the lane's column
+    const BiasLds bl = bias_lds(a.lut_n, a.nb);
+    float2 *lut = reinterpret_cast<float2 *>(bias_mem);
+    float *sums = bias_mem + bl.sums;
+    float *mine = sums + wave * a.nb * 32 + (lane & 31);   // the lane's column
+    const int run_n = a.lut_n + 2 * kRunPad;
+    float *skew = bias_mem + bl.skew + wave * kSkewRows * kSkewRow, *run = bias_mem + bl.run + wave * run_n;
+    const bool small_lut = a.nb && a.lut_n <= kRunLut;
     const int n_blocks = a.B * a.Hkv * a.splits * a.row_tiles;
     int i0 = xcd_block(n_blocks);
     if (i0 < 0) return;
@@ -279,6 +298,8 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     const bool active = __any(kept);
     if (a.nb)
         for (int e = tid; e < a.lut_n; e += kAttnThreads) lut[e].y = __int_as_float(bucket_of(a, a.lut_base + e));
+    if (small_lut)
+        for (int i = lane; i < kSkewRows * kSkewRow; i += 64) skew[i] = 0.0f;
     Frag<NP> k[DP / 16], v[DP / 16];
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
@@ -297,6 +318,10 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     const float c = fabsf(a.scale) * kLog2e;
     const int pos = kept ? (a.k_pos ? a.k_pos[k0 + j] : j) : 0;
     const int pos_lo = wave_min(kept ? pos : 0x7fffffff), pos_hi = wave_max(kept ? pos : (int)0x80000000);
+
+    // kept keys whose positions run: the first key's position
+    const int key_base = pos - (lane & 31), key0 = wave_min(kept ? key_base : 0x7fffffff);
+    const bool key_run = small_lut && !__any(kept && (key_base != key0 || abs(pos) >= 1 << 30));
 
     // the rows of all heads that share these keys, head by head
     const int per_head = (nq + kRows - 1) / kRows, n_tiles = per_head * a.G, per = (n_tiles + a.splits - 1) / a.splits;
@@ -331,9 +356,12 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 info[buf].delta[lane] = ri.y;
                 info[buf].pos[lane] = ri_pos;
             }
+            const int first = uniform(ri_pos);
+            const bool gap = __any(in && (ri_pos != first + lane || abs(ri_pos) >= 1 << 30));
             if (lane == 0) {
                 info[buf].lo = lo;
                 info[buf].hi = hi;
+                info[buf].run = !gap;
             }
         }
     };
@@ -344,30 +372,38 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         for (int i = 0; i < 16; ++i) dk[e][i] = dv[e][i] = 0.0f;
     float run_ds = 0.0f;        // of the tiles since the bucket last changed
     int run_bucket = -1, head = -1;
+    auto add_column = [&](int bk, float x) {
+        if (half == 0) atomicAdd(mine + bk * 32, x);
+        __builtin_amdgcn_wave_barrier();
+        if (half == 1) atomicAdd(mine + bk * 32, x);
+        __builtin_amdgcn_wave_barrier();
+    };
     auto flush = [&]() {
-        if (run_bucket < 0) return;
-        if (kCols == 64 || half == 0) atomicAdd(mine + run_bucket * kCols, run_ds);
-        if (kCols != 64) {
-            __builtin_amdgcn_wave_barrier();
-            if (half == 1) atomicAdd(mine + run_bucket * kCols, run_ds);
-        }
+        if (run_bucket >= 0) add_column(run_bucket, run_ds);
         run_ds = 0.0f;
         run_bucket = -1;
     };
-    // the head's sums are complete: every bucket adds its columns in order
+    // the head's sums are complete: every bucket adds its columns and its
+    // offsets in order
     auto finish_head = [&]() {
         flush();
         __syncthreads();
         for (int i = tid; i < a.nb * 4; i += kAttnThreads) {
             const int wv = i / a.nb, bk = i % a.nb;
             float s = 0.0f;
-            for (int k = 0; k < kCols; ++k) s += sums[(wv * a.nb + bk) * kCols + (k + bk) % kCols];
-            sums[(wv * a.nb + bk) * kCols] = s;
+            for (int k = 0; k < 32; ++k) s += sums[(wv * a.nb + bk) * 32 + (k + bk) % 32];
+            if (small_lut) {
+                const int from = bk == 0 ? 0 : (int)((int64_t)a.thr[bk - 1] - a.lut_base) + kRunPad;
+                const int to = bk == a.nb - 1 ? run_n : (int)((int64_t)a.thr[bk] - a.lut_base) + kRunPad;
+                for (int e = from; e < to; ++e) s += bias_mem[bl.run + wv * run_n + e];
+            }
+            sums[(wv * a.nb + bk) * 32 + bk % 32] = s;
         }
         __syncthreads();
-        for (int bk = tid; bk < a.nb; bk += kAttnThreads)
-            part[head * a.nb + bk] = (sums[bk * kCols] + sums[(a.nb + bk) * kCols]) +
-                                     (sums[(2 * a.nb + bk) * kCols] + sums[(3 * a.nb + bk) * kCols]);
+        for (int bk = tid; bk < a.nb; bk += kAttnThreads) {
+            const float *s = sums + bk * 32 + bk % 32;
+            part[head * a.nb + bk] = (s[0] + s[a.nb * 32]) + (s[2 * a.nb * 32] + s[3 * a.nb * 32]);
+        }
         __syncthreads();
     };
     if (a.nb)   // heads that this split does not reach
@@ -379,14 +415,16 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     }
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
+        const int buf = kBuf == 2 ? (t - t0) & 1 : 0;
         if (t + 1 < t1) load(t + 1);
         if (a.nb && t / per_head != head) {   // every wavefront is past the last use of the table (barrier below)
             if (head >= 0) finish_head();
             head = t / per_head;
             for (int e = tid; e < a.lut_n; e += kAttnThreads)
                 lut[e].x = a.bias[(int64_t)(hk * a.G + head) * a.nb + __float_as_int(lut[e].y)] * kLog2e;
-            for (int i = tid; i < 4 * a.nb * kCols; i += kAttnThreads) sums[i] = 0.0f;
+            for (int i = tid; i < 4 * a.nb * 32; i += kAttnThreads) sums[i] = 0.0f;
+            if (small_lut)
+                for (int i = tid; i < 4 * run_n; i += kAttnThreads) bias_mem[bl.run + i] = 0.0f;
             __syncthreads();
         }
         const bf16 *qt = tiles[buf][0], *gt = tiles[buf][1];
@@ -402,7 +440,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             settle(s);
             settle(dp);
             float mul = c, add = 0.0f;
-            int bk[16], bucket = -1;
+            int bucket = -1;
             bool table = false;
             if (a.nb) {
                 const int lo = uniform(ri_t.lo), hi = uniform(ri_t.hi);
@@ -415,9 +453,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                     mul = 1.0f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 e = lut[lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))];
-                        s[i] = fmaf(s[i], c, e.x);
-                        bk[i] = __float_as_int(e.y);
+                        s[i] = fmaf(s[i], c, lut[lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))].x);
                     }
                 }
             }
@@ -434,17 +470,28 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                     run_bucket = bucket;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) run_ds += kept ? dp[i] : 0.0f;
-                } else if (kCols == 64) {
-                    if (kept)
+                } else if (key_run && uniform(ri_t.run)) {
+                    const int first = uniform(ri_t.pos[0]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) atomicAdd(mine + bk[i] * kCols, dp[i]);
+                    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            skew[((lane & 31) + 15) * kSkewRow + 8 * (i / 4) + 4 * half + i % 4] =
+                                kept ? dp[8 * u + i] : 0.0f;
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        float x = 0.0f;   // offset key - row = lane - 15
+                        if (lane < 47) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) x += skew[lane * kSkewRow + i * (kSkewRow + 1)];
+                            run[key0 - (first + 16 * u) + (lane - 15) - a.lut_base + kRunPad] += x;
+                        }
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    }
                 } else {
 #pragma unroll
-                    for (int turn = 0; turn < 2; ++turn) {
-                        if (kept && half == turn)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) atomicAdd(mine + bk[i] * kCols, dp[i]);
-                        __builtin_amdgcn_wave_barrier();
+                    for (int i = 0; i < 16; ++i) {
+                        const int e = lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]));
+                        add_column(__float_as_int(lut[e].y), kept ? dp[i] : 0.0f);
                     }
                 }
             }
@@ -464,7 +511,8 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 }
             }
         }
-        if (t + 1 < t1) store(t + 1, buf ^ 1);
+        if constexpr (kBuf == 1) __syncthreads();
+        if (t + 1 < t1) store(t + 1, kBuf == 2 ? buf ^ 1 : 0);
         __syncthreads();
     }
     if (a.nb && head >= 0) finish_head();
@@ -551,7 +599,7 @@ sn_status launch(const AttnArgs &a0, const BwdArgs &g, const BwdPlan &p, hipStre
         a.row_tiles = p.key_tiles;
         a.splits = p.splits;
         attn_dkv_kernel<NP, DP, FAST><<<xcd_grid(a.B * a.Hkv * a.splits * a.row_tiles), kAttnThreads,
-                                        dkv_lds<NP, DP>(a), s>>>(a, g);
+                                        a.nb ? bias_lds(a.lut_n, a.nb).total * sizeof(float) : 0, s>>>(a, g);
         SN_TRY(launch_status());
         if (a.splits > 1) {
             const int64_t n = (int64_t)a.n_k * a.Hkv * 2 * a.D;
