@@ -94,36 +94,78 @@ __device__ inline int tile_at(int row, int chunk) {
     return row * DP + ((chunk ^ swizzle<DP>(row)) << 3);
 }
 
-// Rows row0 .. row0 + 31, elements 16 s + 8 (l/32) ..: an A operand whose
-// rows are tile rows.  Planes lie `plane` elements apart.
-template <int NP, int DP>
-__device__ inline Frag<NP> frag_rows(const bf16 *tile, int plane, int row0, int s, int lane) {
-    Frag<NP> f;
-    const int at = tile_at<DP>(row0 + (lane & 31), 2 * s + (lane >> 5));
-#pragma unroll
-    for (int n = 0; n < NP; ++n) f.p[n] = *reinterpret_cast<const bf16x8 *>(tile + n * plane + at);
-    return f;
+// LDS addresses are byte offsets: a tile's (uniform, a multiple of 256) plus a
+// lane's.
+typedef __attribute__((address_space(3))) char *lds_ptr;
+__device__ inline uint32_t lds_offset(const void *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)(const char *)p;
 }
 
-// Elements 32 e .. 32 e + 31 as rows, tile rows row0 .. row0 + 15 as k in the
-// order of a score tile's registers: the transposing LDS read hands lane i
-// of sixteen the column i of the 4 x 16 block that the sixteen lanes address.
-template <int NP, int DP>
-__device__ inline Frag<NP> frag_cols(const bf16 *tile, int plane, int row0, int e, int lane) {
-    Frag<NP> f;
-    const int i = lane & 15, row = row0 + 4 * (lane >> 5) + (i >> 2);
-    const int d = 32 * e + (lane & 16) + 4 * (i & 3);
-    typedef __attribute__((address_space(3))) short4v *lds4;
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds4)(tile + n * plane + tile_at<DP>(row, d >> 3) + (d & 7)));
-        short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds4)(tile + n * plane + tile_at<DP>(row + 8, d >> 3) + (d & 7)));
-        const bf16x4 a = __builtin_bit_cast(bf16x4, lo), b = __builtin_bit_cast(bf16x4, hi);
-        f.p[n] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+// A lane's places in a tile.  The swizzle leaves the chunk's upper bits to
+// the fragment's index alone, so an index is one exclusive-or away, and rows
+// 16 further are a constant.
+template <int DP>
+struct TileLane {
+    uint32_t rows, cols, cols8;
+    __device__ inline TileLane(int lane) {
+        rows = 2 * tile_at<DP>(lane & 31, lane >> 5);
+        const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2), d = (lane & 16) + 4 * (i & 3);
+        cols = 2 * (tile_at<DP>(row, d >> 3) + (d & 7));
+        cols8 = 2 * (tile_at<DP>(row + 8, d >> 3) + (d & 7));
     }
+    // Rows row0 .. row0 + 31 of the tile (row0 a multiple of 32), elements
+    // 16 s + 8 (l/32) ..: an A operand whose rows are tile rows.
+    __device__ inline bf16x8 frag_rows(uint32_t tile, int row0, int s) const {
+        const uint32_t at = (rows + tile) ^ (s << 5);
+        return *(__attribute__((address_space(3))) const bf16x8 *)(lds_ptr)(uintptr_t)(at + row0 * 2 * DP);
+    }
+    // Elements 32 e .. 32 e + 31 as rows, tile rows row0 .. row0 + 15 (a
+    // multiple of 16) as k in the order of a score tile's registers: the
+    // transposing LDS read hands lane i of sixteen the column i of the 4 x 16
+    // block that the sixteen lanes address.
+    __device__ inline bf16x8 frag_cols(uint32_t tile, int row0, int e) const {
+        typedef __attribute__((address_space(3))) short4v *lds4;
+        const uint32_t a0 = ((cols + tile) ^ (e << 6)) + row0 * 2 * DP, a1 = ((cols8 + tile) ^ (e << 6)) + row0 * 2 * DP;
+        const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)a0));
+        const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)a1));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+// The same with NP planes, `plane` bytes apart.
+template <int NP, int DP>
+__device__ inline Frag<NP> frag_rows(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0, int s) {
+    Frag<NP> f;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) f.p[n] = l.frag_rows(tile + n * plane, row0, s);
     return f;
+}
+template <int NP, int DP>
+__device__ inline Frag<NP> frag_cols(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0, int e) {
+    Frag<NP> f;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) f.p[n] = l.frag_cols(tile + n * plane, row0, e);
+    return f;
+}
+// x += A B over all of a row's elements, A the tile's rows row0 .. row0 + 31.
+// One plane: every operand is on its way before the first product.
+template <int NP, int DP>
+__device__ inline floatx16 rows_product(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0,
+                                        const Frag<NP> (&b)[DP / 16]) {
+    floatx16 x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+    if constexpr (NP == 1) {
+        bf16x8 f[DP / 16];
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) f[s] = l.frag_rows(tile, row0, s);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[s], b[s].p[0], x, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) x = mma<NP>(frag_rows<NP, DP>(l, tile, plane, row0, s), b[s], x);
+    }
+    return x;
 }
 
 // Eight elements at `p` (elements d .. d + 7 of a row of D; zero beyond D),
@@ -298,6 +340,9 @@ __device__ inline bool locate(const AttnArgs &a, RowBlock &w) {
     w.gs = min(a.Gs, a.G - w.sub * a.Gs);
     segment_rows(a.q_ptr, w.b, a.B, a.n_q, a.max_q, a.status, w.q0, w.nq);
     segment_rows(a.k_ptr, w.b, a.B, a.n_k, a.max_k, a.status, w.k0, w.nk);
+    // in scalar registers: the tiles' buffer descriptors are made of them
+    w.q0 = uniform(w.q0); w.nq = uniform(w.nq);
+    w.k0 = uniform(w.k0); w.nk = uniform(w.nk);
     return true;
 }
 

@@ -57,7 +57,7 @@ template <int NP, int DP, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * kDqKeys * DP;
-    __shared__ __align__(16) bf16 tiles[2][2][kTile];   // [buffer][K, V]
+    __shared__ __align__(256) bf16 tiles[2][2][kTile];   // [buffer][K, V]
     __shared__ KeyInfo<kDqKeys> info[2];
     __shared__ float lut[kLutMax];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5;
@@ -132,6 +132,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[e][i] = 0.0f;
     float row_ds = 0.0f;    // sum of the row's dS (this half's keys)
+    const TileLane<DP> tl(lane);
+    const uint32_t lds0 = lds_offset(tiles);
+    constexpr uint32_t kPlane = kDqKeys * DP * sizeof(bf16), kBytes = NP * kPlane;
     uint64_t mask = 0;
     if (n_tiles > 0) {
         load(0);
@@ -141,16 +144,10 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
     for (int t = 0; t < n_tiles; ++t) {
         const int buf = t & 1;
         if (t + 1 < n_tiles) load(t + 1);
-        const bf16 *kt = tiles[buf][0], *vt = tiles[buf][1];
+        const uint32_t kt = lds0 + 2 * buf * kBytes, vt = kt + kBytes;
         const KeyInfo<kDqKeys> &ki = info[buf];
         if (active && mask) {
-            floatx16 s, dp;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) s = mma<NP>(frag_rows<NP, DP>(kt, kDqKeys * DP, 0, k, lane), q[k], s);
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) dp = mma<NP>(frag_rows<NP, DP>(vt, kDqKeys * DP, 0, k, lane), dO[k], dp);
+            floatx16 s = rows_product<NP, DP>(tl, kt, kPlane, 0, q), dp = rows_product<NP, DP>(tl, vt, kPlane, 0, dO);
             settle(s);
             settle(dp);
             float mul = c, less = -L;
@@ -190,7 +187,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
                 const Frag<NP> ds = split8f<NP>(x);
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e)
-                    dq[e] = mma<NP>(frag_cols<NP, DP>(kt, kDqKeys * DP, 16 * u, e, lane), ds, dq[e]);
+                    dq[e] = mma<NP>(frag_cols<NP, DP>(tl, kt, kPlane, 16 * u, e), ds, dq[e]);
             }
         }
         if (t + 1 < n_tiles) mask = store(buf ^ 1);
@@ -267,7 +264,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     using T = typename RowOf<NP>::T;
     constexpr int kRows = 32, kTile = NP * kRows * DP;
     constexpr int kBuf = dkv_buffers<NP, DP>();
-    __shared__ __align__(16) bf16 tiles[kBuf][2][kTile];   // [buffer][q, dO]
+    __shared__ __align__(256) bf16 tiles[kBuf][2][kTile];   // [buffer][q, dO]
     __shared__ RowInfo info[kBuf];
     extern __shared__ __align__(16) float bias_mem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5;
@@ -287,6 +284,8 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     int q0, nq, k0, nk;
     segment_rows(a.q_ptr, b, a.B, a.n_q, a.max_q, a.status, q0, nq);
     segment_rows(a.k_ptr, b, a.B, a.n_k, a.max_k, a.status, k0, nk);
+    q0 = uniform(q0); nq = uniform(nq);
+    k0 = uniform(k0); nk = uniform(nk);
     float *part = a.nb ? g.part_bias + (((int64_t)hk * a.B + b) * a.row_tiles * a.splits + key_tile * a.splits + split) * a.G * a.nb
                        : nullptr;
     if (key_tile * 128 >= nk) {
@@ -365,6 +364,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             }
         }
     };
+    const TileLane<DP> tl(lane);
+    const uint32_t lds0 = lds_offset(tiles);
+    constexpr uint32_t kPlane = kRows * DP * sizeof(bf16), kBytes = NP * kPlane;
     floatx16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
@@ -427,16 +429,10 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 for (int i = tid; i < 4 * run_n; i += kAttnThreads) bias_mem[bl.run + i] = 0.0f;
             __syncthreads();
         }
-        const bf16 *qt = tiles[buf][0], *gt = tiles[buf][1];
+        const uint32_t qt = lds0 + 2 * buf * kBytes, gt = qt + kBytes;
         const RowInfo &ri_t = info[buf];
         if (active) {
-            floatx16 s, dp;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-            for (int e = 0; e < DP / 16; ++e) s = mma<NP>(frag_rows<NP, DP>(qt, kRows * DP, 0, e, lane), k[e], s);
-#pragma unroll
-            for (int e = 0; e < DP / 16; ++e) dp = mma<NP>(frag_rows<NP, DP>(gt, kRows * DP, 0, e, lane), v[e], dp);
+            floatx16 s = rows_product<NP, DP>(tl, qt, kPlane, 0, k), dp = rows_product<NP, DP>(tl, gt, kPlane, 0, v);
             settle(s);
             settle(dp);
             float mul = c, add = 0.0f;
@@ -506,8 +502,8 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 const Frag<NP> p = split8f<NP>(x), ds = split8f<NP>(y);
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e) {
-                    dv[e] = mma<NP>(frag_cols<NP, DP>(gt, kRows * DP, 16 * u, e, lane), p, dv[e]);
-                    dk[e] = mma<NP>(frag_cols<NP, DP>(qt, kRows * DP, 16 * u, e, lane), ds, dk[e]);
+                    dv[e] = mma<NP>(frag_cols<NP, DP>(tl, gt, kPlane, 16 * u, e), p, dv[e]);
+                    dk[e] = mma<NP>(frag_cols<NP, DP>(tl, qt, kPlane, 16 * u, e), ds, dk[e]);
                 }
             }
         }

@@ -65,21 +65,25 @@ struct RowState {
             for (int i = 0; i < 16; ++i) o[e][i] = 0.0f;
     }
 
-    // One tile of KT keys (KT / 32 score tiles).  mask: the kept keys; ki:
-    // their positions (used with a bias).
+    // One tile of KT keys (KT / 32 score tiles) at the LDS offsets kt, vt.
+    // mask: the kept keys; ki: their positions (used with a bias).
     template <int KT>
-    __device__ inline void step(const AttnArgs &a, const bf16 *kt, const bf16 *vt, uint64_t mask, const KeyInfo<KT> &ki,
-                                const float *lut, int lane) {
+    __device__ inline void step(const AttnArgs &a, const TileLane<DP> &tl, uint32_t kt, uint32_t vt, uint64_t mask,
+                                const KeyInfo<KT> &ki, const float *lut, int lane) {
         constexpr int NS = KT / 32;
+        constexpr uint32_t kPlane = KT * DP * sizeof(bf16);
         const int half = lane >> 5;
         floatx16 s[NS];
 #pragma unroll
-        for (int u = 0; u < NS; ++u) {
+        for (int u = 0; u < NS; ++u) s[u] = rows_product<NP, DP>(tl, kt, kPlane, 32 * u, q);
+        // one plane: the values are on their way during the softmax
+        bf16x8 vf[NP == 1 ? NS * 2 * (DP / 32) : 1];
+        if constexpr (NP == 1) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+            for (int u = 0; u < 2 * NS; ++u)
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k)
-                s[u] = mma<NP>(frag_rows<NP, DP>(kt, KT * DP, 32 * u, k, lane), q[k], s[u]);
+                for (int e = 0; e < DP / 32; ++e) vf[u * (DP / 32) + e] = tl.frag_cols(vt, 16 * u, e);
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int u = 0; u < NS; ++u) settle(s[u]);
@@ -147,8 +151,12 @@ struct RowState {
                 // term of O, as much as rounding o itself costs
                 const Frag<NP> p = split8f<NP>(x);
 #pragma unroll
-                for (int e = 0; e < DP / 32; ++e)
-                    o[e] = mma<NP>(frag_cols<NP, DP>(vt, KT * DP, 32 * u + 16 * t, e, lane), p, o[e]);
+                for (int e = 0; e < DP / 32; ++e) {
+                    if constexpr (NP == 1)
+                        o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[(2 * u + t) * (DP / 32) + e], p.p[0], o[e], 0, 0, 0);
+                    else
+                        o[e] = mma<NP>(frag_cols<NP, DP>(tl, vt, kPlane, 32 * u + 16 * t, e), p, o[e]);
+                }
             }
         }
     }
@@ -194,7 +202,7 @@ template <int NP, int DP, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * KT * DP;
-    __shared__ __align__(16) bf16 tiles[2][2][kTile];   // [buffer][K, V]
+    __shared__ __align__(256) bf16 tiles[2][2][kTile];   // [buffer][K, V]
     __shared__ KeyInfo<KT> info[2];
     __shared__ float lut[kLutMax];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -208,6 +216,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kerne
 
     RowState<NP, DP, FAST> st;
     st.init(a, w, w.tile * 128 + wave * 32, lane);
+    const TileLane<DP> tl(lane);
+    const uint32_t lds0 = lds_offset(tiles);
+    constexpr uint32_t kBytes = kTile * sizeof(bf16);
     const bool active = __any(st.row >= 0);
     TileMove<NP, DP, KT, kAttnThreads, FAST> mk, mv;
     KeyLoad<KT> kl;
@@ -234,7 +245,8 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kerne
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1;
         if (t + 1 < t1) load(t + 1);
-        if (active && mask) st.template step<KT>(a, tiles[buf][0], tiles[buf][1], mask, info[buf], lut, lane);
+        if (active && mask)
+            st.template step<KT>(a, tl, lds0 + 2 * buf * kBytes, lds0 + (2 * buf + 1) * kBytes, mask, info[buf], lut, lane);
         if (t + 1 < t1) mask = store(buf ^ 1);
         __syncthreads();
     }
@@ -260,7 +272,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     constexpr int kTile = NP * 32 * DP;
     constexpr int kJoin = DP * 33 * 2;   // O^T of all rows in fp32, as bf16 elements
     constexpr int kLds = 2 * NW * kTile > kJoin ? 2 * NW * kTile : kJoin;
-    __shared__ __align__(16) bf16 lds[kLds];
+    __shared__ __align__(256) bf16 lds[kLds];
     __shared__ KeyInfo<32> info[NW];
     __shared__ float lut[kLutMax];
     __shared__ float wave_m[NW][32], wave_l[NW][32];
@@ -287,6 +299,8 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     if (a.nb) fill_lut(a, w, lut);
     RowState<NP, DP, FAST> st;
     st.init(a, w, w.tile * 32, lane);
+    const TileLane<DP> tl(lane);
+    const uint32_t lds_k = uniform((int)lds_offset(kt)), lds_v = lds_k + kTile * sizeof(bf16);
     __syncthreads();
     for (; t < t1; t += NW) {
         const uint64_t mask = kl.mask();
@@ -295,7 +309,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
         if (a.nb) kl.store(info[wave], lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (t + NW < t1) load(t + NW);
-        if (mask) st.template step<32>(a, kt, vt, mask, info[wave], lut, lane);
+        if (mask) st.template step<32>(a, tl, lds_k, lds_v, mask, info[wave], lut, lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     // join the wavefronts' rows, in their order
@@ -390,7 +404,7 @@ sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) 
     if (few)
         attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, 0, s>>>(a, out);
     else
-        attn_rows_kernel<NP, DP, NP == 1 ? 64 : 32, FAST><<<grid, kAttnThreads, 0, s>>>(a, out);
+        attn_rows_kernel<NP, DP, NP == 1 && DP < 128 ? 64 : 32, FAST><<<grid, kAttnThreads, 0, s>>>(a, out);
     SN_TRY(launch_status());
     if (a.splits > 1) {
         attn_join_kernel<NP><<<(int)(((int64_t)a.n_q * a.H + 3) / 4), 256, 0, s>>>(a, out);
