@@ -300,10 +300,14 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 
 // --------------------------------------------------------------- positions
 
+// thr is padded with the type's largest value, so eight are read and
+// compared at a time.
 __device__ inline int bucket_of(const AttnArgs &a, int rel) {
     int n = 0;
-    for (int t = 0; t + 1 < a.nb; ++t) n += rel >= a.thr[t];
-    return n;
+    for (int t = 0; t < a.nb - 1; t += 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n += rel >= a.thr[t + j];
+    return min(n, a.nb - 1);
 }
 // Entry of the position table for one offset: the table holds every offset
 // from below the first threshold to the last one, its ends stand for all
@@ -312,6 +316,15 @@ __device__ inline int lut_index(const AttnArgs &a, int rel) {
     return min(max(rel, a.lut_base), a.lut_base + (a.lut_n - 1)) - a.lut_base;
 }
 __device__ inline int offset_of(int k_pos, int q_pos) { return __builtin_elementwise_sub_sat(k_pos, q_pos); }
+// In LDS a table has kLutPad more entries at each end, copies of its ends.
+// Where one side's positions run without gaps, up to 64 consecutive offsets
+// are then consecutive entries from run_index() on, wherever they lie, and
+// an element's entry is a constant away.
+constexpr int kLutPad = 64;
+__device__ inline int lut_stride(const AttnArgs &a) { return a.lut_n + 2 * kLutPad; }
+__device__ inline int run_index(const AttnArgs &a, int first_rel) {
+    return min(max(first_rel, a.lut_base - kLutPad), a.lut_base + a.lut_n) - (a.lut_base - kLutPad);
+}
 
 // --------------------------------------------------------------- rows of a block
 
@@ -348,9 +361,9 @@ __device__ inline bool locate(const AttnArgs &a, RowBlock &w) {
 
 // Position table of the subgroup's heads, in log2 units.
 __device__ inline void fill_lut(const AttnArgs &a, const RowBlock &w, float *lut) {
-    for (int e = threadIdx.x; e < a.lut_n; e += blockDim.x) {
-        const int bk = bucket_of(a, a.lut_base + e);
-        for (int g = 0; g < w.gs; ++g) lut[g * a.lut_n + e] = a.bias[(int64_t)(w.h0 + g) * a.nb + bk] * kLog2e;
+    for (int e = threadIdx.x; e < lut_stride(a); e += blockDim.x) {
+        const int bk = bucket_of(a, a.lut_base + min(max(e - kLutPad, 0), a.lut_n - 1));
+        for (int g = 0; g < w.gs; ++g) lut[g * lut_stride(a) + e] = a.bias[(int64_t)(w.h0 + g) * a.nb + bk] * kLog2e;
     }
 }
 
@@ -360,14 +373,16 @@ template <int KT>
 struct KeyInfo {
     int pos[KT];
     int lo, hi;     // of the kept keys
+    int run;        // the positions are pos[0], pos[0] + 1, ...
 };
 template <int KT>
 struct KeyLoad {
     int pos;
+    bool in;
     uint8_t kept;
     __device__ inline void load(const AttnArgs &a, const RowBlock &w, int key0, bool positions, int lane) {
         const int j = key0 + lane;
-        const bool in = lane < KT && j < w.nk;
+        in = lane < KT && j < w.nk;
         kept = in;
         pos = j;
         if (positions && a.k_pos && in) pos = a.k_pos[w.k0 + j];
@@ -377,10 +392,12 @@ struct KeyLoad {
     __device__ inline void store(KeyInfo<KT> &k, int lane) const {
         const bool ok = kept != 0;
         const int lo = wave_min(ok ? pos : 0x7fffffff), hi = wave_max(ok ? pos : (int)0x80000000);
+        const bool gap = __any(in && (pos != uniform(pos) + lane || abs(pos) >= 1 << 30));
         if (lane < KT) k.pos[lane] = pos;
         if (lane == 0) {
             k.lo = lo;
             k.hi = hi;
+            k.run = !gap;
         }
     }
 };

@@ -59,54 +59,11 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
     constexpr int kTile = NP * kDqKeys * DP;
     __shared__ __align__(256) bf16 tiles[2][2][kTile];   // [buffer][K, V]
     __shared__ KeyInfo<kDqKeys> info[2];
-    __shared__ float lut[kLutMax];
+    extern __shared__ float lut[];   // [head of the subgroup][lut_stride]
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5;
     RowBlock w;
     if (!locate(a, w)) return;
     if (w.tile * 128 >= w.nq * w.gs) return;
-    if (a.nb) fill_lut(a, w, lut);
-
-    const int r = w.tile * 128 + wave * 32 + (lane & 31), qi = r / w.gs, hg = r % w.gs;
-    const int row = qi < w.nq ? w.q0 + qi : -1;
-    const int64_t at = (int64_t)row * a.H + w.h0 + hg;
-    const bool active = __any(row >= 0);
-    const float c = fabsf(a.scale) * kLog2e;
-    Frag<NP> q[DP / 16], dO[DP / 16];
-    float delta = 0.0f, L = INFINITY;
-#pragma unroll
-    for (int s = 0; s < DP / 16; ++s) {
-        const int d = 16 * s + 8 * half;
-        Raw8<NP> rq = raw_zero<NP>(), rg = rq, ro = rq;
-        if (row >= 0) {
-            rq = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + hg) * a.qh + d, d, a.D, FAST);
-            rg = load8<NP>((const T *)a.d_o + row * a.gs + (w.h0 + hg) * a.gh + d, d, a.D, FAST);
-            ro = load8<NP>((const T *)g.o + at * a.D + d, d, a.D, FAST);
-        }
-        q[s] = to_frag<NP>(rq);
-        dO[s] = to_frag<NP>(rg);
-        if (a.scale < 0.0f)
-#pragma unroll
-            for (int n = 0; n < NP; ++n) q[s].p[n] = -q[s].p[n];
-        const Frag<NP> fo = to_frag<NP>(ro);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float x = 0.0f, y = 0.0f;
-#pragma unroll
-            for (int n = NP - 1; n >= 0; --n) {
-                x += (float)dO[s].p[n][j];
-                y += (float)fo.p[n][j];
-            }
-            delta = fmaf(x, y, delta);
-        }
-    }
-    delta += half_swap(delta);
-    int pos = 0;
-    if (row >= 0) {
-        pos = a.q_pos ? a.q_pos[row] : qi;
-        const float lse = g.lse[at];
-        L = lse == -INFINITY ? INFINITY : lse * kLog2e - kLift;
-    }
-    const int pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff), pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
 
     const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
     const int n_tiles = (w.nk + kDqKeys - 1) / kDqKeys;
@@ -126,6 +83,58 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
         if (a.nb && wave == 0) kl.store(info[buf], lane);
         return mask;
     };
+
+    // the first tile, the rows and the bias are on their way together
+    const int r = w.tile * 128 + wave * 32 + (lane & 31), qi = r / w.gs, hg = r % w.gs;
+    const int row = qi < w.nq ? w.q0 + qi : -1;
+    const int64_t at = (int64_t)row * a.H + w.h0 + hg;
+    const bool active = __any(row >= 0);
+    const float c = fabsf(a.scale) * kLog2e;
+    Raw8<NP> rq[DP / 16], rg[DP / 16], ro[DP / 16];
+    if (n_tiles > 0) load(0);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) rq[s] = rg[s] = ro[s] = raw_zero<NP>();
+    int pos = 0;
+    float lse = -INFINITY;
+    if (row >= 0) {
+        const T *pq = (const T *)a.q + row * a.qs + (w.h0 + hg) * a.qh;
+        const T *pg = (const T *)a.d_o + row * a.gs + (w.h0 + hg) * a.gh, *po = (const T *)g.o + at * a.D;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+            const int d = 16 * s + 8 * half;
+            rq[s] = load8<NP>(pq + d, d, a.D, FAST);
+            rg[s] = load8<NP>(pg + d, d, a.D, FAST);
+            ro[s] = load8<NP>(po + d, d, a.D, FAST);
+        }
+        pos = a.q_pos ? a.q_pos[row] : qi;
+        lse = g.lse[at];
+    }
+    if (a.nb) fill_lut(a, w, lut);
+    Frag<NP> q[DP / 16], dO[DP / 16];
+    float delta = 0.0f;
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+        q[s] = to_frag<NP>(rq[s]);
+        dO[s] = to_frag<NP>(rg[s]);
+        if (a.scale < 0.0f)
+#pragma unroll
+            for (int n = 0; n < NP; ++n) q[s].p[n] = -q[s].p[n];
+        const Frag<NP> fo = to_frag<NP>(ro[s]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float x = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int n = NP - 1; n >= 0; --n) {
+                x += (float)dO[s].p[n][j];
+                y += (float)fo.p[n][j];
+            }
+            delta = fmaf(x, y, delta);
+        }
+    }
+    delta += half_swap(delta);
+    const float L = lse == -INFINITY ? INFINITY : lse * kLog2e - kLift;
+    const int pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff), pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
+
     floatx16 dq[DP / 32];
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
@@ -136,10 +145,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
     const uint32_t lds0 = lds_offset(tiles);
     constexpr uint32_t kPlane = kDqKeys * DP * sizeof(bf16), kBytes = NP * kPlane;
     uint64_t mask = 0;
-    if (n_tiles > 0) {
-        load(0);
-        mask = store(0);
-    }
+    if (n_tiles > 0) mask = store(0);
     __syncthreads();
     for (int t = 0; t < n_tiles; ++t) {
         const int buf = t & 1;
@@ -154,14 +160,20 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
             if (a.nb) {
                 const int lo = uniform(ki.lo), hi = uniform(ki.hi);
                 const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
+                const float *mine = lut + hg * lut_stride(a);
                 if (first == last) {
-                    less += lut[hg * a.lut_n + first];
+                    less += mine[kLutPad + first];
+                } else if (a.lut_run && uniform(ki.run)) {
+                    mul = 1.0f;
+                    mine += run_index(a, offset_of(uniform(ki.pos[0]), pos)) + 4 * half;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, mine[8 * (i / 4) + i % 4]);
                 } else {
                     mul = 1.0f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = lut_index(a, offset_of(ki.pos[8 * (i / 4) + 4 * half + i % 4], pos));
-                        s[i] = fmaf(s[i], c, lut[hg * a.lut_n + e]);
+                        s[i] = fmaf(s[i], c, mine[kLutPad + e]);
                     }
                 }
             }
@@ -250,7 +262,7 @@ struct BiasLds {
 __host__ __device__ inline BiasLds bias_lds(int lut_n, int nb) {
     BiasLds l;
     l.lut = 0;                                  // {bias log2e, bucket} of one head
-    l.sums = 2 * lut_n;                         // [wavefront][bucket][32]
+    l.sums = 2 * (lut_n + 2 * kLutPad);         // [wavefront][bucket][32]
     l.skew = l.sums + 4 * 32 * nb;              // [wavefront][kSkewRows][kSkewRow]
     l.run = l.skew + (lut_n <= kRunLut ? 4 * kSkewRows * kSkewRow : 0);   // [wavefront][lut_n + 2 kRunPad]
     l.total = l.run + (lut_n <= kRunLut ? 4 * (lut_n + 2 * kRunPad) : 0);
@@ -292,36 +304,6 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         for (int i = tid; a.nb && i < a.G * a.nb; i += kAttnThreads) part[i] = 0.0f;
         return;
     }
-    const int j = key_tile * 128 + wave * 32 + (lane & 31);
-    const bool have = j < nk, kept = have && (!a.keep || a.keep[k0 + j]);
-    const bool active = __any(kept);
-    if (a.nb)
-        for (int e = tid; e < a.lut_n; e += kAttnThreads) lut[e].y = __int_as_float(bucket_of(a, a.lut_base + e));
-    if (small_lut)
-        for (int i = lane; i < kSkewRows * kSkewRow; i += 64) skew[i] = 0.0f;
-    Frag<NP> k[DP / 16], v[DP / 16];
-#pragma unroll
-    for (int s = 0; s < DP / 16; ++s) {
-        const int d = 16 * s + 8 * half;
-        Raw8<NP> rk = raw_zero<NP>(), rv = rk;
-        if (kept) {
-            rk = load8<NP>((const T *)a.k + (int64_t)(k0 + j) * a.ks + hk * a.kh + d, d, a.D, FAST);
-            rv = load8<NP>((const T *)a.v + (int64_t)(k0 + j) * a.vs + hk * a.vh + d, d, a.D, FAST);
-        }
-        k[s] = to_frag<NP>(rk);
-        v[s] = to_frag<NP>(rv);
-        if (a.scale < 0.0f)
-#pragma unroll
-            for (int n = 0; n < NP; ++n) k[s].p[n] = -k[s].p[n];
-    }
-    const float c = fabsf(a.scale) * kLog2e;
-    const int pos = kept ? (a.k_pos ? a.k_pos[k0 + j] : j) : 0;
-    const int pos_lo = wave_min(kept ? pos : 0x7fffffff), pos_hi = wave_max(kept ? pos : (int)0x80000000);
-
-    // kept keys whose positions run: the first key's position
-    const int key_base = pos - (lane & 31), key0 = wave_min(kept ? key_base : 0x7fffffff);
-    const bool key_run = small_lut && !__any(kept && (key_base != key0 || abs(pos) >= 1 << 30));
-
     // the rows of all heads that share these keys, head by head
     const int per_head = (nq + kRows - 1) / kRows, n_tiles = per_head * a.G, per = (n_tiles + a.splits - 1) / a.splits;
     const int t0 = split * per, t1 = min(n_tiles, t0 + per);
@@ -344,6 +326,50 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             }
         }
     };
+
+    // the first tile, the keys and the bias are on their way together
+    const int j = key_tile * 128 + wave * 32 + (lane & 31);
+    const bool have = j < nk;
+    Raw8<NP> rk[DP / 16], rv[DP / 16];
+    if (t0 < t1) load(t0);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) rk[s] = rv[s] = raw_zero<NP>();
+    uint8_t keep = have;
+    int pos = j;
+    if (have) {
+        const T *pk = (const T *)a.k + (int64_t)(k0 + j) * a.ks + hk * a.kh;
+        const T *pv = (const T *)a.v + (int64_t)(k0 + j) * a.vs + hk * a.vh;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+            const int d = 16 * s + 8 * half;
+            rk[s] = load8<NP>(pk + d, d, a.D, FAST);
+            rv[s] = load8<NP>(pv + d, d, a.D, FAST);
+        }
+        if (a.keep) keep = a.keep[k0 + j];
+        if (a.k_pos) pos = a.k_pos[k0 + j];
+    }
+    if (a.nb)
+        for (int e = tid; e < lut_stride(a); e += kAttnThreads)
+            lut[e].y = __int_as_float(bucket_of(a, a.lut_base + min(max(e - kLutPad, 0), a.lut_n - 1)));
+    if (small_lut)
+        for (int i = lane; i < kSkewRows * kSkewRow; i += 64) skew[i] = 0.0f;
+    const bool kept = keep != 0, active = __any(kept);
+    Frag<NP> k[DP / 16], v[DP / 16];
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+        k[s] = to_frag<NP>(kept ? rk[s] : raw_zero<NP>());
+        v[s] = to_frag<NP>(kept ? rv[s] : raw_zero<NP>());
+        if (a.scale < 0.0f)
+#pragma unroll
+            for (int n = 0; n < NP; ++n) k[s].p[n] = -k[s].p[n];
+    }
+    const float c = fabsf(a.scale) * kLog2e;
+    const int pos_lo = wave_min(kept ? pos : 0x7fffffff), pos_hi = wave_max(kept ? pos : (int)0x80000000);
+
+    // kept keys whose positions run: the first key's position
+    const int key_base = pos - (lane & 31), key0 = wave_min(kept ? key_base : 0x7fffffff);
+    const bool key_run = small_lut && !__any(kept && (key_base != key0 || abs(pos) >= 1 << 30));
+
     auto store = [&](int t, int buf) {
         mq.store(tiles[buf][0], tid, false, 0);
         mg.store(tiles[buf][1], tid, false, 0);
@@ -411,10 +437,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     if (a.nb)   // heads that this split does not reach
         for (int i = tid; i < a.G * a.nb; i += kAttnThreads)
             if (t0 >= t1 || i / a.nb < t0 / per_head || i / a.nb > (t1 - 1) / per_head) part[i] = 0.0f;
-    if (t0 < t1) {
-        load(t0);
-        store(t0, 0);
-    }
+    if (t0 < t1) store(t0, 0);
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         const int buf = kBuf == 2 ? (t - t0) & 1 : 0;
@@ -422,7 +445,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         if (a.nb && t / per_head != head) {   // every wavefront is past the last use of the table (barrier below)
             if (head >= 0) finish_head();
             head = t / per_head;
-            for (int e = tid; e < a.lut_n; e += kAttnThreads)
+            for (int e = tid; e < lut_stride(a); e += kAttnThreads)
                 lut[e].x = a.bias[(int64_t)(hk * a.G + head) * a.nb + __float_as_int(lut[e].y)] * kLog2e;
             for (int i = tid; i < 4 * a.nb * 32; i += kAttnThreads) sums[i] = 0.0f;
             if (small_lut)
@@ -443,13 +466,18 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 const int first = lut_index(a, offset_of(pos_lo, hi)), last = lut_index(a, offset_of(pos_hi, lo));
                 table = first != last;
                 if (!table) {
-                    add = lut[first].x;
-                    bucket = uniform(__float_as_int(lut[first].y));
+                    add = lut[kLutPad + first].x;
+                    bucket = uniform(__float_as_int(lut[kLutPad + first].y));
+                } else if (a.lut_run && uniform(ri_t.run)) {   // later rows, smaller offsets
+                    mul = 1.0f;
+                    const float2 *mine = lut + run_index(a, offset_of(pos, uniform(ri_t.pos[0]) + 31)) + 3 - 4 * half;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, mine[28 - 8 * (i / 4) - i % 4].x);
                 } else {
                     mul = 1.0f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        s[i] = fmaf(s[i], c, lut[lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))].x);
+                        s[i] = fmaf(s[i], c, lut[kLutPad + lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))].x);
                     }
                 }
             }
@@ -487,7 +515,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]));
-                        add_column(__float_as_int(lut[e].y), kept ? dp[i] : 0.0f);
+                        add_column(__float_as_int(lut[kLutPad + e].y), kept ? dp[i] : 0.0f);
                     }
                 }
             }
@@ -588,7 +616,8 @@ sn_status launch(const AttnArgs &a0, const BwdArgs &g, const BwdPlan &p, hipStre
     if (a.n_q) {
         a.row_tiles = p.row_tiles;
         a.splits = 1;
-        attn_dq_kernel<NP, DP, FAST><<<xcd_grid(a.B * a.Hkv * a.subs * a.row_tiles), kAttnThreads, 0, s>>>(a, g);
+        attn_dq_kernel<NP, DP, FAST><<<xcd_grid(a.B * a.Hkv * a.subs * a.row_tiles), kAttnThreads,
+                                       a.nb ? (size_t)a.Gs * (a.lut_n + 2 * kLutPad) * sizeof(float) : 0, s>>>(a, g);
         SN_TRY(launch_status());
     }
     if (a.n_k) {

@@ -35,26 +35,31 @@ struct RowState {
     int pos_lo, pos_hi;     // of the wavefront's rows
     float c;                // |scale| log2e; the sign of the scale is in q
 
-    __device__ inline void init(const AttnArgs &a, const RowBlock &w, int r0, int lane) {
+    // begin() issues the loads of the rows, finish() uses them.
+    __device__ inline void begin(const AttnArgs &a, const RowBlock &w, int r0, int lane, Raw8<NP> (&raw)[DP / 16]) {
         using T = typename RowOf<NP>::T;
         const int r = r0 + (lane & 31), qi = r / w.gs;
         g = r % w.gs;
         row = qi < w.nq ? w.q0 + qi : -1;
-        pos = 0;
-        const bool neg = a.scale < 0.0f;
-        c = fabsf(a.scale) * kLog2e;
+        pos = qi;
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s) {
             const int d = 16 * s + 8 * (lane >> 5);
-            Raw8<NP> raw = raw_zero<NP>();
+            raw[s] = raw_zero<NP>();
             if (row >= 0)
-                raw = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + g) * a.qh + d, d, a.D, FAST);
-            q[s] = to_frag<NP>(raw);
-            if (neg)
+                raw[s] = load8<NP>((const T *)a.q + row * a.qs + (w.h0 + g) * a.qh + d, d, a.D, FAST);
+        }
+        if (row >= 0 && a.q_pos) pos = a.q_pos[row];
+    }
+    __device__ inline void finish(const AttnArgs &a, const Raw8<NP> (&raw)[DP / 16]) {
+        c = fabsf(a.scale) * kLog2e;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+            q[s] = to_frag<NP>(raw[s]);
+            if (a.scale < 0.0f)
 #pragma unroll
                 for (int n = 0; n < NP; ++n) q[s].p[n] = -q[s].p[n];
         }
-        if (row >= 0) pos = a.q_pos ? a.q_pos[row] : qi;
         pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff);
         pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
         m = -INFINITY;
@@ -93,8 +98,16 @@ struct RowState {
         if (a.nb) {
             const int lo = uniform(ki.lo), hi = uniform(ki.hi);
             const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
+            const float *mine = lut + g * lut_stride(a);
             if (first == last) {
-                add = lut[g * a.lut_n + first];
+                add = mine[kLutPad + first];
+            } else if (a.lut_run && uniform(ki.run)) {
+                mul = 1.0f;
+                mine += run_index(a, offset_of(uniform(ki.pos[0]), pos)) + 4 * half;
+#pragma unroll
+                for (int u = 0; u < NS; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[u][i] = fmaf(s[u][i], c, mine[32 * u + 8 * (i / 4) + i % 4]);
             } else {
                 mul = 1.0f;
 #pragma unroll
@@ -102,7 +115,7 @@ struct RowState {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int at = lut_index(a, offset_of(ki.pos[32 * u + 8 * (i / 4) + 4 * half + i % 4], pos));
-                        s[u][i] = fmaf(s[u][i], c, lut[g * a.lut_n + at]);
+                        s[u][i] = fmaf(s[u][i], c, mine[kLutPad + at]);
                     }
             }
         }
@@ -196,30 +209,31 @@ __device__ inline void write_stats(const AttnArgs &a, const FwdOut &out, int spl
         out.lse[at] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// Keys of a tile: 64 halve the barriers and the running sums' exchanges, 32
+// where 64 would not leave registers for two blocks on a CU.
+template <int NP, int DP>
+constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
+
 // Many rows: each wavefront owns 32 of the block's 128 rows and all of them
 // read the same key tiles, staged in LDS while the tile before is computed.
 template <int NP, int DP, int KT, bool FAST>
-__global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
+__global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * KT * DP;
     __shared__ __align__(256) bf16 tiles[2][2][kTile];   // [buffer][K, V]
     __shared__ KeyInfo<KT> info[2];
-    __shared__ float lut[kLutMax];
+    extern __shared__ float lut[];   // [head of the subgroup][lut_stride]
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     RowBlock w;
     if (!locate(a, w)) return;
     if (w.tile * 128 >= w.nq * w.gs) return;
-    if (a.nb) fill_lut(a, w, lut);
     const T *K = (const T *)a.k + w.k0 * a.ks + w.hk * a.kh, *V = (const T *)a.v + w.k0 * a.vs + w.hk * a.vh;
     const int n_tiles = (w.nk + KT - 1) / KT, per = (n_tiles + a.splits - 1) / a.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
 
-    RowState<NP, DP, FAST> st;
-    st.init(a, w, w.tile * 128 + wave * 32, lane);
     const TileLane<DP> tl(lane);
     const uint32_t lds0 = lds_offset(tiles);
     constexpr uint32_t kBytes = kTile * sizeof(bf16);
-    const bool active = __any(st.row >= 0);
     TileMove<NP, DP, KT, kAttnThreads, FAST> mk, mv;
     KeyLoad<KT> kl;
     mk.init(a.ks, a.D, tid);
@@ -236,11 +250,16 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_rows_kerne
         if (a.nb && wave == 0) kl.store(info[buf], lane);
         return mask;
     };
+    // the first tile, the rows and the bias are on their way together
     uint64_t mask = 0;
-    if (t0 < t1) {
-        load(t0);
-        mask = store(0);
-    }
+    RowState<NP, DP, FAST> st;
+    Raw8<NP> raw[DP / 16];
+    if (t0 < t1) load(t0);
+    st.begin(a, w, w.tile * 128 + wave * 32, lane, raw);
+    if (a.nb) fill_lut(a, w, lut);
+    if (t0 < t1) mask = store(0);
+    st.finish(a, raw);
+    const bool active = __any(st.row >= 0);
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1;
@@ -274,7 +293,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     constexpr int kLds = 2 * NW * kTile > kJoin ? 2 * NW * kTile : kJoin;
     __shared__ __align__(256) bf16 lds[kLds];
     __shared__ KeyInfo<32> info[NW];
-    __shared__ float lut[kLutMax];
+    extern __shared__ float lut[];   // [head of the subgroup][lut_stride]
     __shared__ float wave_m[NW][32], wave_l[NW][32];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     RowBlock w;
@@ -296,9 +315,11 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     };
     int t = t0 + wave;
     if (t < t1) load(t);
-    if (a.nb) fill_lut(a, w, lut);
     RowState<NP, DP, FAST> st;
-    st.init(a, w, w.tile * 32, lane);
+    Raw8<NP> raw[DP / 16];
+    st.begin(a, w, w.tile * 32, lane, raw);
+    if (a.nb) fill_lut(a, w, lut);
+    st.finish(a, raw);
     const TileLane<DP> tl(lane);
     const uint32_t lds_k = uniform((int)lds_offset(kt)), lds_v = lds_k + kTile * sizeof(bf16);
     __syncthreads();
@@ -401,10 +422,11 @@ template <int NP, int DP, bool FAST>
 sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
     const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
     constexpr int NW = NP == 3 && DP == 128 ? 2 : 4;
+    const size_t lut = a.nb ? (size_t)a.Gs * (a.lut_n + 2 * kLutPad) * sizeof(float) : 0;
     if (few)
-        attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, 0, s>>>(a, out);
+        attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);
     else
-        attn_rows_kernel<NP, DP, NP == 1 && DP < 128 ? 64 : 32, FAST><<<grid, kAttnThreads, 0, s>>>(a, out);
+        attn_rows_kernel<NP, DP, kRowKeys<NP, DP>, FAST><<<grid, kAttnThreads, lut, s>>>(a, out);
     SN_TRY(launch_status());
     if (a.splits > 1) {
         attn_join_kernel<NP><<<(int)(((int64_t)a.n_q * a.H + 3) / 4), 256, 0, s>>>(a, out);

@@ -54,7 +54,8 @@ struct AttnArgs {
     int Gs, subs;                             // heads of a row block's subgroup, subgroups of a key/value head
     int row_tiles, splits;                    // row tiles of the longest segment, key splits
     int lut_base, lut_n;                      // first offset and length of the position table
-    int32_t thr[SN_MAX_BUCKETS - 1];
+    int lut_run;                              // its offsets stay clear of the type's ends
+    int32_t thr[SN_MAX_BUCKETS];              // padded with the largest value
 };
 
 size_t attn_forward_workspace(const sn_cross_attention &op);

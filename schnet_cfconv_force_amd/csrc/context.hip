@@ -2,6 +2,7 @@
 // packing.  The kernels are in attention.hip and norm.hip.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "context.h"
@@ -82,13 +83,14 @@ AttnArgs attn_args(const sn_cross_attention &op, void *ws) {
     a.nb = op.bias ? op.n_buckets : 0;
     a.q_pos = op.q_pos; a.k_pos = op.k_pos;
     a.status = reinterpret_cast<int *>(ws);
-    for (int i = 0; i + 1 < a.nb; ++i) a.thr[i] = op.thresholds[i];
+    for (int i = 0; i < SN_MAX_BUCKETS; ++i) a.thr[i] = i + 1 < a.nb ? op.thresholds[i] : INT32_MAX;
     if (a.nb > 1) {   // from one below the first threshold (if there is one below) to the last
         a.lut_base = a.thr[0] == INT32_MIN ? INT32_MIN : a.thr[0] - 1;
         a.lut_n = (int)((int64_t)a.thr[a.nb - 2] - a.lut_base + 1);
     } else {
         a.lut_n = a.nb;
     }
+    a.lut_run = std::abs((int64_t)a.lut_base) < (1 << 30);
     a.fast = rows_fast(op, op.q, op.q_stride, op.q_head_stride) && rows_fast(op, op.k, op.k_stride, op.k_head_stride) &&
              rows_fast(op, op.v, op.v_stride, op.v_head_stride);
     return a;
