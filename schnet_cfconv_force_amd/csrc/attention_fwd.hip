@@ -289,7 +289,7 @@ template <int NP, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * 32 * DP;
-    constexpr int kJoin = DP * 33 * 2;   // O^T of all rows in fp32, as bf16 elements
+    constexpr int kJoin = NW * DP * 33 * 2;   // the wavefronts' O^T in fp32, as bf16 elements
     constexpr int kLds = 2 * NW * kTile > kJoin ? 2 * NW * kTile : kJoin;
     __shared__ __align__(256) bf16 lds[kLds];
     __shared__ KeyInfo<32> info[NW];
@@ -346,30 +346,26 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
         if (wave_l[v][lane & 31] > 0.0f || wave_l[v][lane & 31] != wave_l[v][lane & 31])
             l += wave_l[v][lane & 31] * __builtin_amdgcn_exp2f(wave_m[v][lane & 31] - m);
     const float f = st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m);
-    float *rows = reinterpret_cast<float *>(lds);   // [DP][33]
-    for (int v = 0; v < NW; ++v) {
-        if (wave == v)
+    float *rows = reinterpret_cast<float *>(lds);   // [wavefront][DP][33]
 #pragma unroll
-            for (int e = 0; e < DP / 32; ++e)
+    for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float &x = rows[(32 * e + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)];
-                    x = v == 0 ? st.o[e][i] * f : fmaf(st.o[e][i], f, x);
-                }
-        __syncthreads();
-    }
-    if (tid < 32 && st.row >= 0) {
-        wave_l[0][lane] = l > 0.0f ? 1.0f / l : 0.0f;
-        write_stats(a, out, w.split, (int64_t)st.row * a.H + w.h0 + st.g, m, l);
-    }
+        for (int i = 0; i < 16; ++i)
+            rows[(wave * DP + 32 * e + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] = st.o[e][i] * f;
+    __syncthreads();
+    if (tid < 32 && st.row >= 0) write_stats(a, out, w.split, (int64_t)st.row * a.H + w.h0 + st.g, m, l);
+    if (wave == 0 && lane < 32) wave_l[0][lane] = l > 0.0f ? 1.0f / l : 0.0f;
     __syncthreads();
     const int n = min(32, w.nq * w.gs - w.tile * 32);
     for (int i = tid; i < n * (DP / 4); i += 64 * NW) {
         const int r = i / (DP / 4), d = (i % (DP / 4)) * 4, rr = w.tile * 32 + r;
         const int64_t at = (int64_t)(w.q0 + rr / w.gs) * a.H + w.h0 + rr % w.gs;
-        write_row4<NP>(a, out, w.split, at, d,
-                       floatx4{rows[d * 33 + r], rows[(d + 1) * 33 + r], rows[(d + 2) * 33 + r], rows[(d + 3) * 33 + r]},
-                       wave_l[0][r]);
+        floatx4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < NW; ++v)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] += rows[(v * DP + d + j) * 33 + r];
+        write_row4<NP>(a, out, w.split, at, d, x, wave_l[0][r]);
     }
 }
 
@@ -421,7 +417,7 @@ FwdPlan fwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
 template <int NP, int DP, bool FAST>
 sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
     const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
-    constexpr int NW = NP == 3 && DP == 128 ? 2 : 4;
+    constexpr int NW = NP * DP <= 96 ? 8 : NP * DP <= 192 ? 4 : 2;   // 160 KB of LDS hold their tiles
     const size_t lut = a.nb ? (size_t)a.Gs * (a.lut_n + 2 * kLutPad) * sizeof(float) : 0;
     if (few)
         attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);

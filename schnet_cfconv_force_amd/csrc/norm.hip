@@ -140,19 +140,47 @@ __device__ inline F half_wave_sum(F v) {
     return v;
 }
 
-// Sums of every thread's v over the threads of its group; out[group].
-// Thirty-two lanes add a group's threads in strides, then one another.
-__device__ inline void group_sums(const Slab &s, float v, float *buf, float *out) {
+// Sum of v over the threads of each group, returned to all of them.  Where
+// the vectors of a row and of a group are powers of two, a group's lanes
+// differ from the others' in whole bits of the lane index: those of a
+// wavefront add by exchanges, the wavefronts through buf [wavefront][group]
+// (zeroed before).  Otherwise 32 lanes add a group's threads in strides.
+constexpr int kWaves = kThreads / 64;
+struct SumLds {
+    float wave[2][kWaves][kMaxGroups], all[kThreads], out[kMaxGroups];
+};
+__device__ inline void clear_sums(SumLds &l) {
+    if (threadIdx.x < 2 * kWaves * kMaxGroups) (&l.wave[0][0][0])[threadIdx.x] = 0.0f;
     __syncthreads();
-    buf[threadIdx.x] = v;
+}
+__device__ inline bool in_bits(const Slab &s) { return (s.cv & (s.cv - 1)) == 0 && (s.wv & (s.wv - 1)) == 0; }
+__device__ inline float group_sum(const Slab &s, float v, SumLds &l, int turn) {
+    if (in_bits(s)) {
+        int mine = 0;   // lane bits that are summed over
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1)
+            if (o < s.wv || o >= s.cv) {
+                v += __shfl_xor(v, o, 64);
+                mine |= o;
+            }
+        if ((threadIdx.x & 63 & mine) == 0 && s.col >= 0) l.wave[turn][threadIdx.x >> 6][s.group] = v;
+        __syncthreads();
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum += l.wave[turn][w][s.group];
+        return sum;
+    }
     __syncthreads();
-    const int g = threadIdx.x >> 5, l = threadIdx.x & 31;
+    l.all[threadIdx.x] = v;
+    __syncthreads();
+    const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float sum = 0.0f;
     if (g < s.gs)
-        for (int i = l; i < s.rp * s.wv; i += 32) sum += buf[i / s.wv * s.cv + g * s.wv + i % s.wv];
+        for (int i = lane; i < s.rp * s.wv; i += 32) sum += l.all[i / s.wv * s.cv + g * s.wv + i % s.wv];
     sum = half_wave_sum(sum);
-    if (g < s.gs && l == 0) out[g] = sum;
+    if (g < s.gs && lane == 0) l.out[g] = sum;
     __syncthreads();
+    return l.out[s.group];
 }
 
 template <int V>
@@ -169,22 +197,17 @@ __device__ inline void load_affine(const NormArgs &a, const Slab &s, float (&ga)
     }
 }
 
-// The chunk's mean and sum of squared differences from it, per group, from
-// the vectors held in registers.
+// The chunk's mean and sum of squared differences from it, of the thread's
+// group, from the vectors held in registers.
 template <typename T, int V, int IT>
-__device__ inline void chunk_stats(const NormArgs &a, const NormCut &k, const Slab &s, const Vec<T, V> (&x)[IT],
-                                   float *buf, float *mean, float *m2) {
+__device__ inline float2 chunk_stats(const Slab &s, const Vec<T, V> (&x)[IT], SumLds &lds) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < IT; ++i)
         if (s.col >= 0 && s.row + i * s.rp < s.rows)
 #pragma unroll
             for (int j = 0; j < V; ++j) sum += to_f32(x[i].v[j]);
-    group_sums(s, sum, buf, mean);
-    const float cnt = (float)s.rows * (s.wv * V);
-    if (threadIdx.x < s.gs) mean[threadIdx.x] /= cnt;
-    __syncthreads();
-    const float mu = mean[s.group];
+    const float mu = group_sum(s, sum, lds, 0) / ((float)s.rows * (s.wv * V));
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < IT; ++i)
@@ -194,7 +217,7 @@ __device__ inline void chunk_stats(const NormArgs &a, const NormCut &k, const Sl
                 const float d = to_f32(x[i].v[j]) - mu;
                 sum = fmaf(d, d, sum);
             }
-    group_sums(s, sum, buf, m2);
+    return make_float2(mu, group_sum(s, sum, lds, 1));
 }
 
 template <typename T, int V, int IT>
@@ -223,7 +246,7 @@ __device__ inline void write_y(const NormArgs &a, const Vec<T, V> &x, float mu, 
 // The whole segment in registers: statistics and output in one pass.
 template <typename T, int V, int IT>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut k, T *y, float *mean, float *rstd) {
-    __shared__ float buf[kThreads], mu[kMaxGroups], m2[kMaxGroups];
+    __shared__ SumLds lds;
     Slab s;
     const bool any = locate(a, k, blockIdx.x, s);
     if (!any) {   // an empty segment
@@ -237,15 +260,15 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut 
     load_rows<T, V, IT>(k, s, (const T *)a.x, a.xs, x);
     float ga[V], be[V];
     load_affine<V>(a, s, ga, be);
-    chunk_stats<T, V, IT>(a, k, s, x, buf, mu, m2);
-    const float cnt = (float)s.rows * a.width;
-    if (threadIdx.x < s.gs) {
-        const int at = s.b * a.groups + s.g0 + threadIdx.x;
-        if (mean) mean[at] = mu[threadIdx.x];
-        if (rstd) rstd[at] = 1.0f / sqrtf(m2[threadIdx.x] / cnt + a.eps);
-    }
+    clear_sums(lds);
+    const float2 st = chunk_stats<T, V, IT>(s, x, lds);
     if (s.col < 0) return;
-    const float m = mu[s.group], r = 1.0f / sqrtf(m2[s.group] / cnt + a.eps);
+    const float m = st.x, r = 1.0f / sqrtf(st.y / ((float)s.rows * a.width) + a.eps);
+    if (s.row == 0 && s.col % s.wv == 0) {
+        const int at = s.b * a.groups + s.g0 + s.group;
+        if (mean) mean[at] = m;
+        if (rstd) rstd[at] = r;
+    }
     T *p = y + (int64_t)s.r0 * a.C + s.c0 + s.col * V;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -258,15 +281,15 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut 
 // differences} of each group
 template <typename T, int V, int IT>
 __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a, NormCut k, float2 *part) {
-    __shared__ float buf[kThreads], mu[kMaxGroups], m2[kMaxGroups];
+    __shared__ SumLds lds;
     Slab s;
     if (!locate(a, k, blockIdx.x, s)) return;
     Vec<T, V> x[IT];
     load_rows<T, V, IT>(k, s, (const T *)a.x, a.xs, x);
-    chunk_stats<T, V, IT>(a, k, s, x, buf, mu, m2);
-    if (threadIdx.x < s.gs)
-        part[((int64_t)s.b * a.groups + s.g0 + threadIdx.x) * k.chunks * s.pieces + s.chunk * s.pieces + s.piece] =
-            make_float2(mu[threadIdx.x], m2[threadIdx.x]);
+    clear_sums(lds);
+    const float2 st = chunk_stats<T, V, IT>(s, x, lds);
+    if (s.row == 0 && s.col >= 0 && s.col % s.wv == 0)
+        part[((int64_t)s.b * a.groups + s.g0 + s.group) * k.chunks * s.pieces + s.chunk * s.pieces + s.piece] = st;
 }
 
 // Joins the chunks' statistics and writes this chunk's rows.
@@ -335,34 +358,55 @@ __device__ inline void write_dx(const NormArgs &a, const Vec<T, V> &x, const Vec
     store_vec<T, V>(p, dz);
 }
 
-// Sums over the block's rows of every channel's two values: threads write
-// theirs to buf [2][rp][cs], then kThreads / cs threads per channel add the
-// rows in strides into buf's head, then one thread the rest.  out [2][cs].
+// Sums over the block's rows of every channel's two values, out [2][cs].
+// Rows of one wavefront (a row's vectors a power of two below 64) add by
+// exchanges; what remains goes to buf [2][rows][cs], kThreads / cs threads per
+// channel add the rows in strides, then one thread the rest.
 template <int V>
-__device__ inline void channel_sums(const Slab &s, const float (&sx)[V], const float (&sz)[V], float *buf, float *join,
-                                    float *out) {
+struct ChannelLds {
+    float buf[2 * kThreads * V];
+    float join[2 * kThreads];
+    float out[2 * kThreads * V];
+};
+template <int V>
+__device__ inline void channel_sums(const Slab &s, float (&sx)[V], float (&sz)[V], ChannelLds<V> &l) {
     const int t = threadIdx.x;
-    if (s.col >= 0)
+    int rows = s.rp, row = s.row;
+    bool writes = s.col >= 0;
+    if ((s.cv & (s.cv - 1)) == 0 && s.cv < 64) {
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1)
+            if (o >= s.cv)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    sx[j] += __shfl_xor(sx[j], o, 64);
+                    sz[j] += __shfl_xor(sz[j], o, 64);
+                }
+        rows = kWaves;
+        row = t >> 6;
+        writes = (t & 63) < s.cv;
+    }
+    if (writes)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            buf[s.row * s.cs + s.col * V + j] = sx[j];
-            buf[(s.rp + s.row) * s.cs + s.col * V + j] = sz[j];
+            l.buf[row * s.cs + s.col * V + j] = sx[j];
+            l.buf[(rows + row) * s.cs + s.col * V + j] = sz[j];
         }
     __syncthreads();
-    const int parts = max(1, min(kThreads / s.cs, s.rp));
+    const int parts = max(1, min(kThreads / s.cs, rows / 4));
     for (int i = t; i < parts * s.cs; i += kThreads) {
         const int c = i % s.cs, q = i / s.cs;
         float x = 0.0f, z = 0.0f;
-        for (int r = q; r < s.rp; r += parts) {
-            x += buf[r * s.cs + c];
-            z += buf[(s.rp + r) * s.cs + c];
+        for (int r = q; r < rows; r += parts) {
+            x += l.buf[r * s.cs + c];
+            z += l.buf[(rows + r) * s.cs + c];
         }
         if (parts == 1) {
-            out[c] = x;
-            out[s.cs + c] = z;
+            l.out[c] = x;
+            l.out[s.cs + c] = z;
         } else {
-            join[q * s.cs + c] = x;
-            join[(parts + q) * s.cs + c] = z;
+            l.join[q * s.cs + c] = x;
+            l.join[(parts + q) * s.cs + c] = z;
         }
     }
     __syncthreads();
@@ -370,22 +414,15 @@ __device__ inline void channel_sums(const Slab &s, const float (&sx)[V], const f
         for (int c = t; c < s.cs; c += kThreads) {
             float x = 0.0f, z = 0.0f;
             for (int q = 0; q < parts; ++q) {
-                x += join[q * s.cs + c];
-                z += join[(parts + q) * s.cs + c];
+                x += l.join[q * s.cs + c];
+                z += l.join[(parts + q) * s.cs + c];
             }
-            out[c] = x;
-            out[s.cs + c] = z;
+            l.out[c] = x;
+            l.out[s.cs + c] = z;
         }
         __syncthreads();
     }
 }
-
-template <int V>
-struct ChannelLds {
-    float buf[2 * kThreads * V];
-    float join[2 * kThreads];
-    float out[2 * kThreads * V];
-};
 
 // The whole segment in registers.  seg [b][2][C]: its sums of dz xh and dz.
 template <typename T, int V, int IT>
@@ -421,7 +458,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut 
                 sz[j] += dz[j];
             }
         }
-    channel_sums<V>(s, sx, sz, lds.buf, lds.join, lds.out);
+    channel_sums<V>(s, sx, sz, lds);
     for (int c = threadIdx.x; c < s.cs; c += kThreads) {
         seg[(int64_t)s.b * 2 * a.C + s.c0 + c] = lds.out[c];
         seg[((int64_t)s.b * 2 + 1) * a.C + s.c0 + c] = lds.out[s.cs + c];
@@ -480,7 +517,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, Nor
             }
         }
     }
-    channel_sums<V>(s, sx, sz, lds.buf, lds.join, lds.out);
+    channel_sums<V>(s, sx, sz, lds);
     float *p = part + ((int64_t)s.b * k.chunks + s.chunk) * 2 * a.C + s.c0;
     for (int c = threadIdx.x; c < s.cs; c += kThreads) {
         p[c] = lds.out[c];
@@ -604,7 +641,9 @@ constexpr int kHoldStats = 8;    // of a chunk
 constexpr int kWantBlocks = 512; // two for every CU
 
 // V: the widest vector that divides a group and suits every tensor.
-NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V) {
+// backward: its chunks need not fit the registers, and a longer one spares
+// joins of a channel's sums.
+NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V, bool backward) {
     NormCut k{};
     const int width = C / groups;
     k.V = V;
@@ -615,10 +654,12 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V) {
     };
     auto rows_held = [&](int gs, int it) { return kThreads / (gs * wv) * it; };
     if (wv <= kThreads) {
-        // one launch: full 128-byte lines where the segment still fits
+        // one launch: full 128-byte lines where the segment still fits and
+        // they make a block for every CU
         for (int bytes = 128; bytes >= 16; bytes /= 2) {
             const int gs = whole(bytes);
             if (rows_held(gs, kHold) < max_rows) continue;
+            if (bytes > 32 && gs > 1 && (int64_t)B * ((groups + gs - 1) / gs) < 256) continue;
             k.gs = gs;
             k.slabs = (groups + gs - 1) / gs;
             k.chunks = 1;
@@ -635,8 +676,9 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V) {
     }
     const int cv = k.piece ? kThreads : k.gs * wv, rp = kThreads / cv;
     const int64_t blocks = (int64_t)B * k.slabs;
-    const int least = (max_rows + rp * kHoldStats - 1) / (rp * kHoldStats);
-    const int want = (int)std::min<int64_t>((max_rows + rp - 1) / rp, (kWantBlocks + blocks - 1) / blocks);
+    const int least = backward ? 1 : (max_rows + rp * kHoldStats - 1) / (rp * kHoldStats);
+    const int want_blocks = backward ? 2 * kWantBlocks : kWantBlocks;
+    const int want = (int)std::min<int64_t>((max_rows + rp - 1) / rp, (want_blocks + blocks - 1) / blocks);
     k.chunks = std::max(1, std::max(least, want));
     k.chunk_rows = (std::max(1, max_rows) + k.chunks - 1) / k.chunks;
     k.chunk_rows = (k.chunk_rows + rp - 1) / rp * rp;
@@ -672,7 +714,7 @@ bool fused(const NormCut &k) { return k.chunks == 1 && !k.piece; }
 
 template <typename T, int V>
 sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
-    const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V);
+    const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, false);
     const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
     const int grid = a.B * k.slabs * k.chunks;
     if (fused(k)) {
@@ -692,7 +734,7 @@ sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *
 template <typename T, int V>
 sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta,
                      char *ws, hipStream_t s) {
-    const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V);
+    const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, true);
     const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
     const int grid = a.B * k.slabs * k.chunks, params = dgamma || dbeta ? (a.C + 63) / 64 : 0;
     float *seg = reinterpret_cast<float *>(ws + L.seg), *part = reinterpret_cast<float *>(ws + L.part);
@@ -732,8 +774,10 @@ size_t norm_workspace(const sn_group_norm &op) {
     size_t need = kWsBase;
     for (int V = 16 / es; V >= 1; V /= 2)   // which one depends on the tensors
         if (width % V == 0)
-            need = std::max(need, norm_layout(norm_cut(op.n_segments, op.max_rows, op.n_channels, op.n_groups, es, V),
-                                              op.n_segments, op.n_channels, op.n_groups).total);
+            for (bool backward : {false, true})
+                need = std::max(need, norm_layout(norm_cut(op.n_segments, op.max_rows, op.n_channels, op.n_groups, es, V,
+                                                           backward),
+                                                  op.n_segments, op.n_channels, op.n_groups).total);
     return need;
 }
 
