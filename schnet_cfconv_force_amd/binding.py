@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -188,9 +189,15 @@ def quantize_filter_weights(packed: np.ndarray, hyper: dict):
 
 # ------------------------------------------------------------------ device objects
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t) -> Optional[int]:
@@ -396,17 +403,18 @@ def _ragged(ptr, name: str):
 
 
 def _rows(t, name: str, shape, dtype, device):
-    """Check a row tensor (its last index contiguous); returns its address."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or (t.stride(-1) != 1 and shape[-1] > 1):
+    """Check a row tensor (its last index contiguous); returns its strides."""
+    strides = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.device != device or (strides[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on {device} whose last index is contiguous, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
-    return t.data_ptr()
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {strides}")
+    return strides
 
 
-def _flat(t, name: str, shape, dtypes, device):
-    """Check an optional contiguous tensor; returns its address or None."""
+def _flat(t, name: str, shape, dtypes, device) -> int:
+    """Check an optional contiguous tensor; returns its address or 0."""
     if t is None:
-        return None
+        return 0
     if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor {tuple(shape)} on {device}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -415,13 +423,19 @@ def _flat(t, name: str, shape, dtypes, device):
 
 def _launch_stream(plan, stream, *outputs) -> int:
     """The raw stream of a call; outputs allocated on the current stream are tied to an explicit one."""
-    torch = _torch()
     if stream is None:
-        return torch.cuda.current_stream(plan.device).cuda_stream
+        return plan.current_stream(plan.device.index)
     for t in outputs:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
+
+
+def _current_stream_getter():
+    """A function from a device index to its current raw stream (torch's own accessor where it has one)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
 def _zeroed_workspace(plan):
@@ -437,6 +451,11 @@ def relative_thresholds(n_buckets: int = 32, max_distance: int = 128) -> np.ndar
     out = np.zeros(max(int(n_buckets) - 1, 1), np.int32)
     _check(lib().sn_relative_thresholds(int(n_buckets), int(max_distance), out.ctypes.data), "sn_relative_thresholds")
     return out
+
+
+# the fields of SnCrossAttention and SnGroupNorm that a call fills in: everything from q and from x on
+_ATTENTION_CALL = struct.Struct("@PPP6qPPiPPP")
+_NORM_CALL = struct.Struct("@PqPP")
 
 
 class CrossAttention:
@@ -473,29 +492,26 @@ class CrossAttention:
         self.c.bias = None
         if self.workspace_bytes == 0:
             raise SnError(SN_ERR_INVALID, "sn_cross_attention")
+        self.head = bytes(self.c)[:SnCrossAttention.q.offset]
+        self.current_stream = _current_stream_getter()
         self.q_shape = torch.Size((self.n_q, self.n_heads, self.head_dim))
         self.k_shape = torch.Size((self.n_k, self.n_kv_heads, self.head_dim))
 
-    def _bind(self, q, k, v, bias, q_pos, k_pos, keep):
-        torch = _torch()
-        op = SnCrossAttention.from_buffer_copy(self.c)    # calls from several threads do not share it
-        op.q = _rows(q, "q", self.q_shape, self.dtype, self.device)
-        op.k = _rows(k, "k", self.k_shape, self.dtype, self.device)
-        op.v = _rows(v, "v", self.k_shape, self.dtype, self.device)
-        op.q_stride, op.q_head_stride, _ = q.stride()
-        op.k_stride, op.k_head_stride, _ = k.stride()
-        op.v_stride, op.v_head_stride, _ = v.stride()
-        if bias is not None:
-            if not self.n_buckets:
-                raise ValueError("a bias needs the plan's thresholds")
-            op.bias = _flat(bias, "bias", (self.n_heads, self.n_buckets), (torch.float32,), self.device)
-        if q_pos is not None:
-            op.q_pos = _flat(q_pos, "q_pos", (self.n_q,), (torch.int32,), self.device)
-        if k_pos is not None:
-            op.k_pos = _flat(k_pos, "k_pos", (self.n_k,), (torch.int32,), self.device)
-        if keep is not None:
-            op.keep = _flat(keep, "keep", (self.n_k,), (torch.bool, torch.uint8), self.device)
-        return op
+    def _bind(self, q, k, v, bias, q_pos, k_pos, keep) -> bytes:
+        """The descriptor of one call (its own bytes: calls from several threads share nothing)."""
+        torch, device, dtype = _torch(), self.device, self.dtype
+        qs, qh, _ = _rows(q, "q", self.q_shape, dtype, device)
+        ks, kh, _ = _rows(k, "k", self.k_shape, dtype, device)
+        vs, vh, _ = _rows(v, "v", self.k_shape, dtype, device)
+        if bias is not None and not self.n_buckets:
+            raise ValueError("a bias needs the plan's thresholds")
+        return self.head + _ATTENTION_CALL.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, qh, ks, kh, vs, vh,
+            _flat(keep, "keep", (self.n_k,), (torch.bool, torch.uint8), device),
+            _flat(bias, "bias", (self.n_heads, self.n_buckets), (torch.float32,), device),
+            self.n_buckets, self.c.thresholds or 0,
+            _flat(q_pos, "q_pos", (self.n_q,), (torch.int32,), device),
+            _flat(k_pos, "k_pos", (self.n_k,), (torch.int32,), device))
 
 
 def cross_attention_workspace(plan: CrossAttention):
@@ -510,9 +526,9 @@ def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=
     [n_k] int32 (default: the index in the segment); keep bool [n_k], False: the key is absent."""
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
-    o = torch.empty(plan.q_shape, dtype=plan.dtype, device=plan.device)
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device) if save else None
-    st = lib().sn_cross_attention_forward(ctypes.byref(op), o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
+    st = lib().sn_cross_attention_forward(op, o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
                                           _launch_stream(plan, stream, o, lse))
     _check(st, "sn_cross_attention_forward")
     return (o, (o, lse)) if save else o
@@ -525,15 +541,14 @@ def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
     o, lse = saved
-    g = _rows(d_o, "d_o", plan.q_shape, plan.dtype, plan.device)
-    dq = torch.empty(plan.q_shape, dtype=plan.dtype, device=plan.device)
-    dk = torch.empty(plan.k_shape, dtype=plan.dtype, device=plan.device)
-    dv = torch.empty(plan.k_shape, dtype=plan.dtype, device=plan.device)
-    dbias = None if bias is None else torch.empty((plan.n_heads, plan.n_buckets), dtype=torch.float32,
-                                                  device=plan.device)
+    gs, gh, _ = _rows(d_o, "d_o", plan.q_shape, plan.dtype, plan.device)
+    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+    dv = torch.empty_like(v, memory_format=torch.contiguous_format)
+    dbias = None if bias is None else torch.empty_like(bias)
     st = lib().sn_cross_attention_backward(
-        ctypes.byref(op), _flat(o, "saved[0]", plan.q_shape, (plan.dtype,), plan.device),
-        _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), g, d_o.stride(0), d_o.stride(1),
+        op, _flat(o, "saved[0]", plan.q_shape, (plan.dtype,), plan.device),
+        _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), d_o.data_ptr(), gs, gh,
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(),
         _launch_stream(plan, stream, dq, dk, dv, dbias))
     _check(st, "sn_cross_attention_backward")
@@ -560,16 +575,17 @@ class GroupNorm:
         self.workspace_bytes = int(lib().sn_group_norm_workspace_bytes(ctypes.byref(self.c)))
         if self.workspace_bytes == 0:
             raise SnError(SN_ERR_INVALID, "sn_group_norm")
+        self.head = bytes(self.c)[:SnGroupNorm.x.offset]
+        self.current_stream = _current_stream_getter()
         self.shape = torch.Size((self.n_rows, self.n_channels))
 
-    def _bind(self, x, gamma, beta):
-        torch = _torch()
-        op = SnGroupNorm.from_buffer_copy(self.c)
-        op.x = _rows(x, "x", self.shape, self.dtype, self.device)
-        op.x_stride = x.stride(0)
-        op.gamma = _flat(gamma, "gamma", (self.n_channels,), (torch.float32,), self.device)
-        op.beta = _flat(beta, "beta", (self.n_channels,), (torch.float32,), self.device)
-        return op
+    def _bind(self, x, gamma, beta) -> bytes:
+        """The descriptor of one call (its own bytes: calls from several threads share nothing)."""
+        f32 = (_torch().float32,)
+        stride, _ = _rows(x, "x", self.shape, self.dtype, self.device)
+        return self.head + _NORM_CALL.pack(x.data_ptr(), stride,
+                                           _flat(gamma, "gamma", (self.n_channels,), f32, self.device),
+                                           _flat(beta, "beta", (self.n_channels,), f32, self.device))
 
 
 def group_norm_workspace(plan: GroupNorm):
@@ -582,11 +598,11 @@ def group_norm_forward(plan: GroupNorm, x, gamma, beta, ws, save: bool = False, 
     gamma, beta: float32 [C], or None for 1 and 0."""
     torch = _torch()
     op = plan._bind(x, gamma, beta)
-    y = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = rstd = None
     if save:
         mean, rstd = torch.empty((2, plan.n_segments, plan.n_groups), dtype=torch.float32, device=plan.device)
-    st = lib().sn_group_norm_forward(ctypes.byref(op), y.data_ptr(), _ptr(mean), _ptr(rstd), ws.data_ptr(),
+    st = lib().sn_group_norm_forward(op, y.data_ptr(), _ptr(mean), _ptr(rstd), ws.data_ptr(),
                                      ws.numel(), _launch_stream(plan, stream, y, mean, rstd))
     _check(st, "sn_group_norm_forward")
     return (y, (mean, rstd)) if save else y
@@ -596,13 +612,13 @@ def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=N
     """sn_group_norm_backward -> (dx, dgamma, dbeta) from the forward's `saved` and the gradient dy of y."""
     torch = _torch()
     op = plan._bind(x, gamma, beta)
-    g = _rows(dy, "dy", plan.shape, plan.dtype, plan.device)
+    dy_stride, _ = _rows(dy, "dy", plan.shape, plan.dtype, plan.device)
     stats = (plan.n_segments, plan.n_groups)
-    dx = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     dgamma, dbeta = torch.empty((2, plan.n_channels), dtype=torch.float32, device=plan.device)
     st = lib().sn_group_norm_backward(
-        ctypes.byref(op), _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
-        _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), g, dy.stride(0), dx.data_ptr(),
+        op, _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
+        _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), dy.data_ptr(), dy_stride, dx.data_ptr(),
         dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel(),
         _launch_stream(plan, stream, dx, dgamma, dbeta))
     _check(st, "sn_group_norm_backward")

@@ -18,6 +18,7 @@
 // digits of the variance.  All sums are fp32 in a block and fp64 in a join,
 // each in one order.
 #include <algorithm>
+#include <type_traits>
 
 #include "context.h"
 
@@ -27,14 +28,16 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxGroups = kThreads / 32;   // groups of a slab: 32 lanes join each
 
-__device__ inline float act_fwd(float z, int act) {
-    if (act == SN_ACT_SSP) return ssp(z);
-    if (act == SN_ACT_SILU) return z * sigm(z);
+template <int ACT>
+__device__ inline float act_fwd(float z) {
+    if constexpr (ACT == SN_ACT_SSP) return ssp(z);
+    if constexpr (ACT == SN_ACT_SILU) return z * sigm(z);
     return z;
 }
-__device__ inline float act_grad(float z, int act) {
-    if (act == SN_ACT_SSP) return sigm(z);
-    if (act == SN_ACT_SILU) {
+template <int ACT>
+__device__ inline float act_grad(float z) {
+    if constexpr (ACT == SN_ACT_SSP) return sigm(z);
+    if constexpr (ACT == SN_ACT_SILU) {
         const float s = sigm(z);
         return s * (1.0f + z * (1.0f - s));
     }
@@ -232,19 +235,19 @@ __device__ inline void load_rows(const NormCut &k, const Slab &s, const T *base,
     }
 }
 
-template <typename T, int V>
-__device__ inline void write_y(const NormArgs &a, const Vec<T, V> &x, float mu, float r, const float (&ga)[V],
+template <typename T, int V, int ACT>
+__device__ inline void write_y(const Vec<T, V> &x, float mu, float r, const float (&ga)[V],
                                const float (&be)[V], T *p) {
     float y[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) y[j] = act_fwd(fmaf((to_f32(x.v[j]) - mu) * r, ga[j], be[j]), a.act);
+    for (int j = 0; j < V; ++j) y[j] = act_fwd<ACT>(fmaf((to_f32(x.v[j]) - mu) * r, ga[j], be[j]));
     store_vec<T, V>(p, y);
 }
 
 // ------------------------------------------------------------------ forward
 
 // The whole segment in registers: statistics and output in one pass.
-template <typename T, int V, int IT>
+template <typename T, int V, int IT, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut k, T *y, float *mean, float *rstd) {
     __shared__ SumLds lds;
     Slab s;
@@ -273,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut 
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int row = s.row + i * s.rp;
-        if (row < s.rows) write_y<T, V>(a, x[i], m, r, ga, be, p + (int64_t)row * a.C);
+        if (row < s.rows) write_y<T, V, ACT>(x[i], m, r, ga, be, p + (int64_t)row * a.C);
     }
 }
 
@@ -293,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a, NormCu
 }
 
 // Joins the chunks' statistics and writes this chunk's rows.
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCut k, const float2 *part, T *y,
                                                               float *mean, float *rstd) {
     __shared__ float mu[kMaxGroups], rs[kMaxGroups];
@@ -333,26 +336,26 @@ __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCu
     T *py = y + base * a.C + s.c0 + s.col * V;
 #pragma unroll 4
     for (int row = s.row; row < s.rows; row += s.rp)
-        write_y<T, V>(a, load_vec<T, V>(px + row * a.xs), m, r, ga, be, py + (int64_t)row * a.C);
+        write_y<T, V, ACT>(load_vec<T, V>(px + row * a.xs), m, r, ga, be, py + (int64_t)row * a.C);
 }
 
 // ------------------------------------------------------------------ backward
 
 // dz and xh of one vector.
-template <typename T, int V>
-__device__ inline void dz_xh(const NormArgs &a, const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r,
+template <typename T, int V, int ACT>
+__device__ inline void dz_xh(const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r,
                              const float (&ga)[V], const float (&be)[V], float (&dz)[V], float (&xh)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         xh[j] = (to_f32(x.v[j]) - mu) * r;
-        dz[j] = to_f32(dy.v[j]) * act_grad(fmaf(xh[j], ga[j], be[j]), a.act);
+        dz[j] = to_f32(dy.v[j]) * act_grad<ACT>(fmaf(xh[j], ga[j], be[j]));
     }
 }
-template <typename T, int V>
-__device__ inline void write_dx(const NormArgs &a, const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r, float m1,
+template <typename T, int V, int ACT>
+__device__ inline void write_dx(const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r, float m1,
                                 float m2, const float (&ga)[V], const float (&be)[V], T *p) {
     float dz[V], xh[V];
-    dz_xh<T, V>(a, x, dy, mu, r, ga, be, dz, xh);
+    dz_xh<T, V, ACT>(x, dy, mu, r, ga, be, dz, xh);
 #pragma unroll
     for (int j = 0; j < V; ++j) dz[j] = r * (dz[j] * ga[j] - m1 - xh[j] * m2);
     store_vec<T, V>(p, dz);
@@ -425,7 +428,7 @@ __device__ inline void channel_sums(const Slab &s, float (&sx)[V], float (&sz)[V
 }
 
 // The whole segment in registers.  seg [b][2][C]: its sums of dz xh and dz.
-template <typename T, int V, int IT>
+template <typename T, int V, int IT, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut k, const float *mean,
                                                             const float *rstd, T *dx, float *seg) {
     __shared__ ChannelLds<V> lds;
@@ -451,7 +454,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut 
     for (int i = 0; i < IT; ++i)
         if (s.row + i * s.rp < s.rows) {
             float dz[V], xh[V];
-            dz_xh<T, V>(a, x[i], dy[i], mu, r, ga, be, dz, xh);
+            dz_xh<T, V, ACT>(x[i], dy[i], mu, r, ga, be, dz, xh);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 sx[j] = fmaf(dz[j], xh[j], sx[j]);
@@ -486,12 +489,12 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut 
     for (int i = 0; i < IT; ++i) {
         const int row = s.row + i * s.rp;
         if (row < s.rows)
-            write_dx<T, V>(a, x[i], dy[i], mu, r, gm[0][s.group], gm[1][s.group], ga, be, p + (int64_t)row * a.C);
+            write_dx<T, V, ACT>(x[i], dy[i], mu, r, gm[0][s.group], gm[1][s.group], ga, be, p + (int64_t)row * a.C);
     }
 }
 
 // part [b][chunk][2][C]: the chunk's sums of dz xh and dz
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, NormCut k, const float *mean,
                                                                  const float *rstd, float *part) {
     __shared__ ChannelLds<V> lds;
@@ -509,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, Nor
 #pragma unroll 4
         for (int row = s.row; row < s.rows; row += s.rp) {
             float dz[V], xh[V];
-            dz_xh<T, V>(a, load_vec<T, V>(px + row * a.xs), load_vec<T, V>(pg + row * a.dys), mu, r, ga, be, dz, xh);
+            dz_xh<T, V, ACT>(load_vec<T, V>(px + row * a.xs), load_vec<T, V>(pg + row * a.dys), mu, r, ga, be, dz, xh);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 sx[j] = fmaf(dz[j], xh[j], sx[j]);
@@ -607,7 +610,7 @@ __global__ __launch_bounds__(kThreads) void norm_param_kernel(NormArgs a, const 
 
 // dx of a chunk's rows; the first `params` blocks sum dgamma and dbeta
 // instead (one launch less).
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, NormCut k, const float *mean,
                                                                   const float *rstd, const float2 *gmean, T *dx,
                                                                   const float *seg, float *dgamma, float *dbeta,
@@ -630,7 +633,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, No
     T *pd = dx + base * a.C + s.c0 + s.col * V;
 #pragma unroll 4
     for (int row = s.row; row < s.rows; row += s.rp)
-        write_dx<T, V>(a, load_vec<T, V>(px + row * a.xs), load_vec<T, V>(pg + row * a.dys), mu, r, m.x, m.y, ga, be,
+        write_dx<T, V, ACT>(load_vec<T, V>(px + row * a.xs), load_vec<T, V>(pg + row * a.dys), mu, r, m.x, m.y, ga, be,
                        pd + (int64_t)row * a.C);
 }
 
@@ -712,26 +715,26 @@ NormLayout norm_layout(const NormCut &k, int64_t B, int64_t C, int64_t groups) {
 
 bool fused(const NormCut &k) { return k.chunks == 1 && !k.piece; }
 
-template <typename T, int V>
+template <typename T, int V, int ACT>
 sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
     const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, false);
     const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
     const int grid = a.B * k.slabs * k.chunks;
     if (fused(k)) {
         if (k.it == 4)
-            norm_fwd_kernel<T, V, 4><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
+            norm_fwd_kernel<T, V, 4, ACT><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
         else
-            norm_fwd_kernel<T, V, kHold><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
+            norm_fwd_kernel<T, V, kHold, ACT><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
         return launch_status();
     }
     float2 *part = reinterpret_cast<float2 *>(ws + L.part);
     norm_stats_kernel<T, V, kHoldStats><<<grid, kThreads, 0, s>>>(a, k, part);
     SN_TRY(launch_status());
-    norm_apply_kernel<T, V><<<grid, kThreads, 0, s>>>(a, k, part, (T *)y, mean, rstd);
+    norm_apply_kernel<T, V, ACT><<<grid, kThreads, 0, s>>>(a, k, part, (T *)y, mean, rstd);
     return launch_status();
 }
 
-template <typename T, int V>
+template <typename T, int V, int ACT>
 sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta,
                      char *ws, hipStream_t s) {
     const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, true);
@@ -741,18 +744,18 @@ sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, vo
     float2 *gmean = reinterpret_cast<float2 *>(ws + L.gmean);
     if (fused(k)) {
         if (k.it == 4)
-            norm_bwd_kernel<T, V, 4><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
+            norm_bwd_kernel<T, V, 4, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
         else
-            norm_bwd_kernel<T, V, kHold><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
+            norm_bwd_kernel<T, V, kHold, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
         SN_TRY(launch_status());
         if (params) norm_param_kernel<<<params, kThreads, 0, s>>>(a, seg, dgamma, dbeta);
         return launch_status();
     }
-    norm_bwd_sums_kernel<T, V><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, part);
+    norm_bwd_sums_kernel<T, V, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, part);
     SN_TRY(launch_status());
     norm_bwd_join_kernel<<<a.B * a.groups, 256, 0, s>>>(a, k, part, seg, gmean);
     SN_TRY(launch_status());
-    norm_bwd_apply_kernel<T, V><<<grid + params, kThreads, 0, s>>>(a, k, mean, rstd, gmean, (T *)dx, seg, dgamma,
+    norm_bwd_apply_kernel<T, V, ACT><<<grid + params, kThreads, 0, s>>>(a, k, mean, rstd, gmean, (T *)dx, seg, dgamma,
                                                                   dbeta, params);
     return launch_status();
 }
@@ -765,6 +768,35 @@ int widest(const NormArgs &a, const void *out, bool backward) {
     V = vector_of(V, out, a.C, sizeof(T));
     if (backward) V = vector_of(V, a.dy, a.dys, sizeof(T));
     return V;
+}
+
+// Calls f with the vector and the activation as constants.
+template <int V, typename F>
+sn_status with_act(int act, F f) {
+    using std::integral_constant;
+    return act == SN_ACT_SSP    ? f(integral_constant<int, V>(), integral_constant<int, SN_ACT_SSP>())
+           : act == SN_ACT_SILU ? f(integral_constant<int, V>(), integral_constant<int, SN_ACT_SILU>())
+                                : f(integral_constant<int, V>(), integral_constant<int, SN_ACT_NONE>());
+}
+template <typename T, typename F>
+sn_status with_vector(int V, int act, F f) {
+    if constexpr (sizeof(T) == 2)
+        if (V == 8) return with_act<8>(act, f);
+    return V == 4 ? with_act<4>(act, f) : V == 2 ? with_act<2>(act, f) : with_act<1>(act, f);
+}
+
+template <typename T>
+sn_status forward_t(const NormArgs &a, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
+    return with_vector<T>(widest<T>(a, y, false), a.act, [&](auto V, auto ACT) {
+        return forward_v<T, V.value, ACT.value>(a, y, mean, rstd, ws, s);
+    });
+}
+template <typename T>
+sn_status backward_t(const NormArgs &a, const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta,
+                     char *ws, hipStream_t s) {
+    return with_vector<T>(widest<T>(a, dx, true), a.act, [&](auto V, auto ACT) {
+        return backward_v<T, V.value, ACT.value>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
+    });
 }
 
 }  // namespace
@@ -783,33 +815,14 @@ size_t norm_workspace(const sn_group_norm &op) {
 
 sn_status norm_forward(const NormArgs &a, int dtype, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
     ProfScope prof(K_NORM_FWD, s);
-    if (dtype == SN_F32) {
-        const int V = widest<float>(a, y, false);
-        return V == 4   ? forward_v<float, 4>(a, y, mean, rstd, ws, s)
-               : V == 2 ? forward_v<float, 2>(a, y, mean, rstd, ws, s)
-                        : forward_v<float, 1>(a, y, mean, rstd, ws, s);
-    }
-    const int V = widest<bf16>(a, y, false);
-    return V == 8   ? forward_v<bf16, 8>(a, y, mean, rstd, ws, s)
-           : V == 4 ? forward_v<bf16, 4>(a, y, mean, rstd, ws, s)
-           : V == 2 ? forward_v<bf16, 2>(a, y, mean, rstd, ws, s)
-                    : forward_v<bf16, 1>(a, y, mean, rstd, ws, s);
+    return dtype == SN_F32 ? forward_t<float>(a, y, mean, rstd, ws, s) : forward_t<bf16>(a, y, mean, rstd, ws, s);
 }
 
 sn_status norm_backward(const NormArgs &a, int dtype, const float *mean, const float *rstd, void *dx, float *dgamma,
                         float *dbeta, char *ws, hipStream_t s) {
     ProfScope prof(K_NORM_BWD, s);
-    if (dtype == SN_F32) {
-        const int V = widest<float>(a, dx, true);
-        return V == 4   ? backward_v<float, 4>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
-               : V == 2 ? backward_v<float, 2>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
-                        : backward_v<float, 1>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
-    }
-    const int V = widest<bf16>(a, dx, true);
-    return V == 8   ? backward_v<bf16, 8>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
-           : V == 4 ? backward_v<bf16, 4>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
-           : V == 2 ? backward_v<bf16, 2>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
-                    : backward_v<bf16, 1>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
+    return dtype == SN_F32 ? backward_t<float>(a, mean, rstd, dx, dgamma, dbeta, ws, s)
+                           : backward_t<bf16>(a, mean, rstd, dx, dgamma, dbeta, ws, s);
 }
 
 }  // namespace sn
