@@ -130,13 +130,6 @@ __device__ inline bool locate(const NormArgs &a, const NormCut &k, int block, Sl
     return s.rows > 0;
 }
 
-// Elements of one group in chunk c (piece p) of a segment of n rows.
-__device__ inline int64_t part_count(const NormArgs &a, const NormCut &k, int n, int c, int p) {
-    const int rows = min(k.chunk_rows, n - c * k.chunk_rows);
-    const int width = k.piece ? min(k.piece, a.width - p * k.piece) : a.width;
-    return (int64_t)max(rows, 0) * width;
-}
-
 template <typename F>
 __device__ inline F half_wave_sum(F v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor(v, o, 32);
@@ -303,18 +296,29 @@ __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCu
     Slab s;
     const bool any = locate(a, k, gridDim.x - 1 - blockIdx.x, s);   // the rows read last are the likeliest in a cache
     if (!any && s.chunk > 0) return;
+    float ga[V], be[V];
+    load_affine<V>(a, s, ga, be);
     const int g = threadIdx.x >> 5, l = threadIdx.x & 31;
     if (g < s.gs) {
-        const int n = (s.n + k.chunk_rows - 1) / k.chunk_rows * s.pieces;
+        // every chunk but the last has the same rows, every piece but the last the same channels
+        const int chunks = (s.n + k.chunk_rows - 1) / k.chunk_rows, n = chunks * s.pieces;
+        const int last_rows = s.n - (chunks - 1) * k.chunk_rows;
+        const int width = k.piece ? k.piece : a.width, last_width = a.width - (s.pieces - 1) * width;
+        auto count = [&](int i) {
+            const int c = s.pieces == 1 ? i : i / s.pieces, p = s.pieces == 1 ? 0 : i % s.pieces;
+            return (double)(c == chunks - 1 ? last_rows : k.chunk_rows) * (p == s.pieces - 1 ? last_width : width);
+        };
         const float2 *p = part + ((int64_t)s.b * a.groups + s.g0 + g) * k.chunks * s.pieces;
         const double cnt = (double)s.n * a.width;
         double sum = 0.0;
-        for (int i = l; i < n; i += 32) sum += (double)part_count(a, k, s.n, i / s.pieces, i % s.pieces) * p[i].x;
+#pragma unroll 8
+        for (int i = l; i < n; i += 32) sum += count(i) * p[i].x;
         const double m = s.n ? half_wave_sum(sum) / cnt : 0.0;
         sum = 0.0;
+#pragma unroll 8
         for (int i = l; i < n; i += 32) {
             const double d = p[i].x - m;
-            sum += p[i].y + (double)part_count(a, k, s.n, i / s.pieces, i % s.pieces) * d * d;
+            sum += p[i].y + count(i) * d * d;
         }
         const double var = s.n ? half_wave_sum(sum) / cnt : 0.0;
         if (l == 0) {
@@ -328,8 +332,6 @@ __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCu
     }
     __syncthreads();
     if (s.col < 0 || !any) return;
-    float ga[V], be[V];
-    load_affine<V>(a, s, ga, be);
     const float m = mu[s.group], r = rs[s.group];
     const int64_t base = s.r0 + s.first;
     const T *px = (const T *)a.x + base * a.xs + s.c0 + s.col * V;
@@ -641,7 +643,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, No
 
 constexpr int kHold = 16;        // vectors that a thread of a fused launch can hold
 constexpr int kHoldStats = 8;    // of a chunk
-constexpr int kWantBlocks = 512; // two for every CU
+constexpr int kWantBlocks = 256; // one for every CU
 
 // V: the widest vector that divides a group and suits every tensor.
 // backward: its chunks need not fit the registers, and a longer one spares
@@ -670,7 +672,7 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V, bool bac
             k.it = rows_held(gs, 4) >= max_rows ? 4 : kHold;
             return k;
         }
-        k.gs = whole(256);
+        k.gs = whole(128);
         k.slabs = (groups + k.gs - 1) / k.gs;
     } else {
         k.gs = 1;
