@@ -146,6 +146,18 @@ __device__ inline Frag<NP> frag_cols(const TileLane<DP> &l, uint32_t tile, uint3
     for (int n = 0; n < NP; ++n) f.p[n] = l.frag_cols(tile + n * plane, row0, e);
     return f;
 }
+// One plane: the column fragments of a 32-row tile on their way ahead of
+// their use, [16 rows][element block].
+template <int DP>
+struct ColsAhead {
+    bf16x8 f[2][DP / 32];
+    __device__ inline void load(const TileLane<DP> &l, uint32_t tile, int row0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e) f[u][e] = l.frag_cols(tile, row0 + 16 * u, e);
+    }
+};
 // x += A B over all of a row's elements, A the tile's rows row0 .. row0 + 31.
 // One plane: every operand is on its way before the first product.
 template <int NP, int DP>
@@ -292,6 +304,16 @@ __device__ inline int wave_min(int v) {
 }
 __device__ inline int wave_max(int v) { return ~wave_min(~v); }
 
+// Orders a wavefront's own exchange through LDS: what its lanes wrote before
+// is what they read after.  The hardware keeps the order of one wavefront's
+// LDS operations; the barrier (no instruction) keeps the compiler from
+// sending some lanes ahead of others past it, which a fence alone does not.
+__device__ inline void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The value of the lane's other half (lane ^ 32).
 __device__ inline float half_swap(float v) { return __shfl_xor(v, 32, 64); }
 
@@ -377,27 +399,37 @@ struct KeyInfo {
 };
 template <int KT>
 struct KeyLoad {
-    int pos;
-    bool in;
+    int pos, key0, n;
     uint8_t kept;
-    __device__ inline void load(const AttnArgs &a, const RowBlock &w, int key0, bool positions, int lane) {
+    __device__ inline void load(const AttnArgs &a, const RowBlock &w, int first_key, bool positions, int lane) {
+        key0 = first_key;
+        n = min(w.nk - key0, KT);
         const int j = key0 + lane;
-        in = lane < KT && j < w.nk;
-        kept = in;
+        kept = 0;
         pos = j;
-        if (positions && a.k_pos && in) pos = a.k_pos[w.k0 + j];
-        if (a.keep && in) kept = a.keep[w.k0 + j];
+        if (lane < n) {
+            if (positions && a.k_pos) pos = a.k_pos[w.k0 + j];
+            if (a.keep) kept = a.keep[w.k0 + j];
+        }
     }
-    __device__ inline uint64_t mask() const { return __ballot(kept != 0); }
-    __device__ inline void store(KeyInfo<KT> &k, int lane) const {
-        const bool ok = kept != 0;
-        const int lo = wave_min(ok ? pos : 0x7fffffff), hi = wave_max(ok ? pos : (int)0x80000000);
-        const bool gap = __any(in && (pos != uniform(pos) + lane || abs(pos) >= 1 << 30));
+    __device__ inline uint64_t mask(const AttnArgs &a) const {
+        return a.keep ? __ballot(kept != 0) : n >= 64 ? ~0ull : (1ull << n) - 1;
+    }
+    __device__ inline void store(KeyInfo<KT> &k, uint64_t mask, int lane) const {
+        const int first = uniform(pos);
+        const bool run = !__any(lane < n && (pos != first + lane || abs(pos) >= 1 << 30));
+        // (an empty mask: the tile is passed over)
+        int lo = first + __ffsll((unsigned long long)mask) - 1, hi = first + 63 - __clzll((long long)mask);
+        if (!run) {
+            const bool ok = (mask >> lane) & 1;
+            lo = wave_min(ok ? pos : 0x7fffffff);
+            hi = wave_max(ok ? pos : (int)0x80000000);
+        }
         if (lane < KT) k.pos[lane] = pos;
         if (lane == 0) {
             k.lo = lo;
             k.hi = hi;
-            k.run = !gap;
+            k.run = run;
         }
     }
 };

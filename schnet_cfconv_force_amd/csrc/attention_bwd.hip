@@ -54,7 +54,7 @@ __device__ inline void write4(T *row, int d, int D, floatx4 v) {
 }
 
 template <int NP, int DP, bool FAST>
-__global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(AttnArgs a, BwdArgs g) {
+__global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void attn_dq_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * kDqKeys * DP;
     __shared__ __align__(256) bf16 tiles[2][2][kTile];   // [buffer][K, V]
@@ -77,10 +77,10 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
         kl.load(a, w, t * kDqKeys, a.nb && wave == 0, lane);
     };
     auto store = [&](int buf) {
-        const uint64_t mask = kl.mask();
+        const uint64_t mask = kl.mask(a);
         mk.store(tiles[buf][0], tid, a.keep && is_partial<kDqKeys>(mask), mask);
         mv.store(tiles[buf][1], tid, a.keep && is_partial<kDqKeys>(mask), mask);
-        if (a.nb && wave == 0) kl.store(info[buf], lane);
+        if (a.nb && wave == 0) kl.store(info[buf], mask, lane);
         return mask;
     };
 
@@ -154,6 +154,11 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
         const KeyInfo<kDqKeys> &ki = info[buf];
         if (active && mask) {
             floatx16 s = rows_product<NP, DP>(tl, kt, kPlane, 0, q), dp = rows_product<NP, DP>(tl, vt, kPlane, 0, dO);
+            ColsAhead<DP> kf;
+            if constexpr (NP == 1) {
+                kf.load(tl, kt, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             settle(s);
             settle(dp);
             float mul = c, less = -L;
@@ -198,8 +203,12 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 ? 2 : 1) void attn_dq_kernel(
                 // forward pass: at most 2^-8 of each term, as rounding dq
                 const Frag<NP> ds = split8f<NP>(x);
 #pragma unroll
-                for (int e = 0; e < DP / 32; ++e)
-                    dq[e] = mma<NP>(frag_cols<NP, DP>(tl, kt, kPlane, 16 * u, e), ds, dq[e]);
+                for (int e = 0; e < DP / 32; ++e) {
+                    if constexpr (NP == 1)
+                        dq[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf.f[u][e], ds.p[0], dq[e], 0, 0, 0);
+                    else
+                        dq[e] = mma<NP>(frag_cols<NP, DP>(tl, kt, kPlane, 16 * u, e), ds, dq[e]);
+                }
             }
         }
         if (t + 1 < n_tiles) mask = store(buf ^ 1);
@@ -239,7 +248,7 @@ __global__ __launch_bounds__(1024) void attn_dbias_kernel(AttnArgs a, const floa
 
 // What the rows of a tile need beside q and dO.
 struct RowInfo {
-    float L[32], delta[32];
+    float less[32], delta[32];   // -L
     int pos[32];
     int lo, hi;
     int run;        // the positions are pos[0], pos[0] + 1, ...
@@ -272,7 +281,7 @@ template <int NP, int DP>
 constexpr int dkv_buffers() { return NP == 3 && DP == 128 ? 1 : 2; }   // 160 KB of LDS
 
 template <int NP, int DP, bool FAST>
-__global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void attn_dkv_kernel(AttnArgs a, BwdArgs g) {
+__global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2 : 1) void attn_dkv_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
     constexpr int kRows = 32, kTile = NP * kRows * DP;
     constexpr int kBuf = dkv_buffers<NP, DP>();
@@ -310,20 +319,27 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     TileMove<NP, DP, kRows, kAttnThreads, FAST> mq, mg;
     mq.init(a.qs, a.D, tid);
     mg.init(a.gs, a.D, tid);
+    // the tile that is loaded next: its head (of the G) and first row
+    int next_head = t0 < t1 ? t0 / per_head : 0, next_row = t0 < t1 ? t0 % per_head * kRows : 0;
     float2 ri;
-    int ri_pos;
-    auto load = [&](int t) {
-        const int h = hk * a.G + t / per_head, r0 = t % per_head * kRows;
+    int ri_pos, ri_n;
+    auto load = [&]() {
+        const int h = hk * a.G + next_head, r0 = next_row;
         mq.load((const T *)a.q + (q0 + r0) * a.qs + h * a.qh, a.qs, nq - r0, a.D, tid);
         mg.load((const T *)a.d_o + (q0 + r0) * a.gs + h * a.gh, a.gs, nq - r0, a.D, tid);
-        if (tid < kRows) {
-            const int row = r0 + tid;
+        if (wave == 0) {
+            ri_n = min(nq - r0, kRows);
             ri = make_float2(INFINITY, 0.0f);
-            ri_pos = row;
-            if (row < nq) {
-                ri = g.row[(int64_t)(q0 + row) * a.H + h];
-                if (a.q_pos) ri_pos = a.q_pos[q0 + row];
+            ri_pos = r0 + lane;
+            if (lane < ri_n) {
+                ri = g.row[(int64_t)(q0 + r0 + lane) * a.H + h];
+                if (a.q_pos) ri_pos = a.q_pos[q0 + r0 + lane];
             }
+        }
+        next_row += kRows;
+        if (next_row >= nq) {
+            next_row = 0;
+            ++next_head;
         }
     };
 
@@ -331,7 +347,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     const int j = key_tile * 128 + wave * 32 + (lane & 31);
     const bool have = j < nk;
     Raw8<NP> rk[DP / 16], rv[DP / 16];
-    if (t0 < t1) load(t0);
+    if (t0 < t1) load();
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) rk[s] = rv[s] = raw_zero<NP>();
     uint8_t keep = have;
@@ -364,29 +380,33 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             for (int n = 0; n < NP; ++n) k[s].p[n] = -k[s].p[n];
     }
     const float c = fabsf(a.scale) * kLog2e;
+    const float kept_add = kept ? 0.0f : -INFINITY;   // an absent key's column of p, and with it of dS, is zero
     const int pos_lo = wave_min(kept ? pos : 0x7fffffff), pos_hi = wave_max(kept ? pos : (int)0x80000000);
 
     // kept keys whose positions run: the first key's position
     const int key_base = pos - (lane & 31), key0 = wave_min(kept ? key_base : 0x7fffffff);
     const bool key_run = small_lut && !__any(kept && (key_base != key0 || abs(pos) >= 1 << 30));
 
-    auto store = [&](int t, int buf) {
+    auto store = [&](int buf) {
         mq.store(tiles[buf][0], tid, false, 0);
         mg.store(tiles[buf][1], tid, false, 0);
         if (wave == 0) {
-            const bool in = lane < kRows && t % per_head * kRows + lane < nq;
-            const int lo = wave_min(in ? ri_pos : 0x7fffffff), hi = wave_max(in ? ri_pos : (int)0x80000000);
+            const int first = uniform(ri_pos);
+            const bool run = !__any(lane < ri_n && (ri_pos != first + lane || abs(ri_pos) >= 1 << 30));
+            int lo = first, hi = first + ri_n - 1;
+            if (!run) {
+                lo = wave_min(lane < ri_n ? ri_pos : 0x7fffffff);
+                hi = wave_max(lane < ri_n ? ri_pos : (int)0x80000000);
+            }
             if (lane < kRows) {
-                info[buf].L[lane] = ri.x;
+                info[buf].less[lane] = -ri.x;
                 info[buf].delta[lane] = ri.y;
                 info[buf].pos[lane] = ri_pos;
             }
-            const int first = uniform(ri_pos);
-            const bool gap = __any(in && (ri_pos != first + lane || abs(ri_pos) >= 1 << 30));
             if (lane == 0) {
                 info[buf].lo = lo;
                 info[buf].hi = hi;
-                info[buf].run = !gap;
+                info[buf].run = run;
             }
         }
     };
@@ -402,9 +422,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     int run_bucket = -1, head = -1;
     auto add_column = [&](int bk, float x) {
         if (half == 0) atomicAdd(mine + bk * 32, x);
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (half == 1) atomicAdd(mine + bk * 32, x);
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
     };
     auto flush = [&]() {
         if (run_bucket >= 0) add_column(run_bucket, run_ds);
@@ -437,14 +457,19 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
     if (a.nb)   // heads that this split does not reach
         for (int i = tid; i < a.G * a.nb; i += kAttnThreads)
             if (t0 >= t1 || i / a.nb < t0 / per_head || i / a.nb > (t1 - 1) / per_head) part[i] = 0.0f;
-    if (t0 < t1) store(t0, 0);
+    int tile_head = 0, loaded_head = next_row == 0 ? next_head - 1 : next_head;   // of the tiles in LDS and in registers
+    if (t0 < t1) store(0);
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         const int buf = kBuf == 2 ? (t - t0) & 1 : 0;
-        if (t + 1 < t1) load(t + 1);
-        if (a.nb && t / per_head != head) {   // every wavefront is past the last use of the table (barrier below)
+        tile_head = loaded_head;
+        if (t + 1 < t1) {
+            loaded_head = next_head;
+            load();
+        }
+        if (a.nb && tile_head != head) {   // every wavefront is past the last use of the table (barrier below)
             if (head >= 0) finish_head();
-            head = t / per_head;
+            head = tile_head;
             for (int e = tid; e < lut_stride(a); e += kAttnThreads)
                 lut[e].x = a.bias[(int64_t)(hk * a.G + head) * a.nb + __float_as_int(lut[e].y)] * kLog2e;
             for (int i = tid; i < 4 * a.nb * 32; i += kAttnThreads) sums[i] = 0.0f;
@@ -455,10 +480,22 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
         const uint32_t qt = lds0 + 2 * buf * kBytes, gt = qt + kBytes;
         const RowInfo &ri_t = info[buf];
         if (active) {
+            float less[16], delta[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                less[i] = ri_t.less[8 * (i / 4) + 4 * half + i % 4];
+                delta[i] = ri_t.delta[8 * (i / 4) + 4 * half + i % 4];
+            }
             floatx16 s = rows_product<NP, DP>(tl, qt, kPlane, 0, k), dp = rows_product<NP, DP>(tl, gt, kPlane, 0, v);
+            ColsAhead<DP> qf, gf;
+            if constexpr (NP == 1) {
+                gf.load(tl, gt, 0);
+                qf.load(tl, qt, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             settle(s);
             settle(dp);
-            float mul = c, add = 0.0f;
+            float mul = c, add = kept_add;
             int bucket = -1;
             bool table = false;
             if (a.nb) {
@@ -466,7 +503,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 const int first = lut_index(a, offset_of(pos_lo, hi)), last = lut_index(a, offset_of(pos_hi, lo));
                 table = first != last;
                 if (!table) {
-                    add = lut[kLutPad + first].x;
+                    add += lut[kLutPad + first].x;
                     bucket = uniform(__float_as_int(lut[kLutPad + first].y));
                 } else if (a.lut_run && uniform(ri_t.run)) {   // later rows, smaller offsets
                     mul = 1.0f;
@@ -483,17 +520,16 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int row = 8 * (i / 4) + 4 * half + i % 4;
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], mul, add - ri_t.L[row]));
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], mul, add + less[i]));
                 s[i] = p;
-                dp[i] = p * (dp[i] - ri_t.delta[row]);
+                dp[i] = p * (dp[i] - delta[i]);
             }
             if (a.nb) {
                 if (!table) {
                     if (bucket != run_bucket) flush();
                     run_bucket = bucket;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) run_ds += kept ? dp[i] : 0.0f;
+                    for (int i = 0; i < 16; ++i) run_ds += dp[i];
                 } else if (key_run && uniform(ri_t.run)) {
                     const int first = uniform(ri_t.pos[0]);
 #pragma unroll
@@ -501,21 +537,21 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             skew[((lane & 31) + 15) * kSkewRow + 8 * (i / 4) + 4 * half + i % 4] =
-                                kept ? dp[8 * u + i] : 0.0f;
-                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                                dp[8 * u + i];
+                        wave_sync();
                         float x = 0.0f;   // offset key - row = lane - 15
                         if (lane < 47) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) x += skew[lane * kSkewRow + i * (kSkewRow + 1)];
                             run[key0 - (first + 16 * u) + (lane - 15) - a.lut_base + kRunPad] += x;
                         }
-                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        wave_sync();
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]));
-                        add_column(__float_as_int(lut[kLutPad + e].y), kept ? dp[i] : 0.0f);
+                        add_column(__float_as_int(lut[kLutPad + e].y), dp[i]);
                     }
                 }
             }
@@ -530,19 +566,24 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
                 const Frag<NP> p = split8f<NP>(x), ds = split8f<NP>(y);
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e) {
-                    dv[e] = mma<NP>(frag_cols<NP, DP>(tl, gt, kPlane, 16 * u, e), p, dv[e]);
-                    dk[e] = mma<NP>(frag_cols<NP, DP>(tl, qt, kPlane, 16 * u, e), ds, dk[e]);
+                    if constexpr (NP == 1) {
+                        dv[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(gf.f[u][e], p.p[0], dv[e], 0, 0, 0);
+                        dk[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf.f[u][e], ds.p[0], dk[e], 0, 0, 0);
+                    } else {
+                        dv[e] = mma<NP>(frag_cols<NP, DP>(tl, gt, kPlane, 16 * u, e), p, dv[e]);
+                        dk[e] = mma<NP>(frag_cols<NP, DP>(tl, qt, kPlane, 16 * u, e), ds, dk[e]);
+                    }
                 }
             }
         }
         if constexpr (kBuf == 1) __syncthreads();
-        if (t + 1 < t1) store(t + 1, kBuf == 2 ? buf ^ 1 : 0);
+        if (t + 1 < t1) store(kBuf == 2 ? buf ^ 1 : 0);
         __syncthreads();
     }
     if (a.nb && head >= 0) finish_head();
     if (!have) return;
     const int64_t at = (int64_t)(k0 + j) * a.Hkv + hk;
-    const float fk = kept ? a.scale * kUnlift : 0.0f, fv = kept ? kUnlift : 0.0f;
+    const float fk = a.scale * kUnlift;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
@@ -550,9 +591,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 && DP < 128 ? 2 : 1) void att
             const int d = 32 * e + 8 * i + 4 * half;
             floatx4 xk, xv;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {   // an absent key's column holds anything
-                xk[n] = kept ? dk[e][4 * i + n] * fk : 0.0f;
-                xv[n] = kept ? dv[e][4 * i + n] * fv : 0.0f;
+            for (int n = 0; n < 4; ++n) {
+                xk[n] = dk[e][4 * i + n] * fk;
+                xv[n] = dv[e][4 * i + n] * kUnlift;
             }
             if (a.splits > 1) {
                 float *p = g.part_kv + (((int64_t)split * a.n_k * a.Hkv + at) * 2) * a.D;

@@ -82,12 +82,10 @@ struct RowState {
 #pragma unroll
         for (int u = 0; u < NS; ++u) s[u] = rows_product<NP, DP>(tl, kt, kPlane, 32 * u, q);
         // one plane: the values are on their way during the softmax
-        bf16x8 vf[NP == 1 ? NS * 2 * (DP / 32) : 1];
+        ColsAhead<DP> vf[NS];
         if constexpr (NP == 1) {
 #pragma unroll
-            for (int u = 0; u < 2 * NS; ++u)
-#pragma unroll
-                for (int e = 0; e < DP / 32; ++e) vf[u * (DP / 32) + e] = tl.frag_cols(vt, 16 * u, e);
+            for (int u = 0; u < NS; ++u) vf[u].load(tl, vt, 32 * u);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -166,7 +164,7 @@ struct RowState {
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e) {
                     if constexpr (NP == 1)
-                        o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[(2 * u + t) * (DP / 32) + e], p.p[0], o[e], 0, 0, 0);
+                        o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u].f[t][e], p.p[0], o[e], 0, 0, 0);
                     else
                         o[e] = mma<NP>(frag_cols<NP, DP>(tl, vt, kPlane, 32 * u + 16 * t, e), p, o[e]);
                 }
@@ -244,10 +242,10 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
         kl.load(a, w, t * KT, a.nb && wave == 0, lane);
     };
     auto store = [&](int buf) {
-        const uint64_t mask = kl.mask();
+        const uint64_t mask = kl.mask(a);
         mk.store(tiles[buf][0], tid, a.keep && is_partial<KT>(mask), mask);
         mv.store(tiles[buf][1], tid, a.keep && is_partial<KT>(mask), mask);
-        if (a.nb && wave == 0) kl.store(info[buf], lane);
+        if (a.nb && wave == 0) kl.store(info[buf], mask, lane);
         return mask;
     };
     // the first tile, the rows and the bias are on their way together
@@ -324,14 +322,14 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     const uint32_t lds_k = uniform((int)lds_offset(kt)), lds_v = lds_k + kTile * sizeof(bf16);
     __syncthreads();
     for (; t < t1; t += NW) {
-        const uint64_t mask = kl.mask();
+        const uint64_t mask = kl.mask(a);
         mk.store(kt, lane, a.keep && is_partial<32>(mask), mask);
         mv.store(vt, lane, a.keep && is_partial<32>(mask), mask);
-        if (a.nb) kl.store(info[wave], lane);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (a.nb) kl.store(info[wave], mask, lane);
+        wave_sync();
         if (t + NW < t1) load(t + NW);
         if (mask) st.template step<32>(a, tl, lds_k, lds_v, mask, info[wave], lut, lane);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        wave_sync();
     }
     // join the wavefronts' rows, in their order
     const float lw = st.l + half_swap(st.l);
