@@ -158,27 +158,32 @@ struct ColsAhead {
             for (int e = 0; e < DP / 32; ++e) f[u][e] = l.frag_cols(tile, row0 + 16 * u, e);
     }
 };
-// x += A B over all of a row's elements, A the tile's rows row0 .. row0 + 31.
-// One plane: every operand is on its way before the first product.
+// A B over all of a row's elements, A the tile's rows row0 .. row0 + 31.  One
+// plane: begin() sends for every operand, and what is computed until finish()
+// covers their way.
 template <int NP, int DP>
-__device__ inline floatx16 rows_product(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0,
-                                        const Frag<NP> (&b)[DP / 16]) {
-    floatx16 x;
+struct RowsProduct {
+    bf16x8 f[NP == 1 ? DP / 16 : 1];
+    __device__ inline void begin(const TileLane<DP> &l, uint32_t tile, int row0) {
+        if constexpr (NP == 1)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-    if constexpr (NP == 1) {
-        bf16x8 f[DP / 16];
-#pragma unroll
-        for (int s = 0; s < DP / 16; ++s) f[s] = l.frag_rows(tile, row0, s);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int s = 0; s < DP / 16; ++s) x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[s], b[s].p[0], x, 0, 0, 0);
-    } else {
-#pragma unroll
-        for (int s = 0; s < DP / 16; ++s) x = mma<NP>(frag_rows<NP, DP>(l, tile, plane, row0, s), b[s], x);
+            for (int s = 0; s < DP / 16; ++s) f[s] = l.frag_rows(tile, row0, s);
     }
-    return x;
-}
+    __device__ inline floatx16 finish(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0,
+                                      const Frag<NP> (&b)[DP / 16]) const {
+        floatx16 x;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+            if constexpr (NP == 1)
+                x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[s], b[s].p[0], x, 0, 0, 0);
+            else
+                x = mma<NP>(frag_rows<NP, DP>(l, tile, plane, row0, s), b[s], x);
+        }
+        return x;
+    }
+};
 
 // Eight elements at `p` (elements d .. d + 7 of a row of D; zero beyond D),
 // as loaded.  vec: the row and its strides are 16-byte aligned and D is a
@@ -242,19 +247,29 @@ struct TileMove {
     static constexpr bool kExact = IT * NT == R * CH;
     Raw8<NP> raw[IT];
     uint32_t off, step;
-    __device__ inline void init(int64_t stride, int D, int tid) {
+    const T *next;      // first row of the tile that load() takes
+    int left;           // rows from there on
+    int full;           // bytes of a full tile
+    int64_t stride;
+    __device__ inline void init(int64_t row_stride, int D, int tid) {
+        stride = row_stride;
         if constexpr (FAST) {
             const int c = tid % CH;
             off = (kExact || tid < R * CH) && 8 * c < D ? (uint32_t)((tid / CH) * stride + 8 * c) * sizeof(T) : 0x80000000u;
             step = (uint32_t)(NT / CH * stride) * sizeof(T);
+            full = (int)(((R - 1) * stride + D) * sizeof(T));
         }
     }
-    // tile rows 0 .. R - 1 at base, `stride` apart, those from `rows` on zero
-    __device__ inline void load(const T *base, int64_t stride, int rows, int D, int tid) {
+    __device__ inline void seek(const T *base, int rows) {
+        next = base;
+        left = rows;
+    }
+    // the tile's rows at `next`, those from `left` on zero; goes on by `rows`
+    __device__ inline void load(int D, int tid, int rows = R) {
         if constexpr (FAST) {
-            const int n = min(rows, R);
-            const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<T *>(base), 0, n > 0 ? (int)(((n - 1) * stride + D) * sizeof(T)) : 0, 0x00020000);
+            const int bytes = left >= R ? full : left > 0 ? (int)(((left - 1) * stride + D) * sizeof(T)) : 0;
+            const __amdgpu_buffer_rsrc_t rsrc =
+                __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(next), 0, bytes, 0x00020000);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const uint32_t at = off + it * step;
@@ -267,9 +282,11 @@ struct TileMove {
             for (int it = 0; it < IT; ++it) {
                 const int c = tid + it * NT, row = c / CH, d = (c % CH) * 8;
                 raw[it] = raw_zero<NP>();
-                if (row < rows && row < R) raw[it] = load8<NP>(base + row * stride + d, d, D, false);
+                if (row < left && row < R) raw[it] = load8<NP>(next + row * stride + d, d, D, false);
             }
         }
+        next += rows * stride;
+        left -= rows;
     }
     // partial: rows whose bit in `kept` is clear become zero
     __device__ inline void store(bf16 *tile, int tid, bool partial, uint64_t kept) {
@@ -314,8 +331,17 @@ __device__ inline void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The value of the lane's other half (lane ^ 32).
-__device__ inline float half_swap(float v) { return __shfl_xor(v, 32, 64); }
+// Sum and maximum of a lane's value and that of its other half (lane ^ 32):
+// the swap instruction leaves the lower half's value in one register of every
+// lane and the upper half's in the other.
+__device__ inline float half_sum(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline float half_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // A value that is the same in every lane, in scalar registers.
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -393,9 +419,8 @@ __device__ inline void fill_lut(const AttnArgs &a, const RowBlock &w, float *lut
 // positions, which one wavefront leaves in LDS for all.
 template <int KT>
 struct KeyInfo {
+    int4 head;      // smallest and largest of the kept keys, whether all run (first, first + 1, ...), the first
     int pos[KT];
-    int lo, hi;     // of the kept keys
-    int run;        // the positions are pos[0], pos[0] + 1, ...
 };
 template <int KT>
 struct KeyLoad {
@@ -407,10 +432,8 @@ struct KeyLoad {
         const int j = key0 + lane;
         kept = 0;
         pos = j;
-        if (lane < n) {
-            if (positions && a.k_pos) pos = a.k_pos[w.k0 + j];
-            if (a.keep) kept = a.keep[w.k0 + j];
-        }
+        if (positions && a.k_pos && lane < n) pos = a.k_pos[w.k0 + j];
+        if (a.keep && lane < n) kept = a.keep[w.k0 + j];
     }
     __device__ inline uint64_t mask(const AttnArgs &a) const {
         return a.keep ? __ballot(kept != 0) : n >= 64 ? ~0ull : (1ull << n) - 1;
@@ -426,13 +449,15 @@ struct KeyLoad {
             hi = wave_max(ok ? pos : (int)0x80000000);
         }
         if (lane < KT) k.pos[lane] = pos;
-        if (lane == 0) {
-            k.lo = lo;
-            k.hi = hi;
-            k.run = run;
-        }
+        if (lane == 0) k.head = make_int4(lo, hi, run, first);
     }
 };
+
+// Where one side's positions lie, in scalar registers.
+struct PosRange {
+    int lo, hi, run, first;
+};
+__device__ inline PosRange uniform_range(int4 v) { return {uniform(v.x), uniform(v.y), uniform(v.z), uniform(v.w)}; }
 template <int KT>
 __device__ inline bool is_partial(uint64_t mask) { return mask != (KT == 64 ? ~0ull : 0xffffffffull); }
 

@@ -71,9 +71,11 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
     KeyLoad<kDqKeys> kl;
     mk.init(a.ks, a.D, tid);
     mv.init(a.vs, a.D, tid);
+    mk.seek(K, w.nk);
+    mv.seek(V, w.nk);
     auto load = [&](int t) {
-        mk.load(K + t * kDqKeys * a.ks, a.ks, w.nk - t * kDqKeys, a.D, tid);
-        mv.load(V + t * kDqKeys * a.vs, a.vs, w.nk - t * kDqKeys, a.D, tid);
+        mk.load(a.D, tid);
+        mv.load(a.D, tid);
         kl.load(a, w, t * kDqKeys, a.nb && wave == 0, lane);
     };
     auto store = [&](int buf) {
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
             delta = fmaf(x, y, delta);
         }
     }
-    delta += half_swap(delta);
+    delta = half_sum(delta);
     const float L = lse == -INFINITY ? INFINITY : lse * kLog2e - kLift;
     const int pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff), pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
 
@@ -146,14 +148,30 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
     constexpr uint32_t kPlane = kDqKeys * DP * sizeof(bf16), kBytes = NP * kPlane;
     uint64_t mask = 0;
     if (n_tiles > 0) mask = store(0);
+    if (n_tiles > 1) load(1);
     __syncthreads();
-    for (int t = 0; t < n_tiles; ++t) {
+    for (int t = 0; t < n_tiles; ++t) {   // tile t is in LDS, t + 1 in registers or on its way there
         const int buf = t & 1;
-        if (t + 1 < n_tiles) load(t + 1);
         const uint32_t kt = lds0 + 2 * buf * kBytes, vt = kt + kBytes;
         const KeyInfo<kDqKeys> &ki = info[buf];
         if (active && mask) {
-            floatx16 s = rows_product<NP, DP>(tl, kt, kPlane, 0, q), dp = rows_product<NP, DP>(tl, vt, kPlane, 0, dO);
+            int4 range;
+            if (a.nb) range = ki.head;
+            RowsProduct<NP, DP> rs, rd;
+            rs.begin(tl, kt, 0);
+            rd.begin(tl, vt, 0);
+            float mul = c, less = -L;
+            const float *mine = lut + hg * lut_stride(a);
+            PosRange keys{};
+            bool table = false;
+            if (a.nb) {
+                keys = uniform_range(range);
+                const int first = lut_index(a, offset_of(keys.lo, pos_hi)), last = lut_index(a, offset_of(keys.hi, pos_lo));
+                table = first != last;
+                if (!table) less += mine[kLutPad + first];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            floatx16 s = rs.finish(tl, kt, kPlane, 0, q), dp = rd.finish(tl, vt, kPlane, 0, dO);
             ColsAhead<DP> kf;
             if constexpr (NP == 1) {
                 kf.load(tl, kt, 0);
@@ -161,20 +179,13 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
             }
             settle(s);
             settle(dp);
-            float mul = c, less = -L;
-            if (a.nb) {
-                const int lo = uniform(ki.lo), hi = uniform(ki.hi);
-                const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
-                const float *mine = lut + hg * lut_stride(a);
-                if (first == last) {
-                    less += mine[kLutPad + first];
-                } else if (a.lut_run && uniform(ki.run)) {
-                    mul = 1.0f;
-                    mine += run_index(a, offset_of(uniform(ki.pos[0]), pos)) + 4 * half;
+            if (table) {
+                mul = 1.0f;
+                if (a.lut_run && keys.run) {
+                    const float *at = mine + run_index(a, offset_of(keys.first, pos)) + 4 * half;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, mine[8 * (i / 4) + i % 4]);
+                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, at[8 * (i / 4) + i % 4]);
                 } else {
-                    mul = 1.0f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = lut_index(a, offset_of(ki.pos[8 * (i / 4) + 4 * half + i % 4], pos));
@@ -212,10 +223,11 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
             }
         }
         if (t + 1 < n_tiles) mask = store(buf ^ 1);
+        if (t + 2 < n_tiles) load(t + 2);
         __syncthreads();
     }
     // the row's sum of dS in units of p (sum_j p_ij is 2^24 by construction)
-    const float err = (row_ds + half_swap(row_ds)) * kUnlift;
+    const float err = half_sum(row_ds) * kUnlift;
     if (row >= 0) {
         T *out = (T *)g.dq + at * a.D;
 #pragma unroll
@@ -248,10 +260,9 @@ __global__ __launch_bounds__(1024) void attn_dbias_kernel(AttnArgs a, const floa
 
 // What the rows of a tile need beside q and dO.
 struct RowInfo {
+    int4 head;                   // smallest and largest position, whether all run (first, first + 1, ...), the first
     float less[32], delta[32];   // -L
     int pos[32];
-    int lo, hi;
-    int run;        // the positions are pos[0], pos[0] + 1, ...
 };
 
 // The bias sums of a tile whose offsets span several buckets.  LDS float
@@ -321,12 +332,18 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
     mg.init(a.gs, a.D, tid);
     // the tile that is loaded next: its head (of the G) and first row
     int next_head = t0 < t1 ? t0 / per_head : 0, next_row = t0 < t1 ? t0 % per_head * kRows : 0;
+    auto seek = [&]() {   // (past the last head: never loaded)
+        const int h = hk * a.G + next_head;
+        mq.seek((const T *)a.q + (q0 + next_row) * a.qs + h * a.qh, nq - next_row);
+        mg.seek((const T *)a.d_o + (q0 + next_row) * a.gs + h * a.gh, nq - next_row);
+    };
+    seek();
     float2 ri;
     int ri_pos, ri_n;
     auto load = [&]() {
         const int h = hk * a.G + next_head, r0 = next_row;
-        mq.load((const T *)a.q + (q0 + r0) * a.qs + h * a.qh, a.qs, nq - r0, a.D, tid);
-        mg.load((const T *)a.d_o + (q0 + r0) * a.gs + h * a.gh, a.gs, nq - r0, a.D, tid);
+        mq.load(a.D, tid);
+        mg.load(a.D, tid);
         if (wave == 0) {
             ri_n = min(nq - r0, kRows);
             ri = make_float2(INFINITY, 0.0f);
@@ -340,6 +357,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
         if (next_row >= nq) {
             next_row = 0;
             ++next_head;
+            seek();
         }
     };
 
@@ -403,11 +421,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
                 info[buf].delta[lane] = ri.y;
                 info[buf].pos[lane] = ri_pos;
             }
-            if (lane == 0) {
-                info[buf].lo = lo;
-                info[buf].hi = hi;
-                info[buf].run = run;
-            }
+            if (lane == 0) info[buf].head = make_int4(lo, hi, run, first);
         }
     };
     const TileLane<DP> tl(lane);
@@ -459,14 +473,14 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             if (t0 >= t1 || i / a.nb < t0 / per_head || i / a.nb > (t1 - 1) / per_head) part[i] = 0.0f;
     int tile_head = 0, loaded_head = next_row == 0 ? next_head - 1 : next_head;   // of the tiles in LDS and in registers
     if (t0 < t1) store(0);
+    tile_head = loaded_head;
+    if (t0 + 1 < t1) {
+        loaded_head = next_head;
+        load();
+    }
     __syncthreads();
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0; t < t1; ++t) {   // tile t is in LDS, t + 1 in registers or on its way there
         const int buf = kBuf == 2 ? (t - t0) & 1 : 0;
-        tile_head = loaded_head;
-        if (t + 1 < t1) {
-            loaded_head = next_head;
-            load();
-        }
         if (a.nb && tile_head != head) {   // every wavefront is past the last use of the table (barrier below)
             if (head >= 0) finish_head();
             head = tile_head;
@@ -480,13 +494,33 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
         const uint32_t qt = lds0 + 2 * buf * kBytes, gt = qt + kBytes;
         const RowInfo &ri_t = info[buf];
         if (active) {
+            int4 range;
+            if (a.nb) range = ri_t.head;
+            RowsProduct<NP, DP> rs, rd;
+            rs.begin(tl, qt, 0);
+            rd.begin(tl, gt, 0);
             float less[16], delta[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 less[i] = ri_t.less[8 * (i / 4) + 4 * half + i % 4];
                 delta[i] = ri_t.delta[8 * (i / 4) + 4 * half + i % 4];
             }
-            floatx16 s = rows_product<NP, DP>(tl, qt, kPlane, 0, k), dp = rows_product<NP, DP>(tl, gt, kPlane, 0, v);
+            float mul = c, add = kept_add;
+            PosRange rows{};
+            int bucket = -1;
+            bool table = false;
+            if (a.nb) {
+                rows = uniform_range(range);
+                const int first = lut_index(a, offset_of(pos_lo, rows.hi)), last = lut_index(a, offset_of(pos_hi, rows.lo));
+                table = first != last;
+                if (!table) {
+                    const float2 e = lut[kLutPad + first];
+                    add += e.x;
+                    bucket = uniform(__float_as_int(e.y));
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            floatx16 s = rs.finish(tl, qt, kPlane, 0, k), dp = rd.finish(tl, gt, kPlane, 0, v);
             ColsAhead<DP> qf, gf;
             if constexpr (NP == 1) {
                 gf.load(tl, gt, 0);
@@ -495,27 +529,16 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             }
             settle(s);
             settle(dp);
-            float mul = c, add = kept_add;
-            int bucket = -1;
-            bool table = false;
-            if (a.nb) {
-                const int lo = uniform(ri_t.lo), hi = uniform(ri_t.hi);
-                const int first = lut_index(a, offset_of(pos_lo, hi)), last = lut_index(a, offset_of(pos_hi, lo));
-                table = first != last;
-                if (!table) {
-                    add += lut[kLutPad + first].x;
-                    bucket = uniform(__float_as_int(lut[kLutPad + first].y));
-                } else if (a.lut_run && uniform(ri_t.run)) {   // later rows, smaller offsets
-                    mul = 1.0f;
-                    const float2 *mine = lut + run_index(a, offset_of(pos, uniform(ri_t.pos[0]) + 31)) + 3 - 4 * half;
+            if (table) {
+                mul = 1.0f;
+                if (a.lut_run && rows.run) {   // later rows, smaller offsets
+                    const float2 *at = lut + run_index(a, offset_of(pos, rows.first + 31)) + 3 - 4 * half;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, mine[28 - 8 * (i / 4) - i % 4].x);
+                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, at[28 - 8 * (i / 4) - i % 4].x);
                 } else {
-                    mul = 1.0f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 16; ++i)
                         s[i] = fmaf(s[i], c, lut[kLutPad + lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))].x);
-                    }
                 }
             }
 #pragma unroll
@@ -530,8 +553,8 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
                     run_bucket = bucket;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) run_ds += dp[i];
-                } else if (key_run && uniform(ri_t.run)) {
-                    const int first = uniform(ri_t.pos[0]);
+                } else if (key_run && rows.run) {
+                    const int first = rows.first;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -577,7 +600,14 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             }
         }
         if constexpr (kBuf == 1) __syncthreads();
-        if (t + 1 < t1) store(kBuf == 2 ? buf ^ 1 : 0);
+        if (t + 1 < t1) {
+            store(kBuf == 2 ? buf ^ 1 : 0);
+            tile_head = loaded_head;
+        }
+        if (t + 2 < t1) {
+            loaded_head = next_head;
+            load();
+        }
         __syncthreads();
     }
     if (a.nb && head >= 0) finish_head();

@@ -78,9 +78,27 @@ struct RowState {
         constexpr int NS = KT / 32;
         constexpr uint32_t kPlane = KT * DP * sizeof(bf16);
         const int half = lane >> 5;
+        int4 head;
+        if (a.nb) head = ki.head;
+        RowsProduct<NP, DP> rp[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) rp[u].begin(tl, kt, 32 * u);
+        // x = s c + add, in log2 units: one bias for a tile whose offsets all
+        // fall in one bucket, else c is folded in below, element by element
+        float mul = c, add = 0.0f;
+        const float *mine = lut + g * lut_stride(a);
+        PosRange keys{};
+        bool table = false;
+        if (a.nb) {
+            keys = uniform_range(head);
+            const int first = lut_index(a, offset_of(keys.lo, pos_hi)), last = lut_index(a, offset_of(keys.hi, pos_lo));
+            table = first != last;
+            if (!table) add = mine[kLutPad + first];
+        }
+        __builtin_amdgcn_sched_barrier(0);
         floatx16 s[NS];
 #pragma unroll
-        for (int u = 0; u < NS; ++u) s[u] = rows_product<NP, DP>(tl, kt, kPlane, 32 * u, q);
+        for (int u = 0; u < NS; ++u) s[u] = rp[u].finish(tl, kt, kPlane, 32 * u, q);
         // one plane: the values are on their way during the softmax
         ColsAhead<DP> vf[NS];
         if constexpr (NP == 1) {
@@ -90,24 +108,15 @@ struct RowState {
         }
 #pragma unroll
         for (int u = 0; u < NS; ++u) settle(s[u]);
-        // x = s c + add, in log2 units: one bias for a tile whose offsets all
-        // fall in one bucket, else c is folded in here, element by element
-        float mul = c, add = 0.0f;
-        if (a.nb) {
-            const int lo = uniform(ki.lo), hi = uniform(ki.hi);
-            const int first = lut_index(a, offset_of(lo, pos_hi)), last = lut_index(a, offset_of(hi, pos_lo));
-            const float *mine = lut + g * lut_stride(a);
-            if (first == last) {
-                add = mine[kLutPad + first];
-            } else if (a.lut_run && uniform(ki.run)) {
-                mul = 1.0f;
-                mine += run_index(a, offset_of(uniform(ki.pos[0]), pos)) + 4 * half;
+        if (table) {
+            mul = 1.0f;
+            if (a.lut_run && keys.run) {
+                const float *at = mine + run_index(a, offset_of(keys.first, pos)) + 4 * half;
 #pragma unroll
                 for (int u = 0; u < NS; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[u][i] = fmaf(s[u][i], c, mine[32 * u + 8 * (i / 4) + i % 4]);
+                    for (int i = 0; i < 16; ++i) s[u][i] = fmaf(s[u][i], c, at[32 * u + 8 * (i / 4) + i % 4]);
             } else {
-                mul = 1.0f;
 #pragma unroll
                 for (int u = 0; u < NS; ++u)
 #pragma unroll
@@ -130,7 +139,7 @@ struct RowState {
         for (int u = 0; u < NS; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
-        mx = fmaxf(mx, half_swap(mx));
+        mx = half_max(mx);
         mx = mx == -INFINITY ? mx : fmaf(mx, mul, add);   // no key, whatever the scale
         if (__any(mx > m + 8.0f)) {
             const float mn = fmaxf(m, mx);
@@ -236,9 +245,11 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
     KeyLoad<KT> kl;
     mk.init(a.ks, a.D, tid);
     mv.init(a.vs, a.D, tid);
+    mk.seek(K + t0 * KT * a.ks, w.nk - t0 * KT);
+    mv.seek(V + t0 * KT * a.vs, w.nk - t0 * KT);
     auto load = [&](int t) {
-        mk.load(K + t * KT * a.ks, a.ks, w.nk - t * KT, a.D, tid);
-        mv.load(V + t * KT * a.vs, a.vs, w.nk - t * KT, a.D, tid);
+        mk.load(a.D, tid);
+        mv.load(a.D, tid);
         kl.load(a, w, t * KT, a.nb && wave == 0, lane);
     };
     auto store = [&](int buf) {
@@ -256,19 +267,20 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
     st.begin(a, w, w.tile * 128 + wave * 32, lane, raw);
     if (a.nb) fill_lut(a, w, lut);
     if (t0 < t1) mask = store(0);
+    if (t0 + 1 < t1) load(t0 + 1);
     st.finish(a, raw);
     const bool active = __any(st.row >= 0);
     __syncthreads();
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0; t < t1; ++t) {   // tile t is in LDS, t + 1 in registers or on its way there
         const int buf = (t - t0) & 1;
-        if (t + 1 < t1) load(t + 1);
         if (active && mask)
             st.template step<KT>(a, tl, lds0 + 2 * buf * kBytes, lds0 + (2 * buf + 1) * kBytes, mask, info[buf], lut, lane);
         if (t + 1 < t1) mask = store(buf ^ 1);
+        if (t + 2 < t1) load(t + 2);
         __syncthreads();
     }
     if (st.row < 0) return;
-    const float l = st.l + half_swap(st.l), inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float l = half_sum(st.l), inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int64_t at = (int64_t)st.row * a.H + w.h0 + st.g;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
@@ -306,12 +318,14 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     KeyLoad<32> kl;
     mk.init(a.ks, a.D, lane);
     mv.init(a.vs, a.D, lane);
+    int t = t0 + wave;
+    mk.seek(K + t * 32 * a.ks, w.nk - t * 32);
+    mv.seek(V + t * 32 * a.vs, w.nk - t * 32);
     auto load = [&](int t) {
-        mk.load(K + t * 32 * a.ks, a.ks, w.nk - t * 32, a.D, lane);
-        mv.load(V + t * 32 * a.vs, a.vs, w.nk - t * 32, a.D, lane);
+        mk.load(a.D, lane, 32 * NW);
+        mv.load(a.D, lane, 32 * NW);
         kl.load(a, w, t * 32, a.nb, lane);
     };
-    int t = t0 + wave;
     if (t < t1) load(t);
     RowState<NP, DP, FAST> st;
     Raw8<NP> raw[DP / 16];
@@ -332,7 +346,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
         wave_sync();
     }
     // join the wavefronts' rows, in their order
-    const float lw = st.l + half_swap(st.l);
+    const float lw = half_sum(st.l);
     if (lane < 32) {
         wave_m[wave][lane] = st.m;
         wave_l[wave][lane] = lw;
