@@ -25,8 +25,12 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
+# accumulators of 16 registers stay whole where paths join: taken apart, they
+# are copied back into consecutive registers every tile
+WHOLE_VECTORS = ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=false"]
 # the neighbour predicate must round every operation on its own
-PER_FILE = {"neighbors.hip": ["-ffp-contract=off"]}
+PER_FILE = {"neighbors.hip": ["-ffp-contract=off"],
+            "attention_fwd.hip": WHOLE_VECTORS, "attention_bwd.hip": WHOLE_VECTORS}
 
 
 def _compile(src: str) -> str:

@@ -26,6 +26,10 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
+__device__ inline floatx16 zero16() {
+    return floatx16{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kAttnThreads = 256;   // four wavefronts
 constexpr int kLutMax = 2048;       // entries of a position table (SN_MAX_BUCKET_SPAN + 2)
@@ -171,9 +175,7 @@ struct RowsProduct {
     }
     __device__ inline floatx16 finish(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0,
                                       const Frag<NP> (&b)[DP / 16]) const {
-        floatx16 x;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+        floatx16 x = zero16();
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s) {
             if constexpr (NP == 1)

@@ -139,9 +139,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
 
     floatx16 dq[DP / 32];
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dq[e][i] = 0.0f;
+    for (int e = 0; e < DP / 32; ++e) dq[e] = zero16();
     float row_ds = 0.0f;    // sum of the row's dS (this half's keys)
     const TileLane<DP> tl(lane);
     const uint32_t lds0 = lds_offset(tiles);
@@ -429,9 +427,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
     constexpr uint32_t kPlane = kRows * DP * sizeof(bf16), kBytes = NP * kPlane;
     floatx16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dk[e][i] = dv[e][i] = 0.0f;
+    for (int e = 0; e < DP / 32; ++e) dk[e] = dv[e] = zero16();
     float run_ds = 0.0f;        // of the tiles since the bucket last changed
     int run_bucket = -1, head = -1;
     auto add_column = [&](int bk, float x) {

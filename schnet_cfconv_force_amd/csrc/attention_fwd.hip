@@ -65,9 +65,7 @@ struct RowState {
         m = -INFINITY;
         l = 0.0f;
 #pragma unroll
-        for (int e = 0; e < DP / 32; ++e)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[e][i] = 0.0f;
+        for (int e = 0; e < DP / 32; ++e) o[e] = zero16();
     }
 
     // One tile of KT keys (KT / 32 score tiles) at the LDS offsets kt, vt.
@@ -147,9 +145,7 @@ struct RowState {
             m = mn;
             l *= f;
 #pragma unroll
-            for (int e = 0; e < DP / 32; ++e)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[e][i] *= f;
+            for (int e = 0; e < DP / 32; ++e) o[e] *= f;
         }
         // p = 2^(x - m); a row without a key so far: 2^-inf = 0.  An absent
         // key must stay at -inf: a zero multiplier would make it NaN
