@@ -350,13 +350,13 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 
 // --------------------------------------------------------------- positions
 
-// thr is padded with the type's largest value, so eight are read and
-// compared at a time.
+// thr is padded with the type's largest value, so 32 are read at a
+// time.
 __device__ inline int bucket_of(const AttnArgs &a, int rel) {
     int n = 0;
-    for (int t = 0; t < a.nb - 1; t += 8)
+    for (int t = 0; t < a.nb - 1; t += 32)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) n += rel >= a.thr[t + j];
+        for (int j = 0; j < 32; ++j) n += rel >= a.thr[t + j];
     return min(n, a.nb - 1);
 }
 // Entry of the position table for one offset: the table holds every offset

@@ -448,26 +448,31 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
         run_ds = 0.0f;
         run_bucket = -1;
     };
-    // the head's sums are complete: every bucket adds its columns and its
-    // offsets in order
+    // the head's sums are complete: the wavefronts' tables of offsets become
+    // one, then four threads per bucket add its columns and its offsets, in
+    // one order
     auto finish_head = [&]() {
         flush();
         __syncthreads();
-        for (int i = tid; i < a.nb * 4; i += kAttnThreads) {
-            const int wv = i / a.nb, bk = i % a.nb;
+        float *all = bias_mem + bl.run;
+        if (small_lut)
+            for (int e = tid; e < run_n; e += kAttnThreads)
+                all[e] = (all[e] + all[run_n + e]) + (all[2 * run_n + e] + all[3 * run_n + e]);
+        __syncthreads();
+        const int bk = tid >> 2, q = tid & 3;
+        if (bk < a.nb) {
             float s = 0.0f;
-            for (int k = 0; k < 32; ++k) s += sums[(wv * a.nb + bk) * 32 + (k + bk) % 32];
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) s += sums[(q * a.nb + bk) * 32 + (k + bk) % 32];
             if (small_lut) {
                 const int from = bk == 0 ? 0 : (int)((int64_t)a.thr[bk - 1] - a.lut_base) + kRunPad;
                 const int to = bk == a.nb - 1 ? run_n : (int)((int64_t)a.thr[bk] - a.lut_base) + kRunPad;
-                for (int e = from; e < to; ++e) s += bias_mem[bl.run + wv * run_n + e];
+#pragma unroll 4
+                for (int e = from + q; e < to; e += 4) s += all[e];
             }
-            sums[(wv * a.nb + bk) * 32 + bk % 32] = s;
-        }
-        __syncthreads();
-        for (int bk = tid; bk < a.nb; bk += kAttnThreads) {
-            const float *s = sums + bk * 32 + bk % 32;
-            part[head * a.nb + bk] = (s[0] + s[a.nb * 32]) + (s[2 * a.nb * 32] + s[3 * a.nb * 32]);
+            s += __shfl_xor(s, 1, 64);
+            s += __shfl_xor(s, 2, 64);
+            if (q == 0) part[head * a.nb + bk] = s;
         }
         __syncthreads();
     };

@@ -24,7 +24,9 @@ __device__ inline T from_f32(float v) { return (T)v; }
 // contradicts the sizes that the host was given (flagged in the status word).
 __device__ inline void segment_rows(const int32_t *ptr, int b, int n_segments, int n_rows, int max_rows, int *status,
                                     int &start, int &len) {
-    const int s = ptr[b], e = ptr[b + 1];
+    // b is the same in the whole block: scalar reads, straight into scalar registers
+    const auto p = (const __attribute__((address_space(4))) int32_t *)(uintptr_t)ptr;
+    const int s = p[b], e = p[b + 1];
     start = s;
     len = e - s;
     if (s < 0 || e < s || e > n_rows || e - s > max_rows || (b == 0 && s != 0) ||
