@@ -407,3 +407,31 @@ def test_norm_gradient_matches_differences(sn):
         mag = float((ref[grad][1].cuda() * e.double().abs()).sum())
         print(f"   {grad}: {slope:.6g} against {want:.6g} (magnitudes {mag:.3g})", flush=True)
         assert abs(slope - want) <= h * h * mag
+
+
+# ------------------------------------------------------------------ the operators together
+
+def test_context_embedding_example(sn):
+    """The block begins as the identity: its rows give the plain model's energies and forces bit for bit.  Fitted, it
+    explains most of its target, and the model runs on its rows."""
+    import os
+    import sys
+
+    import torch
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import context_embedding as ex
+    print("[example] context embedding", flush=True)
+    cfg, x, states, state_ptr, target = ex.make_inputs(2)
+    block = ex.ContextBlock(cfg["replica_ptr"], state_ptr, cfg["hyper"]["n_features"])
+    pos = torch.from_numpy(cfg["pos"]).cuda()
+    plain = ex.evaluate(sn.Model(cfg["params"], cfg["hyper"]), sn.System(cfg["replica_ptr"], cfg["types"], cfg["box"]), cfg, pos)
+    with torch.no_grad():
+        same = ex.evaluate(*ex.model_of_rows(cfg, block(x, states)), cfg, pos)
+    assert torch.equal(plain[0], same[0]) and torch.equal(plain[1], same[1])
+    losses = ex.fit(block, x, states, target, steps=100)
+    print(f"   relative error {losses[-1]:.3f}", flush=True)
+    assert np.all(np.isfinite(losses)) and losses[-1] < 0.5 * losses[0]
+    with torch.no_grad():
+        energy, forces, ws, _ = ex.evaluate(*ex.model_of_rows(cfg, block(x, states)), cfg, pos)
+    assert sn.read_status(ws) == sn.SN_OK and bool(torch.isfinite(forces).all())
+    assert not torch.equal(energy, plain[0])
