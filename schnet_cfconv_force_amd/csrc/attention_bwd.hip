@@ -630,8 +630,8 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             floatx4 xk, xv;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                xk[n] = dk[e][4 * i + n] * fk;
-                xv[n] = dv[e][4 * i + n] * kUnlift;
+                xk[n] = kept ? dk[e][4 * i + n] * fk : 0.0f;   // zero whatever the rows hold
+                xv[n] = kept ? dv[e][4 * i + n] * kUnlift : 0.0f;
             }
             if (a.splits > 1) {
                 float *p = g.part_kv + (((int64_t)split * a.n_k * a.Hkv + at) * 2) * a.D;

@@ -205,11 +205,18 @@ __device__ inline void write_row4(const AttnArgs &a, const FwdOut &out, int spli
         if (d + i < a.D) o[d + i] = (T)v[i];
 }
 
+// Of a row's maximum (log2) and sum; no key: -inf, and the row is zeros.  A sum
+// that is not a number stays one.
+__device__ inline float log_sum(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+}
+__device__ inline float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
 __device__ inline void write_stats(const AttnArgs &a, const FwdOut &out, int split, int64_t at, float m, float l) {
     if (a.splits > 1)
         out.part_ml[(int64_t)split * a.n_q * a.H + at] = make_float2(m, l);
     else if (out.lse)
-        out.lse[at] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -INFINITY;
+        out.lse[at] = log_sum(m, l);
 }
 
 // Keys of a tile: 64 halve the barriers and the running sums' exchanges, 32
@@ -276,7 +283,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
         __syncthreads();
     }
     if (st.row < 0) return;
-    const float l = half_sum(st.l), inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float l = half_sum(st.l), inv = inverse(l);
     const int64_t at = (int64_t)st.row * a.H + w.h0 + st.g;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
@@ -351,7 +358,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     float m = -INFINITY, l = 0.0f;
     for (int v = 0; v < NW; ++v) m = fmaxf(m, wave_m[v][lane & 31]);
     for (int v = 0; v < NW; ++v)
-        if (wave_l[v][lane & 31] > 0.0f || wave_l[v][lane & 31] != wave_l[v][lane & 31])
+        if (wave_l[v][lane & 31] != 0.0f)
             l += wave_l[v][lane & 31] * __builtin_amdgcn_exp2f(wave_m[v][lane & 31] - m);
     const float f = st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m);
     float *rows = reinterpret_cast<float *>(lds);   // [wavefront][DP][33]
@@ -362,7 +369,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
             rows[(wave * DP + 32 * e + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] = st.o[e][i] * f;
     __syncthreads();
     if (tid < 32 && st.row >= 0) write_stats(a, out, w.split, (int64_t)st.row * a.H + w.h0 + st.g, m, l);
-    if (wave == 0 && lane < 32) wave_l[0][lane] = l > 0.0f ? 1.0f / l : 0.0f;
+    if (wave == 0 && lane < 32) wave_l[0][lane] = inverse(l);
     __syncthreads();
     const int n = min(32, w.nq * w.gs - w.tile * 32);
     for (int i = tid; i < n * (DP / 4); i += 64 * NW) {
@@ -389,19 +396,19 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, FwdOut out) 
     float acc[2] = {0.0f, 0.0f};
     for (int k = 0; k < a.splits; ++k) {
         const float2 p = out.part_ml[k * rows + at];
-        if (p.x == -INFINITY) continue;   // no key in this split: its row was not computed
+        if (p.y == 0.0f) continue;   // no key in this split
         const float f = __builtin_amdgcn_exp2f(p.x - m);
         l = fmaf(p.y, f, l);
         for (int u = 0; u < 2; ++u)
             if (lane + 64 * u < a.D) acc[u] = fmaf(out.part_o[(k * rows + at) * a.D + lane + 64 * u], f, acc[u]);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = inverse(l);
     for (int u = 0; u < 2; ++u) {
         const int d = lane + 64 * u;
         if (d >= a.D) continue;
         ((T *)out.o)[at * a.D + d] = (T)(acc[u] * inv);
     }
-    if (lane == 0 && out.lse) out.lse[at] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0 && out.lse) out.lse[at] = log_sum(m, l);
 }
 
 // How the rows are cut: few rows or many, row tiles, key splits.

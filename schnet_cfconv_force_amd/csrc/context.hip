@@ -1,5 +1,6 @@
 // C-ABI entry points of the context operators: argument checks and argument
-// packing.  The kernels are in attention.hip and norm.hip.
+// packing.  The kernels are in attention_fwd.hip,
+// attention_bwd.hip and norm.hip.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -26,7 +27,7 @@ sn_status check_attn_sizes(const sn_cross_attention *op) {
     if ((int64_t)op->max_q * op->n_segments < op->n_q || (int64_t)op->max_k * op->n_segments < op->n_k)
         return SN_ERR_INVALID;
     if (op->n_heads < 1 || op->n_kv_heads < 1 || op->n_heads % op->n_kv_heads != 0) return SN_ERR_INVALID;
-    if (op->n_heads > 65536) return SN_ERR_INVALID;
+    if (op->n_heads > 65535) return SN_ERR_INVALID;
     if (op->head_dim < 1 || op->head_dim > SN_MAX_HEAD_DIM) return SN_ERR_INVALID;
     if (op->dtype != SN_F32 && op->dtype != SN_BF16) return SN_ERR_INVALID;
     // rows are counted with their heads in 32-bit block and row indices

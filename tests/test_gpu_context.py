@@ -133,6 +133,57 @@ def test_attention_masks_and_layouts(sn, layout, keep, few, dtype):
     attention_check(attention_run(sn, plan, c, where), ref, factor, dtype)
 
 
+#        lq, lk, H, Hkv, D, thresholds, scale: what the shapes above do not reach
+SPLIT = [
+    # few key/value heads and segments: the keys of many rows are cut and joined, a segment without keys in a cut
+    ([40], [1200], 2, 2, 32, True, None), ([130, 40, 33], [1800, 700, 3], 2, 1, 64, True, None), ([35], [2100], 1, 1, 128, False, None),
+    # ... and the keys of few rows
+    ([1], [5000], 2, 1, 64, True, None), ([9, 2], [3000, 40], 3, 3, 33, True, None),
+    # many rows per key: the rows of the dk, dv pass are cut and joined
+    ([700], [40], 4, 2, 32, True, None), ([700, 5], [40, 129], 4, 1, 64, True, None), ([900], [33], 3, 1, 128, False, None),
+    # a table of offsets that only one or two heads of a subgroup fit
+    ([20, 150], [170, 60], 6, 1, 32, "wide", None), ([3], [900], 8, 1, 64, "half", None), ([80], [90], 16, 1, 16, "half", None),
+    # scales of either sign and none
+    ([70, 3], [100, 40], 4, 2, 40, True, -0.3), ([70, 3], [100, 40], 2, 2, 64, True, 0.0), ([5], [700], 2, 2, 16, False, -1.0),
+]
+SPANS = {"wide": [-1023, -8, 1, 9, 1023], "half": [-500, -4, 0, 4, 500]}
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("shape", SPLIT, ids=lambda s: "x".join(str(v).replace(" ", "") for v in s))
+def test_attention_splits_subgroups_and_scales(sn, shape, dtype):
+    print(f"[attention] {shape} {dtype}", flush=True)
+    lq, lk, H, Hkv, D, thr, scale = shape
+    thr = np.array(SPANS[thr], np.int32) if isinstance(thr, str) else thr
+    plan, c, where, ref, factor = attention_case(sn, lq, lk, H, Hkv, D, dtype, thr, True, "plain", seed=len(str(shape)) + 50,
+                                                 scale=scale)
+    attention_check(attention_run(sn, plan, c, where), ref, factor, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("lq", [[3, 2, 5], [40, 33, 50], [35]], ids=str)
+def test_attention_keeps_nan_where_it_belongs(sn, lq, name, dtype):
+    """A NaN in a row that counts reaches exactly the outputs that depend on it, in its head and segment."""
+    import torch
+    print(f"[attention] NaN in {name}, rows {lq} {dtype}", flush=True)
+    lk = [70, 90, 600] if len(lq) > 1 else [1100]
+    plan, c, where, ref, factor = attention_case(sn, lq, lk, 4, 2, 32, dtype, False, True, "plain", seed=60)
+    where["keep"][lk[0] - 1:lk[0] + 1] = True
+    at = lq[0] - 1 if name == "q" else lk[0] - 1
+    c[name][at, 1, 3] = float("nan")
+    clean = {n: c[n] if n not in ("k", "v") else torch.where(where["keep"][:, None, None], c[n], torch.zeros_like(c[n])) for n in c}
+    ref, factor = R.attention(clean["q"], clean["k"], clean["v"], plan.q_ptr.cpu().numpy(), plan.k_ptr.cpu().numpy(), plan.scale,
+                              keep=where["keep"], d_o=c["d_o"])
+    got = attention_run(sn, plan, c, where)
+    for n, g in got.items():
+        value, mag = ref["o" if n == "served" else n]
+        bad = torch.isnan(value)
+        assert torch.equal(torch.isnan(g.cpu()), bad), n
+        fine = torch.where(bad, torch.zeros_like(value), value), torch.where(bad, torch.zeros_like(mag), mag)
+        R.check(n, torch.where(bad.cuda(), torch.zeros_like(g), g), fine, factor, dtype == "bfloat16" and n != "lse")
+
+
 THRESHOLDS = {"one": [], "two": [0], "equal": [-3, -3, 0, 0, 5], "wide": [-1000, -40, 0, 40, 1046],
               "many": list(range(-31, 32)), "far": [2 ** 31 - 9, 2 ** 31 - 1], "low": [-2 ** 31, -2 ** 31 + 3]}
 
@@ -316,6 +367,19 @@ def test_norm_matches_the_reference(sn, shape, act, dtype):
 def test_norm_layouts_without_parameters(sn, shape, layout, dtype):
     print(f"[norm] {shape} {layout} {dtype}", flush=True)
     plan, *args, ref, factor = norm_case(sn, *shape, "silu", dtype, layout=layout, affine=False, seed=4)
+    norm_check(norm_run(sn, plan, *args), ref, factor, dtype)
+
+
+# groups wider than a block's vectors, whole and with short last pieces, and many short segments
+WIDE = [([40, 3], 8192, 1), ([700], 4096, 1), ([30, 0, 9], 6000, 2), ([7], 65536, 1), ([300, 2], 1500, 1), ([1] * 300, 16, 4)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("layout", ["plain", "odd"])
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: f"{len(s[0])}x{max(s[0])}x{s[1]}x{s[2]}")
+def test_norm_wide_groups(sn, shape, layout, dtype):
+    print(f"[norm] wide {shape[1:]} {layout} {dtype}", flush=True)
+    plan, *args, ref, factor = norm_case(sn, *shape, "ssp", dtype, layout=layout, seed=9)
     norm_check(norm_run(sn, plan, *args), ref, factor, dtype)
 
 
