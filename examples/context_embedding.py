@@ -44,15 +44,15 @@ class GroupNormFn(torch.autograd.Function):
 class CrossAttentionFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, bias, plan, ws, q_pos, k_pos):
-        o, (_, lse) = sn.cross_attention_forward(plan, q, k, v, ws, bias=bias, q_pos=q_pos, k_pos=k_pos, save=True)
-        ctx.save_for_backward(q, k, v, bias, o, lse)
+        o, saved = sn.cross_attention_forward(plan, q, k, v, ws, bias=bias, q_pos=q_pos, k_pos=k_pos, save=True)
+        ctx.save_for_backward(q, k, v, bias, *saved)
         ctx.plan, ctx.ws, ctx.pos = plan, ws, {"q_pos": q_pos, "k_pos": k_pos}
         return o
 
     @staticmethod
     def backward(ctx, d_o):
-        q, k, v, bias, o, lse = ctx.saved_tensors
-        grads = sn.cross_attention_backward(ctx.plan, q, k, v, (o, lse), d_o, ctx.ws, bias=bias, **ctx.pos)
+        q, k, v, bias, *saved = ctx.saved_tensors
+        grads = sn.cross_attention_backward(ctx.plan, q, k, v, saved, d_o, ctx.ws, bias=bias, **ctx.pos)
         return (*grads, None, None, None, None)
 
 

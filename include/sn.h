@@ -364,16 +364,22 @@ sn_status sn_relative_thresholds(int32_t n_buckets, int32_t max_distance, int32_
  * `op` is read).  0 for a descriptor that they would refuse for its sizes. */
 size_t sn_cross_attention_workspace_bytes(const sn_cross_attention *op);
 
-/* o [n_q][H][D] (op->dtype); for the backward pass (may be NULL)
- * lse [n_q][H], the logarithm of the sum of exp(s). */
+/* o [n_q][H][D] (op->dtype); lse [n_q][H] (may be NULL), the logarithm of
+ * the sum of exp(s). */
 sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *lse, void *ws, size_t ws_bytes,
                                      void *stream);
 
-/* Gradients of the forward's o from that o, its lse and d_o
+/* The same with a backward pass to come: also rows, o before its rounding in
+ * fp32 (SN_F32: o is that, and rows may be NULL).  SN_BF16: its o is the
+ * nearer one, the weights of the values keep 16 bits here and 8 above. */
+sn_status sn_cross_attention_forward_train(const sn_cross_attention *op, void *o, float *rows, float *lse, void *ws,
+                                           size_t ws_bytes, void *stream);
+
+/* Gradients of the forward's o from its rows (SN_F32: its o), lse and d_o
  * [n_q][H][D]: dq [n_q][H][D], dk and dv [n_k][n_kv_heads][D] (op->dtype;
  * shared heads summed), dbias [H][n_buckets] (fp32, NULL without bias).
  * d_o holds finite values. */
-sn_status sn_cross_attention_backward(const sn_cross_attention *op, const void *o, const float *lse, const void *d_o,
+sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float *rows, const float *lse, const void *d_o,
                                       int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk, void *dv,
                                       float *dbias, void *ws, size_t ws_bytes, void *stream);
 

@@ -41,7 +41,7 @@ EXPORTED = (
     "sn_filter_forward", "sn_read_status", "sn_profile_enable", "sn_profile_classes", "sn_profile_name",
     "sn_profile_collect", "sn_energy_forces_static",
     "sn_relative_thresholds", "sn_cross_attention_workspace_bytes", "sn_cross_attention_forward",
-    "sn_cross_attention_backward", "sn_group_norm_workspace_bytes", "sn_group_norm_forward",
+    "sn_cross_attention_forward_train", "sn_cross_attention_backward", "sn_group_norm_workspace_bytes", "sn_group_norm_forward",
     "sn_group_norm_backward",
 )
 SN_STATIC_SCRATCH_BYTES = 64 << 20
@@ -125,6 +125,7 @@ def lib() -> ctypes.CDLL:
         "sn_relative_thresholds": (i32, [i32, i32, vp]),
         "sn_cross_attention_workspace_bytes": (sz, [vp]),
         "sn_cross_attention_forward": (i32, [vp, vp, vp, vp, sz, vp]),
+        "sn_cross_attention_forward_train": (i32, [vp, vp, vp, vp, vp, sz, vp]),
         "sn_cross_attention_backward": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
         "sn_group_norm_workspace_bytes": (sz, [vp]),
         "sn_group_norm_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
@@ -521,17 +522,24 @@ def cross_attention_workspace(plan: CrossAttention):
 
 def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=None, k_pos=None, keep=None,
                             save: bool = False, stream=None):
-    """sn_cross_attention_forward -> o [n_q, H, D]; with save=True -> (o, saved), saved = (o, lse) for the
-    backward pass.  q [n_q, H, D], k and v [n_k, Hkv, D]; bias float32 [H, n_buckets]; q_pos [n_q] and k_pos
-    [n_k] int32 (default: the index in the segment); keep bool [n_k], False: the key is absent."""
+    """sn_cross_attention_forward -> o [n_q, H, D]; with save=True -> (o, saved), saved = (o before its rounding, lse)
+    for the backward pass (sn_cross_attention_forward_train).  q [n_q, H, D], k and v [n_k, Hkv, D]; bias float32
+    [H, n_buckets]; q_pos [n_q] and k_pos [n_k] int32 (default: the index in the segment); keep bool [n_k], False:
+    the key is absent."""
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device) if save else None
-    st = lib().sn_cross_attention_forward(op, o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                                          _launch_stream(plan, stream, o, lse))
-    _check(st, "sn_cross_attention_forward")
-    return (o, (o, lse)) if save else o
+    if not save:
+        st = lib().sn_cross_attention_forward(op, o.data_ptr(), None, ws.data_ptr(), ws.numel(),
+                                              _launch_stream(plan, stream, o))
+        _check(st, "sn_cross_attention_forward")
+        return o
+    lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device)
+    rows = o if plan.dtype == torch.float32 else torch.empty(plan.q_shape, dtype=torch.float32, device=plan.device)
+    st = lib().sn_cross_attention_forward_train(op, o.data_ptr(), rows.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                                ws.numel(), _launch_stream(plan, stream, o, rows, lse))
+    _check(st, "sn_cross_attention_forward_train")
+    return o, (rows, lse)
 
 
 def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias=None, q_pos=None, k_pos=None,
@@ -540,14 +548,14 @@ def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias
     dbias is None without a bias.  The other arguments are the forward's."""
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
-    o, lse = saved
+    rows, lse = saved
     gs, gh, _ = _rows(d_o, "d_o", plan.q_shape, plan.dtype, plan.device)
     dq = torch.empty_like(q, memory_format=torch.contiguous_format)
     dk = torch.empty_like(k, memory_format=torch.contiguous_format)
     dv = torch.empty_like(v, memory_format=torch.contiguous_format)
     dbias = None if bias is None else torch.empty_like(bias)
     st = lib().sn_cross_attention_backward(
-        op, _flat(o, "saved[0]", plan.q_shape, (plan.dtype,), plan.device),
+        op, _flat(rows, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
         _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), d_o.data_ptr(), gs, gh,
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(),
         _launch_stream(plan, stream, dq, dk, dv, dbias))

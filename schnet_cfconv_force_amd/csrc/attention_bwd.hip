@@ -9,10 +9,11 @@
 // one order, so there are no atomics and the bits repeat.  Shared heads are
 // further rows of the second pass and sum there.
 //
-// delta starts as dO_i.o_i from the rounded o.  What that (and the forward's
-// 16-bit p) leaves is exactly what the row's dS fails to sum to zero by:
+// delta starts as dO_i.o_i of the unrounded o.  What that and the forward's
+// roundings leave is exactly what the row's dS fails to sum to zero by:
 // e_i = sum_j dS_ij, as sum_j p_ij = 1.  The second pass takes delta + e; the
-// bias sums, which are fp32 whatever the rows are, are taken there.
+// bias sums, which are fp32 whatever the rows are, are taken there.  A single
+// key has p = 1 whatever its score: its dS is zero, not what rounding leaves.
 #include <algorithm>
 
 #include "attention.h"
@@ -20,18 +21,21 @@
 namespace sn {
 namespace {
 
-// p and dS are carried times 2^24 and the factor is taken out of the
+// p and dS are carried times 2^12 and the factor is taken out of the
 // finished sums: exp flushes what is below 2^-126 to zero, which moves the
-// smallest p that counts to 2^-150 (a key that no row attends to has
-// gradients of that size, and they are still right).
-constexpr float kLift = 24.0f;
-constexpr float kUnlift = 1.0f / 16777216.0f;
+// smallest p that counts to 2^-138 (a key that no row attends to has
+// gradients of that size, and they are still right).  The factor is part of
+// exp's argument, whose rounding is the largest error of an fp32 p: 12 is
+// about what p = 1/length needs to leave it near zero (2^24 doubled the error
+// of the gradients).
+constexpr float kLift = 12.0f;
+constexpr float kUnlift = 1.0f / 4096.0f;
 
 struct BwdArgs {
-    const void *o;
+    const float *o;     // before its rounding
     const float *lse;
     void *dq, *dk, *dv;
-    float2 *row;        // [n_q H] {lse log2e - 24 (+inf: no key), delta}
+    float2 *row;        // [n_q H] {lse log2e - 12 (+inf: no key), delta}
     float *part_bias;   // [Hkv][B key_tiles splits][G nb]
     float *part_kv;     // [split][n_k Hkv][2][D] (splits > 1)
 };
@@ -96,21 +100,26 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
     const int64_t at = (int64_t)row * a.H + w.h0 + hg;
     const bool active = __any(row >= 0);
     const float c = fabsf(a.scale) * kLog2e;
-    Raw8<NP> rq[DP / 16], rg[DP / 16], ro[DP / 16];
+    Raw8<NP> rq[DP / 16], rg[DP / 16];
+    Raw8<3> ro[DP / 16];
     if (n_tiles > 0) load(0);
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) rq[s] = rg[s] = ro[s] = raw_zero<NP>();
+    for (int s = 0; s < DP / 16; ++s) {
+        rq[s] = rg[s] = raw_zero<NP>();
+        ro[s] = raw_zero<3>();
+    }
     int pos = 0;
     float lse = -INFINITY;
     if (row >= 0) {
         const T *pq = (const T *)a.q + row * a.qs + (w.h0 + hg) * a.qh;
-        const T *pg = (const T *)a.d_o + row * a.gs + (w.h0 + hg) * a.gh, *po = (const T *)g.o + at * a.D;
+        const T *pg = (const T *)a.d_o + row * a.gs + (w.h0 + hg) * a.gh;
+        const float *po = g.o + at * a.D;
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s) {
             const int d = 16 * s + 8 * half;
             rq[s] = load8<NP>(pq + d, d, a.D, FAST);
             rg[s] = load8<NP>(pg + d, d, a.D, FAST);
-            ro[s] = load8<NP>(po + d, d, a.D, FAST);
+            ro[s] = load8<3>(po + d, d, a.D, FAST);
         }
         pos = a.q_pos ? a.q_pos[row] : qi;
         lse = g.lse[at];
@@ -125,20 +134,18 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
         if (a.scale < 0.0f)
 #pragma unroll
             for (int n = 0; n < NP; ++n) q[s].p[n] = -q[s].p[n];
-        const Frag<NP> fo = to_frag<NP>(ro[s]);
+        const float y[8] = {ro[s].v[0].x, ro[s].v[0].y, ro[s].v[0].z, ro[s].v[0].w,
+                            ro[s].v[1].x, ro[s].v[1].y, ro[s].v[1].z, ro[s].v[1].w};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float x = 0.0f, y = 0.0f;
+            float x = 0.0f;
 #pragma unroll
-            for (int n = NP - 1; n >= 0; --n) {
-                x += (float)dO[s].p[n][j];
-                y += (float)fo.p[n][j];
-            }
-            delta = fmaf(x, y, delta);
+            for (int n = NP - 1; n >= 0; --n) x += (float)dO[s].p[n][j];
+            delta = fmaf(x, y[j], delta);
         }
     }
     delta = half_sum(delta);
-    const float L = lse == -INFINITY ? INFINITY : lse * kLog2e - kLift;
+    const float L = lse == -INFINITY ? INFINITY : fmaf(lse, kLog2e, -kLift);
     const int pos_lo = wave_min(row >= 0 ? pos : 0x7fffffff), pos_hi = wave_max(row >= 0 ? pos : (int)0x80000000);
 
     floatx16 dq[DP / 32];
@@ -231,17 +238,17 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
         if (t + 2 < n_tiles) load(t + 2);
         __syncthreads();
     }
-    // the row's sum of dS in units of p (sum_j p_ij is 2^24 by construction)
+    // the row's sum of dS in units of p (sum_j p_ij is 2^12 by construction)
     const float err = half_sum(row_ds) * kUnlift;
     if (row >= 0) {
         T *out = (T *)g.dq + at * a.D;
+        const float f = w.nk == 1 ? 0.0f : a.scale * kUnlift;
 #pragma unroll
         for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 write4<T>(out, 32 * e + 8 * i + 4 * half, a.D,
-                          floatx4{dq[e][4 * i], dq[e][4 * i + 1], dq[e][4 * i + 2], dq[e][4 * i + 3]} *
-                              (a.scale * kUnlift));
+                          floatx4{dq[e][4 * i], dq[e][4 * i + 1], dq[e][4 * i + 2], dq[e][4 * i + 3]} * f);
         if (half == 0) g.row[at] = make_float2(L, delta + err);
     }
 }
@@ -472,7 +479,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             }
             s += __shfl_xor(s, 1, 64);
             s += __shfl_xor(s, 2, 64);
-            if (q == 0) part[head * a.nb + bk] = s;
+            if (q == 0) part[head * a.nb + bk] = nk == 1 ? 0.0f : s;
         }
         __syncthreads();
     };
@@ -621,7 +628,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
     if (a.nb && head >= 0) finish_head();
     if (!have) return;
     const int64_t at = (int64_t)(k0 + j) * a.Hkv + hk;
-    const float fk = a.scale * kUnlift;
+    const float fk = nk == 1 ? 0.0f : a.scale * kUnlift;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
@@ -740,7 +747,7 @@ size_t attn_backward_workspace(const sn_cross_attention &op) {
     return need;
 }
 
-sn_status attn_backward(AttnArgs a, int dtype, const void *o, const float *lse, void *dq, void *dk, void *dv,
+sn_status attn_backward(AttnArgs a, int dtype, const float *o, const float *lse, void *dq, void *dk, void *dv,
                         float *dbias, char *ws, hipStream_t s) {
     ProfScope prof(K_ATTN_BWD, s);
     const BwdPlan p = bwd_plan(a.B, a.Hkv, a.G, a.max_q, a.max_k, a.lut_n);

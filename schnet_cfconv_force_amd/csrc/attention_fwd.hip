@@ -20,13 +20,15 @@ namespace {
 
 struct FwdOut {
     void *o;
+    float *rows;        // o before its rounding, for the backward pass (bf16; or null)
     float *lse;
     float *part_o;      // [split][n_q H][D] unnormalised rows (splits > 1)
     float2 *part_ml;    // [split][n_q H] their maximum (log2) and sum
 };
 
-// What a wavefront keeps of its 32 rows (a lane: row lane % 32).
-template <int NP, int DP, bool FAST>
+// What a wavefront keeps of its 32 rows (a lane: row lane % 32).  PP: planes
+// of p; see the product with v.
+template <int NP, int PP, int DP, bool FAST>
 struct RowState {
     Frag<NP> q[DP / 16];
     floatx16 o[DP / 32];
@@ -164,13 +166,18 @@ struct RowState {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = s[u][8 * t + j];
                 // bf16 rows: p is rounded to 8 bits here, at most 2^-8 of each
-                // term of O, as much as rounding o itself costs
-                const Frag<NP> p = split8f<NP>(x);
+                // term of O, as much as rounding o itself costs.  With a
+                // backward pass to come it keeps 16: an error of O is one of
+                // delta, which dq has no other sum to correct by (rows of few
+                // keys: dq 2.4 times as far off as its rounding, now 1.4)
+                const Frag<PP> p = split8f<PP>(x);
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e) {
-                    if constexpr (NP == 1)
+                    if constexpr (NP == 1) {
+                        if constexpr (PP == 2)
+                            o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u].f[t][e], p.p[1], o[e], 0, 0, 0);
                         o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u].f[t][e], p.p[0], o[e], 0, 0, 0);
-                    else
+                    } else
                         o[e] = mma<NP>(frag_cols<NP, DP>(tl, vt, kPlane, 32 * u + 16 * t, e), p, o[e]);
                 }
             }
@@ -192,6 +199,10 @@ __device__ inline void write_row4(const AttnArgs &a, const FwdOut &out, int spli
     }
     T *o = (T *)out.o + at * a.D;
     v *= inv;
+    if (NP == 1 && out.rows)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d + i < a.D) out.rows[at * a.D + d + i] = v[i];
     if (a.D % 4 == 0) {   // rows are then aligned for four elements
         if (d >= a.D) return;
         if constexpr (NP == 1)
@@ -226,7 +237,7 @@ constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
 
 // Many rows: each wavefront owns 32 of the block's 128 rows and all of them
 // read the same key tiles, staged in LDS while the tile before is computed.
-template <int NP, int DP, int KT, bool FAST>
+template <int NP, int PP, int DP, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * KT * DP;
@@ -264,7 +275,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
     };
     // the first tile, the rows and the bias are on their way together
     uint64_t mask = 0;
-    RowState<NP, DP, FAST> st;
+    RowState<NP, PP, DP, FAST> st;
     Raw8<NP> raw[DP / 16];
     if (t0 < t1) load(t0);
     st.begin(a, w, w.tile * 128 + wave * 32, lane, raw);
@@ -298,7 +309,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
 // holds all of them and takes every NW-th tile of 32 keys, with tiles of its
 // own in LDS, so no wavefront waits for another until the rows are joined at
 // the end.  The keys and values are read once, and that is what bounds it.
-template <int NP, int DP, int NW, bool FAST>
+template <int NP, int PP, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * 32 * DP;
@@ -330,7 +341,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
         kl.load(a, w, t * 32, a.nb, lane);
     };
     if (t < t1) load(t);
-    RowState<NP, DP, FAST> st;
+    RowState<NP, PP, DP, FAST> st;
     Raw8<NP> raw[DP / 16];
     st.begin(a, w, w.tile * 32, lane, raw);
     if (a.nb) fill_lut(a, w, lut);
@@ -407,6 +418,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, FwdOut out) 
         const int d = lane + 64 * u;
         if (d >= a.D) continue;
         ((T *)out.o)[at * a.D + d] = (T)(acc[u] * inv);
+        if (NP == 1 && out.rows) out.rows[at * a.D + d] = acc[u] * inv;
     }
     if (lane == 0 && out.lse) out.lse[at] = log_sum(m, l);
 }
@@ -429,15 +441,15 @@ FwdPlan fwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
     return p;
 }
 
-template <int NP, int DP, bool FAST>
+template <int NP, int PP, int DP, bool FAST>
 sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
     const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
     constexpr int NW = NP * DP <= 96 ? 8 : NP * DP <= 192 ? 4 : 2;   // 160 KB of LDS hold their tiles
     const size_t lut = a.nb ? (size_t)a.Gs * (a.lut_n + 2 * kLutPad) * sizeof(float) : 0;
     if (few)
-        attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);
+        attn_few_kernel<NP, PP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);
     else
-        attn_rows_kernel<NP, DP, kRowKeys<NP, DP>, FAST><<<grid, kAttnThreads, lut, s>>>(a, out);
+        attn_rows_kernel<NP, PP, DP, kRowKeys<NP, DP>, FAST><<<grid, kAttnThreads, lut, s>>>(a, out);
     SN_TRY(launch_status());
     if (a.splits > 1) {
         attn_join_kernel<NP><<<(int)(((int64_t)a.n_q * a.H + 3) / 4), 256, 0, s>>>(a, out);
@@ -446,11 +458,11 @@ sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) 
     return SN_OK;
 }
 
-template <int NP, bool FAST>
+template <int NP, int PP, bool FAST>
 sn_status launch_dim(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
-    if (a.D <= 32) return launch<NP, 32, FAST>(a, out, few, s);
-    if (a.D <= 64) return launch<NP, 64, FAST>(a, out, few, s);
-    return launch<NP, 128, FAST>(a, out, few, s);
+    if (a.D <= 32) return launch<NP, PP, 32, FAST>(a, out, few, s);
+    if (a.D <= 64) return launch<NP, PP, 64, FAST>(a, out, few, s);
+    return launch<NP, PP, 128, FAST>(a, out, few, s);
 }
 
 }  // namespace
@@ -466,19 +478,19 @@ size_t attn_forward_workspace(const sn_cross_attention &op) {
     return kWsBase + align256(rows * splits * sizeof(float2)) + align256(rows * splits * op.head_dim * sizeof(float));
 }
 
-sn_status attn_forward(AttnArgs a, int dtype, void *o, float *lse, char *ws, hipStream_t s) {
+sn_status attn_forward(AttnArgs a, int dtype, void *o, float *rows, float *lse, char *ws, hipStream_t s) {
     ProfScope prof(K_ATTN_FWD, s);
     const FwdPlan p = fwd_plan(a.B, a.Hkv, a.G, a.max_q, a.max_k, a.lut_n);
     a.Gs = p.Gs; a.subs = p.subs; a.row_tiles = p.row_tiles; a.splits = p.splits;
-    const size_t rows = (size_t)a.n_q * a.H;
-    FwdOut out{o, lse, nullptr, nullptr};
+    const size_t n = (size_t)a.n_q * a.H;
+    FwdOut out{o, dtype == SN_BF16 ? rows : nullptr, lse, nullptr, nullptr};
     if (p.splits > 1) {
         out.part_ml = reinterpret_cast<float2 *>(ws + kWsBase);
-        out.part_o = reinterpret_cast<float *>(ws + kWsBase + align256(rows * p.splits * sizeof(float2)));
+        out.part_o = reinterpret_cast<float *>(ws + kWsBase + align256(n * p.splits * sizeof(float2)));
     }
-    if (a.fast)
-        return dtype == SN_F32 ? launch_dim<3, true>(a, out, p.few, s) : launch_dim<1, true>(a, out, p.few, s);
-    return dtype == SN_F32 ? launch_dim<3, false>(a, out, p.few, s) : launch_dim<1, false>(a, out, p.few, s);
+    if (dtype == SN_F32) return a.fast ? launch_dim<3, 3, true>(a, out, p.few, s) : launch_dim<3, 3, false>(a, out, p.few, s);
+    if (out.rows) return a.fast ? launch_dim<1, 2, true>(a, out, p.few, s) : launch_dim<1, 2, false>(a, out, p.few, s);
+    return a.fast ? launch_dim<1, 1, true>(a, out, p.few, s) : launch_dim<1, 1, false>(a, out, p.few, s);
 }
 
 }  // namespace sn

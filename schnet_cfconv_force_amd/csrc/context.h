@@ -62,8 +62,8 @@ struct AttnArgs {
 
 size_t attn_forward_workspace(const sn_cross_attention &op);
 size_t attn_backward_workspace(const sn_cross_attention &op);
-sn_status attn_forward(AttnArgs a, int dtype, void *o, float *lse, char *ws, hipStream_t s);
-sn_status attn_backward(AttnArgs a, int dtype, const void *o, const float *lse, void *dq, void *dk, void *dv,
+sn_status attn_forward(AttnArgs a, int dtype, void *o, float *rows, float *lse, char *ws, hipStream_t s);
+sn_status attn_backward(AttnArgs a, int dtype, const float *o, const float *lse, void *dq, void *dk, void *dv,
                         float *dbias, char *ws, hipStream_t s);
 
 // --------------------------------------------------------------- group norm

@@ -119,6 +119,16 @@ sn_status check_norm(const sn_group_norm *op) {
     return SN_OK;
 }
 
+sn_status attn_forward_checked(const sn_cross_attention *op, void *o, float *rows, float *lse, void *ws, size_t ws_bytes,
+                               void *stream) {
+    SN_TRY(check_attn(op));
+    SN_TRY(check_ctx_ws(ws, ws_bytes, attn_workspace(*op)));
+    if (op->n_q == 0) return SN_OK;
+    if (!o || !aligned_for(o, op->dtype)) return SN_ERR_INVALID;
+    return attn_forward(attn_args(*op, ws), op->dtype, o, rows, lse, static_cast<char *>(ws),
+                        reinterpret_cast<hipStream_t>(stream));
+}
+
 NormArgs norm_args(const sn_group_norm &op, void *ws) {
     NormArgs a{};
     a.B = op.n_segments; a.n_rows = op.n_rows; a.max_rows = op.max_rows;
@@ -158,31 +168,33 @@ size_t sn_cross_attention_workspace_bytes(const sn_cross_attention *op) {
 
 sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, float *lse, void *ws, size_t ws_bytes,
                                      void *stream) {
-    SN_TRY(check_attn(op));
-    SN_TRY(check_ctx_ws(ws, ws_bytes, attn_workspace(*op)));
-    if (op->n_q == 0) return SN_OK;
-    if (!o || !aligned_for(o, op->dtype)) return SN_ERR_INVALID;
-    return attn_forward(attn_args(*op, ws), op->dtype, o, lse, static_cast<char *>(ws),
-                        reinterpret_cast<hipStream_t>(stream));
+    return attn_forward_checked(op, o, nullptr, lse, ws, ws_bytes, stream);
 }
 
-sn_status sn_cross_attention_backward(const sn_cross_attention *op, const void *o, const float *lse, const void *d_o,
+sn_status sn_cross_attention_forward_train(const sn_cross_attention *op, void *o, float *rows, float *lse, void *ws,
+                                           size_t ws_bytes, void *stream) {
+    SN_TRY(check_attn(op));
+    if (op->n_q > 0 && (!lse || (op->dtype == SN_BF16 && !rows) || !aligned_for(rows, SN_F32))) return SN_ERR_INVALID;
+    return attn_forward_checked(op, o, rows, lse, ws, ws_bytes, stream);
+}
+
+sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float *rows, const float *lse, const void *d_o,
                                       int64_t d_o_stride, int64_t d_o_head_stride, void *dq, void *dk, void *dv,
                                       float *dbias, void *ws, size_t ws_bytes, void *stream) {
     SN_TRY(check_attn(op));
     SN_TRY(check_ctx_ws(ws, ws_bytes, attn_workspace(*op)));
-    if (op->n_q > 0 && (!o || !lse || !d_o || !dq)) return SN_ERR_INVALID;
+    if (op->n_q > 0 && (!rows || !lse || !d_o || !dq)) return SN_ERR_INVALID;
     if (op->n_k > 0 && (!dk || !dv)) return SN_ERR_INVALID;
     if (op->bias && !dbias) return SN_ERR_INVALID;
-    if (!aligned_for(o, op->dtype) || !aligned_for(d_o, op->dtype) || !aligned_for(dq, op->dtype) || !aligned_for(dk, op->dtype) ||
-        !aligned_for(dv, op->dtype))
+    if (!aligned_for(rows, SN_F32) || !aligned_for(d_o, op->dtype) || !aligned_for(dq, op->dtype) ||
+        !aligned_for(dk, op->dtype) || !aligned_for(dv, op->dtype))
         return SN_ERR_INVALID;
     AttnArgs a = attn_args(*op, ws);
     a.d_o = d_o;
     a.gs = d_o_stride;
     a.gh = d_o_head_stride;
-    a.fast = a.fast && rows_fast(*op, d_o, d_o_stride, d_o_head_stride) && (reinterpret_cast<uintptr_t>(o) & 15) == 0;
-    return attn_backward(a, op->dtype, o, lse, dq, dk, dv, op->bias ? dbias : nullptr, static_cast<char *>(ws),
+    a.fast = a.fast && rows_fast(*op, d_o, d_o_stride, d_o_head_stride) && (reinterpret_cast<uintptr_t>(rows) & 15) == 0;
+    return attn_backward(a, op->dtype, rows, lse, dq, dk, dv, op->bias ? dbias : nullptr, static_cast<char *>(ws),
                          reinterpret_cast<hipStream_t>(stream));
 }
 

@@ -356,6 +356,8 @@ __device__ inline void dz_xh(const Vec<T, V> &x, const Vec<T, V> &dy, float mu, 
 template <typename T, int V, int ACT>
 __device__ inline void write_dx(const Vec<T, V> &x, const Vec<T, V> &dy, float mu, float r, float m1,
                                 float m2, const float (&ga)[V], const float (&be)[V], T *p) {
+    // dz gamma rounded as it is in the mean: a group of one element gives 0
+#pragma clang fp contract(off)
     float dz[V], xh[V];
     dz_xh<T, V, ACT>(x, dy, mu, r, ga, be, dz, xh);
 #pragma unroll

@@ -221,3 +221,14 @@ def test_reference_norm_gradients_match_differences(act):
         ends = [(run(**{name: args[name] + s * h * e})["y"][0] * dy).sum() for s in (1, -1)]
         value, mag = ref["d" + name]
         assert abs(float(ends[0] - ends[1]) / (2 * h) - float((value * e).sum())) <= 1e-7 * float((mag * e.abs()).sum())
+
+
+def test_training_forward_needs_what_the_backward_reads():
+    sn = _sn()
+    lib, S = sn.lib(), sn.binding.SnCrossAttention
+    for dtype, rows, lse, n_q, want in ((sn.SN_BF16, None, 256, 6, sn.SN_ERR_INVALID), (sn.SN_BF16, 256, None, 6, sn.SN_ERR_INVALID),
+                                        (sn.SN_F32, None, None, 6, sn.SN_ERR_INVALID), (sn.SN_BF16, 258, 256, 6, sn.SN_ERR_INVALID),
+                                        (sn.SN_BF16, None, None, 0, sn.SN_OK)):
+        d = S(2, n_q, 9, min(n_q, 4), 5, 256, 256, 4, 2, 32, dtype, 0.5, 256, 256, 256, 128, 32, 64, 32, 64, 32)
+        got = lib.sn_cross_attention_forward_train(ctypes.byref(d), 256, rows, lse, 256, 1 << 40, None)
+        assert got == want, (dtype, rows, lse, n_q)

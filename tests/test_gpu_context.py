@@ -280,6 +280,20 @@ def test_attention_flags_contradicting_pointers(sn, few):
     assert sn.read_status(ws) == sn.SN_ERR_INVALID
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lq", [[3, 1], [200, 77]], ids=str)
+def test_attention_of_a_single_key_has_no_score_gradient(sn, lq, dtype):
+    """Whatever its score, the only key has the weight one: o is its value, dq, dk and dbias are zeros."""
+    import torch
+    print(f"[attention] single keys {lq} {dtype}", flush=True)
+    plan, c, where, ref, factor = attention_case(sn, lq, [1, 1], 4, 2, 40, dtype, True, False, "plain", seed=61, spread=20.0)
+    got = attention_run(sn, plan, c, where)
+    R.check("dv", got["dv"], ref["dv"], factor, dtype == "bfloat16")
+    R.check("o", got["o"], ref["o"], factor, dtype == "bfloat16")
+    for name in ("dq", "dk", "dbias"):
+        assert not bool(got[name].any()), name
+
+
 def test_attention_gradient_matches_differences(sn):
     """Along a random direction, (L(x + h e) - L(x - h e)) / 2h of L = sum(o d_o) against <grad, e>.  With h = 2^-5
     the third-order term is below h^2 = 1e-3 of the magnitudes, the fp32 noise far below."""
@@ -400,6 +414,14 @@ def test_norm_constant_rows_give_beta(sn, rows_):
     beta = torch.arange(32, dtype=torch.float32, device="cuda")
     got = norm_run(sn, plan, x, None, beta, torch.ones_like(x))
     assert torch.equal(got["y"], beta.expand(rows_, 32)) and bool(torch.isfinite(got["dx"]).all())
+
+
+def test_norm_of_single_elements_has_no_gradient(sn):
+    """A group of one element is beta whatever x is."""
+    import torch
+    print("[norm] single elements", flush=True)
+    plan, x, gamma, beta, dy, ref, factor = norm_case(sn, [1, 1, 1], 24, 24, "silu", "float32", seed=10)
+    assert not bool(norm_run(sn, plan, x, gamma, beta, dy)["dx"].any())
 
 
 def test_norm_repeats_bit_for_bit_on_any_stream_and_in_a_graph(sn):
