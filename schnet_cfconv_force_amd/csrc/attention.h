@@ -61,9 +61,16 @@ __device__ inline Frag<NP> split8f(const float (&x)[8]) {
     return f;
 }
 
-template <int NP>
+// SWAPPED: the order of mma(b, a), so that a product and its transpose agree.
+template <int NP, bool SWAPPED = false>
 __device__ inline floatx16 mma(const Frag<NP> &a, const Frag<NP> &b, floatx16 c) {
-    if constexpr (NP == 3) {   // the small terms first
+    if constexpr (NP == 3 && SWAPPED) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+    } else if constexpr (NP == 3) {   // the small terms first
         c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
         c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
         c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
@@ -173,6 +180,7 @@ struct RowsProduct {
 #pragma unroll
             for (int s = 0; s < DP / 16; ++s) f[s] = l.frag_rows(tile, row0, s);
     }
+    template <bool SWAPPED = false>
     __device__ inline floatx16 finish(const TileLane<DP> &l, uint32_t tile, uint32_t plane, int row0,
                                       const Frag<NP> (&b)[DP / 16]) const {
         floatx16 x = zero16();
@@ -181,7 +189,7 @@ struct RowsProduct {
             if constexpr (NP == 1)
                 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[s], b[s].p[0], x, 0, 0, 0);
             else
-                x = mma<NP>(frag_rows<NP, DP>(l, tile, plane, row0, s), b[s], x);
+                x = mma<NP, SWAPPED>(frag_rows<NP, DP>(l, tile, plane, row0, s), b[s], x);
         }
         return x;
     }

@@ -12,8 +12,12 @@
 // delta starts as dO_i.o_i of the unrounded o.  What that and the forward's
 // roundings leave is exactly what the row's dS fails to sum to zero by:
 // e_i = sum_j dS_ij, as sum_j p_ij = 1.  The second pass takes delta + e; the
-// bias sums, which are fp32 whatever the rows are, are taken there.  A single
-// key has p = 1 whatever its score: its dS is zero, not what rounding leaves.
+// bias sums, which are fp32 whatever the rows are, are taken there.  For that
+// both passes round alike: the scores' products in one order, the exponents as
+// s scale + (bias - lse), whichever way a tile's bias is read, and
+// sums over many rows are joined pairwise (fp32, 1272 rows of 16 keys: dbias
+// 2.0e-6 of its norm off without the two, 2.9e-7 with them).  A single key has
+// p = 1 whatever its score: its dS is zero, not what rounding leaves.
 #include <algorithm>
 
 #include "attention.h"
@@ -45,6 +49,18 @@ struct BwdArgs {
 // 2048, heads of 64: 302 -> 288 us for the training step).
 template <int NP, int DP>
 constexpr int kDqTile = NP * DP <= 96 ? 64 : 32;
+
+// Pairwise: sums over thousands of rows that cancel keep their digits.
+__device__ inline float tree_sum(const floatx16 &x) {
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = x[i] + x[i + 8];
+#pragma unroll
+    for (int n = 4; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i) s[i] += s[i + n];
+    return s[0];
+}
 
 template <typename T>
 __device__ inline void write4(T *row, int d, int D, floatx4 v) {
@@ -164,7 +180,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
         const uint32_t kt = lds0 + 2 * buf * kBytes, vt = kt + kBytes;
         const KeyInfo<kDqKeys> &ki = info[buf];
         if (active && mask) {
-            float mul = c, less = -L;
+            float less = -L;
             const float *mine = lut + hg * lut_stride(a);
             PosRange keys{};
             bool table = false;
@@ -181,8 +197,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
                     keys = uniform_range(range);
                     const int first = lut_index(a, offset_of(keys.lo, pos_hi)), last = lut_index(a, offset_of(keys.hi, pos_lo));
                     table = first != last;
-                    if (table) mul = 1.0f;
-                    else less += mine[kLutPad + first];
+                    if (!table) less += mine[kLutPad + first];
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 floatx16 s = rs.finish(tl, kt, kPlane, 32 * sub, q), dp = rd.finish(tl, vt, kPlane, 32 * sub, dO);
@@ -197,25 +212,27 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
                     if (a.lut_run && keys.run) {
                         const float *at = mine + run_index(a, offset_of(keys.first, pos)) + 4 * half + 32 * sub;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, at[8 * (i / 4) + i % 4]);
+                        for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, at[8 * (i / 4) + i % 4] + less);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int e = lut_index(a, offset_of(ki.pos[32 * sub + 8 * (i / 4) + 4 * half + i % 4], pos));
-                            s[i] = fmaf(s[i], c, mine[kLutPad + e]);
+                            s[i] = fmaf(s[i], c, mine[kLutPad + e] + less);
                         }
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, less);
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], mul, less)) * (dp[i] - delta);
+                for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i]) * (dp[i] - delta);
                 if (sub_mask != 0xffffffffu) {
                     const uint32_t kept = sub_mask >> (4 * half);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (!((kept >> (8 * (i / 4) + i % 4)) & 1)) s[i] = 0.0f;
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) row_ds += s[i];
+                row_ds += tree_sum(s);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float x[8];
@@ -517,10 +534,10 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             float less[16], delta[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                less[i] = ri_t.less[8 * (i / 4) + 4 * half + i % 4];
+                less[i] = ri_t.less[8 * (i / 4) + 4 * half + i % 4] + kept_add;
                 delta[i] = ri_t.delta[8 * (i / 4) + 4 * half + i % 4];
             }
-            float mul = c, add = kept_add;
+            float add = 0.0f;
             PosRange rows{};
             int bucket = -1;
             bool table = false;
@@ -530,12 +547,12 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
                 table = first != last;
                 if (!table) {
                     const float2 e = lut[kLutPad + first];
-                    add += e.x;
+                    add = e.x;
                     bucket = uniform(__float_as_int(e.y));
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            floatx16 s = rs.finish(tl, qt, kPlane, 0, k), dp = rd.finish(tl, gt, kPlane, 0, v);
+            floatx16 s = rs.template finish<true>(tl, qt, kPlane, 0, k), dp = rd.template finish<true>(tl, gt, kPlane, 0, v);
             ColsAhead<DP> qf, gf;
             if constexpr (NP == 1) {
                 gf.load(tl, gt, 0);
@@ -545,20 +562,22 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             settle(s);
             settle(dp);
             if (table) {
-                mul = 1.0f;
                 if (a.lut_run && rows.run) {   // later rows, smaller offsets
                     const float2 *at = lut + run_index(a, offset_of(pos, rows.first + 31)) + 3 - 4 * half;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, at[28 - 8 * (i / 4) - i % 4].x);
+                    for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, at[28 - 8 * (i / 4) - i % 4].x + less[i]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        s[i] = fmaf(s[i], c, lut[kLutPad + lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))].x);
+                        s[i] = fmaf(s[i], c, lut[kLutPad + lut_index(a, offset_of(pos, ri_t.pos[8 * (i / 4) + 4 * half + i % 4]))].x + less[i]);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], c, add + less[i]);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], mul, add + less[i]));
+                const float p = __builtin_amdgcn_exp2f(s[i]);
                 s[i] = p;
                 dp[i] = p * (dp[i] - delta[i]);
             }
@@ -566,8 +585,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
                 if (!table) {
                     if (bucket != run_bucket) flush();
                     run_bucket = bucket;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) run_ds += dp[i];
+                    run_ds += tree_sum(dp);
                 } else if (key_run && rows.run) {
                     const int first = rows.first;
 #pragma unroll
