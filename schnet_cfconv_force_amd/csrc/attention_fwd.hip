@@ -199,12 +199,10 @@ __device__ inline void write_row4(const AttnArgs &a, const FwdOut &out, int spli
     }
     T *o = (T *)out.o + at * a.D;
     v *= inv;
-    if (NP == 1 && out.rows)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (d + i < a.D) out.rows[at * a.D + d + i] = v[i];
+    float *rows = NP == 1 && out.rows ? out.rows + at * a.D : nullptr;
     if (a.D % 4 == 0) {   // rows are then aligned for four elements
         if (d >= a.D) return;
+        if (rows) *reinterpret_cast<floatx4 *>(rows + d) = v;
         if constexpr (NP == 1)
             *reinterpret_cast<bf16x4 *>(o + d) = __builtin_convertvector(v, bf16x4);
         else
@@ -213,7 +211,10 @@ __device__ inline void write_row4(const AttnArgs &a, const FwdOut &out, int spli
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (d + i < a.D) o[d + i] = (T)v[i];
+        if (d + i < a.D) {
+            o[d + i] = (T)v[i];
+            if (rows) rows[d + i] = v[i];
+        }
 }
 
 // Of a row's maximum (log2) and sum; no key: -inf, and the row is zeros.  A sum
