@@ -643,9 +643,19 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, No
 
 // ------------------------------------------------------------------ launches
 
-constexpr int kHold = 16;        // vectors that a thread of a fused launch can hold
+// Vectors that a thread of a fused launch can hold.  The launch takes the
+// smallest of 4, 8 and 16 that the longest segment needs: more registers are
+// fewer blocks on a CU (256 segments of 269 rows of 128 in fp32: 17 and 37 us
+// forward and backward with 8, 22 and 48 us with 16).  Backward holds x and
+// dy, so that 16 of both lose to a second read (64 segments of 1500 rows: 55
+// us against 50); forward 16 still win (28 us against 32).
+constexpr int kHold = 16, kHoldBwd = 8;
 constexpr int kHoldStats = 8;    // of a chunk
-constexpr int kWantBlocks = 256; // one for every CU
+// One block for every CU, and two in the backward pass, whose chunks are
+// cheap: 15668 rows of 128 as one segment take 16 and 21 us forward and
+// backward; with a quarter of the chunks 18 and 23 (8 segments of 16384 rows
+// of 512 in bf16: backward 130 -> 276 us), with four times as many 29 and 26.
+constexpr int kWantBlocks = 256;
 
 // V: the widest vector that divides a group and suits every tensor.
 // backward: its chunks need not fit the registers, and a longer one spares
@@ -665,13 +675,13 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V, bool bac
         // they make a block for every CU
         for (int bytes = 128; bytes >= 16; bytes /= 2) {
             const int gs = whole(bytes);
-            if (rows_held(gs, kHold) < max_rows) continue;
+            if (rows_held(gs, backward ? kHoldBwd : kHold) < max_rows) continue;
             if (bytes > 32 && gs > 1 && (int64_t)B * ((groups + gs - 1) / gs) < 256) continue;
             k.gs = gs;
             k.slabs = (groups + gs - 1) / gs;
             k.chunks = 1;
             k.chunk_rows = std::max(1, max_rows);
-            k.it = rows_held(gs, 4) >= max_rows ? 4 : kHold;
+            k.it = rows_held(gs, 4) >= max_rows ? 4 : rows_held(gs, 8) >= max_rows ? 8 : kHold;
             return k;
         }
         k.gs = whole(128);
@@ -727,6 +737,8 @@ sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *
     if (fused(k)) {
         if (k.it == 4)
             norm_fwd_kernel<T, V, 4, ACT><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
+        else if (k.it == 8)
+            norm_fwd_kernel<T, V, 8, ACT><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
         else
             norm_fwd_kernel<T, V, kHold, ACT><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
         return launch_status();
@@ -750,7 +762,7 @@ sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, vo
         if (k.it == 4)
             norm_bwd_kernel<T, V, 4, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
         else
-            norm_bwd_kernel<T, V, kHold, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
+            norm_bwd_kernel<T, V, kHoldBwd, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
         SN_TRY(launch_status());
         if (params) norm_param_kernel<<<params, kThreads, 0, s>>>(a, seg, dgamma, dbeta);
         return launch_status();
