@@ -14,9 +14,6 @@ typedef __bf16 bf16;
 
 __device__ inline float to_f32(float v) { return v; }
 __device__ inline float to_f32(bf16 v) { return (float)v; }
-// the output's own type, rounded to nearest even once
-template <typename T>
-__device__ inline T from_f32(float v) { return (T)v; }
 
 // --------------------------------------------------------------- ragged rows
 

@@ -239,7 +239,10 @@ __device__ inline void write_y(const Vec<T, V> &x, float mu, float r, const floa
 
 // ------------------------------------------------------------------ forward
 
-// The whole segment in registers: statistics and output in one pass.
+// The whole segment in registers: statistics and output in one pass, x read
+// once.  269 rows of 128 in fp32: 6.4 us, a launch and two sums over a block;
+// 64 such segments: 7 us for 17.6 MB, 2.5 TB/s, one wave of 512 blocks whose
+// loads, sums and stores follow each other.
 template <typename T, int V, int IT, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut k, T *y, float *mean, float *rstd) {
     __shared__ SumLds lds;
@@ -273,6 +276,8 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut 
     }
 }
 
+// Memory bound: 8 segments of up to 16384 rows of 512 in bf16 at 5.9 TB/s (22
+// us; part of it comes from the last-level cache).
 // part [b][group][chunk pieces + piece]: the chunk's {mean, sum of squared
 // differences} of each group
 template <typename T, int V, int IT>
@@ -288,7 +293,8 @@ __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a, NormCu
         part[((int64_t)s.b * a.groups + s.g0 + s.group) * k.chunks * s.pieces + s.chunk * s.pieces + s.piece] = st;
 }
 
-// Joins the chunks' statistics and writes this chunk's rows.
+// Joins the chunks' statistics (each block for itself: a launch less) and
+// writes this chunk's rows; the same segments at 5.8 TB/s (46 us).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCut k, const float2 *part, T *y,
                                                               float *mean, float *rstd) {
@@ -431,7 +437,8 @@ __device__ inline void channel_sums(const Slab &s, float (&sx)[V], float (&sz)[V
     }
 }
 
-// The whole segment in registers.  seg [b][2][C]: its sums of dz xh and dz.
+// The whole segment in registers, x and dy read once.  seg [b][2][C]: its sums
+// of dz xh and dz.  64 segments of 269 rows of 128 in fp32: 9 us for 26 MB.
 template <typename T, int V, int IT, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut k, const float *mean,
                                                             const float *rstd, T *dx, float *seg) {
@@ -497,7 +504,9 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut 
     }
 }
 
-// part [b][chunk][2][C]: the chunk's sums of dz xh and dz
+// part [b][chunk][2][C]: the chunk's sums of dz xh and dz.  8 segments of up
+// to 16384 rows of 512 in bf16: 59 us, 4.5 TB/s, two streams beside the
+// activation's slope (an exponential and a reciprocal an element).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, NormCut k, const float *mean,
                                                                  const float *rstd, float *part) {
@@ -533,7 +542,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, Nor
 }
 
 // Joins the chunks of a segment, one block per segment and group: seg
-// [b][2][C] and the group's means of dz gamma and dz gamma xh.
+// [b][2][C] and the group's means of dz gamma and dz gamma xh (5 us).
 __global__ __launch_bounds__(256) void norm_bwd_join_kernel(NormArgs a, NormCut k, const float *part, float *seg,
                                                             float2 *gmean) {
     __shared__ double red[2][256];
@@ -612,7 +621,7 @@ __global__ __launch_bounds__(kThreads) void norm_param_kernel(NormArgs a, const 
     param_sums(blockIdx.x, a, seg, dgamma, dbeta, red);
 }
 
-// dx of a chunk's rows; the first `params` blocks sum dgamma and dbeta
+// dx of a chunk's rows (the same segments: 68 us, 5.9 TB/s); the first `params` blocks sum dgamma and dbeta
 // instead (one launch less).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, NormCut k, const float *mean,
@@ -672,7 +681,9 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V, bool bac
     auto rows_held = [&](int gs, int it) { return kThreads / (gs * wv) * it; };
     if (wv <= kThreads) {
         // one launch: full 128-byte lines where the segment still fits and
-        // they make a block for every CU
+        // they make a block for every CU (64 segments of 700 rows of 128 in
+        // bf16: 19 us forward without the narrower slabs, 15 us with them;
+        // 64 of 269 rows in fp32 13 us in two launches, 10 us in one)
         for (int bytes = 128; bytes >= 16; bytes /= 2) {
             const int gs = whole(bytes);
             if (rows_held(gs, backward ? kHoldBwd : kHold) < max_rows) continue;
