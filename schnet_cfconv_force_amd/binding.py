@@ -609,7 +609,7 @@ def group_norm_forward(plan: GroupNorm, x, gamma, beta, ws, save: bool = False, 
     y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = rstd = None
     if save:
-        mean, rstd = torch.empty((2, plan.n_segments, plan.n_groups), dtype=torch.float32, device=plan.device)
+        mean, rstd = torch.empty((2, plan.n_segments, plan.n_groups), dtype=torch.float32, device=plan.device).unbind(0)
     st = lib().sn_group_norm_forward(op, y.data_ptr(), _ptr(mean), _ptr(rstd), ws.data_ptr(),
                                      ws.numel(), _launch_stream(plan, stream, y, mean, rstd))
     _check(st, "sn_group_norm_forward")
@@ -623,7 +623,7 @@ def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=N
     dy_stride, _ = _rows(dy, "dy", plan.shape, plan.dtype, plan.device)
     stats = (plan.n_segments, plan.n_groups)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-    dgamma, dbeta = torch.empty((2, plan.n_channels), dtype=torch.float32, device=plan.device)
+    dgamma, dbeta = torch.empty((2, plan.n_channels), dtype=torch.float32, device=plan.device).unbind(0)
     st = lib().sn_group_norm_backward(
         op, _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
         _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), dy.data_ptr(), dy_stride, dx.data_ptr(),

@@ -99,8 +99,11 @@ struct Slab {
 };
 
 __device__ inline bool locate(const NormArgs &a, const NormCut &k, int block, Slab &s) {
-    s.chunk = block % k.chunks;
-    s.slab = block / k.chunks % k.slabs;
+    // a segment's rows in order, all their slabs before the next rows: what lies
+    // beyond a short segment is spread over the dies (8 segments of up to 16384
+    // rows of 512 in bf16: forward 74 -> 67 us against slab by slab)
+    s.slab = block % k.slabs;
+    s.chunk = block / k.slabs % k.chunks;
     s.b = block / k.chunks / k.slabs;
     segment_rows(a.ptr, s.b, a.B, a.n_rows, a.max_rows, a.status, s.r0, s.n);
     s.first = s.chunk * k.chunk_rows;
@@ -241,7 +244,7 @@ __device__ inline void write_y(const Vec<T, V> &x, float mu, float r, const floa
 
 // The whole segment in registers: statistics and output in one pass, x read
 // once.  269 rows of 128 in fp32: 6.4 us, a launch and two sums over a block;
-// 64 such segments: 7 us for 17.6 MB, 2.5 TB/s, one wave of 512 blocks whose
+// 64 segments of up to as many: 7 us for 8.4 MB, one wave of 256 blocks whose
 // loads, sums and stores follow each other.
 template <typename T, int V, int IT, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut k, T *y, float *mean, float *rstd) {
@@ -276,8 +279,9 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut 
     }
 }
 
-// Memory bound: 8 segments of up to 16384 rows of 512 in bf16 at 5.9 TB/s (22
-// us; part of it comes from the last-level cache).
+// Memory bound: 8 segments of 16384 rows of 512 in bf16, 134 MB, take 77 us with
+// the launch that follows, 5.2 TB/s; of ragged ones (81 MB in all) the blocks
+// are one wave on the card, whose start and end cost a third: 24 us, 3.4 TB/s.
 // part [b][group][chunk pieces + piece]: the chunk's {mean, sum of squared
 // differences} of each group
 template <typename T, int V, int IT>
@@ -294,7 +298,7 @@ __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a, NormCu
 }
 
 // Joins the chunks' statistics (each block for itself: a launch less) and
-// writes this chunk's rows; the same segments at 5.8 TB/s (46 us).
+// writes this chunk's rows; the same ragged segments in 42 us, 3.8 TB/s.
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCut k, const float2 *part, T *y,
                                                               float *mean, float *rstd) {
@@ -438,7 +442,8 @@ __device__ inline void channel_sums(const Slab &s, float (&sx)[V], float (&sz)[V
 }
 
 // The whole segment in registers, x and dy read once.  seg [b][2][C]: its sums
-// of dz xh and dz.  64 segments of 269 rows of 128 in fp32: 9 us for 26 MB.
+// of dz xh and dz.  64 segments of up to 269 rows of 128 in fp32: 8.5 us for 12.6
+// MB, as the forward launch.
 template <typename T, int V, int IT, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut k, const float *mean,
                                                             const float *rstd, T *dx, float *seg) {
@@ -504,9 +509,10 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut 
     }
 }
 
-// part [b][chunk][2][C]: the chunk's sums of dz xh and dz.  8 segments of up
-// to 16384 rows of 512 in bf16: 59 us, 4.5 TB/s, two streams beside the
-// activation's slope (an exponential and a reciprocal an element).
+// part [b][chunk][2][C]: the chunk's sums of dz xh and dz.  8 segments of
+// 16384 rows of 512 in bf16: 127 us with the two launches that follow, 5.3
+// TB/s; ragged ones (81 MB a tensor) in 58 us, 2.8 TB/s, two streams beside
+// the activation's slope (an exponential and a reciprocal an element).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, NormCut k, const float *mean,
                                                                  const float *rstd, float *part) {
@@ -621,7 +627,8 @@ __global__ __launch_bounds__(kThreads) void norm_param_kernel(NormArgs a, const 
     param_sums(blockIdx.x, a, seg, dgamma, dbeta, red);
 }
 
-// dx of a chunk's rows (the same segments: 68 us, 5.9 TB/s); the first `params` blocks sum dgamma and dbeta
+// dx of a chunk's rows (the same ragged segments: 67
+// us, 3.6 TB/s); the first `params` blocks sum dgamma and dbeta
 // instead (one launch less).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, NormCut k, const float *mean,
