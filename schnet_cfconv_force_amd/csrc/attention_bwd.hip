@@ -82,8 +82,8 @@ __device__ inline void write4(T *row, int d, int D, floatx4 v) {
 // scores in one lane, so L and delta are one register each, and dS^T is the
 // next product's operand as it lies.  Bound by the vector instructions between
 // the products (an exponential and eight others a score) and, for short
-// segments, by the start: 2 x 2048 x 2048, 16 heads of 64, bf16: 98 us, 350
-// TFLOP/s; 64 segments of 269 x 271, 4 heads of 32, fp32: 33 us.
+// segments, by the start: two segments of up to 2048 x 2048, 16 heads of 64, bf16:
+// 98 us, 290 TFLOP/s; 64 of up to 269 x 271, 4 heads of 32, fp32: 34 us.
 template <int NP, int DP, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void attn_dq_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
@@ -329,11 +329,11 @@ __host__ __device__ inline BiasLds bias_lds(int lut_n, int nb) {
 // dk, dv and the bias sums: a wavefront owns 32 keys, the block's four share
 // the tiles of 32 rows of every head that reads these keys.  S and dP put a
 // key's column in one lane; p and dS are the operands of dv and dk as they
-// lie.  Four products of a tile against three instructions' worth of vector
-// work for each: bound by both, and by two wavefronts on a SIMD to overlap
-// them (tiles of 64 rows spilled).  2 x 2048 x 2048, 16 heads of 64, bf16: 138
-// us, 330 TFLOP/s with the bias sums (about 25 us of it); 64 segments of 269 x
-// 271, 4 heads of 32, fp32: 48 us.
+// lie.  Bound by the vector instructions between the four products, with two
+// wavefronts on a SIMD to overlap them (tiles of 64 rows spilled).  Two
+// segments of up to 2048 x 2048, 16 heads of 64, bf16: 136 us, 280 TFLOP/s
+// (without a bias the backward pass takes 169 us instead of 206 on segments of
+// equal length); 64 segments of up to 269 x 271, 4 heads of 32, fp32: 48 us.
 template <int NP, int DP>
 constexpr int dkv_buffers() { return NP == 3 && DP == 128 ? 1 : 2; }   // 160 KB of LDS
 

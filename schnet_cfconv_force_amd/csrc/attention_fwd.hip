@@ -246,7 +246,7 @@ constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
 // instructions and an exponential, about as long as two products of 128.
 // Measured: 2 x 4096 x 4096, 16 heads of 128 on 4, bf16: 416 us, 660 TFLOP/s
 // (a large library product reaches 1220); fp32, six products for one: 64
-// segments of 269 x 271, 4 heads of 32: 27 us, 38 TFLOP/s.
+// segments of up to 269 x 271, 4 heads of 32: 26 us, 40 TFLOP/s.
 template <int NP, int PP, int DP, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
 }
 
 // Join the key splits of a row: one wavefront per row and head (9 us for 1024
-// rows of 128 in 4 splits, a launch and two dependent loads).
+// rows of 128 in 4 splits: a launch and two dependent loads).
 template <int NP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
