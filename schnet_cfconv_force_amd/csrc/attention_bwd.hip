@@ -190,17 +190,18 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
             float less = -L;
             const float *mine = lut + hg * lut_stride(a);
             PosRange keys{};
-            bool table = false;
+            bool table = false, undecided = a.nb;   // the tile's bias is looked up once, by the first half that has a key
 #pragma unroll
             for (int sub = 0; sub < kDqKeys / 32; ++sub) {
                 const uint32_t sub_mask = (uint32_t)(mask >> (32 * sub));
                 if (kDqKeys > 32 && !sub_mask) continue;
                 int4 range;
-                if (a.nb && sub == 0) range = ki.head;
+                if (undecided) range = ki.head;
                 RowsProduct<NP, DP> rs, rd;
                 rs.begin(tl, kt, 32 * sub);
                 rd.begin(tl, vt, 32 * sub);
-                if (a.nb && sub == 0) {
+                if (undecided) {
+                    undecided = false;
                     keys = uniform_range(range);
                     const int first = lut_index(a, offset_of(keys.lo, pos_hi)), last = lut_index(a, offset_of(keys.hi, pos_lo));
                     table = first != last;

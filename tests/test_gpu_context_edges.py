@@ -1,0 +1,44 @@
+"""GPU: the context operators at masks, sizes and addresses where they can go wrong, against 64-bit references
+(context_ref.py states how the tolerances are derived)."""
+import numpy as np
+import pytest
+
+import context_ref as R
+from test_gpu_context import attention_case, attention_check, attention_run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sn():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import schnet_cfconv_force_amd as sn
+    sn.lib()
+    return sn
+
+
+# ------------------------------------------------------------------ cross attention: masks in runs
+
+MASKS = {"first32": lambda j, n: j >= 32, "first40": lambda j, n: j >= 40, "first96": lambda j, n: j >= 96,
+         "alternate": lambda j, n: j // 32 % 2 == 1, "last": lambda j, n: j == n - 1}
+
+
+@pytest.mark.parametrize("positions", ["default", "scattered"])
+@pytest.mark.parametrize("thr", ["one", "several"])
+@pytest.mark.parametrize("mask", list(MASKS))
+@pytest.mark.parametrize("dtype,D", [("float32", 16), ("float32", 32), ("bfloat16", 40), ("bfloat16", 64), ("float32", 128)])
+def test_attention_masks_in_runs_of_keys(sn, dtype, D, mask, thr, positions):
+    """Absent keys in runs, with a bias: a tile whose first half has no key still takes its bias from the second."""
+    import torch
+    print(f"[attention] {mask} thresholds {thr} positions {positions} {dtype} {D}", flush=True)
+    lk = [150, 64, 0, 129]
+    bias = np.zeros(0, np.int32) if thr == "one" else True
+    plan, c, where, ref, factor = attention_case(sn, [70, 3, 2, 33], lk, 4, 2, D, dtype, bias, False, "plain", seed=70,
+                                                 gen_pos=positions)
+    keep = np.concatenate([MASKS[mask](np.arange(n), n) for n in lk])
+    where["keep"] = torch.from_numpy(keep).cuda()
+    thresholds = bias if thr == "one" else sn.relative_thresholds(32, 128)
+    ref, factor = R.attention(c["q"], c["k"], c["v"], plan.q_ptr.cpu().numpy(), plan.k_ptr.cpu().numpy(), plan.scale,
+                              where["bias"], thresholds, where["q_pos"], where["k_pos"], where["keep"], c["d_o"])
+    attention_check(attention_run(sn, plan, c, where), ref, factor, dtype)
