@@ -79,9 +79,10 @@ struct NormCut {
     int gs;         // groups of a slab (1 where a slab is a piece of a group)
     int piece;      // channels of a piece; 0: slabs hold whole groups
     int slabs;      // slabs of a row
-    int chunks;     // chunks of the longest segment (1: fused)
+    int chunks;     // chunks of the longest segment
     int chunk_rows;
     int it;         // vectors that a thread holds of a chunk
+    bool fused;     // one launch: a thread holds all its vectors of a segment
 };
 
 // A block's slab.
@@ -700,6 +701,7 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V, bool bac
             k.chunks = 1;
             k.chunk_rows = std::max(1, max_rows);
             k.it = rows_held(gs, 4) >= max_rows ? 4 : rows_held(gs, 8) >= max_rows ? 8 : kHold;
+            k.fused = true;
             return k;
         }
         k.gs = whole(128);
@@ -738,21 +740,19 @@ NormLayout norm_layout(const NormCut &k, int64_t B, int64_t C, int64_t groups) {
     L.seg = take(B * 2 * C * sizeof(float));
     L.gmean = take(B * groups * sizeof(float2));
     const int64_t pieces = k.piece ? k.slabs / groups : 1;
-    L.part = take(k.chunks > 1 || k.piece ? std::max(B * groups * k.chunks * pieces * (int64_t)sizeof(float2),
-                                                     B * k.chunks * 2 * C * (int64_t)sizeof(float))
-                                          : 0);
+    L.part = take(k.fused ? 0
+                          : std::max(B * groups * k.chunks * pieces * (int64_t)sizeof(float2),
+                                     B * k.chunks * 2 * C * (int64_t)sizeof(float)));
     L.total = o;
     return L;
 }
-
-bool fused(const NormCut &k) { return k.chunks == 1 && !k.piece; }
 
 template <typename T, int V, int ACT>
 sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
     const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, false);
     const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
     const int grid = a.B * k.slabs * k.chunks;
-    if (fused(k)) {
+    if (k.fused) {
         if (k.it == 4)
             norm_fwd_kernel<T, V, 4, ACT><<<grid, kThreads, 0, s>>>(a, k, (T *)y, mean, rstd);
         else if (k.it == 8)
@@ -776,7 +776,7 @@ sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, vo
     const int grid = a.B * k.slabs * k.chunks, params = dgamma || dbeta ? (a.C + 63) / 64 : 0;
     float *seg = reinterpret_cast<float *>(ws + L.seg), *part = reinterpret_cast<float *>(ws + L.part);
     float2 *gmean = reinterpret_cast<float2 *>(ws + L.gmean);
-    if (fused(k)) {
+    if (k.fused) {
         if (k.it == 4)
             norm_bwd_kernel<T, V, 4, ACT><<<grid, kThreads, 0, s>>>(a, k, mean, rstd, (T *)dx, seg);
         else

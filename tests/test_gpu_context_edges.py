@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import context_ref as R
-from test_gpu_context import attention_case, attention_check, attention_run
+from test_gpu_context import attention_case, attention_check, attention_run, norm_case, norm_check, norm_run
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,15 @@ def test_attention_masks_in_runs_of_keys(sn, dtype, D, mask, thr, positions):
     ref, factor = R.attention(c["q"], c["k"], c["v"], plan.q_ptr.cpu().numpy(), plan.k_ptr.cpu().numpy(), plan.scale,
                               where["bias"], thresholds, where["q_pos"], where["k_pos"], where["keep"], c["d_o"])
     attention_check(attention_run(sn, plan, c, where), ref, factor, dtype)
+
+
+# ------------------------------------------------------------------ group norm: many long segments
+
+@pytest.mark.parametrize("lengths,C,groups,dtype", [
+    ([1500, 40] * 64, 128, 8, "float32"), ([1500, 0, 3] * 50, 128, 8, "float32"), ([5000] + [20] * 130, 512, 32, "bfloat16"),
+    ([4200] + [7] * 600, 40, 5, "bfloat16"), ([1100] + [9] * 700, 33, 3, "float32")], ids=lambda v: f"{v[0]}of{len(v)}" if isinstance(v, list) else str(v))
+def test_norm_backward_of_many_segments_longer_than_a_block_holds(sn, lengths, C, groups, dtype):
+    """Enough segments that none of them is cut into chunks, and rows beyond what one launch holds in registers."""
+    print(f"[norm] {len(lengths)} segments of up to {max(lengths)} {C} {groups} {dtype}", flush=True)
+    plan, *args, ref, factor = norm_case(sn, lengths, C, groups, "ssp", dtype, seed=70)
+    norm_check(norm_run(sn, plan, *args), ref, factor, dtype)
