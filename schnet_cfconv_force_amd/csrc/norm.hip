@@ -668,6 +668,10 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, No
 // us against 50); forward 16 still win (28 us against 32).
 constexpr int kHold = 16, kHoldBwd = 8;
 constexpr int kHoldStats = 8;    // of a chunk
+// Vectors that a thread of the backward pass adds one after the other: its fp32
+// sums lose up to half a unit of the sum so far with each, and chunks are
+// joined in fp64.
+constexpr int kSerial = 64;
 // One block for every CU, and two in the backward pass, whose chunks are
 // cheap: 15668 rows of 128 as one segment take 16 and 21 us forward and
 // backward; with a quarter of the chunks 18 and 23 (8 segments of 16384 rows
@@ -713,7 +717,7 @@ NormCut norm_cut(int B, int max_rows, int C, int groups, int es, int V, bool bac
     }
     const int cv = k.piece ? kThreads : k.gs * wv, rp = kThreads / cv;
     const int64_t blocks = (int64_t)B * k.slabs;
-    const int least = backward ? 1 : (max_rows + rp * kHoldStats - 1) / (rp * kHoldStats);
+    const int most = rp * (backward ? kSerial : kHoldStats), least = (max_rows + most - 1) / most;
     const int want_blocks = backward ? 2 * kWantBlocks : kWantBlocks;
     const int want = (int)std::min<int64_t>((max_rows + rp - 1) / rp, (want_blocks + blocks - 1) / blocks);
     k.chunks = std::max(1, std::max(least, want));

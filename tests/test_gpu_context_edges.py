@@ -54,3 +54,19 @@ def test_norm_backward_of_many_segments_longer_than_a_block_holds(sn, lengths, C
     print(f"[norm] {len(lengths)} segments of up to {max(lengths)} {C} {groups} {dtype}", flush=True)
     plan, *args, ref, factor = norm_case(sn, lengths, C, groups, "ssp", dtype, seed=70)
     norm_check(norm_run(sn, plan, *args), ref, factor, dtype)
+
+
+def test_norm_backward_sums_of_long_columns_keep_their_digits(sn):
+    """One long segment among many, wide rows and equal addends of one sign, whose serial fp32 sum would drift by a
+    multiple of its tolerance (n / 4 roundings of one direction on n rows): dbeta is n times the addend."""
+    import torch
+    print("[norm] long columns", flush=True)
+    n, C = 12000, 2048
+    plan = sn.GroupNorm(np.concatenate([[0], n + np.arange(521)]).astype(np.int32), C, 1)
+    x = torch.randn((plan.n_rows, C), generator=torch.Generator(device="cuda").manual_seed(71), device="cuda")
+    dy = torch.full_like(x, 0.1)
+    got = norm_run(sn, plan, x, None, None, dy)
+    want = plan.n_rows * float(dy[0, 0].double())
+    worst = float((got["dbeta"].double() / want - 1).abs().max())
+    print(f"   dbeta: {worst / (64 * R.U32):.2g} of the tolerance", flush=True)
+    assert worst <= 64 * R.U32
