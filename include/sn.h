@@ -370,8 +370,7 @@ sn_status sn_cross_attention_forward(const sn_cross_attention *op, void *o, floa
                                      void *stream);
 
 /* The same with a backward pass to come: also rows, o before its rounding in
- * fp32 (SN_F32: o is that, and rows may be NULL).  SN_BF16: its o is the
- * nearer one, the weights of the values keep 16 bits here and 8 above. */
+ * fp32 (SN_F32: o is that, and rows may be NULL). */
 sn_status sn_cross_attention_forward_train(const sn_cross_attention *op, void *o, float *rows, float *lse, void *ws,
                                            size_t ws_bytes, void *stream);
 

@@ -26,10 +26,10 @@ struct FwdOut {
     float2 *part_ml;    // [split][n_q H] their maximum (log2) and sum
 };
 
-// What a wavefront keeps of its 32 rows (a lane: row lane % 32).  PP: planes
-// of p; see the product with v.
-template <int NP, int PP, int DP, bool FAST>
+// What a wavefront keeps of its 32 rows (a lane: row lane % 32).
+template <int NP, int DP, bool FAST>
 struct RowState {
+    static constexpr int PP = NP == 1 ? 2 : NP;   // planes of p; see the product with v
     Frag<NP> q[DP / 16];
     floatx16 o[DP / 32];
     float m, l;
@@ -165,17 +165,16 @@ struct RowState {
                 float x[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = s[u][8 * t + j];
-                // bf16 rows: p is rounded to 8 bits here, at most 2^-8 of each
-                // term of O, as much as rounding o itself costs.  With a
-                // backward pass to come it keeps 16: an error of O is one of
-                // delta, which dq has no other sum to correct by (rows of few
-                // keys: dq 2.4 times as far off as its rounding, now 1.4)
+                // bf16 rows: p keeps 16 bits.  8 would cost O as much as its
+                // own rounding (2.3e-3 of its norm off instead of 1.7e-3), and
+                // an error of O is one of the backward pass's delta, which dq
+                // has no other sum to correct by (rows of few keys: dq 2.4
+                // times as far off as its rounding, 1.4 with 16)
                 const Frag<PP> p = split8f<PP>(x);
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e) {
                     if constexpr (NP == 1) {
-                        if constexpr (PP == 2)
-                            o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u].f[t][e], p.p[1], o[e], 0, 0, 0);
+                        o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u].f[t][e], p.p[1], o[e], 0, 0, 0);
                         o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u].f[t][e], p.p[0], o[e], 0, 0, 0);
                     } else
                         o[e] = mma<NP>(frag_cols<NP, DP>(tl, vt, kPlane, 32 * u + 16 * t, e), p, o[e]);
@@ -244,10 +243,10 @@ constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
 // Two blocks on a CU let one wavefront's products run beside the other's
 // softmax.  What bounds it is the softmax: a score takes ten vector
 // instructions and an exponential, about as long as two products of 128.
-// Measured: 2 x 4096 x 4096, 16 heads of 128 on 4, bf16: 416 us, 660 TFLOP/s
-// (a large library product reaches 1220); fp32, six products for one: 64
+// Measured: 2 x 4096 x 4096, 16 heads of 128 on 4, bf16: 482 us, 570 TFLOP/s
+// (a large library product reaches 1220; 416 us with p in 8 bits); fp32, six products for one: 64
 // segments of up to 269 x 271, 4 heads of 32: 26 us, 40 TFLOP/s.
-template <int NP, int PP, int DP, int KT, bool FAST>
+template <int NP, int DP, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * KT * DP;
@@ -285,7 +284,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
     };
     // the first tile, the rows and the bias are on their way together
     uint64_t mask = 0;
-    RowState<NP, PP, DP, FAST> st;
+    RowState<NP, DP, FAST> st;
     Raw8<NP> raw[DP / 16];
     if (t0 < t1) load(t0);
     st.begin(a, w, w.tile * 128 + wave * 32, lane, raw);
@@ -322,7 +321,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
 // 32 sequences of up to 16384 keys, 8 heads of 128, bf16: 290 us, 5.0 TB/s,
 // the rate of a large copy.  One row over 269 keys: 10 us, a launch and one
 // chain of dependent loads, products and exchanges.
-template <int NP, int PP, int DP, int NW, bool FAST>
+template <int NP, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
     constexpr int kTile = NP * 32 * DP;
@@ -354,7 +353,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
         kl.load(a, w, t * 32, a.nb, lane);
     };
     if (t < t1) load(t);
-    RowState<NP, PP, DP, FAST> st;
+    RowState<NP, DP, FAST> st;
     Raw8<NP> raw[DP / 16];
     st.begin(a, w, w.tile * 32, lane, raw);
     if (a.nb) fill_lut(a, w, lut);
@@ -469,15 +468,15 @@ FwdPlan fwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
     return p;
 }
 
-template <int NP, int PP, int DP, bool FAST>
+template <int NP, int DP, bool FAST>
 sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
     const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
     constexpr int NW = NP * DP <= 96 ? 8 : NP * DP <= 192 ? 4 : 2;   // 160 KB of LDS hold their tiles
     const size_t lut = a.nb ? (size_t)a.Gs * (a.lut_n + 2 * kLutPad) * sizeof(float) : 0;
     if (few)
-        attn_few_kernel<NP, PP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);
+        attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);
     else
-        attn_rows_kernel<NP, PP, DP, kRowKeys<NP, DP>, FAST><<<grid, kAttnThreads, lut, s>>>(a, out);
+        attn_rows_kernel<NP, DP, kRowKeys<NP, DP>, FAST><<<grid, kAttnThreads, lut, s>>>(a, out);
     SN_TRY(launch_status());
     if (a.splits > 1) {
         attn_join_kernel<NP><<<(int)(((int64_t)a.n_q * a.H + 3) / 4), 256, 0, s>>>(a, out);
@@ -486,11 +485,11 @@ sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) 
     return SN_OK;
 }
 
-template <int NP, int PP, bool FAST>
+template <int NP, bool FAST>
 sn_status launch_dim(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
-    if (a.D <= 32) return launch<NP, PP, 32, FAST>(a, out, few, s);
-    if (a.D <= 64) return launch<NP, PP, 64, FAST>(a, out, few, s);
-    return launch<NP, PP, 128, FAST>(a, out, few, s);
+    if (a.D <= 32) return launch<NP, 32, FAST>(a, out, few, s);
+    if (a.D <= 64) return launch<NP, 64, FAST>(a, out, few, s);
+    return launch<NP, 128, FAST>(a, out, few, s);
 }
 
 }  // namespace
@@ -516,9 +515,8 @@ sn_status attn_forward(AttnArgs a, int dtype, void *o, float *rows, float *lse, 
         out.part_ml = reinterpret_cast<float2 *>(ws + kWsBase);
         out.part_o = reinterpret_cast<float *>(ws + kWsBase + align256(n * p.splits * sizeof(float2)));
     }
-    if (dtype == SN_F32) return a.fast ? launch_dim<3, 3, true>(a, out, p.few, s) : launch_dim<3, 3, false>(a, out, p.few, s);
-    if (out.rows) return a.fast ? launch_dim<1, 2, true>(a, out, p.few, s) : launch_dim<1, 2, false>(a, out, p.few, s);
-    return a.fast ? launch_dim<1, 1, true>(a, out, p.few, s) : launch_dim<1, 1, false>(a, out, p.few, s);
+    if (dtype == SN_F32) return a.fast ? launch_dim<3, true>(a, out, p.few, s) : launch_dim<3, false>(a, out, p.few, s);
+    return a.fast ? launch_dim<1, true>(a, out, p.few, s) : launch_dim<1, false>(a, out, p.few, s);
 }
 
 }  // namespace sn

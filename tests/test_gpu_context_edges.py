@@ -44,6 +44,26 @@ def test_attention_masks_in_runs_of_keys(sn, dtype, D, mask, thr, positions):
     attention_check(attention_run(sn, plan, c, where), ref, factor, dtype)
 
 
+# ------------------------------------------------------------------ cross attention: bits of the weights
+
+@pytest.mark.parametrize("lq,lk,D", [([70, 3], [400, 65], 64), ([150], [1300], 128), ([2, 1], [700, 300], 128), ([9], [2500], 40)],
+                         ids=str)
+def test_attention_weights_of_bf16_rows_keep_16_bits(sn, lq, lk, D):
+    """Served or saved, o is the nearest bf16 to rows whose weights have 16 bits: each term of a row is at most 2^-17 of
+    itself off, so its norm over the output is at most 2^-17 of the terms' sums of magnitudes, beside fp32 scores."""
+    import torch
+    print(f"[attention] 16-bit weights {lq} {lk} {D}", flush=True)
+    plan, c, where, ref, factor = attention_case(sn, lq, lk, 4, 2, D, "bfloat16", True, False, "plain", seed=72)
+    ws = sn.cross_attention_workspace(plan)
+    o, (rows, lse) = sn.cross_attention_forward(plan, c["q"], c["k"], c["v"], ws, save=True, **where)
+    served = sn.cross_attention_forward(plan, c["q"], c["k"], c["v"], ws, **where)
+    assert torch.equal(o, rows.bfloat16()) and torch.equal(served, o)
+    value, mag = ref["o"]
+    off = float((rows.double().cpu() - value).norm() / mag.norm())
+    print(f"   rows: {off:.2g} of the magnitudes", flush=True)
+    assert off <= 2.0 ** -17 + factor
+
+
 # ------------------------------------------------------------------ group norm: many long segments
 
 @pytest.mark.parametrize("lengths,C,groups,dtype", [
