@@ -62,9 +62,10 @@ __device__ inline float tree_sum(const floatx16 &x) {
     return s[0];
 }
 
+// four: the row is aligned for four elements and D a multiple of them.
 template <typename T>
-__device__ inline void write4(T *row, int d, int D, floatx4 v) {
-    if (D % 4 == 0) {
+__device__ inline void write4(T *row, int d, int D, bool four, floatx4 v) {
+    if (four) {
         if (d >= D) return;
         if constexpr (sizeof(T) == 2)
             *reinterpret_cast<bf16x4 *>(row + d) = __builtin_convertvector(v, bf16x4);
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
         for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                write4<T>(out, 32 * e + 8 * i + 4 * half, a.D,
+                write4<T>(out, 32 * e + 8 * i + 4 * half, a.D, a.out4,
                           floatx4{dq[e][4 * i], dq[e][4 * i + 1], dq[e][4 * i + 2], dq[e][4 * i + 3]} * f);
         if (half == 0) g.row[at] = make_float2(L, delta + err);
     }
@@ -678,11 +679,11 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             }
             if (a.splits > 1) {
                 float *p = g.part_kv + (((int64_t)split * a.n_k * a.Hkv + at) * 2) * a.D;
-                write4<float>(p, d, a.D, xk);
-                write4<float>(p + a.D, d, a.D, xv);
+                write4<float>(p, d, a.D, a.D % 4 == 0, xk);
+                write4<float>(p + a.D, d, a.D, a.D % 4 == 0, xv);
             } else {
-                write4<T>((T *)g.dk + at * a.D, d, a.D, xk);
-                write4<T>((T *)g.dv + at * a.D, d, a.D, xv);
+                write4<T>((T *)g.dk + at * a.D, d, a.D, a.out4, xk);
+                write4<T>((T *)g.dv + at * a.D, d, a.D, a.out4, xv);
             }
         }
 }

@@ -199,7 +199,7 @@ __device__ inline void write_row4(const AttnArgs &a, const FwdOut &out, int spli
     T *o = (T *)out.o + at * a.D;
     v *= inv;
     float *rows = NP == 1 && out.rows ? out.rows + at * a.D : nullptr;
-    if (a.D % 4 == 0) {   // rows are then aligned for four elements
+    if (a.out4) {
         if (d >= a.D) return;
         if (rows) *reinterpret_cast<floatx4 *>(rows + d) = v;
         if constexpr (NP == 1)

@@ -50,6 +50,7 @@ struct AttnArgs {
     int *status;
     // derived
     int fast;                                 // every tensor's rows suit 16-byte reads at 31-bit offsets in a tile
+    int out4;                                 // every output's rows suit stores of four elements
     int Gs, subs;                             // heads of a row block's subgroup, subgroups of a key/value head
     int row_tiles, splits;                    // row tiles of the longest segment, key splits
     int lut_base, lut_n;                      // first offset and length of the position table

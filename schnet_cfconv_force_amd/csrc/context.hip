@@ -67,6 +67,11 @@ bool rows_fast(const sn_cross_attention &op, const void *p, int64_t stride, int6
            op.head_dim % 8 == 0 && stride >= 0 && stride < (1ll << 24) / (op.dtype == SN_F32 ? 4 : 2);
 }
 
+// Whether a contiguous output's rows can be written four elements at a time.
+bool rows_of_four(const sn_cross_attention &op, const void *p, int dtype) {
+    return op.head_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (dtype == SN_F32 ? 15 : 7)) == 0;
+}
+
 AttnArgs attn_args(const sn_cross_attention &op, void *ws) {
     AttnArgs a{};
     a.B = op.n_segments;
@@ -125,8 +130,9 @@ sn_status attn_forward_checked(const sn_cross_attention *op, void *o, float *row
     SN_TRY(check_ctx_ws(ws, ws_bytes, attn_workspace(*op)));
     if (op->n_q == 0) return SN_OK;
     if (!o || !aligned_for(o, op->dtype)) return SN_ERR_INVALID;
-    return attn_forward(attn_args(*op, ws), op->dtype, o, rows, lse, static_cast<char *>(ws),
-                        reinterpret_cast<hipStream_t>(stream));
+    AttnArgs a = attn_args(*op, ws);
+    a.out4 = rows_of_four(*op, o, op->dtype) && rows_of_four(*op, rows, SN_F32);
+    return attn_forward(a, op->dtype, o, rows, lse, static_cast<char *>(ws), reinterpret_cast<hipStream_t>(stream));
 }
 
 NormArgs norm_args(const sn_group_norm &op, void *ws) {
@@ -193,6 +199,7 @@ sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float 
     a.d_o = d_o;
     a.gs = d_o_stride;
     a.gh = d_o_head_stride;
+    a.out4 = rows_of_four(*op, dq, op->dtype) && rows_of_four(*op, dk, op->dtype) && rows_of_four(*op, dv, op->dtype);
     a.fast = a.fast && rows_fast(*op, d_o, d_o_stride, d_o_head_stride) && (reinterpret_cast<uintptr_t>(rows) & 15) == 0;
     return attn_backward(a, op->dtype, rows, lse, dq, dk, dv, op->bias ? dbias : nullptr, static_cast<char *>(ws),
                          reinterpret_cast<hipStream_t>(stream));

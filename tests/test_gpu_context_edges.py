@@ -64,6 +64,44 @@ def test_attention_weights_of_bf16_rows_keep_16_bits(sn, lq, lk, D):
     assert off <= 2.0 ** -17 + factor
 
 
+# ------------------------------------------------------------------ outputs at any element
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lq,lk", [([2], [300]), ([70, 5], [130, 40]), ([40], [1200]), ([700], [40])], ids=str)
+def test_attention_outputs_at_any_element(sn, lq, lk, dtype):
+    """The C entry points take any element-aligned address: outputs one element beyond an aligned one hold the same bits
+    (rows stored whole, key splits joined, row splits joined), and nothing beside them is written."""
+    import torch
+    print(f"[attention] outputs off alignment {lq} {lk} {dtype}", flush=True)
+    plan, c, where, ref, factor = attention_case(sn, lq, lk, 2, 2, 32, dtype, True, True, "plain", seed=73)
+    want = attention_run(sn, plan, c, where)
+    ws = sn.cross_attention_workspace(plan)
+    stream = torch.cuda.current_stream().cuda_stream
+    op = plan._bind(c["q"], c["k"], c["v"], **where)
+    got, guard = {}, 7.0
+
+    def off(name, like, kind):
+        buf = torch.full((like.numel() + 2,), guard, dtype=kind, device="cuda")
+        got[name] = buf
+        return buf[1:].data_ptr()
+
+    f32 = torch.float32
+    at = {"o": off("o", c["q"], plan.dtype), "lse": off("lse", want["lse"], f32), "rows": off("rows", c["q"], f32)}
+    if dtype == "float32":
+        at["rows"] = at["o"]
+    st = sn.lib().sn_cross_attention_forward_train(op, at["o"], at["rows"], at["lse"], ws.data_ptr(), ws.numel(), stream)
+    assert st == sn.SN_OK
+    grads = {n: off(n, like, plan.dtype) for n, like in (("dq", c["q"]), ("dk", c["k"]), ("dv", c["v"]))}
+    grads["dbias"] = off("dbias", where["bias"], f32)
+    H, D = plan.n_heads, plan.head_dim
+    st = sn.lib().sn_cross_attention_backward(op, at["rows"], at["lse"], c["d_o"].data_ptr(), H * D, D, grads["dq"], grads["dk"],
+                                              grads["dv"], grads["dbias"], ws.data_ptr(), ws.numel(), stream)
+    assert st == sn.SN_OK and sn.read_status(ws) == sn.SN_OK
+    for name in ("o", "lse", "dq", "dk", "dv", "dbias"):
+        assert torch.equal(got[name][1:-1].view(want[name].shape), want[name]), name
+        assert float(got[name][0]) == guard and float(got[name][-1]) == guard, name
+
+
 # ------------------------------------------------------------------ group norm: many long segments
 
 @pytest.mark.parametrize("lengths,C,groups,dtype", [
