@@ -382,6 +382,9 @@ def read_status(ws, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ context operators
+#
+# `stream` of the calls below: None is the current stream.  Another one waits for the current stream's work so far, so
+# inputs and workspaces that were made there are ready; what uses the outputs elsewhere has to wait for it.
 
 _ACTIVATIONS = {"none": SN_ACT_NONE, "ssp": SN_ACT_SSP, "silu": SN_ACT_SILU}
 
@@ -422,14 +425,20 @@ def _flat(t, name: str, shape, dtypes, device) -> int:
     return t.data_ptr()
 
 
-def _launch_stream(plan, stream, *outputs) -> int:
-    """The raw stream of a call; outputs allocated on the current stream are tied to an explicit one."""
-    if stream is None:
-        return plan.current_stream(plan.device.index)
-    for t in outputs:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _launch(plan, name: str, stream, ws, inputs, outputs, *args):
+    """Call the entry point `name` with `args`, the workspace and the stream.
+
+    An explicit stream waits for what the current one has been given so far (the outputs' memory may still be in use
+    there, and the inputs or the workspace's zeroing on their way), and every tensor of the call is tied to it."""
+    device = plan.device
+    raw = plan.current_stream(device.index)
+    if stream is not None and stream.cuda_stream != raw:
+        stream.wait_stream(_torch().cuda.current_stream(device))
+        for t in (ws, *plan.pointers, *inputs, *outputs):
+            if t is not None:
+                t.record_stream(stream)
+        raw = stream.cuda_stream
+    _check(getattr(lib(), name)(*args, ws.data_ptr(), ws.numel(), raw), name)
 
 
 def _current_stream_getter():
@@ -494,6 +503,7 @@ class CrossAttention:
         if self.workspace_bytes == 0:
             raise SnError(SN_ERR_INVALID, "sn_cross_attention")
         self.head = bytes(self.c)[:SnCrossAttention.q.offset]
+        self.pointers = (self.q_ptr, self.k_ptr)
         self.current_stream = _current_stream_getter()
         self.q_shape = torch.Size((self.n_q, self.n_heads, self.head_dim))
         self.k_shape = torch.Size((self.n_k, self.n_kv_heads, self.head_dim))
@@ -529,16 +539,14 @@ def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    inputs = (q, k, v, bias, q_pos, k_pos, keep)
     if not save:
-        st = lib().sn_cross_attention_forward(op, o.data_ptr(), None, ws.data_ptr(), ws.numel(),
-                                              _launch_stream(plan, stream, o))
-        _check(st, "sn_cross_attention_forward")
+        _launch(plan, "sn_cross_attention_forward", stream, ws, inputs, (o,), op, o.data_ptr(), None)
         return o
     lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device)
     rows = o if plan.dtype == torch.float32 else torch.empty(plan.q_shape, dtype=torch.float32, device=plan.device)
-    st = lib().sn_cross_attention_forward_train(op, o.data_ptr(), rows.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                                ws.numel(), _launch_stream(plan, stream, o, rows, lse))
-    _check(st, "sn_cross_attention_forward_train")
+    _launch(plan, "sn_cross_attention_forward_train", stream, ws, inputs, (o, rows, lse), op, o.data_ptr(),
+            rows.data_ptr(), lse.data_ptr())
     return o, (rows, lse)
 
 
@@ -554,12 +562,10 @@ def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias
     dk = torch.empty_like(k, memory_format=torch.contiguous_format)
     dv = torch.empty_like(v, memory_format=torch.contiguous_format)
     dbias = None if bias is None else torch.empty_like(bias)
-    st = lib().sn_cross_attention_backward(
-        op, _flat(rows, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
-        _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), d_o.data_ptr(), gs, gh,
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(),
-        _launch_stream(plan, stream, dq, dk, dv, dbias))
-    _check(st, "sn_cross_attention_backward")
+    _launch(plan, "sn_cross_attention_backward", stream, ws, (q, k, v, rows, lse, d_o, bias, q_pos, k_pos, keep),
+            (dq, dk, dv, dbias), op, _flat(rows, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
+            _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), d_o.data_ptr(), gs, gh,
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias))
     return dq, dk, dv, dbias
 
 
@@ -584,6 +590,7 @@ class GroupNorm:
         if self.workspace_bytes == 0:
             raise SnError(SN_ERR_INVALID, "sn_group_norm")
         self.head = bytes(self.c)[:SnGroupNorm.x.offset]
+        self.pointers = (self.row_ptr,)
         self.current_stream = _current_stream_getter()
         self.shape = torch.Size((self.n_rows, self.n_channels))
 
@@ -610,9 +617,8 @@ def group_norm_forward(plan: GroupNorm, x, gamma, beta, ws, save: bool = False, 
     mean = rstd = None
     if save:
         mean, rstd = torch.empty((2, plan.n_segments, plan.n_groups), dtype=torch.float32, device=plan.device).unbind(0)
-    st = lib().sn_group_norm_forward(op, y.data_ptr(), _ptr(mean), _ptr(rstd), ws.data_ptr(),
-                                     ws.numel(), _launch_stream(plan, stream, y, mean, rstd))
-    _check(st, "sn_group_norm_forward")
+    _launch(plan, "sn_group_norm_forward", stream, ws, (x, gamma, beta), (y, mean, rstd), op, y.data_ptr(), _ptr(mean),
+            _ptr(rstd))
     return (y, (mean, rstd)) if save else y
 
 
@@ -624,12 +630,10 @@ def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=N
     stats = (plan.n_segments, plan.n_groups)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     dgamma, dbeta = torch.empty((2, plan.n_channels), dtype=torch.float32, device=plan.device).unbind(0)
-    st = lib().sn_group_norm_backward(
-        op, _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
-        _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), dy.data_ptr(), dy_stride, dx.data_ptr(),
-        dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel(),
-        _launch_stream(plan, stream, dx, dgamma, dbeta))
-    _check(st, "sn_group_norm_backward")
+    _launch(plan, "sn_group_norm_backward", stream, ws, (x, gamma, beta, *saved, dy), (dx, dgamma, dbeta), op,
+            _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
+            _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), dy.data_ptr(), dy_stride, dx.data_ptr(),
+            dgamma.data_ptr(), dbeta.data_ptr())
     return dx, dgamma, dbeta
 
 

@@ -1,0 +1,87 @@
+"""CPU checks of how the context operators' calls reach the library: streams, devices and workspaces, with stand-ins for
+what needs a GPU."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from schnet_cfconv_force_amd import binding
+
+
+class Stand:
+    """A tensor, a stream or the library that notes what is done to it, in order."""
+
+    def __init__(self, name, log, raw=0, device="cuda:0", dtype=torch.uint8):
+        self.name, self.log, self.cuda_stream = name, log, raw
+        self.device, self.dtype = torch.device(device), dtype
+
+    def record_stream(self, stream):
+        self.log.append(("tied", self.name, stream.name))
+
+    def wait_stream(self, other):
+        self.log.append(("waits", self.name, other.name))
+
+    def data_ptr(self):
+        return 256
+
+    def numel(self):
+        return 1024
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """A plan on cuda:0 whose current stream is 7, and an entry point that notes its stream and the current device."""
+    log, state = [], SimpleNamespace(device=0)
+    current = Stand("current", log, raw=7)
+
+    def entry(*args):
+        log.append(("call", args[-1], state.device))
+        return state.status
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, state.device = state.device, self.device.index
+
+        def __exit__(self, *_):
+            state.device = self.before
+
+    state.status = 0
+    monkeypatch.setattr(binding, "lib", lambda: SimpleNamespace(sn_some_call=entry, sn_status_string=lambda status: b"refused"))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state.device)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    plan = SimpleNamespace(device=torch.device("cuda:0"), current_stream=lambda index: 7,
+                           pointers=(Stand("pointers", log),))
+
+    def call(stream=None, **ws):
+        tensors = (Stand("input", log), None), (Stand("output", log), None)
+        binding._launch(plan, "sn_some_call", stream, Stand("ws", log, **ws), *tensors)
+
+    return SimpleNamespace(log=log, plan=plan, state=state, call=call)
+
+
+def test_a_call_on_the_current_stream_only_launches(world):
+    world.call()
+    world.call(Stand("same", world.log, raw=7))
+    assert world.log == [("call", 7, 0)] * 2
+
+
+def test_a_call_on_another_stream_is_ordered_behind_the_current_one(world):
+    """Outputs come from the current stream's memory, whose blocks its pending work may still use, and inputs and the
+    workspace's zeroing may be on their way there: the stream waits first, and all tensors are tied to it."""
+    world.call(Stand("side", world.log, raw=9))
+    assert world.log[0] == ("waits", "side", "current")
+    assert world.log[-1] == ("call", 9, 0)
+    assert {e[1] for e in world.log if e[0] == "tied" and e[2] == "side"} == {"ws", "pointers", "input", "output"}
+
+
+def test_a_refused_call_raises(world):
+    world.state.status = binding.SN_ERR_INVALID
+    with pytest.raises(binding.SnError):
+        world.call()

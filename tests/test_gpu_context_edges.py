@@ -128,3 +128,44 @@ def test_norm_backward_sums_of_long_columns_keep_their_digits(sn):
     worst = float((got["dbeta"].double() / want - 1).abs().max())
     print(f"   dbeta: {worst / (64 * R.U32):.2g} of the tolerance", flush=True)
     assert worst <= 64 * R.U32
+
+
+# ------------------------------------------------------------------ streams
+
+@pytest.mark.parametrize("what", ["attention", "norm"])
+def test_a_side_stream_needs_no_wait_of_its_own(sn, what):
+    """Inputs made on the current stream behind a queue of other work, whose temporaries are freed right before the
+    call: the call on another stream sees the inputs, and its outputs are not written over."""
+    import torch
+    print(f"[streams] {what}", flush=True)
+    side, busy = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    if what == "attention":
+        plan, c, where, ref, factor = attention_case(sn, [300, 90], [330, 150], 4, 2, 64, "bfloat16", True, True, "plain", seed=74)
+        want = attention_run(sn, plan, c, where)
+        make_ws, names = sn.cross_attention_workspace, ("q", "k", "v")
+    else:
+        plan, x, gamma, beta, dy, ref, factor = norm_case(sn, [900, 500], 128, 8, "ssp", "float32", seed=74)
+        want = norm_run(sn, plan, x, gamma, beta, dy)
+        make_ws, c, names = sn.group_norm_workspace, {"x": x}, ("x",)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(8):
+            busy = busy @ busy * 2.0 ** -12
+        live = {n: c[n].clone() for n in names}
+        spare = [torch.zeros_like(t) for t in live.values()]
+        for t in spare:
+            t.add_(busy[0, 0].to(t.dtype))
+        del spare, t
+        ws = make_ws(plan)
+        if what == "attention":
+            o, saved = sn.cross_attention_forward(plan, *(live[n] for n in names), ws, save=True, stream=side, **where)
+            outs = (o, *sn.cross_attention_backward(plan, *(live[n] for n in names), saved, c["d_o"], ws, stream=side, **where))
+            keys = ("o", "dq", "dk", "dv", "dbias")
+        else:
+            y, saved = sn.group_norm_forward(plan, live["x"], gamma, beta, ws, save=True, stream=side)
+            outs = (y, *sn.group_norm_backward(plan, live["x"], gamma, beta, saved, dy, ws, stream=side))
+            keys = ("y", "dx", "dgamma", "dbeta")
+        del live, ws, saved
+        torch.cuda.current_stream().wait_stream(side)
+        for name, t in zip(keys, outs):
+            assert torch.equal(want[name], t), name
