@@ -426,19 +426,27 @@ def _flat(t, name: str, shape, dtypes, device) -> int:
 
 
 def _launch(plan, name: str, stream, ws, inputs, outputs, *args):
-    """Call the entry point `name` with `args`, the workspace and the stream.
+    """Call the entry point `name` with `args`, the workspace and the stream, on the plan's device.
 
     An explicit stream waits for what the current one has been given so far (the outputs' memory may still be in use
     there, and the inputs or the workspace's zeroing on their way), and every tensor of the call is tied to it."""
-    device = plan.device
+    torch, device = _torch(), plan.device
     raw = plan.current_stream(device.index)
     if stream is not None and stream.cuda_stream != raw:
-        stream.wait_stream(_torch().cuda.current_stream(device))
+        if stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the plan to {device}")
+        stream.wait_stream(torch.cuda.current_stream(device))
         for t in (ws, *plan.pointers, *inputs, *outputs):
             if t is not None:
                 t.record_stream(stream)
         raw = stream.cuda_stream
-    _check(getattr(lib(), name)(*args, ws.data_ptr(), ws.numel(), raw), name)
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, ws.data_ptr(), ws.numel(), raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, ws.data_ptr(), ws.numel(), raw)
+    _check(st, name)
 
 
 def _current_stream_getter():

@@ -85,3 +85,18 @@ def test_a_refused_call_raises(world):
     world.state.status = binding.SN_ERR_INVALID
     with pytest.raises(binding.SnError):
         world.call()
+
+
+def test_a_call_launches_on_the_plans_device(world):
+    """The default stream's handle is the same on every device: the plan's has to be the current one."""
+    world.state.device = 1
+    world.call()
+    world.call(Stand("side", world.log, raw=9))
+    assert [e for e in world.log if e[0] == "call"] == [("call", 7, 0), ("call", 9, 0)]
+    assert world.state.device == 1
+
+
+def test_a_stream_of_another_device_is_refused(world):
+    with pytest.raises(ValueError):
+        world.call(Stand("side", world.log, raw=9, device="cuda:1"))
+    assert not world.log
