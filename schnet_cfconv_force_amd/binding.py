@@ -431,6 +431,10 @@ def _launch(plan, name: str, stream, ws, inputs, outputs, *args):
     An explicit stream waits for what the current one has been given so far (the outputs' memory may still be in use
     there, and the inputs or the workspace's zeroing on their way), and every tensor of the call is tied to it."""
     torch, device = _torch(), plan.device
+    # the kernels write the workspace: a host address there would fault
+    if device.type != "cuda" or ws.device != device or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous torch.uint8 tensor on the plan's GPU, not {ws.dtype} on {ws.device} "
+                         f"(the plan lies on {device})")
     raw = plan.current_stream(device.index)
     if stream is not None and stream.cuda_stream != raw:
         if stream.device != device:

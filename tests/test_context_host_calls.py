@@ -100,3 +100,17 @@ def test_a_stream_of_another_device_is_refused(world):
     with pytest.raises(ValueError):
         world.call(Stand("side", world.log, raw=9, device="cuda:1"))
     assert not world.log
+
+
+@pytest.mark.parametrize("ws", [{"device": "cpu"}, {"device": "cuda:1"}, {"dtype": torch.float32}], ids=str)
+def test_a_workspace_that_the_plans_gpu_cannot_use_is_refused(world, ws):
+    with pytest.raises(ValueError):
+        world.call(**ws)
+    assert not world.log
+
+
+def test_a_plan_on_the_host_makes_no_call(world):
+    world.plan.device = torch.device("cpu")
+    with pytest.raises(ValueError):
+        world.call(device="cpu")
+    assert not world.log
