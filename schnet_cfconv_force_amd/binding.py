@@ -415,6 +415,12 @@ def _rows(t, name: str, shape, dtype, device):
     return strides
 
 
+def _gradient(t):
+    """A gradient as it came, or laid out anew where its last index is not contiguous: the backward pass of a sum hands
+    down one number in every place, with strides of zero."""
+    return t if t.dim() == 0 or t.size(-1) <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
 def _flat(t, name: str, shape, dtypes, device) -> int:
     """Check an optional contiguous tensor; returns its address or 0."""
     if t is None:
@@ -564,11 +570,13 @@ def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=
 
 def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias=None, q_pos=None, k_pos=None,
                              keep=None, stream=None):
-    """sn_cross_attention_backward -> (dq, dk, dv, dbias) from the forward's `saved` and the gradient d_o of o;
-    dbias is None without a bias.  The other arguments are the forward's."""
+    """sn_cross_attention_backward -> (dq, dk, dv, dbias) from the forward's `saved` and the gradient d_o of o (any
+    strides; copied if its last index is not contiguous); dbias is None without a bias.  The other arguments are the
+    forward's."""
     torch = _torch()
     op = plan._bind(q, k, v, bias, q_pos, k_pos, keep)
     rows, lse = saved
+    d_o = _gradient(d_o)
     gs, gh, _ = _rows(d_o, "d_o", plan.q_shape, plan.dtype, plan.device)
     dq = torch.empty_like(q, memory_format=torch.contiguous_format)
     dk = torch.empty_like(k, memory_format=torch.contiguous_format)
@@ -635,9 +643,11 @@ def group_norm_forward(plan: GroupNorm, x, gamma, beta, ws, save: bool = False, 
 
 
 def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=None):
-    """sn_group_norm_backward -> (dx, dgamma, dbeta) from the forward's `saved` and the gradient dy of y."""
+    """sn_group_norm_backward -> (dx, dgamma, dbeta) from the forward's `saved` and the gradient dy of y (any strides;
+    copied if its last index is not contiguous)."""
     torch = _torch()
     op = plan._bind(x, gamma, beta)
+    dy = _gradient(dy)
     dy_stride, _ = _rows(dy, "dy", plan.shape, plan.dtype, plan.device)
     stats = (plan.n_segments, plan.n_groups)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format)

@@ -169,3 +169,27 @@ def test_a_side_stream_needs_no_wait_of_its_own(sn, what):
         torch.cuda.current_stream().wait_stream(side)
         for name, t in zip(keys, outs):
             assert torch.equal(want[name], t), name
+
+
+# ------------------------------------------------------------------ gradients as autograd hands them
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_gradients_of_any_strides(sn, dtype):
+    """The gradient of a sum is one number with strides of zero, that of a transposed use has its last index far apart."""
+    import torch
+    print(f"[gradients] strides {dtype}", flush=True)
+    dt = getattr(torch, dtype)
+    plan, c, where, _, _ = attention_case(sn, [70, 3], [65, 20], 4, 2, 32, dtype, True, False, "plain", seed=75)
+    ws = sn.cross_attention_workspace(plan)
+    o, saved = sn.cross_attention_forward(plan, c["q"], c["k"], c["v"], ws, save=True, **where)
+    norm, x, gamma, beta, _, _, _ = norm_case(sn, [70, 3], 32, 4, "silu", dtype, seed=75)
+    nws = sn.group_norm_workspace(norm)
+    y, stats = sn.group_norm_forward(norm, x, gamma, beta, nws, save=True)
+    for like, run in ((o, lambda g: sn.cross_attention_backward(plan, c["q"], c["k"], c["v"], saved, g, ws, **where)),
+                      (y, lambda g: sn.group_norm_backward(norm, x, gamma, beta, stats, g, nws))):
+        one = torch.full((), 0.5, dtype=dt, device="cuda").expand(like.shape)
+        across = c["d_o"].reshape(-1)[:like.numel()].reshape(like.shape[::-1]).permute(*reversed(range(like.dim())))
+        for g in (one, across):
+            assert g.stride(-1) != 1
+            for a, b in zip(run(g), run(g.contiguous())):
+                assert torch.equal(a, b)
