@@ -299,6 +299,9 @@ sn_status sn_read_status(void *ws, void *stream);
  * Any stride and element-aligned pointer is accepted (rows that are
  * 16-byte aligned with strides of 16 bytes load faster).  Outputs are
  * contiguous and are written for every row of every consistent segment.
+ * A launch has a place for the longest segment's rows in every segment and at
+ * most 2^32 threads: sizes beyond that are refused (SN_ERR_INVALID), as for
+ * 65536 segments of which one has 8192 rows of 8 heads.
  * The workspace begins with 256 bytes of status words, which the caller
  * zeroes once, before its first use.  Results do not depend on timing:
  * repeated calls give identical bits.  No call synchronises. */

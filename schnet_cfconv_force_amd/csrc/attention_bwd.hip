@@ -722,6 +722,11 @@ BwdPlan bwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
     return p;
 }
 
+bool fits(const BwdPlan &p, int B, int Hkv) {
+    return grid_fits((int64_t)B * Hkv * p.subs * p.row_tiles + kXcds, kAttnThreads) &&
+           grid_fits((int64_t)B * Hkv * p.splits * p.key_tiles + kXcds, kAttnThreads);
+}
+
 struct BwdLayout {
     size_t row, bias, kv, total;
 };
@@ -777,12 +782,22 @@ __global__ void fill_zero_kernel(float *x, int n) {
 
 }  // namespace
 
+// The thresholds, which are not read here, decide how many heads share a
+// table (1 to 8): the plan of each.
+static BwdPlan plan_of(const sn_cross_attention &op, int heads) {
+    return bwd_plan(op.n_segments, op.n_kv_heads, op.n_heads / op.n_kv_heads, op.max_q, op.max_k, kLutMax / heads);
+}
+
+bool attn_backward_fits(const sn_cross_attention &op) {
+    for (int heads = 1; heads <= 8; ++heads)
+        if (fits(plan_of(op, heads), op.n_segments, op.n_kv_heads)) return true;
+    return false;
+}
+
 size_t attn_backward_workspace(const sn_cross_attention &op) {
-    // the thresholds, which are not read here, decide how many heads share a table
     size_t need = kWsBase;
     for (int heads = 1; heads <= 8; ++heads) {
-        const BwdPlan p = bwd_plan(op.n_segments, op.n_kv_heads, op.n_heads / op.n_kv_heads, op.max_q, op.max_k,
-                                   kLutMax / heads);
+        const BwdPlan p = plan_of(op, heads);
         need = std::max(need, bwd_layout(p, op.n_segments, op.n_kv_heads, op.n_heads, op.n_q, op.n_k, op.head_dim,
                                          SN_MAX_BUCKETS).total);
     }
@@ -793,6 +808,7 @@ sn_status attn_backward(AttnArgs a, int dtype, const float *o, const float *lse,
                         float *dbias, char *ws, hipStream_t s) {
     ProfScope prof(K_ATTN_BWD, s);
     const BwdPlan p = bwd_plan(a.B, a.Hkv, a.G, a.max_q, a.max_k, a.lut_n);
+    if (!fits(p, a.B, a.Hkv)) return SN_ERR_INVALID;
     const BwdLayout L = bwd_layout(p, a.B, a.Hkv, a.H, a.n_q, a.n_k, a.D, a.nb);
     BwdArgs g{o, lse, dq, dk, dv, reinterpret_cast<float2 *>(ws + L.row), reinterpret_cast<float *>(ws + L.bias),
               reinterpret_cast<float *>(ws + L.kv)};

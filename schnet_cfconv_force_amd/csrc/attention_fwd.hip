@@ -468,12 +468,20 @@ FwdPlan fwd_plan(int B, int Hkv, int G, int max_q, int max_k, int lut_n) {
     return p;
 }
 
+// Wavefronts of a few-rows block: 160 KB of LDS hold their tiles.
+constexpr int few_waves(int np, int dp) { return np * dp <= 96 ? 8 : np * dp <= 192 ? 4 : 2; }
+
+bool fits(const FwdPlan &p, int B, int Hkv, int waves) {
+    return grid_fits((int64_t)B * Hkv * p.subs * p.splits * p.row_tiles + kXcds, p.few ? 64 * waves : kAttnThreads);
+}
+
 template <int NP, int DP, bool FAST>
-sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
+sn_status launch(const AttnArgs &a, const FwdOut &out, const FwdPlan &p, hipStream_t s) {
+    if (!fits(p, a.B, a.Hkv, few_waves(NP, DP))) return SN_ERR_INVALID;
     const int grid = xcd_grid(a.B * a.Hkv * a.subs * a.splits * a.row_tiles);
-    constexpr int NW = NP * DP <= 96 ? 8 : NP * DP <= 192 ? 4 : 2;   // 160 KB of LDS hold their tiles
+    constexpr int NW = few_waves(NP, DP);
     const size_t lut = a.nb ? (size_t)a.Gs * (a.lut_n + 2 * kLutPad) * sizeof(float) : 0;
-    if (few)
+    if (p.few)
         attn_few_kernel<NP, DP, NW, FAST><<<grid, 64 * NW, lut, s>>>(a, out);
     else
         attn_rows_kernel<NP, DP, kRowKeys<NP, DP>, FAST><<<grid, kAttnThreads, lut, s>>>(a, out);
@@ -486,20 +494,30 @@ sn_status launch(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) 
 }
 
 template <int NP, bool FAST>
-sn_status launch_dim(const AttnArgs &a, const FwdOut &out, bool few, hipStream_t s) {
-    if (a.D <= 32) return launch<NP, 32, FAST>(a, out, few, s);
-    if (a.D <= 64) return launch<NP, 64, FAST>(a, out, few, s);
-    return launch<NP, 128, FAST>(a, out, few, s);
+sn_status launch_dim(const AttnArgs &a, const FwdOut &out, const FwdPlan &p, hipStream_t s) {
+    if (a.D <= 32) return launch<NP, 32, FAST>(a, out, p, s);
+    if (a.D <= 64) return launch<NP, 64, FAST>(a, out, p, s);
+    return launch<NP, 128, FAST>(a, out, p, s);
 }
 
 }  // namespace
 
-size_t attn_forward_workspace(const sn_cross_attention &op) {
-    // the thresholds, which are not read here, decide how many heads share a table
-    size_t splits = 1;
+// The thresholds, which are not read here, decide how many heads share a
+// table (1 to 8): the plan of each.
+static FwdPlan plan_of(const sn_cross_attention &op, int heads) {
+    return fwd_plan(op.n_segments, op.n_kv_heads, op.n_heads / op.n_kv_heads, op.max_q, op.max_k, kLutMax / heads);
+}
+
+bool attn_forward_fits(const sn_cross_attention &op) {
+    const int dp = op.head_dim <= 32 ? 32 : op.head_dim <= 64 ? 64 : 128;
     for (int heads = 1; heads <= 8; ++heads)
-        splits = std::max<size_t>(splits, fwd_plan(op.n_segments, op.n_kv_heads, op.n_heads / op.n_kv_heads, op.max_q,
-                                                   op.max_k, kLutMax / heads).splits);
+        if (fits(plan_of(op, heads), op.n_segments, op.n_kv_heads, few_waves(op.dtype == SN_F32 ? 3 : 1, dp))) return true;
+    return false;
+}
+
+size_t attn_forward_workspace(const sn_cross_attention &op) {
+    size_t splits = 1;
+    for (int heads = 1; heads <= 8; ++heads) splits = std::max<size_t>(splits, plan_of(op, heads).splits);
     if (splits == 1) return kWsBase;
     const size_t rows = (size_t)op.n_q * op.n_heads;
     return kWsBase + align256(rows * splits * sizeof(float2)) + align256(rows * splits * op.head_dim * sizeof(float));
@@ -515,8 +533,8 @@ sn_status attn_forward(AttnArgs a, int dtype, void *o, float *rows, float *lse, 
         out.part_ml = reinterpret_cast<float2 *>(ws + kWsBase);
         out.part_o = reinterpret_cast<float *>(ws + kWsBase + align256(n * p.splits * sizeof(float2)));
     }
-    if (dtype == SN_F32) return a.fast ? launch_dim<3, true>(a, out, p.few, s) : launch_dim<3, false>(a, out, p.few, s);
-    return a.fast ? launch_dim<1, true>(a, out, p.few, s) : launch_dim<1, false>(a, out, p.few, s);
+    if (dtype == SN_F32) return a.fast ? launch_dim<3, true>(a, out, p, s) : launch_dim<3, false>(a, out, p, s);
+    return a.fast ? launch_dim<1, true>(a, out, p, s) : launch_dim<1, false>(a, out, p, s);
 }
 
 }  // namespace sn

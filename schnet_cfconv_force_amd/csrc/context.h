@@ -15,6 +15,11 @@ typedef __bf16 bf16;
 __device__ inline float to_f32(float v) { return v; }
 __device__ inline float to_f32(bf16 v) { return (float)v; }
 
+// --------------------------------------------------------------- grids
+
+// A launch counts its threads in 32 bits.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads <= UINT32_MAX; }
+
 // --------------------------------------------------------------- ragged rows
 
 // Rows of segment b: start and length, or length 0 where the pointer array
@@ -58,6 +63,10 @@ struct AttnArgs {
     int32_t thr[SN_MAX_BUCKETS];              // padded with the largest value
 };
 
+// Whether a call of these sizes has grids that fit, with some pointers and
+// thresholds; the launches check their own.
+bool attn_forward_fits(const sn_cross_attention &op);
+bool attn_backward_fits(const sn_cross_attention &op);
 size_t attn_forward_workspace(const sn_cross_attention &op);
 size_t attn_backward_workspace(const sn_cross_attention &op);
 sn_status attn_forward(AttnArgs a, int dtype, void *o, float *rows, float *lse, char *ws, hipStream_t s);
@@ -76,6 +85,7 @@ struct NormArgs {
     int *status;
 };
 
+bool norm_fits(const sn_group_norm &op);
 size_t norm_workspace(const sn_group_norm &op);
 sn_status norm_forward(const NormArgs &a, int dtype, void *y, float *mean, float *rstd, char *ws, hipStream_t s);
 sn_status norm_backward(const NormArgs &a, int dtype, const float *mean, const float *rstd, void *dx, float *dgamma,

@@ -33,10 +33,9 @@ sn_status check_attn_sizes(const sn_cross_attention *op) {
     // rows are counted with their heads in 32-bit block and row indices
     if ((int64_t)op->n_q * op->n_heads > INT32_MAX || (int64_t)op->n_k * op->n_kv_heads > INT32_MAX)
         return SN_ERR_INVALID;
-    // the launches hold one block for the longest segment's tiles in every segment
-    const int64_t tiles = ((int64_t)op->max_q * op->n_heads + (int64_t)op->max_k * op->n_kv_heads) / 16 + op->n_heads;
-    if (tiles * op->n_segments > INT32_MAX / 2) return SN_ERR_INVALID;
     if (op->bias && (op->n_buckets < 1 || op->n_buckets > SN_MAX_BUCKETS)) return SN_ERR_INVALID;
+    // the launches hold the longest segment's tiles for every segment
+    if (!attn_forward_fits(*op) || !attn_backward_fits(*op)) return SN_ERR_INVALID;
     return SN_OK;
 }
 
@@ -110,10 +109,7 @@ sn_status check_norm_sizes(const sn_group_norm *op) {
         return SN_ERR_INVALID;
     if (op->dtype != SN_F32 && op->dtype != SN_BF16) return SN_ERR_INVALID;
     if (op->activation < SN_ACT_NONE || op->activation > SN_ACT_SILU) return SN_ERR_INVALID;
-    // blocks are counted in 32 bits: at most one for 2048 elements of every segment's longest, one for each of
-    // its channels and 512 more
-    const double blocks = (double)op->max_rows * op->n_channels / 2048 + op->n_channels + 512;
-    if (blocks * op->n_segments > INT32_MAX) return SN_ERR_INVALID;
+    if (!norm_fits(*op)) return SN_ERR_INVALID;
     return SN_OK;
 }
 

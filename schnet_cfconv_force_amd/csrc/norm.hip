@@ -751,9 +751,15 @@ NormLayout norm_layout(const NormCut &k, int64_t B, int64_t C, int64_t groups) {
     return L;
 }
 
+bool fits(const NormCut &k, int B, int C, int groups) {
+    return grid_fits((int64_t)B * k.slabs * k.chunks + (C + 63) / 64, kThreads) &&
+           (k.fused || grid_fits((int64_t)B * groups, 256));
+}
+
 template <typename T, int V, int ACT>
 sn_status forward_v(const NormArgs &a, void *y, float *mean, float *rstd, char *ws, hipStream_t s) {
     const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, false);
+    if (!fits(k, a.B, a.C, a.groups)) return SN_ERR_INVALID;
     const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
     const int grid = a.B * k.slabs * k.chunks;
     if (k.fused) {
@@ -776,6 +782,7 @@ template <typename T, int V, int ACT>
 sn_status backward_v(const NormArgs &a, const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta,
                      char *ws, hipStream_t s) {
     const NormCut k = norm_cut(a.B, a.max_rows, a.C, a.groups, sizeof(T), V, true);
+    if (!fits(k, a.B, a.C, a.groups)) return SN_ERR_INVALID;
     const NormLayout L = norm_layout(k, a.B, a.C, a.groups);
     const int grid = a.B * k.slabs * k.chunks, params = dgamma || dbeta ? (a.C + 63) / 64 : 0;
     float *seg = reinterpret_cast<float *>(ws + L.seg), *part = reinterpret_cast<float *>(ws + L.part);
@@ -839,15 +846,33 @@ sn_status backward_t(const NormArgs &a, const float *mean, const float *rstd, vo
 
 }  // namespace
 
-size_t norm_workspace(const sn_group_norm &op) {
+// Calls f with the two passes' cuts for each vector (which one is taken
+// depends on the tensors).
+template <typename F>
+static void each_cut(const sn_group_norm &op, F f) {
     const int es = op.dtype == SN_F32 ? 4 : 2, width = op.n_channels / op.n_groups;
+    auto cut = [&](int V, bool backward) {
+        return norm_cut(op.n_segments, op.max_rows, op.n_channels, op.n_groups, es, V, backward);
+    };
+    for (int V = 16 / es; V >= 1; V /= 2)
+        if (width % V == 0) f(cut(V, false), cut(V, true));
+}
+
+bool norm_fits(const sn_group_norm &op) {
+    bool some = false;
+    each_cut(op, [&](const NormCut &fwd, const NormCut &bwd) {
+        some = some || (fits(fwd, op.n_segments, op.n_channels, op.n_groups) &&
+                        fits(bwd, op.n_segments, op.n_channels, op.n_groups));
+    });
+    return some;
+}
+
+size_t norm_workspace(const sn_group_norm &op) {
     size_t need = kWsBase;
-    for (int V = 16 / es; V >= 1; V /= 2)   // which one depends on the tensors
-        if (width % V == 0)
-            for (bool backward : {false, true})
-                need = std::max(need, norm_layout(norm_cut(op.n_segments, op.max_rows, op.n_channels, op.n_groups, es, V,
-                                                           backward),
-                                                  op.n_segments, op.n_channels, op.n_groups).total);
+    each_cut(op, [&](const NormCut &fwd, const NormCut &bwd) {
+        for (const NormCut &k : {fwd, bwd})
+            need = std::max(need, norm_layout(k, op.n_segments, op.n_channels, op.n_groups).total);
+    });
     return need;
 }
 

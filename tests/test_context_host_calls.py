@@ -1,5 +1,7 @@
 """CPU checks of how the context operators' calls reach the library: streams, devices and workspaces, with stand-ins for
 what needs a GPU."""
+import ctypes
+import os
 from types import SimpleNamespace
 
 import pytest
@@ -114,3 +116,30 @@ def test_a_plan_on_the_host_makes_no_call(world):
     with pytest.raises(ValueError):
         world.call(device="cpu")
     assert not world.log
+
+
+# ------------------------------------------------------------------ grids
+
+def _lib():
+    if not os.path.exists(binding.LIB_PATH):
+        from schnet_cfconv_force_amd import build
+        build.build(verbose=False)
+    return binding.lib()
+
+
+@pytest.mark.parametrize("segments,fits", [(1 << 10, True), (1 << 14, True), (1 << 16, False)])
+def test_sizes_whose_grids_a_launch_cannot_hold_are_refused(segments, fits):
+    """One long segment among many: 64 tiles of 128 rows and 8 heads, or 16 chunks of 16 slabs, for each of them; a
+    launch has at most 2^32 threads, 2^24 blocks of 256 or 2^23 of 512."""
+    lib = _lib()
+    for side in ("q", "k"):
+        n = {"q": (segments, 1), "k": (segments, 1), side: (segments + 8191, 8192)}
+        d = binding.SnCrossAttention(segments, n["q"][0], n["k"][0], n["q"][1], n["k"][1], 256, 256, 8, 8, 32, binding.SN_BF16, 1.0,
+                                     256, 256, 256, 256, 32, 256, 32, 256, 32)
+        assert (lib.sn_cross_attention_workspace_bytes(ctypes.byref(d)) > 0) == fits, side
+        if not fits:
+            assert lib.sn_cross_attention_forward(ctypes.byref(d), 256, None, 256, 1 << 60, None) == binding.SN_ERR_INVALID
+    d = binding.SnGroupNorm(segments, segments + 8191, 8192, 256, 512, 32, binding.SN_ACT_SSP, binding.SN_F32, 1e-5, 256, 512)
+    assert (lib.sn_group_norm_workspace_bytes(ctypes.byref(d)) > 0) == fits
+    if not fits:
+        assert lib.sn_group_norm_forward(ctypes.byref(d), 256, None, None, 256, 1 << 60, None) == binding.SN_ERR_INVALID
