@@ -16,8 +16,9 @@
 // both passes round alike: the scores' products in one order, the exponents as
 // s scale + (bias - lse), whichever way a tile's bias is read, and
 // sums over many rows are joined pairwise (fp32, 1272 rows of 16 keys: dbias
-// 2.0e-6 of its norm off without the two, 2.9e-7 with them).  A single key has
-// p = 1 whatever its score: its dS is zero, not what rounding leaves.
+// 2.0e-6 of its norm off without the two, 2.9e-7 with them).  A segment's only
+// kept key has p = 1 whatever its score: its dS is zero, not what rounding
+// leaves.  The first pass counts the kept keys for the second.
 #include <algorithm>
 
 #include "attention.h"
@@ -42,6 +43,7 @@ struct BwdArgs {
     float2 *row;        // [n_q H] {lse log2e - 12 (+inf: no key), delta}
     float *part_bias;   // [Hkv][B key_tiles splits][G nb]
     float *part_kv;     // [split][n_k Hkv][2][D] (splits > 1)
+    int *kept;          // [B] kept keys (with a mask, of the segments that have rows)
 };
 
 // Keys of a tile in LDS, of which 32 at a time are computed: 64 halve the
@@ -176,6 +178,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e) dq[e] = zero16();
     float row_ds = 0.0f;    // sum of the row's dS (this half's keys)
+    int n_kept = 0;
     const TileLane<DP> tl(lane);
     const uint32_t lds0 = lds_offset(tiles);
     constexpr uint32_t kPlane = kDqKeys * DP * sizeof(bf16), kBytes = NP * kPlane;
@@ -187,6 +190,7 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
         const int buf = t & 1;
         const uint32_t kt = lds0 + 2 * buf * kBytes, vt = kt + kBytes;
         const KeyInfo<kDqKeys> &ki = info[buf];
+        n_kept += __popcll(mask);
         if (active && mask) {
             float less = -L;
             const float *mine = lut + hg * lut_stride(a);
@@ -266,9 +270,10 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
     }
     // the row's sum of dS in units of p (sum_j p_ij is 2^12 by construction)
     const float err = half_sum(row_ds) * kUnlift;
+    if (a.keep && w.tile == 0 && w.sub == 0 && w.hk == 0 && tid == 0) g.kept[w.b] = n_kept;
     if (row >= 0) {
         T *out = (T *)g.dq + at * a.D;
-        const float f = w.nk == 1 ? 0.0f : a.scale * kUnlift;
+        const float f = n_kept == 1 ? 0.0f : a.scale * kUnlift;
 #pragma unroll
         for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
@@ -372,6 +377,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
         for (int i = tid; a.nb && i < a.G * a.nb; i += kAttnThreads) part[i] = 0.0f;
         return;
     }
+    const bool lone = (a.keep && nq > 0 ? g.kept[b] : nk) == 1;   // one kept key in the segment
     // the rows of all heads that share these keys, head by head
     const int per_head = (nq + kRows - 1) / kRows, n_tiles = per_head * a.G, per = (n_tiles + a.splits - 1) / a.splits;
     const int t0 = split * per, t1 = min(n_tiles, t0 + per);
@@ -515,7 +521,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             }
             s += __shfl_xor(s, 1, 64);
             s += __shfl_xor(s, 2, 64);
-            if (q == 0) part[head * a.nb + bk] = nk == 1 ? 0.0f : s;
+            if (q == 0) part[head * a.nb + bk] = lone ? 0.0f : s;
         }
         __syncthreads();
     };
@@ -665,7 +671,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
     if (a.nb && head >= 0) finish_head();
     if (!have) return;
     const int64_t at = (int64_t)(k0 + j) * a.Hkv + hk;
-    const float fk = nk == 1 ? 0.0f : a.scale * kUnlift;
+    const float fk = lone ? 0.0f : a.scale * kUnlift;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
@@ -728,7 +734,7 @@ bool fits(const BwdPlan &p, int B, int Hkv) {
 }
 
 struct BwdLayout {
-    size_t row, bias, kv, total;
+    size_t row, bias, kv, kept, total;
 };
 BwdLayout bwd_layout(const BwdPlan &p, int B, int Hkv, int H, int64_t n_q, int64_t n_k, int D, int nb) {
     BwdLayout L;
@@ -737,6 +743,7 @@ BwdLayout bwd_layout(const BwdPlan &p, int B, int Hkv, int H, int64_t n_q, int64
     L.row = take(n_q * H * sizeof(float2));
     L.bias = take((size_t)H * B * p.key_tiles * p.splits * nb * sizeof(float));
     L.kv = take(p.splits > 1 ? (size_t)p.splits * n_k * Hkv * 2 * D * sizeof(float) : 0);
+    L.kept = take(B * sizeof(int));
     L.total = o;
     return L;
 }
@@ -811,7 +818,7 @@ sn_status attn_backward(AttnArgs a, int dtype, const float *o, const float *lse,
     if (!fits(p, a.B, a.Hkv)) return SN_ERR_INVALID;
     const BwdLayout L = bwd_layout(p, a.B, a.Hkv, a.H, a.n_q, a.n_k, a.D, a.nb);
     BwdArgs g{o, lse, dq, dk, dv, reinterpret_cast<float2 *>(ws + L.row), reinterpret_cast<float *>(ws + L.bias),
-              reinterpret_cast<float *>(ws + L.kv)};
+              reinterpret_cast<float *>(ws + L.kv), reinterpret_cast<int *>(ws + L.kept)};
     if (a.fast)
         SN_TRY((dtype == SN_F32 ? launch_dim<3, true>(a, g, p, s) : launch_dim<1, true>(a, g, p, s)));
     else

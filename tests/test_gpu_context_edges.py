@@ -44,6 +44,27 @@ def test_attention_masks_in_runs_of_keys(sn, dtype, D, mask, thr, positions):
     attention_check(attention_run(sn, plan, c, where), ref, factor, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lq", [[3, 1, 2], [200, 77, 40]], ids=str)
+def test_attention_of_a_single_kept_key_has_no_score_gradient(sn, lq, dtype):
+    """Of the many keys of each segment but the last the mask keeps one: its weight is one whatever its score."""
+    import torch
+    print(f"[attention] single kept keys {lq} {dtype}", flush=True)
+    lk = [150, 90, 70]
+    plan, c, where, ref, factor = attention_case(sn, lq, lk, 4, 2, 40, dtype, True, False, "plain", seed=76, spread=20.0)
+    keep = torch.zeros(sum(lk), dtype=torch.bool, device="cuda")
+    keep[[140, 151]] = True
+    keep[240:] = True
+    where["keep"] = keep
+    ref, factor = R.attention(c["q"], c["k"], c["v"], plan.q_ptr.cpu().numpy(), plan.k_ptr.cpu().numpy(), plan.scale, where["bias"],
+                              sn.relative_thresholds(32, 128), where["q_pos"], where["k_pos"], keep, c["d_o"])
+    got = attention_run(sn, plan, c, where)
+    attention_check(got, ref, factor, dtype)
+    n = sum(lq[:2])
+    assert not bool(got["dq"][:n].any()) and not bool(got["dk"][:240].any())
+    assert bool(got["dq"][n:].any()) and bool(got["dk"][240:].any())
+
+
 # ------------------------------------------------------------------ cross attention: bits of the weights
 
 @pytest.mark.parametrize("lq,lk,D", [([70, 3], [400, 65], 64), ([150], [1300], 128), ([2, 1], [700, 300], 128), ([9], [2500], 40)],
