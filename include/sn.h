@@ -329,6 +329,10 @@ sn_status sn_read_status(void *ws, void *stream);
  *     p    = exp(s) / sum over the kept keys of exp(s)
  *     o_ih = sum over the kept keys of p v_jh
  * A row without a kept key gives o = 0 and lse = -inf, and zero gradients.
+ * A bias of -726817 or less (2^20 ln 2; -inf and the type's lowest value
+ * among them) removes its keys from the row as if they were not kept.  Other
+ * biases are finite, best within +-1e4: a score keeps the fp32 digits that its
+ * bias leaves.
  * Keys that are not kept are never multiplied in: whatever they hold (NaN
  * and infinities too) does not reach an output, and their gradients are 0. */
 typedef struct sn_cross_attention {

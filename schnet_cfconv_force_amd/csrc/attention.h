@@ -417,11 +417,19 @@ __device__ inline bool locate(const AttnArgs &a, RowBlock &w) {
     return true;
 }
 
+// A bias in log2 units; from -2^20 down it removes the key.  Scores that far
+// down have lost their digits beside it, and with every key of a row there the
+// log-sum could not hold what the backward pass's p is made of.
+__device__ inline float bias_log2(float b) {
+    const float x = b * kLog2e;
+    return x <= -1048576.0f ? -INFINITY : x;
+}
+
 // Position table of the subgroup's heads, in log2 units.
 __device__ inline void fill_lut(const AttnArgs &a, const RowBlock &w, float *lut) {
     for (int e = threadIdx.x; e < lut_stride(a); e += blockDim.x) {
         const int bk = bucket_of(a, a.lut_base + min(max(e - kLutPad, 0), a.lut_n - 1));
-        for (int g = 0; g < w.gs; ++g) lut[g * lut_stride(a) + e] = a.bias[(int64_t)(w.h0 + g) * a.nb + bk] * kLog2e;
+        for (int g = 0; g < w.gs; ++g) lut[g * lut_stride(a) + e] = bias_log2(a.bias[(int64_t)(w.h0 + g) * a.nb + bk]);
     }
 }
 

@@ -542,7 +542,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
             if (head >= 0) finish_head();
             head = tile_head;
             for (int e = tid; e < lut_stride(a); e += kAttnThreads)
-                lut[e].x = a.bias[(int64_t)(hk * a.G + head) * a.nb + __float_as_int(lut[e].y)] * kLog2e;
+                lut[e].x = bias_log2(a.bias[(int64_t)(hk * a.G + head) * a.nb + __float_as_int(lut[e].y)]);
             for (int i = tid; i < 4 * a.nb * 32; i += kAttnThreads) sums[i] = 0.0f;
             if (small_lut)
                 for (int i = tid; i < 4 * run_n; i += kAttnThreads) bias_mem[bl.run + i] = 0.0f;

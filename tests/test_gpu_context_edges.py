@@ -65,6 +65,70 @@ def test_attention_of_a_single_kept_key_has_no_score_gradient(sn, lq, dtype):
     assert bool(got["dq"][n:].any()) and bool(got["dk"][240:].any())
 
 
+def attention_dense(plan, c, where, thresholds, allowed):
+    """Values in 64 bits, one head of one segment at a time, over the keys that `allowed` (bias bucket [n, m], kept [m])
+    leaves to each row; a row that it leaves none is zeros.  Also the root of the sum of each output's squared terms."""
+    import torch
+    q, k, v, g = (c[n].double().cpu() for n in ("q", "k", "v", "d_o"))
+    H, G = plan.n_heads, plan.n_heads // plan.n_kv_heads
+    names = {"o": q, "dq": q, "dk": k, "dv": v}
+    out, rss = ({n: torch.zeros_like(t) for n, t in names.items()} for _ in range(2))
+    bias = where["bias"].double().cpu()
+    out["dbias"] = torch.zeros_like(bias)
+    qp, kp = plan.q_ptr.tolist(), plan.k_ptr.tolist()
+    for a, b, e, f in zip(qp[:-1], qp[1:], kp[:-1], kp[1:]):
+        pos = [w[i:j].cpu().numpy().astype(np.int64) if w is not None else np.arange(j - i)
+               for w, i, j in ((where["q_pos"], a, b), (where["k_pos"], e, f))]
+        bk = torch.from_numpy(R.bucket(np.clip(pos[1][None] - pos[0][:, None], -2 ** 31, 2 ** 31 - 1), thresholds))
+        keep = torch.ones(f - e, dtype=torch.bool) if where["keep"] is None else where["keep"][e:f].cpu()
+        for h in range(H):
+            ok = allowed(h, bk) & keep[None]
+            add = torch.where(ok, bias[h][bk], torch.full((), -torch.inf, dtype=torch.float64))
+            x = q[a:b, h] @ k[e:f, h // G].T * plan.scale + add
+            top = x.amax(1, keepdim=True) if f > e else torch.zeros((b - a, 1), dtype=torch.float64)
+            p = torch.exp(x - torch.where(torch.isinf(top), torch.zeros_like(top), top))
+            p = p / p.sum(1, keepdim=True).clamp_min(1e-300)
+            o = p @ v[e:f, h // G]
+            ds = p * (g[a:b, h] @ v[e:f, h // G].T - (g[a:b, h] * o).sum(1, keepdim=True))
+            for name, at, left, right, f_ in (("o", (slice(a, b), h), p, v[e:f, h // G], 1.0),
+                                              ("dq", (slice(a, b), h), ds, k[e:f, h // G], plan.scale),
+                                              ("dk", (slice(e, f), h // G), ds.T, q[a:b, h], plan.scale),
+                                              ("dv", (slice(e, f), h // G), p.T, g[a:b, h], 1.0)):
+                out[name][at] += left @ right * f_
+                rss[name][at] += (left ** 2) @ (right ** 2) * f_ ** 2
+            out["dbias"][h] += torch.bincount(bk.reshape(-1), ds.reshape(-1), minlength=bias.shape[1])
+    return out, {n: t.sqrt() for n, t in rss.items()}
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("low", [-float("inf"), -3.4028234663852886e38, -1e9, -1e6], ids=str)
+@pytest.mark.parametrize("lq,lk", [([2, 1], [300, 40]), ([150, 33], [130, 257])], ids=str)
+def test_attention_biases_that_remove_keys(sn, lq, lk, low, dtype):
+    """A head's buckets of a bias as low as a mask's: their keys count as absent, also where a row has no others."""
+    import torch
+    print(f"[attention] bias {low} {lq} {lk} {dtype}", flush=True)
+    thr = np.array([-60, -20, -3, 0, 5, 40], np.int32)
+    plan, c, where, _, factor = attention_case(sn, lq, lk, 4, 2, 32, dtype, thr, True, "plain", seed=77, gen_pos="default")
+    removed = torch.zeros((4, 7), dtype=torch.bool)
+    removed[0, [3, 4]] = True            # a band
+    removed[1, 4:] = True                # later keys
+    removed[2] = True                    # all: every row of the head is empty
+    where["bias"] = torch.where(removed.cuda(), torch.full((), low, device="cuda"), where["bias"])
+    want, rss = attention_dense(plan, c, {**where, "bias": where["bias"].masked_fill(removed.cuda(), 0.0)}, thr,
+                                lambda h, bk: ~removed[h][bk])
+    got = attention_run(sn, plan, c, where)
+    assert torch.equal(got["o"], got["served"])
+    assert bool(torch.isneginf(got["lse"][:, 2]).all()) and not bool(got["o"][:, 2].any())
+    assert not bool(got["dbias"].cpu()[removed].any())
+    for name, value in want.items():
+        # bf16: two roundings of 2^-8 / sqrt(3) root mean square, of the output and of one operand of each term
+        bound = 2.0 ** -12 if name == "dbias" or dtype == "float32" else 2.0 ** -7.5
+        scale = value.norm() if name not in rss else torch.maximum(value.norm(), rss[name].norm())
+        off = float((got[name].double().cpu() - value).norm() / scale)
+        print(f"   {name}: {off:.2g}", flush=True)
+        assert off <= bound, name
+
+
 # ------------------------------------------------------------------ cross attention: bits of the weights
 
 @pytest.mark.parametrize("lq,lk,D", [([70, 3], [400, 65], 64), ([150], [1300], 128), ([2, 1], [700, 300], 128), ([9], [2500], 40)],
