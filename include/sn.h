@@ -359,12 +359,16 @@ typedef struct sn_cross_attention {
     const int32_t *k_pos;        /* device [n_k], or NULL: the same */
 } sn_cross_attention;
 
-/* Thresholds of the usual logarithmic buckets (host only): n_buckets (even,
- * >= 4) / 2 buckets for rel <= 0 by the distance -rel and as many for
- * rel > 0 by rel - 1; of each half, the nearer half hold one distance each,
- * the others grow by equal ratios up to max_distance, from where the last is
- * open.  Writes n_buckets - 1 values.  SN_ERR_INVALID on an odd or
- * out-of-range count or max_distance <= n_buckets / 4. */
+/* Thresholds of logarithmic buckets (host only): n_buckets (even, >= 4) / 2
+ * buckets for rel <= 0 by the distance -rel and as many for rel > 0 by
+ * rel - 1, so that every bucket is used; of each half, the nearer half hold
+ * one distance each, the others grow by equal ratios up to max_distance, from
+ * where the last is open.  In order of rel: bucket n_buckets/2 - 1 holds
+ * rel = 0, bucket n_buckets/2 holds rel = 1.  (Tables trained with |rel| on
+ * both sides leave the first bucket of rel > 0 empty: lower the thresholds
+ * above 1 by one for those, and put their columns in order of rel.)
+ * Writes n_buckets - 1 values.  SN_ERR_INVALID on an odd or out-of-range
+ * count or max_distance <= n_buckets / 4. */
 sn_status sn_relative_thresholds(int32_t n_buckets, int32_t max_distance, int32_t *thresholds);
 
 /* Bytes of workspace of both calls below (host; sizes only, no pointer of

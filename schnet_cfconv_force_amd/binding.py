@@ -475,7 +475,10 @@ def _zeroed_workspace(plan):
 
 
 def relative_thresholds(n_buckets: int = 32, max_distance: int = 128) -> np.ndarray:
-    """sn_relative_thresholds: int32 [n_buckets - 1]; bucket(rel) = number of thresholds <= rel."""
+    """sn_relative_thresholds: int32 [n_buckets - 1]; bucket(rel) = number of thresholds <= rel.
+
+    Logarithmic by -rel for rel <= 0 and by rel - 1 for rel > 0.  For a table trained with |rel| on both sides, lower
+    the thresholds above 1 by one (thr[thr > 1] -= 1) and put its columns in order of rel."""
     out = np.zeros(max(int(n_buckets) - 1, 1), np.int32)
     _check(lib().sn_relative_thresholds(int(n_buckets), int(max_distance), out.ctypes.data), "sn_relative_thresholds")
     return out

@@ -1,9 +1,11 @@
 """CPU checks of how the context operators' calls reach the library: streams, devices and workspaces, with stand-ins for
 what needs a GPU."""
 import ctypes
+import math
 import os
 from types import SimpleNamespace
 
+import numpy as np
 import pytest
 import torch
 
@@ -143,3 +145,23 @@ def test_sizes_whose_grids_a_launch_cannot_hold_are_refused(segments, fits):
     assert (lib.sn_group_norm_workspace_bytes(ctypes.byref(d)) > 0) == fits
     if not fits:
         assert lib.sn_group_norm_forward(ctypes.byref(d), 256, None, None, 256, 1 << 60, None) == binding.SN_ERR_INVALID
+
+
+# ------------------------------------------------------------------ thresholds of other conventions
+
+@pytest.mark.parametrize("n_buckets,far", [(8, 20), (32, 128), (64, 128)])
+def test_thresholds_of_tables_by_absolute_distance(n_buckets, far):
+    """Logarithmic buckets by |rel| on both sides, one offset at a time: the thresholds above 1 lowered by one give the
+    same classes, in order of rel."""
+    _lib()
+    half, near = n_buckets // 2, n_buckets // 4
+
+    def by_distance(rel):
+        d = abs(rel)
+        j = d if d < near else min(half - 1, near + int(math.log(d / near) / math.log(far / near) * (half - near) + 1e-12))
+        return half - 1 - j if rel <= 0 else half + j
+
+    thr = binding.relative_thresholds(n_buckets, far)
+    thr[thr > 1] -= 1
+    rel = np.arange(-2 * far, 2 * far + 1)
+    assert np.searchsorted(thr, rel, side="right").tolist() == [by_distance(int(r)) for r in rel]
