@@ -334,7 +334,10 @@ sn_status sn_read_status(void *ws, void *stream);
  * biases are finite, best within +-1e4: a score keeps the fp32 digits that its
  * bias leaves.
  * Keys that are not kept are never multiplied in: whatever they hold (NaN
- * and infinities too) does not reach an output, and their gradients are 0. */
+ * and infinities too) does not reach an output, and their gradients are 0.
+ * Infinities and values near the type's end in rows that count give what the
+ * formulas give, in the forward pass (a row of them is computed apart, and
+ * takes longer); the backward pass takes finite rows below 3.39e38. */
 typedef struct sn_cross_attention {
     int32_t n_segments;          /* B >= 1 */
     int32_t n_q, n_k;            /* rows of all segments, >= 0 */

@@ -230,6 +230,84 @@ __device__ inline void write_stats(const AttnArgs &a, const FwdOut &out, int spl
         out.lse[at] = log_sum(m, l);
 }
 
+// One row and head by the definition in fp32, by one wavefront: where the
+// products cannot give it.  They are sums over bf16 parts (of p, and of fp32
+// rows), and the parts of an infinity or of what bf16 rounds to one are no sum;
+// a large value may overflow beside p > 1.  Lanes take a key each for the
+// scores and the running maximum and sum, then an element each for the row.
+// q0, k0, nk: the segment's rows; row: the query's.
+template <int NP>
+__device__ inline void plain_row(const AttnArgs &a, const FwdOut &out, int row, int h, int q0, int k0, int nk, int lane) {
+    using T = typename RowOf<NP>::T;
+    const int hk = h / a.G;
+    const T *q = (const T *)a.q + row * a.qs + h * a.qh;
+    const T *K = (const T *)a.k + k0 * a.ks + hk * a.kh, *V = (const T *)a.v + k0 * a.vs + hk * a.vh;
+    const int pos = a.q_pos ? a.q_pos[row] : row - q0;
+    auto kept = [&](int j) { return j < nk && (!a.keep || a.keep[k0 + j]); };
+    auto score = [&](int j) {   // in log2 units
+        float dot = 0.0f;
+#pragma unroll 1
+        for (int d = 0; d < a.D; ++d) dot = fmaf(to_f32(q[d]), to_f32(K[(int64_t)j * a.ks + d]), dot);
+        const float x = dot * (a.scale * kLog2e);
+        if (!a.nb) return x;
+        return x + bias_log2(a.bias[(int64_t)h * a.nb + bucket_of(a, offset_of(a.k_pos ? a.k_pos[k0 + j] : j, pos))]);
+    };
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+    for (int j = lane; j < nk; j += 64) {
+        const float x = kept(j) ? score(j) : -INFINITY;
+        if (x == -INFINITY) continue;
+        const float mn = fmaxf(m, x);   // (a score that is no number: the sum is none)
+        l = (m == -INFINITY ? l : l * __builtin_amdgcn_exp2f(m - mn)) + __builtin_amdgcn_exp2f(x - mn);
+        m = mn;
+    }
+    float top = m;
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    l = l == 0.0f ? 0.0f : l * __builtin_amdgcn_exp2f(m - top);
+    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o, 64);
+    const float inv = inverse(l);
+    float acc[2] = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int j0 = 0; j0 < nk && l != 0.0f; j0 += 64) {
+        const bool have = kept(j0 + lane);
+        const float p = have ? __builtin_amdgcn_exp2f(score(j0 + lane) - top) * inv : 0.0f;
+        uint64_t left = __ballot(have);
+        while (left) {
+            const int t = __ffsll((unsigned long long)left) - 1;
+            left &= left - 1;
+            const float pt = __shfl(p, t, 64);
+            for (int u = 0; u < 2; ++u)
+                if (lane + 64 * u < a.D) acc[u] = fmaf(pt, to_f32(V[(int64_t)(j0 + t) * a.vs + lane + 64 * u]), acc[u]);
+        }
+    }
+    const int64_t at = (int64_t)row * a.H + h;
+    for (int u = 0; u < 2; ++u) {
+        const int d = lane + 64 * u;
+        if (d >= a.D) continue;
+        ((T *)out.o)[at * a.D + d] = (T)acc[u];
+        if (NP == 1 && out.rows) out.rows[at * a.D + d] = acc[u];
+    }
+    if (lane == 0 && out.lse) out.lse[at] = log_sum(top, l);
+}
+// The kernel's first argument, read anew: what only the path above uses is not
+// kept in scalar registers through the kernel.
+__device__ inline const AttnArgs &args_anew() {
+    auto p = (uint64_t)(const void *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttnArgs *)p;
+}
+// Whether a sum is none of the ordinary ones, so that its row goes there.
+__device__ inline bool beyond(float x) { return !(fabsf(x) <= 0x1p120f); }
+template <int DP>
+__device__ inline bool beyond(const floatx16 (&o)[DP / 32], float l) {
+    bool b = beyond(l);
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b |= beyond(o[e][i]);
+    return b;
+}
+
 // Keys of a tile: 64 halve the barriers and the running sums' exchanges, 32
 // where 64 would not leave registers for two blocks on a CU (2 x 2048 x 2048,
 // 16 heads of 64, bf16: 59 us against 77 with 32; 15668 x 1000, 8 heads of
@@ -243,7 +321,7 @@ constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
 // Two blocks on a CU let one wavefront's products run beside the other's
 // softmax.  What bounds it is the softmax: a score takes ten vector
 // instructions and an exponential, about as long as two products of 128.
-// Measured: 2 x 4096 x 4096, 16 heads of 128 on 4, bf16: 482 us, 570 TFLOP/s
+// Measured: 2 x 4096 x 4096, 16 heads of 128 on 4, bf16: 470 us, 585 TFLOP/s
 // (a large library product reaches 1220; 416 us with p in 8 bits); fp32, six products for one: 64
 // segments of up to 269 x 271, 4 heads of 32: 26 us, 40 TFLOP/s.
 template <int NP, int DP, int KT, bool FAST>
@@ -302,16 +380,24 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
         if (t + 2 < t1) load(t + 2);
         __syncthreads();
     }
-    if (st.row < 0) return;
     const float l = half_sum(st.l), inv = inverse(l);
-    const int64_t at = (int64_t)st.row * a.H + w.h0 + st.g;
+    uint64_t odd = a.splits > 1 ? 0 : __ballot(st.row >= 0 && beyond<DP>(st.o, l));   // (joined first otherwise)
+    odd = (odd | odd >> 32) & 0xffffffffull;
+    if (st.row >= 0 && !((odd >> (lane & 31)) & 1)) {
+        const int64_t at = (int64_t)st.row * a.H + w.h0 + st.g;
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e)
+        for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            write_row4<NP>(a, out, w.split, at, 32 * e + 8 * i + 4 * (lane >> 5),
-                           floatx4{st.o[e][4 * i], st.o[e][4 * i + 1], st.o[e][4 * i + 2], st.o[e][4 * i + 3]}, inv);
-    if (lane < 32) write_stats(a, out, w.split, at, st.m, l);
+            for (int i = 0; i < 4; ++i)
+                write_row4<NP>(a, out, w.split, at, 32 * e + 8 * i + 4 * (lane >> 5),
+                               floatx4{st.o[e][4 * i], st.o[e][4 * i + 1], st.o[e][4 * i + 2], st.o[e][4 * i + 3]}, inv);
+        if (lane < 32) write_stats(a, out, w.split, at, st.m, l);
+    }
+    while (odd) {
+        const int r = w.tile * 128 + wave * 32 + __ffsll((unsigned long long)odd) - 1;
+        odd &= odd - 1;
+        plain_row<NP>(args_anew(), out, w.q0 + r / w.gs, w.h0 + r % w.gs, w.q0, w.k0, w.nk, lane);
+    }
 }
 
 // Few rows (at most 32 of a key/value head's subgroup): every wavefront
@@ -373,9 +459,10 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     }
     // join the wavefronts' rows, in their order
     const float lw = half_sum(st.l);
+    const uint64_t far = __ballot(beyond<DP>(st.o, lw));
     if (lane < 32) {
         wave_m[wave][lane] = st.m;
-        wave_l[wave][lane] = lw;
+        wave_l[wave][lane] = ((far | far >> 32) >> lane) & 1 ? NAN : lw;   // (and so of all of the row)
     }
     __syncthreads();
     float m = -INFINITY, l = 0.0f;
@@ -383,6 +470,8 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
     for (int v = 0; v < NW; ++v)
         if (wave_l[v][lane & 31] != 0.0f)
             l += wave_l[v][lane & 31] * __builtin_amdgcn_exp2f(wave_m[v][lane & 31] - m);
+    const int n = min(32, w.nq * w.gs - w.tile * 32);
+    const uint32_t odd = a.splits > 1 ? 0 : (uint32_t)__ballot(lane < n && beyond(l));   // (split rows: joined first)
     const float f = st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m);
     float *rows = reinterpret_cast<float *>(lds);   // [wavefront][DP][33]
 #pragma unroll
@@ -391,12 +480,12 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
         for (int i = 0; i < 16; ++i)
             rows[(wave * DP + 32 * e + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] = st.o[e][i] * f;
     __syncthreads();
-    if (tid < 32 && st.row >= 0) write_stats(a, out, w.split, (int64_t)st.row * a.H + w.h0 + st.g, m, l);
+    if (tid < 32 && st.row >= 0 && !((odd >> lane) & 1)) write_stats(a, out, w.split, (int64_t)st.row * a.H + w.h0 + st.g, m, l);
     if (wave == 0 && lane < 32) wave_l[0][lane] = inverse(l);
     __syncthreads();
-    const int n = min(32, w.nq * w.gs - w.tile * 32);
     for (int i = tid; i < n * (DP / 4); i += 64 * NW) {
         const int r = i / (DP / 4), d = (i % (DP / 4)) * 4, rr = w.tile * 32 + r;
+        if ((odd >> r) & 1) continue;
         const int64_t at = (int64_t)(w.q0 + rr / w.gs) * a.H + w.h0 + rr % w.gs;
         floatx4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -405,6 +494,11 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut ou
             for (int j = 0; j < 4; ++j) x[j] += rows[(v * DP + d + j) * 33 + r];
         write_row4<NP>(a, out, w.split, at, d, x, wave_l[0][r]);
     }
+    for (int r = wave; r < 32 && odd; r += NW)
+        if ((odd >> r) & 1) {
+            const int rr = w.tile * 32 + r;
+            plain_row<NP>(args_anew(), out, w.q0 + rr / w.gs, w.h0 + rr % w.gs, w.q0, w.k0, w.nk, lane);
+        }
 }
 
 // Join the key splits of a row: one wavefront per row and head (9 us for 1024
@@ -425,6 +519,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, FwdOut out) 
         l = fmaf(p.y, f, l);
         for (int u = 0; u < 2; ++u)
             if (lane + 64 * u < a.D) acc[u] = fmaf(out.part_o[(k * rows + at) * a.D + lane + 64 * u], f, acc[u]);
+    }
+    if (__any(beyond(l) || beyond(acc[0]) || beyond(acc[1]))) {
+        const int row = uniform((int)(at / a.H));
+        int q0 = 0, nq = 0, k0 = 0, nk = 0;
+        for (int b = 0; b < a.B && !(row >= q0 && row < q0 + nq); ++b) {   // its segment
+            segment_rows(a.q_ptr, b, a.B, a.n_q, a.max_q, a.status, q0, nq);
+            segment_rows(a.k_ptr, b, a.B, a.n_k, a.max_k, a.status, k0, nk);
+        }
+        if (row >= q0 && row < q0 + nq) plain_row<NP>(args_anew(), out, row, (int)(at % a.H), q0, k0, nk, lane);
+        return;
     }
     const float inv = inverse(l);
     for (int u = 0; u < 2; ++u) {

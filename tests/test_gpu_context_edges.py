@@ -129,6 +129,64 @@ def test_attention_biases_that_remove_keys(sn, lq, lk, low, dtype):
         assert off <= bound, name
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), 3.3e38, -3.4e38], ids=str)
+@pytest.mark.parametrize("lq,lk", [([2, 1], [90, 40]), ([150, 33], [130, 257]), ([40], [1200]), ([2], [2500])], ids=str)
+def test_attention_of_infinite_and_huge_values(sn, lq, lk, value, dtype):
+    """A kept value that is infinite, or large enough that a partial sum overflows where the result does not, reaches
+    its column of its segment and head as the definition has it; nothing else changes."""
+    import torch
+    print(f"[attention] value {value} {lq} {lk} {dtype}", flush=True)
+    thr = np.array([-60, -20, -3, 0, 5, 40], np.int32)
+    plan, c, where, _, factor = attention_case(sn, lq, lk, 4, 2, 40, dtype, thr, True, "plain", seed=78, gen_pos="default")
+    at = lk[0] - 7
+    where["keep"][at] = True
+    c["v"][at, 1, 5] = value
+    want, _ = attention_dense(plan, c, where, thr, lambda h, bk: torch.ones_like(bk, dtype=torch.bool))
+    got = attention_run(sn, plan, c, where)
+    for name in ("o", "served"):
+        x, y = got[name].double().cpu(), want["o"].to(c["q"].dtype).double()
+        hit = torch.zeros_like(x, dtype=torch.bool)
+        hit[:lq[0], 2:, 5] = True
+        assert torch.equal(torch.isinf(x), torch.isinf(y)) and torch.equal(x[torch.isinf(x)], y[torch.isinf(y)]), name
+        assert not bool(torch.isnan(x).any()), name
+        fine = torch.isfinite(y)
+        off = (x - want["o"]).abs()
+        # beside a huge value: 2^-8 of it for a bf16 output, else the scores' errors in its weight
+        bound = (2.0 ** -7 if dtype == "bfloat16" else factor) * want["o"].abs().clamp_min(1.0)
+        assert bool((off <= bound)[fine].all()), (name, float((off / bound)[fine].max()))
+        assert bool(hit[torch.isinf(y)].all())
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lq,lk", [([2, 1], [90, 40]), ([150, 33], [130, 257]), ([40], [1200]), ([2], [2500])], ids=str)
+def test_attention_of_an_infinite_key_element(sn, lq, lk, dtype):
+    """A kept key with an infinite element has the score of its sign: a row it is minus infinity for passes it over, one
+    it is infinity for is no number."""
+    import torch
+    print(f"[attention] infinite key {lq} {lk} {dtype}", flush=True)
+    plan, c, where, _, factor = attention_case(sn, lq, lk, 4, 2, 40, dtype, np.array([0], np.int32), True, "plain", seed=79,
+                                               gen_pos="default")
+    at = lk[0] - 7
+    where["keep"][at] = True
+    finite = dict(c, k=c["k"].clone())
+    c["k"][at, 1, 5] = -float("inf")
+    got = attention_run(sn, plan, c, where)
+    away = c["q"][:lq[0], 2:, 5] > 0
+    assert bool(away.any()) and bool((~away).any())
+    rest = dict(where, keep=where["keep"].clone())
+    rest["keep"][at] = False
+    want, _ = attention_dense(plan, finite, rest, [0], lambda h, bk: torch.ones_like(bk, dtype=torch.bool))
+    for name in ("o", "served"):
+        x = got[name].double().cpu()
+        assert bool(torch.isnan(x[:lq[0], 2:][~away.cpu()]).all()), name
+        assert bool(torch.isfinite(x[:lq[0], :2]).all() and torch.isfinite(x[lq[0]:]).all()), name
+        fine = torch.zeros(x.shape[:2], dtype=torch.bool)
+        fine[:lq[0], 2:] = away.cpu()
+        off = ((x - want["o"]).abs() / want["o"].abs().clamp_min(1.0))[fine]
+        assert float(off.max()) <= (2.0 ** -7 if dtype == "bfloat16" else factor), name
+
+
 # ------------------------------------------------------------------ cross attention: bits of the weights
 
 @pytest.mark.parametrize("lq,lk,D", [([70, 3], [400, 65], 64), ([150], [1300], 128), ([2, 1], [700, 300], 128), ([9], [2500], 40)],
