@@ -306,7 +306,11 @@ sn_status sn_read_status(void *ws, void *stream);
  * zeroes once, before its first use.  Results do not depend on timing:
  * repeated calls give identical bits.  No call synchronises. */
 
-/* Element type of the row tensors; everything is accumulated in fp32. */
+/* Element type of the row tensors.  Sums, softmax statistics and norms are
+ * fp32 or more whatever it is.  With SN_BF16 the attention's products take p in
+ * 16 bits in the forward pass, and p and dS in 8 in the backward pass, where
+ * each adds to a gradient about what rounding the gradient itself does (dbias,
+ * which is fp32, is summed from unrounded dS); SN_F32 keeps 24 throughout. */
 #define SN_F32 0
 #define SN_BF16 1
 

@@ -251,8 +251,9 @@ __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void att
                     float x[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = s[8 * u + j];
-                    // bf16 rows: dS is rounded to 8 bits here, as p is in the
-                    // forward pass: at most 2^-8 of each term, as rounding dq
+                    // bf16 rows: dS is rounded to 8 bits here, at most 2^-8 of
+                    // each term, as rounding dq: 2.4e-3 of its norm off, 1.7e-3
+                    // of it its own rounding
                     const Frag<NP> ds = split8f<NP>(x);
 #pragma unroll
                     for (int e = 0; e < DP / 32; ++e) {
@@ -644,6 +645,9 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 || (NP == 1 && DP < 128) ? 2
                     x[jj] = s[8 * u + jj];
                     y[jj] = dp[8 * u + jj];
                 }
+                // bf16 rows: 8 bits here too.  dk and dv are 2.3e-3 of their
+                // norms off, 1.7e-3 of it their own rounding; 16 bits are two
+                // products and six instructions a score more
                 const Frag<NP> p = split8f<NP>(x), ds = split8f<NP>(y);
 #pragma unroll
                 for (int e = 0; e < DP / 32; ++e) {

@@ -207,6 +207,30 @@ def test_attention_weights_of_bf16_rows_keep_16_bits(sn, lq, lk, D):
     assert off <= 2.0 ** -17 + factor
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lq,lk,H,Hkv,D", [([260, 33], [300, 129], 4, 2, 32), ([150], [400], 8, 2, 64), ([200, 90], [150, 260], 2, 2, 128),
+                                           ([9, 3], [700, 500], 4, 1, 40), ([600], [70], 6, 3, 64)], ids=str)
+def test_attention_distances_of_whole_tensors(sn, lq, lk, H, Hkv, D, dtype):
+    """Distances by norms, which an allowance by magnitudes alone does not hold where dS cancels.  A bf16 rounding is at
+    most 2^-8 / sqrt(3) of its value in the root mean square; o has its own, dq, dk and dv that and one of an operand of
+    each term (dS, dS, p), independent of each other, so their squares add.  fp32: exponents below 64 are 2^-18 off."""
+    import torch
+    print(f"[attention] distances {lq} {lk} {H} {Hkv} {D} {dtype}", flush=True)
+    thr = np.array([-60, -20, -3, 0, 5, 40], np.int32)
+    plan, c, where, _, _ = attention_case(sn, lq, lk, H, Hkv, D, dtype, thr, True, "plain", seed=80, gen_pos="default")
+    want, rss = attention_dense(plan, c, where, thr, lambda h, bk: torch.ones_like(bk, dtype=torch.bool))
+    got = attention_run(sn, plan, c, where)
+    assert torch.equal(got["o"], got["served"])
+    for name in ("o", "dq", "dk", "dv"):
+        value, terms = float(want[name].norm()), float(rss[name].norm())
+        bound = 2.0 ** -17 * (value + terms)
+        if dtype == "bfloat16":
+            bound += 2.0 ** -8 * 3.0 ** -0.5 * (value if name == "o" else (value ** 2 + terms ** 2) ** 0.5)
+        off = float((got[name].double().cpu() - want[name]).norm())
+        print(f"   {name}: {off / bound:.2g} of the bound, {off / value:.2g} of the norm", flush=True)
+        assert off <= bound, name
+
+
 # ------------------------------------------------------------------ outputs at any element
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
