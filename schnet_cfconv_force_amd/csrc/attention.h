@@ -82,7 +82,7 @@ __device__ inline floatx16 mma(const Frag<NP> &a, const Frag<NP> &b, floatx16 c)
 
 // Ends a chain of products whose sums vector instructions read next: the
 // hardware does not hold such a read back until the last product is through
-// (11 wait states for eight passes), and where a branch lies between, the
+// (12 wait states for eight passes), and where a branch lies between, the
 // compiler (ROCm 7.2) was seen to count the waits along its longer side only,
 // so that the last registers were read early.  Here they pass through this
 // block, in the chain's own straight line.
