@@ -385,6 +385,8 @@ def read_status(ws, stream=None) -> int:
 #
 # `stream` of the calls below: None is the current stream.  Another one waits for the current stream's work so far, so
 # inputs and workspaces that were made there are ready; what uses the outputs elsewhere has to wait for it.
+# The calls record no graph, whether or not an input requires a gradient: the backward calls are the caller's to make
+# (examples/context_embedding.py wraps both in autograd functions).
 
 _ACTIVATIONS = {"none": SN_ACT_NONE, "ssp": SN_ACT_SSP, "silu": SN_ACT_SILU}
 

@@ -83,10 +83,12 @@ __device__ inline void write4(T *row, int d, int D, bool four, floatx4 v) {
 // dq and the rows' delta: a wavefront owns 32 rows, the block's four share the
 // key tiles, as in the forward kernel for many rows.  S^T and dP^T put a row's
 // scores in one lane, so L and delta are one register each, and dS^T is the
-// next product's operand as it lies.  Bound by the vector instructions between
-// the products (an exponential and eight others a score) and, for short
-// segments, by the start: two segments of up to 2048 x 2048, 16 heads of 64, bf16:
-// 98 us, 290 TFLOP/s; 64 of up to 269 x 271, 4 heads of 32, fp32: 34 us.
+// next product's operand as it lies.  Bound by latency: product, exponential
+// and product follow each other, and two wavefronts on a SIMD do not cover it.
+// Two segments of up to 2048 x 2048, 16 heads of 64, bf16: 99 us, 335 TFLOP/s;
+// a wavefront waits a third of its time, the vector units are 31 % busy, the
+// matrix units 14 %.  64 of up to 269 x 271, 4 heads of 32, fp32: 35 us, 44 % of
+// it waiting (the start is as long as the tiles).  <1, 128> spills 26 registers.
 template <int NP, int DP, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, NP == 1 || DP == 32 ? 2 : 1) void attn_dq_kernel(AttnArgs a, BwdArgs g) {
     using T = typename RowOf<NP>::T;
@@ -337,11 +339,13 @@ __host__ __device__ inline BiasLds bias_lds(int lut_n, int nb) {
 // dk, dv and the bias sums: a wavefront owns 32 keys, the block's four share
 // the tiles of 32 rows of every head that reads these keys.  S and dP put a
 // key's column in one lane; p and dS are the operands of dv and dk as they
-// lie.  Bound by the vector instructions between the four products, with two
-// wavefronts on a SIMD to overlap them (tiles of 64 rows spilled).  Two
-// segments of up to 2048 x 2048, 16 heads of 64, bf16: 136 us, 280 TFLOP/s
-// (without a bias the backward pass takes 169 us instead of 206 on segments of
-// equal length); 64 segments of up to 269 x 271, 4 heads of 32, fp32: 48 us.
+// lie.  Bound by latency, with two wavefronts on a SIMD at most and a barrier
+// every 32 rows (tiles of 64 rows spilled).  Two segments of up to 2048 x 2048,
+// 16 heads of 64, bf16: 137 us, 323 TFLOP/s; a wavefront waits 42 % of its
+// time, the vector units are 20 % busy, the matrix units 11 % (without a bias
+// the backward pass takes 170 us instead of 205 on segments of equal length);
+// 64 segments of up to 269 x 271, 4 heads of 32, fp32: 47 us, 52 % waiting.
+// Heads of 128 do not fit the registers: <3, 128> spills 85, <1, 64> three.
 template <int NP, int DP>
 constexpr int dkv_buffers() { return NP == 3 && DP == 128 ? 1 : 2; }   // 160 KB of LDS
 

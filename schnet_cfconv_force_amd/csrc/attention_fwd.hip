@@ -310,8 +310,8 @@ __device__ inline bool beyond(const floatx16 (&o)[DP / 32], float l) {
 
 // Keys of a tile: 64 halve the barriers and the running sums' exchanges, 32
 // where 64 would not leave registers for two blocks on a CU (2 x 2048 x 2048,
-// 16 heads of 64, bf16: 59 us against 77 with 32; 15668 x 1000, 8 heads of
-// 16, fp32: 101 against 109).
+// 16 heads of 64, bf16: 79 us against 97 with 32; 15668 x 1000, 8 heads of
+// 16, fp32: 103 against 111).
 template <int NP, int DP>
 constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
 
@@ -319,11 +319,13 @@ constexpr int kRowKeys = DP == 32 || (NP == 1 && DP == 64) ? 64 : 32;
 // read the same key tiles, staged in LDS while the tile before is computed:
 // a tile is read from memory once for 128 rows and split into planes once.
 // Two blocks on a CU let one wavefront's products run beside the other's
-// softmax.  What bounds it is the softmax: a score takes ten vector
-// instructions and an exponential, about as long as two products of 128.
-// Measured: 2 x 4096 x 4096, 16 heads of 128 on 4, bf16: 470 us, 585 TFLOP/s
-// (a large library product reaches 1220; 416 us with p in 8 bits); fp32, six products for one: 64
-// segments of up to 269 x 271, 4 heads of 32: 26 us, 40 TFLOP/s.
+// softmax.  What bounds it is the softmax in series with the products: a score
+// takes a dozen vector instructions and an exponential.  Measured: 2 x 4096 x
+// 4096, 16 heads of 128 on 4, bf16: 470 us, 585 TFLOP/s of the 1220 that a
+// large library product reaches (416 us with p in 8 bits); the vector units
+// are 53 % busy, the matrix units 35 %, and a wavefront waits 28 % of its time.
+// fp32, six products for one: 64 segments of up to 269 x 271, 4 heads of 32:
+// 26 us, 40 TFLOP/s, half of a wavefront's time in waits (start and five tiles).
 template <int NP, int DP, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a, FwdOut out) {
     using T = typename RowOf<NP>::T;
@@ -544,17 +546,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, FwdOut out) 
 //
 // Few: where a key/value head's rows fill one wavefront at most, each of the
 // others would only repeat or idle (64 segments of 32 x 271, fp32, heads of
-// 32: 12.7 us against 18.8 with the kernel for many; 16 of 32 x 2048, bf16,
-// heads of 64: 24 against 28).  Two wavefronts' rows go to the other (64 x
-// 271: 19.4 against 21.4; 32 of 16 x 1024 with four heads sharing, bf16, 128:
-// 48 against 71).
+// 32: 12.7 us against 19.0 with the kernel for many; 16 of 32 x 2048, bf16,
+// heads of 64: 26 against 30).  Two wavefronts' rows go to the other (64 x
+// 271: 19.5 against 21.9; 64 of 64 x 600, 8 heads, bf16: 32 against 44 for
+// heads of 64, 45 against 73 for 128), also where few blocks of bf16 rows
+// would gain from this one (32 of 64 x 1024, 8 heads of 128: 59 against 49).
 //
 // Splits: as many as give every CU a block (few) or two (many), as long as
 // each has 1024 or 256 keys to pay for its start and the join.  One row over
-// 16384 keys of 8 heads: 160 us unsplit, 52 us from 512 keys, 40 us from
-// 1024, 39 us from 2048, where 4 x 4096 is 32 instead of 26 us; one block for
-// every CU instead of four: 16 x 4096, bf16, heads of 64, 50 -> 34 us.  Many,
-// 40 x 4096 of 8 heads: 79 us unsplit, 29 us with two, 28.5 with four.
+// 16384 keys of 8 heads: 179 us unsplit, 53 us from 512 keys, 42 us from
+// 1024, 43 us from 2048, where 4 x 4096 is 36 instead of 28 us; one block for
+// every CU instead of four: 16 x 4096, bf16, heads of 64, 40 -> 35 us.  Many,
+// 40 x 4096 of 8 heads: 94 us unsplit, 29.3 with two blocks, 29.6 with four.
 struct FwdPlan {
     bool few;
     int Gs, subs, row_tiles, splits;

@@ -281,8 +281,8 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, NormCut 
 }
 
 // Memory bound: 8 segments of 16384 rows of 512 in bf16, 134 MB, take 77 us with
-// the launch that follows, 5.2 TB/s; of ragged ones (81 MB in all) the blocks
-// are one wave on the card, whose start and end cost a third: 24 us, 3.4 TB/s.
+// the launch that follows, 5.2 TB/s; of ragged ones (101 MB a tensor) the blocks
+// are one wave on the card, whose start and end cost a sixth: 24 us, 4.2 TB/s.
 // part [b][group][chunk pieces + piece]: the chunk's {mean, sum of squared
 // differences} of each group
 template <typename T, int V, int IT>
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a, NormCu
 }
 
 // Joins the chunks' statistics (each block for itself: a launch less) and
-// writes this chunk's rows; the same ragged segments in 42 us, 3.8 TB/s.
+// writes this chunk's rows; the same ragged segments in 42 us, 4.8 TB/s.
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, NormCut k, const float2 *part, T *y,
                                                               float *mean, float *rstd) {
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, NormCut 
 
 // part [b][chunk][2][C]: the chunk's sums of dz xh and dz.  8 segments of
 // 16384 rows of 512 in bf16: 127 us with the two launches that follow, 5.3
-// TB/s; ragged ones (81 MB a tensor) in 58 us, 2.8 TB/s, two streams beside
+// TB/s; ragged ones (101 MB a tensor) in 58 us, 3.5 TB/s, two streams beside
 // the activation's slope (an exponential and a reciprocal an element).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_sums_kernel(NormArgs a, NormCut k, const float *mean,
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(kThreads) void norm_param_kernel(NormArgs a, const 
 }
 
 // dx of a chunk's rows (the same ragged segments: 67
-// us, 3.6 TB/s); the first `params` blocks sum dgamma and dbeta
+// us, 4.5 TB/s); the first `params` blocks sum dgamma and dbeta
 // instead (one launch less).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_bwd_apply_kernel(NormArgs a, NormCut k, const float *mean,
