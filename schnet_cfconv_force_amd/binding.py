@@ -420,7 +420,8 @@ def _rows(t, name: str, shape, dtype, device):
 def _gradient(t):
     """A gradient as it came, or laid out anew where its last index is not contiguous: the backward pass of a sum hands
     down one number in every place, with strides of zero."""
-    return t if t.dim() == 0 or t.size(-1) <= 1 or t.stride(-1) == 1 else t.contiguous()
+    strides = t.stride()
+    return t.contiguous() if strides and strides[-1] != 1 else t
 
 
 def _flat(t, name: str, shape, dtypes, device) -> int:
@@ -433,39 +434,41 @@ def _flat(t, name: str, shape, dtypes, device) -> int:
     return t.data_ptr()
 
 
-def _launch(plan, name: str, stream, ws, inputs, outputs, *args):
-    """Call the entry point `name` with `args`, the workspace and the stream, on the plan's device.
+def _launch(plan, entry, stream, ws, tensors, *args):
+    """Call an entry point with `args`, the workspace and the stream, on the plan's device.
 
     An explicit stream waits for what the current one has been given so far (the outputs' memory may still be in use
-    there, and the inputs or the workspace's zeroing on their way), and every tensor of the call is tied to it."""
-    torch, device = _torch(), plan.device
-    # the kernels write the workspace: a host address there would fault
-    if device.type != "cuda" or ws.device != device or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+    there, and the inputs or the workspace's zeroing on their way), and `tensors`, all of the call's, are tied to it."""
+    index = plan.index
+    # the kernels write the workspace: a host address there would fault (get_device() is -1 for a host tensor)
+    if index is None or ws.get_device() != index or ws.dtype is not plan.byte or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous torch.uint8 tensor on the plan's GPU, not {ws.dtype} on {ws.device} "
-                         f"(the plan lies on {device})")
-    raw = plan.current_stream(device.index)
+                         f"(the plan lies on {plan.device})")
+    raw = plan.current_stream(index)
     if stream is not None and stream.cuda_stream != raw:
-        if stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the plan to {device}")
-        stream.wait_stream(torch.cuda.current_stream(device))
-        for t in (ws, *plan.pointers, *inputs, *outputs):
+        if stream.device != plan.device:
+            raise ValueError(f"the stream belongs to {stream.device}, the plan to {plan.device}")
+        stream.wait_stream(_torch().cuda.current_stream(index))
+        for t in (ws, *plan.pointers, *tensors):
             if t is not None:
                 t.record_stream(stream)
         raw = stream.cuda_stream
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, ws.data_ptr(), ws.numel(), raw)
+    if plan.current_device() == index:
+        st = entry(*args, ws.data_ptr(), ws.numel(), raw)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, ws.data_ptr(), ws.numel(), raw)
-    _check(st, name)
+        with _torch().cuda.device(index):
+            st = entry(*args, ws.data_ptr(), ws.numel(), raw)
+    if st != SN_OK:
+        raise SnError(st, entry.__name__)
 
 
-def _current_stream_getter():
-    """A function from a device index to its current raw stream (torch's own accessor where it has one)."""
+def _current_getters():
+    """A function from a device index to its current raw stream, and one to the current device's index (torch's own
+    accessors where it has them: short calls are bound by the host)."""
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream), device or torch.cuda.current_device
 
 
 def _zeroed_workspace(plan):
@@ -527,7 +530,8 @@ class CrossAttention:
             raise SnError(SN_ERR_INVALID, "sn_cross_attention")
         self.head = bytes(self.c)[:SnCrossAttention.q.offset]
         self.pointers = (self.q_ptr, self.k_ptr)
-        self.current_stream = _current_stream_getter()
+        self.index, self.byte = self.device.index, torch.uint8
+        self.current_stream, self.current_device = _current_getters()
         self.q_shape = torch.Size((self.n_q, self.n_heads, self.head_dim))
         self.k_shape = torch.Size((self.n_k, self.n_kv_heads, self.head_dim))
 
@@ -564,11 +568,11 @@ def cross_attention_forward(plan: CrossAttention, q, k, v, ws, bias=None, q_pos=
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     inputs = (q, k, v, bias, q_pos, k_pos, keep)
     if not save:
-        _launch(plan, "sn_cross_attention_forward", stream, ws, inputs, (o,), op, o.data_ptr(), None)
+        _launch(plan, lib().sn_cross_attention_forward, stream, ws, (*inputs, o), op, o.data_ptr(), None)
         return o
     lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device)
     rows = o if plan.dtype == torch.float32 else torch.empty(plan.q_shape, dtype=torch.float32, device=plan.device)
-    _launch(plan, "sn_cross_attention_forward_train", stream, ws, inputs, (o, rows, lse), op, o.data_ptr(),
+    _launch(plan, lib().sn_cross_attention_forward_train, stream, ws, (*inputs, o, rows, lse), op, o.data_ptr(),
             rows.data_ptr(), lse.data_ptr())
     return o, (rows, lse)
 
@@ -587,8 +591,9 @@ def cross_attention_backward(plan: CrossAttention, q, k, v, saved, d_o, ws, bias
     dk = torch.empty_like(k, memory_format=torch.contiguous_format)
     dv = torch.empty_like(v, memory_format=torch.contiguous_format)
     dbias = None if bias is None else torch.empty_like(bias)
-    _launch(plan, "sn_cross_attention_backward", stream, ws, (q, k, v, rows, lse, d_o, bias, q_pos, k_pos, keep),
-            (dq, dk, dv, dbias), op, _flat(rows, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
+    _launch(plan, lib().sn_cross_attention_backward, stream, ws,
+            (q, k, v, rows, lse, d_o, bias, q_pos, k_pos, keep, dq, dk, dv, dbias), op,
+            _flat(rows, "saved[0]", plan.q_shape, (torch.float32,), plan.device),
             _flat(lse, "saved[1]", plan.q_shape[:2], (torch.float32,), plan.device), d_o.data_ptr(), gs, gh,
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias))
     return dq, dk, dv, dbias
@@ -616,7 +621,8 @@ class GroupNorm:
             raise SnError(SN_ERR_INVALID, "sn_group_norm")
         self.head = bytes(self.c)[:SnGroupNorm.x.offset]
         self.pointers = (self.row_ptr,)
-        self.current_stream = _current_stream_getter()
+        self.index, self.byte = self.device.index, torch.uint8
+        self.current_stream, self.current_device = _current_getters()
         self.shape = torch.Size((self.n_rows, self.n_channels))
 
     def _bind(self, x, gamma, beta) -> bytes:
@@ -642,7 +648,7 @@ def group_norm_forward(plan: GroupNorm, x, gamma, beta, ws, save: bool = False, 
     mean = rstd = None
     if save:
         mean, rstd = torch.empty((2, plan.n_segments, plan.n_groups), dtype=torch.float32, device=plan.device).unbind(0)
-    _launch(plan, "sn_group_norm_forward", stream, ws, (x, gamma, beta), (y, mean, rstd), op, y.data_ptr(), _ptr(mean),
+    _launch(plan, lib().sn_group_norm_forward, stream, ws, (x, gamma, beta, y, mean, rstd), op, y.data_ptr(), _ptr(mean),
             _ptr(rstd))
     return (y, (mean, rstd)) if save else y
 
@@ -657,7 +663,7 @@ def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=N
     stats = (plan.n_segments, plan.n_groups)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     dgamma, dbeta = torch.empty((2, plan.n_channels), dtype=torch.float32, device=plan.device).unbind(0)
-    _launch(plan, "sn_group_norm_backward", stream, ws, (x, gamma, beta, *saved, dy), (dx, dgamma, dbeta), op,
+    _launch(plan, lib().sn_group_norm_backward, stream, ws, (x, gamma, beta, *saved, dy, dx, dgamma, dbeta), op,
             _flat(saved[0], "saved[0]", stats, (torch.float32,), plan.device),
             _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), dy.data_ptr(), dy_stride, dx.data_ptr(),
             dgamma.data_ptr(), dbeta.data_ptr())

@@ -109,7 +109,6 @@ sn_status check_norm_sizes(const sn_group_norm *op) {
         return SN_ERR_INVALID;
     if (op->dtype != SN_F32 && op->dtype != SN_BF16) return SN_ERR_INVALID;
     if (op->activation < SN_ACT_NONE || op->activation > SN_ACT_SILU) return SN_ERR_INVALID;
-    if (!norm_fits(*op)) return SN_ERR_INVALID;
     return SN_OK;
 }
 
@@ -202,7 +201,7 @@ sn_status sn_cross_attention_backward(const sn_cross_attention *op, const float 
 }
 
 size_t sn_group_norm_workspace_bytes(const sn_group_norm *op) {
-    return check_norm_sizes(op) == SN_OK ? norm_workspace(*op) : 0;
+    return check_norm_sizes(op) == SN_OK && norm_fits(*op) ? norm_workspace(*op) : 0;
 }
 
 sn_status sn_group_norm_forward(const sn_group_norm *op, void *y, float *mean, float *rstd, void *ws, size_t ws_bytes,

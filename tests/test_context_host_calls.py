@@ -31,6 +31,9 @@ class Stand:
     def numel(self):
         return 1024
 
+    def get_device(self):
+        return -1 if self.device.index is None else self.device.index
+
     def is_contiguous(self):
         return True
 
@@ -46,26 +49,25 @@ def world(monkeypatch):
         return state.status
 
     class Guard:
-        def __init__(self, device):
-            self.device = device
+        def __init__(self, index):
+            self.index = index
 
         def __enter__(self):
-            self.before, state.device = state.device, self.device.index
+            self.before, state.device = state.device, self.index
 
         def __exit__(self, *_):
             state.device = self.before
 
     state.status = 0
-    monkeypatch.setattr(binding, "lib", lambda: SimpleNamespace(sn_some_call=entry, sn_status_string=lambda status: b"refused"))
+    monkeypatch.setattr(binding, "lib", lambda: SimpleNamespace(sn_status_string=lambda status: b"refused"))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: state.device)
     monkeypatch.setattr(torch.cuda, "device", Guard)
-    plan = SimpleNamespace(device=torch.device("cuda:0"), current_stream=lambda index: 7,
-                           pointers=(Stand("pointers", log),))
+    plan = SimpleNamespace(device=torch.device("cuda:0"), index=0, byte=torch.uint8, current_stream=lambda index: 7,
+                           current_device=lambda: state.device, pointers=(Stand("pointers", log),))
 
     def call(stream=None, **ws):
-        tensors = (Stand("input", log), None), (Stand("output", log), None)
-        binding._launch(plan, "sn_some_call", stream, Stand("ws", log, **ws), *tensors)
+        tensors = (Stand("input", log), None, Stand("output", log))
+        binding._launch(plan, entry, stream, Stand("ws", log, **ws), tensors)
 
     return SimpleNamespace(log=log, plan=plan, state=state, call=call)
 
@@ -114,7 +116,7 @@ def test_a_workspace_that_the_plans_gpu_cannot_use_is_refused(world, ws):
 
 
 def test_a_plan_on_the_host_makes_no_call(world):
-    world.plan.device = torch.device("cpu")
+    world.plan.device, world.plan.index = torch.device("cpu"), None
     with pytest.raises(ValueError):
         world.call(device="cpu")
     assert not world.log
