@@ -342,7 +342,7 @@ __host__ __device__ inline BiasLds bias_lds(int lut_n, int nb) {
 // lie.  Bound by latency, with two wavefronts on a SIMD at most and a barrier
 // every 32 rows (tiles of 64 rows spilled).  Two segments of up to 2048 x 2048,
 // 16 heads of 64, bf16: 137 us, 323 TFLOP/s; a wavefront waits 42 % of its
-// time, the vector units are 20 % busy, the matrix units 11 % (without a bias
+// time, the vector units are 21 % busy, the matrix units 12 % (without a bias
 // the backward pass takes 170 us instead of 205 on segments of equal length);
 // 64 segments of up to 269 x 271, 4 heads of 32, fp32: 47 us, 52 % waiting.
 // Heads of 128 do not fit the registers: <3, 128> spills 85, <1, 64> three.

@@ -406,8 +406,8 @@ __global__ __launch_bounds__(kAttnThreads, DP == 32 ? 3 : NP == 1 ? 2 : 1) void 
 // holds all of them and takes every NW-th tile of 32 keys, with tiles of its
 // own in LDS, so no wavefront waits for another until the rows are joined at
 // the end.  The keys and values are read once, and that is what bounds it:
-// 32 sequences of up to 16384 keys, 8 heads of 128, bf16: 290 us, 5.0 TB/s,
-// the rate of a large copy.  One row over 269 keys: 10 us, a launch and one
+// 32 sequences of up to 16384 keys, 8 heads of 128, bf16: 293 us, 4.85 TB/s
+// beside a large copy's 5.06 (1422 MB read, 1421 needed).  One row over 269 keys: 10 us, a launch and one
 // chain of dependent loads, products and exchanges.
 template <int NP, int DP, int NW, bool FAST>
 __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, FwdOut out) {
