@@ -432,6 +432,148 @@ sn_status sn_group_norm_backward(const sn_group_norm *op, const float *mean, con
                                  int64_t dy_stride, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
                                  void *stream);
 
+/* ---------------------------------------------------------------- rotation of heads, state cache
+ *
+ * Around the attention above: the query and key heads' norm and their rotation
+ * by positions, forward and backward; and states that arrive row by row, kept
+ * in pages (as they are or in 8 bits), read back, and attended to by their
+ * sequence's newest rows.  Like the context operators they are extensions of
+ * this library.  Their conventions (strides, workspaces, contradicting device
+ * arrays, determinism, no synchronisation) are the context operators'. */
+
+/* Largest number of position axes. */
+#define SN_MAX_AXES 8
+
+/* Norm and rotation of the heads of rows.  For row i, head h of q with its
+ * weight (and, apart, of k with its own):
+ *     z = w x / sqrt(mean over the head of x^2 + eps)      (norm 0: z = x)
+ *     pair j turns by t = positions[axes[j]][i] freqs[j]:
+ *     y_a = z_a cos t - z_b sin t,  y_b = z_b cos t + z_a sin t
+ * Pair j holds elements a = j, b = j + n_pairs, or, interleaved, a = 2j,
+ * b = 2j + 1; elements from 2 n_pairs on do not turn.  Angles are formed and
+ * reduced in fp64 (positions to the type's ends), all else is fp32 and y is
+ * rounded once.  The sum of a head's squares has to stay within fp32; a NaN or
+ * an infinity reaches its own head of its row only. */
+typedef struct sn_head_rotary {
+    int32_t n_rows;              /* >= 0 */
+    int32_t n_heads;             /* heads of q, >= 1 */
+    int32_t n_kv_heads;          /* heads of k, >= 0 (0: q alone) */
+    int32_t head_dim;            /* D, 1 .. SN_MAX_HEAD_DIM */
+    int32_t dtype;               /* SN_F32 or SN_BF16: q, k and their gradients */
+    int32_t norm;                /* 0 or 1 */
+    float eps;                   /* > 0 (with norm) */
+    int32_t n_pairs;             /* 0 .. D / 2 */
+    int32_t n_axes;              /* 1 .. SN_MAX_AXES (with pairs) */
+    int32_t interleaved;         /* 0 or 1 */
+    const double *freqs;         /* host [n_pairs], finite: radians a position */
+    const int32_t *axes;         /* host [n_pairs], each in [0, n_axes) */
+    const int32_t *positions;    /* device [n_axes][n_rows], contiguous (with pairs) */
+    const void *q;               /* device [n_rows][n_heads][D] */
+    const void *k;               /* device [n_rows][n_kv_heads][D] */
+    int64_t q_stride, q_head_stride;
+    int64_t k_stride, k_head_stride;
+    const float *q_weight;       /* device [D], or NULL: 1 (with norm) */
+    const float *k_weight;
+} sn_head_rotary;
+
+/* Frequencies and axes of n = the sum of the sections' pairs (host only).
+ * Pairs are given to the axes in runs, sections[a] of them to axis a.  shared:
+ * one ladder base^(-j/n) falls over all pairs; else every axis has its own,
+ * base^(-j/sections[a]).  Writes n values each.  SN_ERR_INVALID unless
+ * 1 <= n_axes <= SN_MAX_AXES, every section >= 1, n <= SN_MAX_HEAD_DIM / 2 and
+ * base > 0 is finite. */
+sn_status sn_rotary_frequencies(int32_t n_axes, const int32_t *sections, double base, int32_t shared, double *freqs,
+                                int32_t *axes);
+
+/* Bytes of workspace of both calls below (host; sizes only).  0 for a
+ * descriptor that they would refuse for its sizes. */
+size_t sn_head_rotary_workspace_bytes(const sn_head_rotary *op);
+
+/* q_out [n_rows][n_heads][D], k_out [n_rows][n_kv_heads][D] (op->dtype). */
+sn_status sn_head_rotary_forward(const sn_head_rotary *op, void *q_out, void *k_out, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/* Gradients from those of q_out and k_out (any strides): dq, dk (op->dtype)
+ * and, with norm, dq_weight and dk_weight [D] (fp32; each may be NULL). */
+sn_status sn_head_rotary_backward(const sn_head_rotary *op, const void *d_q, int64_t d_q_stride, int64_t d_q_head_stride,
+                                  const void *d_k, int64_t d_k_stride, int64_t d_k_head_stride, void *dq, void *dk,
+                                  float *dq_weight, float *dk_weight, void *ws, size_t ws_bytes, void *stream);
+
+/* How a cache holds its rows. */
+#define SN_CODES_NONE 0  /* in the rows' own type */
+#define SN_CODES_INT8 1  /* signed 8-bit codes, at most 127 */
+#define SN_CODES_E4M3 2  /* 8-bit floating point, 4 exponent and 3 fraction bits, at most 448 */
+
+/* Elements that a cache gives to a head's row. */
+#define SN_CACHE_ROW(head_dim) (((head_dim) + 15) / 16 * 16)
+
+/* Keys and values of sequences in pages.  Position p of sequence b lies at
+ * place p % page_size of page table[b][p / page_size]; a page holds, head by
+ * head, page_size rows of SN_CACHE_ROW(D) elements (those from D on are zero).
+ * Sequences may share pages that no call writes.  lengths[b] counts the rows of
+ * the sequence, those of the call among them: the call's rows row_ptr[b] ..
+ * row_ptr[b+1] - 1 are the last ones, at positions lengths[b] - count ..
+ * lengths[b] - 1.
+ *
+ * Codes.  For each row and head, in fp32: amax = max |x|,
+ *     scale = amax / top,  code = round(x (top / amax))   (top 127 or 448)
+ * rounded to the nearest code, ties to even; every quotient and product is
+ * rounded on its own, so the codes are the same wherever they are computed.  A
+ * row below 2^-100 is held as zeros with scale 0; one with a NaN or an infinity
+ * as zeros with scale NaN, so that it reads back as NaN.  A value read back is
+ * code scale, rounded to the rows' type.
+ *
+ * Device arrays that contradict the sizes are flagged (SN_ERR_INVALID in the
+ * workspace's status word) and nothing outside is read or written: a sequence
+ * whose length is negative, beyond its table, or below its count of rows (other
+ * than in an attention that is not causal) is skipped; a place whose page is not
+ * in [0, n_pages) is not written, reads back as zeros, and is an absent key.
+ * Entries of the table behind a sequence's length are not read. */
+typedef struct sn_cache {
+    int32_t n_pages;             /* >= 1 */
+    int32_t page_size;           /* rows of a page: a power of two, 16 .. 1024 */
+    int32_t n_kv_heads;
+    int32_t head_dim;            /* D, 1 .. SN_MAX_HEAD_DIM */
+    int32_t dtype;               /* SN_F32 or SN_BF16: the rows given, returned and attending */
+    int32_t codes;               /* SN_CODES_* */
+    void *k, *v;                 /* device [n_pages][n_kv_heads][page_size][SN_CACHE_ROW(D)], 16-byte aligned */
+    float *k_scale, *v_scale;    /* device [n_pages][n_kv_heads][page_size], 16-byte aligned (with codes) */
+    int32_t n_sequences;         /* B >= 1 */
+    int32_t n_rows, max_rows;    /* the call's rows: of all sequences, of the one with the most */
+    int32_t max_pages;           /* entries of a sequence in the table, >= 1 */
+    const int32_t *row_ptr;      /* device [B+1] */
+    const int32_t *table;        /* device [B][max_pages], contiguous */
+    const int32_t *lengths;      /* device [B] */
+    /* read by sn_cache_attend alone */
+    int32_t n_heads;             /* H, a multiple of n_kv_heads */
+    float scale;                 /* finite */
+    int32_t causal;              /* 1: a row sees the positions up to its own; 0: all of its sequence */
+    int32_t window;              /* > 0: of those its own and the window - 1 before it (causal); 0: no limit */
+    const void *q;               /* device [n_rows][H][D] */
+    int64_t q_stride, q_head_stride;
+} sn_cache;
+
+/* Bytes of workspace of the calls below (host; sizes only). */
+size_t sn_cache_workspace_bytes(const sn_cache *op);
+
+/* Writes the rows k and v [n_rows][n_kv_heads][D] (op->dtype, any strides) to
+ * their places.  Two rows of one call must not have the same place. */
+sn_status sn_cache_write(const sn_cache *op, const void *k, int64_t k_stride, int64_t k_head_stride, const void *v,
+                         int64_t v_stride, int64_t v_head_stride, void *ws, size_t ws_bytes, void *stream);
+
+/* Reads the rows' places back: k_out, v_out [n_rows][n_kv_heads][D]. */
+sn_status sn_cache_read(const sn_cache *op, void *k_out, void *v_out, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention of the call's rows over their sequences' pages: for head h, over the
+ * keys j that the row sees,
+ *     s = scale q.k_j,  p = exp(s) / sum of exp(s),  o = sum of p v_j
+ * with o [n_rows][H][D] and lse [n_rows][H] (may be NULL), the logarithm of the
+ * sum of exp(s).  A row that sees no key gives o = 0 and lse = -inf.  Keys that
+ * it does not see reach nothing, whatever they hold.  A long sequence is split
+ * over its length and joined; scores, sums and joins are fp32.  With SN_BF16 p
+ * enters its product in 16 bits. */
+sn_status sn_cache_attend(const sn_cache *op, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- timing */
 
 /* Per-kernel timing with HIP events recorded around every launch on the

@@ -34,6 +34,10 @@ SN_ACT_SILU = 2
 SN_MAX_HEAD_DIM = 128
 SN_MAX_BUCKETS = 64
 SN_MAX_BUCKET_SPAN = 2046
+SN_MAX_AXES = 8
+SN_CODES_NONE = 0
+SN_CODES_INT8 = 1
+SN_CODES_E4M3 = 2
 
 EXPORTED = (
     "sn_param_count", "sn_param_offsets", "sn_quantize_filter_weights", "sn_workspace_bytes",
@@ -43,6 +47,8 @@ EXPORTED = (
     "sn_relative_thresholds", "sn_cross_attention_workspace_bytes", "sn_cross_attention_forward",
     "sn_cross_attention_forward_train", "sn_cross_attention_backward", "sn_group_norm_workspace_bytes", "sn_group_norm_forward",
     "sn_group_norm_backward",
+    "sn_rotary_frequencies", "sn_head_rotary_workspace_bytes", "sn_head_rotary_forward", "sn_head_rotary_backward",
+    "sn_cache_workspace_bytes", "sn_cache_write", "sn_cache_read", "sn_cache_attend",
 )
 SN_STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -82,6 +88,29 @@ class SnGroupNorm(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
                 ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
+class SnHeadRotary(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("n_pairs", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("freqs", ctypes.c_void_p), ("axes", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class SnCache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("codes", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_sequences", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("row_ptr", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("n_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64)]
 
 
 class SnError(RuntimeError):
@@ -130,6 +159,14 @@ def lib() -> ctypes.CDLL:
         "sn_group_norm_workspace_bytes": (sz, [vp]),
         "sn_group_norm_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
         "sn_group_norm_backward": (i32, [vp, vp, vp, vp, i64, vp, vp, vp, vp, sz, vp]),
+        "sn_rotary_frequencies": (i32, [i32, vp, ctypes.c_double, i32, vp, vp]),
+        "sn_head_rotary_workspace_bytes": (sz, [vp]),
+        "sn_head_rotary_forward": (i32, [vp, vp, vp, vp, sz, vp]),
+        "sn_head_rotary_backward": (i32, [vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
+        "sn_cache_workspace_bytes": (sz, [vp]),
+        "sn_cache_write": (i32, [vp, vp, i64, i64, vp, i64, i64, vp, sz, vp]),
+        "sn_cache_read": (i32, [vp, vp, vp, vp, sz, vp]),
+        "sn_cache_attend": (i32, [vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -668,6 +705,251 @@ def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=N
             _flat(saved[1], "saved[1]", stats, (torch.float32,), plan.device), dy.data_ptr(), dy_stride, dx.data_ptr(),
             dgamma.data_ptr(), dbeta.data_ptr())
     return dx, dgamma, dbeta
+
+
+# ------------------------------------------------------------------ rotation of heads
+#
+# The streams, workspaces and autograd conventions of the calls below are the context operators'.
+
+_ROTARY_CALL = struct.Struct("@PPP4qPP")
+
+
+def rotary_frequencies(sections, base: float = 10000.0, shared: bool = True):
+    """sn_rotary_frequencies -> (freqs float64, axes int32), a value for each pair: sections[a] pairs turn by axis a.
+
+    shared: one ladder base^(-j/n) falls over all n pairs; else every axis has a ladder of its own."""
+    sections = np.ascontiguousarray(sections, np.int32).ravel()
+    n = max(int(np.clip(sections, 0, None).sum(dtype=np.int64)), 1)
+    freqs, axes = np.zeros(min(n, SN_MAX_HEAD_DIM), np.float64), np.zeros(min(n, SN_MAX_HEAD_DIM), np.int32)
+    _check(lib().sn_rotary_frequencies(sections.size, sections.ctypes.data, float(base), int(shared), freqs.ctypes.data,
+                                       axes.ctypes.data), "sn_rotary_frequencies")
+    return freqs, axes
+
+
+class HeadRotary:
+    """Head layout, norm and rotation of query and key rows (sn_head_rotary).
+
+    freqs, axes: host arrays with a value for each pair (see rotary_frequencies); None: nothing turns.  axes defaults
+    to one axis.  interleaved: pairs are adjacent elements instead of the halves of the part that turns.
+    norm: heads are divided by their root mean square (and multiplied by a weight) first."""
+
+    def __init__(self, n_rows: int, n_heads: int, head_dim: int, n_kv_heads: int = 0, freqs=None, axes=None,
+                 interleaved: bool = False, norm: bool = True, eps: float = 1e-6, dtype=None, device="cuda"):
+        torch = _torch()
+        self.dtype = torch.float32 if dtype is None else dtype
+        code = _row_type(self.dtype)
+        self.freqs = np.ascontiguousarray([] if freqs is None else freqs, np.float64).ravel().copy()
+        self.n_pairs = self.freqs.size
+        self.axes = np.zeros(self.n_pairs, np.int32) if axes is None else np.ascontiguousarray(axes, np.int32).ravel().copy()
+        if self.axes.size != self.n_pairs:
+            raise ValueError(f"{self.n_pairs} frequencies and {self.axes.size} axes")
+        self.n_axes = int(self.axes.max()) + 1 if self.n_pairs else 0
+        if self.n_pairs and (self.axes.min() < 0 or not np.isfinite(self.freqs).all()):
+            raise ValueError("axes must not be negative, and frequencies have to be finite")
+        self.norm = bool(norm)
+        if self.norm and not 0.0 < eps < np.inf:
+            raise ValueError(f"eps must be positive and finite, not {eps}")
+        self.n_rows, self.n_heads, self.n_kv_heads = int(n_rows), int(n_heads), int(n_kv_heads)
+        self.head_dim = int(head_dim)
+        self.c = SnHeadRotary(self.n_rows, self.n_heads, self.n_kv_heads, self.head_dim, code, int(self.norm), float(eps),
+                              self.n_pairs, self.n_axes, int(bool(interleaved)), self.freqs.ctypes.data, self.axes.ctypes.data)
+        self.workspace_bytes = int(lib().sn_head_rotary_workspace_bytes(ctypes.byref(self.c)))
+        if self.workspace_bytes == 0:
+            raise SnError(SN_ERR_INVALID, "sn_head_rotary")
+        self.head = bytes(self.c)[:SnHeadRotary.positions.offset]
+        self.device = torch.empty(0, device=device).device
+        self.pointers = ()
+        self.index, self.byte = self.device.index, torch.uint8
+        self.current_stream, self.current_device = _current_getters()
+        self.q_shape = torch.Size((self.n_rows, self.n_heads, self.head_dim))
+        self.k_shape = torch.Size((self.n_rows, self.n_kv_heads, self.head_dim))
+
+    def _rows(self, q, k, names):
+        """The strides of a query and a key tensor (k None where the plan has no key heads)."""
+        qs, qh, _ = _rows(q, names[0], self.q_shape, self.dtype, self.device)
+        if self.n_kv_heads == 0:
+            if k is not None:
+                raise ValueError(f"{names[1]} must be None: the plan has no key heads")
+            return qs, qh, 0, 0
+        if k is None:
+            raise ValueError(f"{names[1]} is missing: the plan has {self.n_kv_heads} key heads")
+        ks, kh, _ = _rows(k, names[1], self.k_shape, self.dtype, self.device)
+        return qs, qh, ks, kh
+
+    def _bind(self, q, k, positions, q_weight, k_weight) -> bytes:
+        """The descriptor of one call (its own bytes: calls from several threads share nothing)."""
+        strides = self._rows(q, k, ("q", "k"))
+        if not self.norm and (q_weight is not None or k_weight is not None):
+            raise ValueError("a weight needs the plan's norm")
+        f32, shape = (_torch().float32,), (self.head_dim,)
+        if self.n_pairs and positions is None:
+            raise ValueError("positions are missing: the plan turns pairs")
+        at = _flat(positions, "positions", (self.n_axes, self.n_rows), (_torch().int32,), self.device) if self.n_pairs else 0
+        return self.head + _ROTARY_CALL.pack(at, q.data_ptr(), _ptr(k) or 0, *strides,
+                                             _flat(q_weight, "q_weight", shape, f32, self.device),
+                                             _flat(k_weight, "k_weight", shape, f32, self.device))
+
+
+def head_rotary_workspace(plan: HeadRotary):
+    """A workspace (status words zeroed) for the plan's calls; calls that share one must be ordered on a stream."""
+    return _zeroed_workspace(plan)
+
+
+def head_rotary_forward(plan: HeadRotary, q, k, positions, ws, q_weight=None, k_weight=None, stream=None):
+    """sn_head_rotary_forward -> (q, k) normed and turned.  q [n_rows, H, D], k [n_rows, Hkv, D] (None without key
+    heads, and returned so); positions int32 [n_axes, n_rows]; weights float32 [D], None for 1."""
+    torch = _torch()
+    op = plan._bind(q, k, positions, q_weight, k_weight)
+    q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    _launch(plan, lib().sn_head_rotary_forward, stream, ws, (q, k, positions, q_weight, k_weight, q_out, k_out), op,
+            q_out.data_ptr(), _ptr(k_out))
+    return q_out, k_out
+
+
+def head_rotary_backward(plan: HeadRotary, q, k, positions, d_q, d_k, ws, q_weight=None, k_weight=None, stream=None):
+    """sn_head_rotary_backward -> (dq, dk, dq_weight, dk_weight) from the gradients of the turned rows (any strides;
+    copied if their last index is not contiguous).  The other arguments are the forward's.  The weights' gradients are
+    returned with a norm, also where a weight was None; without one they are None."""
+    torch = _torch()
+    op = plan._bind(q, k, positions, q_weight, k_weight)
+    d_q, d_k = _gradient(d_q), None if d_k is None else _gradient(d_k)
+    gs, gh, ks, kh = plan._rows(d_q, d_k, ("d_q", "d_k"))
+    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    dk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    dqw = dkw = None
+    if plan.norm:
+        dqw, dkw = torch.empty((2, plan.head_dim), dtype=torch.float32, device=plan.device).unbind(0)
+    _launch(plan, lib().sn_head_rotary_backward, stream, ws,
+            (q, k, positions, d_q, d_k, q_weight, k_weight, dq, dk, dqw, dkw), op, d_q.data_ptr(), gs, gh, _ptr(d_k), ks, kh,
+            dq.data_ptr(), _ptr(dk), _ptr(dqw), _ptr(dkw))
+    return dq, dk, dqw, dkw if plan.n_kv_heads else None
+
+
+# ------------------------------------------------------------------ state cache
+
+_CODES = {None: SN_CODES_NONE, "int8": SN_CODES_INT8, "e4m3": SN_CODES_E4M3}
+_CACHE_TABLE = struct.Struct("@PP")
+_CACHE_QUERY = struct.Struct("@P2q")
+
+
+class StateCache:
+    """Pages for the keys and values of sequences (the first part of sn_cache), zeroed.
+
+    codes: None holds rows in dtype; "int8" and "e4m3" hold 8-bit codes with a float32 scale for each row of a head.
+    k, v [n_pages, n_kv_heads, page_size, head_dim] and (with codes) k_scale, v_scale [n_pages, n_kv_heads, page_size]
+    are the storage itself, viewed without the rows' padding."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=None, codes=None, device="cuda"):
+        torch = _torch()
+        self.dtype = torch.float32 if dtype is None else dtype
+        code = _row_type(self.dtype)
+        if codes not in _CODES:
+            raise ValueError(f"codes must be one of {tuple(_CODES)}, not {codes!r}")
+        self.codes = codes
+        self.n_pages, self.page_size = int(n_pages), int(page_size)
+        self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        self.c = SnCache(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, code, _CODES[codes])
+        probe = SnCache.from_buffer_copy(self.c)
+        probe.n_sequences = probe.max_pages = 1
+        probe.n_heads = self.n_kv_heads
+        if lib().sn_cache_workspace_bytes(ctypes.byref(probe)) == 0:
+            raise SnError(SN_ERR_INVALID, "sn_cache")
+        shape = (self.n_pages, self.n_kv_heads, self.page_size, (self.head_dim + 15) // 16 * 16)
+        kind = self.dtype if codes is None else torch.int8
+        pages = [torch.zeros(shape, dtype=kind, device=device) for _ in range(2)]
+        self.k_scale = self.v_scale = None
+        if codes is not None:
+            self.k_scale, self.v_scale = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+        self.c.k, self.c.v, self.c.k_scale, self.c.v_scale = (_ptr(t) for t in (*pages, self.k_scale, self.v_scale))
+        if codes == "e4m3":
+            pages = [t.view(torch.float8_e4m3fn) for t in pages]
+        self.k, self.v = (t[..., :self.head_dim] for t in pages)
+        self.device = self.k.device
+        self.tensors = (self.k, self.v) if codes is None else (self.k, self.v, self.k_scale, self.v_scale)
+
+
+class CacheRows:
+    """The rows of a cache's sequences that a call writes, reads back or attends from (sn_cache).
+
+    row_ptr: host row offsets [B + 1]; the rows of sequence b are its last ones, at positions lengths[b] - count on.
+    max_pages: entries of a sequence in the page table.  For cache_attend: n_heads (default: the cache's), scale
+    (default 1 / sqrt(head_dim)), causal (a row sees the positions up to its own, else all) and window (> 0: only the
+    last `window` of them)."""
+
+    def __init__(self, cache: StateCache, row_ptr, max_pages: int, n_heads=None, scale=None, causal: bool = True,
+                 window: int = 0):
+        torch = _torch()
+        self.cache, self.dtype, self.device = cache, cache.dtype, cache.device
+        rp, most = _ragged(row_ptr, "row_ptr")
+        self.row_ptr = torch.from_numpy(rp).to(self.device)
+        self.n_sequences, self.n_rows, self.max_pages = rp.size - 1, int(rp[-1]), int(max_pages)
+        self.n_heads = cache.n_kv_heads if n_heads is None else int(n_heads)
+        self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        if not np.isfinite(self.scale):
+            raise ValueError(f"scale must be finite, not {scale}")
+        self.c = SnCache.from_buffer_copy(cache.c)
+        self.c.n_sequences, self.c.n_rows, self.c.max_rows, self.c.max_pages = self.n_sequences, self.n_rows, most, self.max_pages
+        self.c.row_ptr = _ptr(self.row_ptr)
+        self.c.n_heads, self.c.scale, self.c.causal, self.c.window = self.n_heads, self.scale, int(bool(causal)), int(window)
+        self.workspace_bytes = int(lib().sn_cache_workspace_bytes(ctypes.byref(self.c)))
+        if self.workspace_bytes == 0:
+            raise SnError(SN_ERR_INVALID, "sn_cache")
+        raw = bytes(self.c)
+        self.head, self.middle = raw[:SnCache.table.offset], raw[SnCache.n_heads.offset:SnCache.q.offset]
+        self.pointers = (self.row_ptr, *cache.tensors)
+        self.index, self.byte = self.device.index, torch.uint8
+        self.current_stream, self.current_device = _current_getters()
+        self.q_shape = torch.Size((self.n_rows, self.n_heads, cache.head_dim))
+        self.k_shape = torch.Size((self.n_rows, cache.n_kv_heads, cache.head_dim))
+
+    def _bind(self, table, lengths, q=None) -> bytes:
+        """The descriptor of one call (its own bytes: calls from several threads share nothing)."""
+        i32 = (_torch().int32,)
+        if table is None or lengths is None:
+            raise ValueError("the page table and the lengths are needed")
+        at = _flat(table, "table", (self.n_sequences, self.max_pages), i32, self.device)
+        held = _flat(lengths, "lengths", (self.n_sequences,), i32, self.device)
+        query = (0, 0, 0)
+        if q is not None:
+            qs, qh, _ = _rows(q, "q", self.q_shape, self.dtype, self.device)
+            query = (q.data_ptr(), qs, qh)
+        return self.head + _CACHE_TABLE.pack(at, held) + self.middle + _CACHE_QUERY.pack(*query)
+
+
+def cache_workspace(plan: CacheRows):
+    """A workspace (status words zeroed) for the plan's calls; calls that share one must be ordered on a stream."""
+    return _zeroed_workspace(plan)
+
+
+def cache_write(plan: CacheRows, k, v, table, lengths, ws, stream=None):
+    """sn_cache_write: the rows k and v [n_rows, Hkv, D] to their places.  table int32 [B, max_pages] holds the pages
+    of each sequence in order, lengths int32 [B] its rows with these among them."""
+    op = plan._bind(table, lengths)
+    ks, kh, _ = _rows(k, "k", plan.k_shape, plan.dtype, plan.device)
+    vs, vh, _ = _rows(v, "v", plan.k_shape, plan.dtype, plan.device)
+    _launch(plan, lib().sn_cache_write, stream, ws, (k, v, table, lengths), op, k.data_ptr(), ks, kh, v.data_ptr(), vs, vh)
+
+
+def cache_read(plan: CacheRows, table, lengths, ws, stream=None):
+    """sn_cache_read -> (k, v) [n_rows, Hkv, D]: the plan's rows as the pages hold them."""
+    torch = _torch()
+    op = plan._bind(table, lengths)
+    k, v = torch.empty((2, *plan.k_shape), dtype=plan.dtype, device=plan.device).unbind(0)
+    _launch(plan, lib().sn_cache_read, stream, ws, (k, v, table, lengths), op, k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+def cache_attend(plan: CacheRows, q, table, lengths, ws, save: bool = False, stream=None):
+    """sn_cache_attend -> o [n_rows, H, D]: attention of the plan's rows q over their sequences' pages; with save=True
+    -> (o, lse), lse float32 [n_rows, H] the logarithm of the sum of exp of the scores, by which parts over different
+    keys can be joined."""
+    torch = _torch()
+    op = plan._bind(table, lengths, q)
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty(plan.q_shape[:2], dtype=torch.float32, device=plan.device) if save else None
+    _launch(plan, lib().sn_cache_attend, stream, ws, (q, table, lengths, o, lse), op, o.data_ptr(), _ptr(lse))
+    return (o, lse) if save else o
 
 
 # ------------------------------------------------------------------ timing

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 OUT = os.path.join(HERE, "libsn.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["neighbors.hip", "graph.hip", "mlp.hip", "filter.hip", "attention_fwd.hip", "attention_bwd.hip", "norm.hip", "context.hip", "api.hip"]
+SOURCES = ["neighbors.hip", "graph.hip", "mlp.hip", "filter.hip", "attention_fwd.hip", "attention_bwd.hip", "norm.hip", "context.hip",
+           "rotary.hip", "cache.hip", "cache_attend.hip", "state.hip", "api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -33,7 +33,8 @@ std::vector<hipEvent_t> g_event_pool;  // reused events (creating events is slow
 const char *kClassNames[K_NUM_CLASSES] = {
     "nb_grid", "nb_bin", "nb_scan", "nb_count", "nb_fill", "nb_rev", "pairs", "mlp",
     "filter_fwd", "cfconv", "filter_bwd", "forces", "verlet", "kinetic", "pack",
-    "attn_fwd", "attn_bwd", "norm_fwd", "norm_bwd"};
+    "attn_fwd", "attn_bwd", "norm_fwd", "norm_bwd",
+    "rotary_fwd", "rotary_bwd", "cache_write", "cache_read", "cache_attend"};
 }  // namespace
 
 static hipEvent_t pooled_event() {
