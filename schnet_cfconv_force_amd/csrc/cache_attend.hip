@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kThreads) void attend_plain_kernel(CacheArgs a, T *
         l = l * keep + block_sum(e, buf);
         m = top;
         p[threadIdx.x] = e == 0.0f ? 0.0f : e * vs;
+        __syncthreads();    // every thread has the sum before its place is used again
         buf[threadIdx.x] = s;
         __syncthreads();
 #pragma unroll
