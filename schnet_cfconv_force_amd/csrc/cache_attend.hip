@@ -28,7 +28,7 @@
 namespace sn {
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -53,6 +53,8 @@ struct Form {
     // registers of a key block and of a value row
     static constexpr int KREGS = F32 ? DP / 4 : ES == 2 ? DP / 8 : DP / 16;
     static constexpr int VREGS = (W * ES + 3) / 4;
+    // blocks that a CU holds: short rows of one tile fit 128 registers
+    static constexpr int BLOCKS = DP == 32 && NR == 1 ? 2 : 1;
 };
 
 struct AttendCut {
@@ -65,8 +67,9 @@ struct AttendCut {
 // A row's statistics in a partial result: maximum (of scores in powers of
 // two) and sum.
 struct Partials {
-    float *o;           // [2 blocks][16 NR][DP], divided by the sum
+    int2 *cuts;         // [sequence][unit]: first and last block that share the unit
     float2 *ml;         // [2 blocks][16 NR]
+    float *o;           // [2 blocks][16 NR][DP], divided by the sum
 };
 
 // --------------------------------------------------------------- sequences
@@ -104,60 +107,76 @@ __device__ inline Sequence uniform_sequence(Sequence s) {
     return s;
 }
 
-// The line of all units' tiles: sequence by sequence, in each unit by unit.
+// The line of all units' tiles, sequence by sequence, in each unit by unit,
+// cut into n shares that differ by one tile at most.  (The host keeps a line
+// below 2^31 tiles.)
 struct Line {
-    int64_t total;
-    int b;              // the sequence asked for
-    int64_t first;      // its first tile in the line
+    int total, part;        // tiles; tiles of the smaller shares
+    int n, more;            // shares; the first `more` have one tile more
+    __device__ inline Line(const AttendCut &c, int total_) : total(total_) {
+        n = min(c.blocks, max(1, total / c.least));
+        part = total / n;
+        more = total - part * n;
+    }
+    __device__ inline int begin(int i) const { return part * i + min(i, more); }
+    __device__ inline int share_of(int tile) const {
+        const int wide = (part + 1) * more;
+        return tile < wide ? tile / (part + 1) : more + (tile - wide) / part;
+    }
 };
-// by_tile: the sequence that holds tile `at`; else the first tile of sequence
-// `at`.  shared: 8 words of LDS.
-template <class F, class At>
-__device__ inline Line line_of(const CacheArgs &a, int units, At at_of, bool by_tile, int64_t *shared) {
-    Line r{0, 0, 0};
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t at = 0;
-    for (int pass = a.B > kThreads ? 0 : 1; pass < 2; ++pass) {     // many sequences: the total first
-        int64_t base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            const int64_t own = b < a.B ? (int64_t)sequence_of<F>(a, b).tiles * units : 0;
-            int64_t sum = own;
+
+// The sequence in which block `id`'s share begins, that sequence's first tile
+// in the line and the line's length.  Every wavefront finds them by itself, a
+// lane for a sequence.
+struct Start {
+    int total, first, b;
+    Sequence s;
+};
+template <class F>
+__device__ inline Start start_of(const CacheArgs &a, const AttendCut &c, int id) {
+    const int lane = threadIdx.x & 63;
+    Start r{0, 0, -1, {}};
+    int at = -1;
+    for (int pass = a.B > 64 ? 0 : 1; pass < 2; ++pass) {       // many sequences: the total first
+        int base = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 64) {
+            Sequence s;
+            s.tiles = 0;
+            if (b0 + lane < a.B) s = sequence_of<F>(a, b0 + lane);
+            const int own = s.tiles * c.units;
+            int sum = own;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
-                const int64_t below = __shfl_up(sum, o);
+                const int below = __shfl_up(sum, o);
                 if (lane >= o) sum += below;
             }
-            if (lane == 63) shared[wave] = sum;
-            __syncthreads();
-            int64_t before = base;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                if (w < wave) before += shared[w];
-                base += shared[w];
+            const int first = base + sum - own;
+            base += __builtin_amdgcn_readlane(sum, 63);
+            if (pass == 0) continue;
+            if (a.B <= 64) {
+                const Line line(c, base);
+                at = id < line.n ? line.begin(id) : -1;
             }
-            if (pass == 1) {
-                if (a.B <= kThreads) at = at_of(base);
-                const int64_t first = before + sum - own;
-                if (b < a.B && (by_tile ? at >= first && at < first + own : at == b)) {
-                    shared[kWaves] = b;
-                    shared[kWaves + 1] = first;
-                }
+            const uint64_t here = __ballot(at >= first && at < first + own);
+            if (here != 0) {
+                const int l = __builtin_ctzll(here);
+                r.b = b0 + l;
+                r.first = __builtin_amdgcn_readlane(first, l);
+                r.s.r0 = __builtin_amdgcn_readlane(s.r0, l);
+                r.s.n = __builtin_amdgcn_readlane(s.n, l);
+                r.s.length = __builtin_amdgcn_readlane(s.length, l);
+                r.s.begin = __builtin_amdgcn_readlane(s.begin, l);
+                r.s.tiles = __builtin_amdgcn_readlane(s.tiles, l);
             }
-            __syncthreads();
         }
         r.total = base;
-        at = at_of(base);
+        if (pass == 0) {
+            const Line line(c, base);
+            at = id < line.n ? line.begin(id) : -1;
+        }
     }
-    r.b = __builtin_amdgcn_readfirstlane((int)shared[kWaves]);
-    r.first = shared[kWaves + 1];
     return r;
 }
-// Blocks that share a line of `total` tiles, and the first tile of block i.
-__device__ inline int sharers(const AttendCut &c, int64_t total) {
-    return (int)min((int64_t)c.blocks, max((int64_t)1, total / c.least));
-}
-__device__ inline int64_t share(int64_t total, int i, int n) { return total * i / n; }
 
 // --------------------------------------------------------------- products
 
@@ -206,32 +225,30 @@ struct Tile {
     uint32_t k[F::NB][F::KREGS];
     uint32_t v[F::NB][4][F::VREGS];
     floatx4 ks[F::CODES ? F::NB : 1], vs[F::CODES ? F::NB : 1];
-    // dims that a row does not have are not loaded: they stay zero
-    __device__ inline Tile() {
-#pragma unroll
-        for (int b = 0; b < F::NB; ++b) {
-#pragma unroll
-            for (int c = 0; c < F::KREGS; ++c) k[b][c] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < F::VREGS; ++c) v[b][i][c] = 0;
-        }
-    }
 };
 
-template <int N>
-__device__ inline void load_regs(uint32_t (&r)[N], int at, const char *p) {
-    if constexpr (N >= 4) {
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[at + i] = v[i];
-    } else if constexpr (N == 2) {
-        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-        r[at] = v[0];
-        r[at + 1] = v[1];
+// Blocks are read through buffer descriptors: the base is scalar, a lane's
+// offset a constant of the walk, and dims that a row does not have are asked
+// for out of range, which gives zeros without a branch.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ inline __amdgpu_buffer_rsrc_t block_at(const void *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7fffffff, 0x00020000);
+}
+template <int BYTES>
+__device__ inline void load_bytes(uint32_t *r, __amdgpu_buffer_rsrc_t block, uint32_t lane, int offset) {
+    if constexpr (BYTES == 2) {
+        r[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(block, lane, offset, 0);
+    } else if constexpr (BYTES == 4) {
+        r[0] = __builtin_amdgcn_raw_buffer_load_b32(block, lane, offset, 0);
+    } else if constexpr (BYTES == 8) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(block, lane, offset, 0));
+        r[0] = v[0];
+        r[1] = v[1];
     } else {
-        r[at] = *reinterpret_cast<const uint32_t *>(p);
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(block, lane, offset, 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = v[i];
+        if constexpr (BYTES == 32) load_bytes<16>(r + 4, block, lane + 16, offset);
     }
 }
 
@@ -241,21 +258,22 @@ struct Walk {
     const CacheArgs &a;
     const __attribute__((address_space(4))) int32_t *table;     // the sequence's pages
     int hk, key0, end;      // key/value head; first key of tile 0 (a multiple of 16), end of the keys
-    uint32_t ko, vo, row;   // byte offsets: the key row's dims, the value rows' dims, a row
-    bool kd[4], vd;         // whether the row has the dims
+    int row;                // bytes of a row
+    static constexpr int KBYTES = F::KREGS == 2 ? 8 : 16, KLOADS = F::KREGS * 4 / KBYTES;
+    uint32_t ko[KLOADS], vo;    // a lane's offsets in a block: its key row's dims, its value row's dims
     int g;
 
     __device__ inline Walk(const CacheArgs &a_) : a(a_) {
         const int lane = threadIdx.x & 63, n = lane & 15;
         g = lane >> 4;
         row = a.Dp * F::ES;
-        const int kd0 = F::F32 ? 4 * g : F::ES == 2 || F::DP == 32 ? 8 * g : 16 * g;      // first dim of a load
-        ko = n * row + kd0 * F::ES;
-        vo = 4 * g * row + n * F::W * F::ES;
-        vd = n * F::W < a.Dp;
-        const int step = F::F32 ? 16 : F::ES == 2 ? 32 : 64;
+        constexpr int per = KBYTES / F::ES;                     // dims of a load; four lanes have a row's next 4 per
 #pragma unroll
-        for (int c = 0; c < 4; ++c) kd[c] = c * step + kd0 < a.Dp;
+        for (int c = 0; c < KLOADS; ++c) {
+            const int d = 4 * per * c + per * g;
+            ko[c] = d < a.Dp ? n * row + d * F::ES : kNowhere;
+        }
+        vo = n * F::W < a.Dp ? 4 * g * row + n * F::W * F::ES : kNowhere;
     }
     __device__ inline int key_of(int tile, int b) const { return key0 + tile * F::TILE + 16 * b; }
     // Pages of a tile's blocks; blocks behind the last key stand for the last one.
@@ -273,33 +291,22 @@ struct Walk {
 #pragma unroll
         for (int b = 0; b < F::NB; ++b) {
             const int64_t at = place(tile, b, pg);
-            const char *p = static_cast<const char *>(a.k) + at * row + ko;
-            if constexpr (F::KREGS == 2) {
-                if (kd[0]) load_regs<2>(t.k[b], 0, p);
-            } else {
+            const __amdgpu_buffer_rsrc_t block = block_at(static_cast<const char *>(a.k) + at * row);
 #pragma unroll
-                for (int c = 0; c < F::KREGS; c += 4)       // 64 bytes of a row between two loads
-                    if (c / 4 < 4 ? kd[c / 4 & 3] : c / 4 * 16 + 4 * g < a.Dp) load_regs<F::KREGS>(t.k[b], c, p + c / 4 * 64);
-            }
-            if constexpr (F::CODES != SN_CODES_NONE) t.ks[b] = *reinterpret_cast<const floatx4 *>(a.k_scale + at + 4 * g);
+            for (int c = 0; c < KLOADS; ++c) load_bytes<KBYTES>(&t.k[b][c * KBYTES / 4], block, ko[c], 0);
+            if constexpr (F::CODES != SN_CODES_NONE)
+                t.ks[b] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(block_at(a.k_scale + at), 16 * g, 0, 0));
         }
     }
     __device__ inline void load_values(int tile, const int (&pg)[F::NB], Tile<F> &t) const {
 #pragma unroll
         for (int b = 0; b < F::NB; ++b) {
             const int64_t at = place(tile, b, pg);
-            const char *p = static_cast<const char *>(a.v) + at * row + vo;
-            if (vd)
+            const __amdgpu_buffer_rsrc_t block = block_at(static_cast<const char *>(a.v) + at * row);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (F::W * F::ES == 2) {
-                        t.v[b][i][0] = *reinterpret_cast<const uint16_t *>(p + i * row);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < F::VREGS; c += 4) load_regs<F::VREGS>(t.v[b][i], c, p + i * row + 4 * c);
-                    }
-                }
-            if constexpr (F::CODES != SN_CODES_NONE) t.vs[b] = *reinterpret_cast<const floatx4 *>(a.v_scale + at + 4 * g);
+            for (int i = 0; i < 4; ++i) load_bytes<F::W * F::ES>(t.v[b][i], block, vo, i * row);
+            if constexpr (F::CODES != SN_CODES_NONE)
+                t.vs[b] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(block_at(a.v_scale + at), 16 * g, 0, 0));
         }
     }
 };
@@ -321,18 +328,44 @@ struct Queries {
             const T *q = static_cast<const T *>(a.q) + (live ? (s.r0 + t) * a.qs + h * a.qh : 0);
             if constexpr (F::F32) {
 #pragma unroll
-                for (int i = 0; i < F::DP / 4; ++i) {
-                    const int d = i / 4 * 16 + 4 * g + i % 4;
-                    x[nr][i] = live && d < a.D ? q[d] : 0.0f;
+                for (int i = 0; i < F::DP / 4; i += 4) {
+                    const int d = i / 4 * 16 + 4 * g;
+                    floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (a.q_vec) {
+                        if (live && d < a.D) y = *reinterpret_cast<const floatx4 *>(q + d);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (live && d + e < a.D) y[e] = q[d + e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[nr][i + e] = y[e];
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < F::DP / 32; ++c) {
                     // dims of product c: of 8-bit rows a lane reads 16, two products' worth
                     const int d0 = F::ES == 2 || F::DP == 32 ? 32 * c + 8 * g : c / 2 * 64 + 16 * g + c % 2 * 8;
+                    T raw[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) raw[e] = (T)0.0f;
+                    if (a.q_vec) {
+                        typedef T vec_t __attribute__((ext_vector_type(16 / sizeof(T))));
+                        if (live && d0 < a.D)
+#pragma unroll
+                            for (int e = 0; e < 8; e += 16 / sizeof(T)) {
+                                const vec_t y = *reinterpret_cast<const vec_t *>(q + d0 + e);
+#pragma unroll
+                                for (int i = 0; i < (int)(16 / sizeof(T)); ++i) raw[e + i] = y[i];
+                            }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (live && d0 + e < a.D) raw[e] = q[d0 + e];
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        float y = live && d0 + e < a.D ? to_f32(q[d0 + e]) : 0.0f;
+                        float y = to_f32(raw[e]);
 #pragma unroll
                         for (int p = 0; p < F::QP; ++p) {
                             f[nr][c][p][e] = (bf16)y;
@@ -683,9 +716,9 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
         Tile<F> tile_regs;
         int pg[F::NB], next_pg[F::NB];
         w.pages(wave, pg);
+        q.load(a, s, hk, tile);
         w.load_keys(wave, pg, tile_regs);
         w.load_values(wave, pg, tile_regs);
-        q.load(a, s, hk, tile);
         w.pages(min(wave + kWaves, tiles - 1), next_pg);
         for (int i = wave; i < tiles; i += kWaves) {
             const int next = i + kWaves;
@@ -758,7 +791,7 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
             x.odd[r] = 1;
             x.any = 1;
         }
-        if (d < a.D) put(r, d, v);
+        if (d < a.D || slot >= 0) put(r, d, v);
     }
     if ((int)threadIdx.x < rows) put_stats(threadIdx.x, x.stats[threadIdx.x][0], x.stats[threadIdx.x][1]);
     __syncthreads();
@@ -776,9 +809,8 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
 }
 
 template <class F>
-__global__ __launch_bounds__(kThreads, 2) void attend_kernel(CacheArgs a, AttendCut c, Partials parts, typename F::T *o, float *lse) {
+__global__ __launch_bounds__(kThreads, 2 * F::BLOCKS) void attend_kernel(CacheArgs a, AttendCut c, Partials parts, typename F::T *o, float *lse) {
     __shared__ Exchange<F> x;
-    __shared__ int64_t words[kWaves + 2];
     if (c.blocks == 0) {        // a unit a block
         const int id = xcd_block(a.B * c.units);
         if (id < 0) return;
@@ -789,108 +821,186 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(CacheArgs a, Attend
     }
     const int id = xcd_block(c.blocks);
     if (id < 0) return;
-    int n = 1;
-    const Line line = line_of<F>(a, c.units, [&](int64_t total) {
-        n = sharers(c, total);
-        return id < n ? share(total, id, n) : (int64_t)-1; }, true, words);
-    if (id >= n || line.total == 0) return;
-    int64_t at = share(line.total, id, n);
-    const int64_t end = share(line.total, id + 1, n);
-    int64_t first = line.first;
-    for (int b = line.b; at < end; ++b) {
-        const Sequence s = uniform_sequence(sequence_of<F>(a, b));
-        if (s.tiles == 0) continue;
-        while (at < end && at < first + (int64_t)s.tiles * c.units) {
-            const int unit = (int)((at - first) / s.tiles);
-            const int64_t u0 = first + (int64_t)unit * s.tiles, u1 = u0 + s.tiles, stop = min(u1, end);
+    const Start start = start_of<F>(a, c, id);
+    if (start.b < 0) return;        // fewer shares than blocks, or no tiles
+    const Line line(c, start.total);
+    int at = line.begin(id), first = start.first, b = start.b;
+    const int end = line.begin(id + 1);
+    Sequence s = start.s;
+    while (true) {
+        while (s.tiles > 0 && at < end && at < first + s.tiles * c.units) {
+            const int unit = (at - first) / s.tiles, u0 = first + unit * s.tiles, u1 = u0 + s.tiles, stop = min(u1, end);
             // the block's first piece may begin inside a unit; else, if it is not whole, its last ends inside
             const int slot = at == u0 && stop == u1 ? -1 : at == u0 ? 2 * id + 1 : 2 * id;
-            piece<F>(a, c, b, s, unit, (int)(at - u0), (int)(stop - u0), slot, parts, o, lse, x);
+            if (at == u0 && threadIdx.x == 0)
+                parts.cuts[(int64_t)b * c.units + unit] = make_int2(id, stop == u1 ? id : line.share_of(u1 - 1));
+            piece<F>(a, c, b, s, unit, at - u0, stop - u0, slot, parts, o, lse, x);
             at = stop;
         }
-        first += (int64_t)s.tiles * c.units;
+        if (at >= end) return;
+        first += s.tiles * c.units;
+        s = uniform_sequence(sequence_of<F>(a, ++b));
     }
 }
 
 // Units that were cut: their rows' partial results on one maximum, in order.
+constexpr int kJoinThreads = 256, kJoinWeights = 4096;
 template <class F>
-__global__ __launch_bounds__(kThreads) void attend_join_kernel(CacheArgs a, AttendCut c, Partials parts, typename F::T *o, float *lse) {
-    __shared__ int64_t words[kWaves + 2];
+__global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(CacheArgs a, AttendCut c, Partials parts, typename F::T *o, float *lse) {
+    constexpr int R = 16 * F::NR;
+    __shared__ float weights[kJoinWeights], sums[R][2];
+    __shared__ alignas(16) float held[kJoinThreads * 4];
     const int b = blockIdx.x / c.units, unit = blockIdx.x % c.units;
-    const Line line = line_of<F>(a, c.units, [&](int64_t) { return (int64_t)b; }, false, words);
+    const int2 cut = parts.cuts[blockIdx.x];
     const Sequence s = uniform_sequence(sequence_of<F>(a, b));
-    if (s.tiles == 0) return;
-    const int n = sharers(c, line.total);
-    const int64_t u0 = line.first + (int64_t)unit * s.tiles, u1 = u0 + s.tiles;
-    // the block of tile t is the last one whose share begins at or before it
-    auto block_of = [&](int64_t t) { return (int)(((t + 1) * n - 1) / line.total); };
-    const int i0 = block_of(u0), i1 = block_of(u1 - 1);
-    if (i0 == i1) return;
-    const int hk = unit / c.row_tiles, tile = unit % c.row_tiles, rows = min(s.n * a.G - tile * 16 * F::NR, 16 * F::NR);
-    auto slot_of = [&](int i) { return share(line.total, i, n) <= u0 ? 2 * i + 1 : 2 * i; };
-    for (int i = threadIdx.x; i < rows * F::DP; i += kThreads) {
-        const int r = i / F::DP, d = i % F::DP;
-        const int row = tile * 16 * F::NR + r, t = row / a.G, h = hk * a.G + row % a.G;
-        float top = -INFINITY, sum = 0.0f, v = 0.0f;
-        for (int k = i0; k <= i1; ++k) top = fmaxf(top, parts.ml[(int64_t)slot_of(k) * 16 * F::NR + r].x);
+    if (s.tiles == 0) return;       // no block wrote here
+    const int hk = unit / c.row_tiles, tile = unit % c.row_tiles, rows = min(s.n * a.G - tile * R, R), n = cut.y - cut.x + 1;
+    if (n <= 1 || rows <= 0) return;
+    // the first piece is its block's last one, the others are their blocks' first
+    auto slot_of = [&](int k) { return k == 0 ? 2 * cut.x + 1 : 2 * (cut.x + k); };
+    auto at_of = [&](int k, int r) { return (int64_t)slot_of(k) * R + r; };
+    // a row's maximum and sum: the sixteen lanes of a group
+    for (int r = threadIdx.x / 16; r < rows; r += kJoinThreads / 16) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int k = threadIdx.x % 16; k < n; k += 16) top = fmaxf(top, parts.ml[at_of(k, r)].x);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
         const float base = top == -INFINITY ? 0.0f : top;
-        for (int k = i0; k <= i1; ++k) {
-            const int64_t at = (int64_t)slot_of(k) * 16 * F::NR + r;
-            const float2 ml = parts.ml[at];
-            if (ml.y == 0.0f) continue;
-            const float e = ml.y * __builtin_amdgcn_exp2f(ml.x - base), x = parts.o[at * F::DP + d];
-            sum += e;
-            v += x * (fabsf(x) < INFINITY ? e : fmaxf(e, 1e-38f));
+        for (int k = threadIdx.x % 16; k < n; k += 16) {
+            const float2 ml = parts.ml[at_of(k, r)];
+            sum += ml.y * __builtin_amdgcn_exp2f(ml.x - base);
         }
-        if (d < a.D) o[((int64_t)(s.r0 + t) * a.H + h) * a.D + d] = (typename F::T)(sum == 0.0f ? 0.0f : v / sum);
-        if (lse && d == 0)
-            lse[(int64_t)(s.r0 + t) * a.H + h] = top == -INFINITY ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor(sum, o);
+        if (threadIdx.x % 16 == 0) {
+            sums[r][0] = top;
+            sums[r][1] = sum;
+        }
+    }
+    // four elements a thread; where the rows are few, several threads share
+    // them and take every parts-th piece
+    const int quads = rows * (F::DP / 4), parallel = max(1, kJoinThreads / quads), part = threadIdx.x / quads;
+    const int chunk = kJoinWeights / R;
+    for (int q0 = 0; q0 < quads; q0 += kJoinThreads) {
+        const int quad = q0 + (parallel > 1 ? (int)threadIdx.x % quads : (int)threadIdx.x), r = quad * 4 / F::DP;
+        const bool has = quad < quads && part < parallel;
+        floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k0 = 0; k0 < n; k0 += chunk) {
+            __syncthreads();
+            const int m = min(chunk, n - k0);
+            for (int i = threadIdx.x; i < m * R; i += kJoinThreads) {
+                if (i % R >= rows) continue;
+                const float2 ml = parts.ml[at_of(k0 + i / R, i % R)];
+                const float top = sums[i % R][0], sum = sums[i % R][1];
+                weights[i] = ml.y * __builtin_amdgcn_exp2f(ml.x - (top == -INFINITY ? 0.0f : top)) / (sum == 0.0f ? 1.0f : sum);
+            }
+            __syncthreads();
+            if (!has) continue;
+            const floatx4 before = v;
+#pragma unroll 8
+            for (int k = part; k < m; k += parallel)
+                v += weights[k * R + r] * *reinterpret_cast<const floatx4 *>(parts.o + at_of(k0 + k, 0) * F::DP + quad * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (fabsf(v[e]) < INFINITY) continue;
+                // a weight that underflows still lets an infinity through
+                v[e] = before[e];
+                for (int k = part; k < m; k += parallel) {
+                    const float w = weights[k * R + r], x = parts.o[at_of(k0 + k, 0) * F::DP + quad * 4 + e];
+                    v[e] += x * (fabsf(x) < INFINITY ? w : fmaxf(w, 1e-38f));
+                }
+            }
+        }
+        if (parallel > 1) {
+            __syncthreads();
+            if (has) *reinterpret_cast<floatx4 *>(&held[threadIdx.x * 4]) = v;
+            __syncthreads();
+            if (part == 0)
+                for (int p = 1; p < parallel; ++p) v += *reinterpret_cast<const floatx4 *>(&held[(p * quads + threadIdx.x) * 4]);
+        }
+        if (!has || part > 0) continue;
+        const int row = tile * R + r, t = row / a.G, h = hk * a.G + row % a.G;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int d = quad * 4 % F::DP + e;
+            if (d < a.D) o[((int64_t)(s.r0 + t) * a.H + h) * a.D + d] = (typename F::T)v[e];
+        }
+        if (lse && quad * 4 % F::DP == 0)
+            lse[(int64_t)(s.r0 + t) * a.H + h] =
+                sums[r][0] == -INFINITY ? -INFINITY : (sums[r][0] + __builtin_amdgcn_logf(sums[r][1])) * kLn2;
     }
 }
 
 // --------------------------------------------------------------- launches
 
-constexpr int kSharers = 512;       // two blocks on each CU
+constexpr int kCus = 256;
 
-inline int rows_per_tile(int rows) { return rows > 16 ? 2 : 1; }
+inline int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+inline int64_t rows_of(int max_rows, int G) { return (int64_t)max_rows * G; }
 
-AttendCut cut_of(int B, int Hkv, int64_t rows, int64_t capacity, int tile_keys) {
-    AttendCut c;
-    const int per = 16 * rows_per_tile((int)std::min<int64_t>(rows, 64));
-    c.row_tiles = (int)std::max<int64_t>(1, (rows + per - 1) / per);
+// Tiles of 16 rows for which a block reads the keys once.  Two halve what is
+// read, but their blocks are half as many and take a CU alone: 64 x 8 rows of
+// 32/8 heads over 1000 keys, bf16, 64: 39 us with one, 30 with two; 128: 56 and
+// 42; 8 x 16 rows over 500 keys, 128: 11.5 and 16.  Heads of 32 gain nothing
+// (19 and 20), and fp32 rows of 128 do not fit the registers twice (114 and
+// 132, 8-bit rows 55 and 63).
+inline int tiles_of_block(int dtype, int DP, int64_t sequences, int Hkv, int64_t rows) {
+    if (rows <= 16 || DP == 32 || (DP == 128 && dtype == SN_F32)) return 1;
+    return sequences * Hkv * ((rows + 15) / 16) >= 2 * kCus ? 2 : 1;
+}
+
+AttendCut cut_of(int Hkv, int64_t rows, int nr) {
+    AttendCut c{};
+    c.row_tiles = (int)std::max<int64_t>(1, (rows + 16 * nr - 1) / (16 * nr));
     c.units = Hkv * c.row_tiles;
     c.least = kWaves;
-    c.blocks = kSharers;
-    const int64_t tiles = (capacity + tile_keys - 1) / tile_keys + 1;
-    if ((int64_t)B * c.units >= 16 * kSharers || tiles <= 4 * kWaves) c.blocks = 0;
     return c;
 }
 
-// A cut for sizes alone; the launch makes its own with the form's tile.
-AttendCut cut_of(const sn_cache &op) {
-    return cut_of(op.n_sequences, op.n_kv_heads, (int64_t)op.max_rows * (op.n_heads / op.n_kv_heads), INT32_MAX, 16);
+// Whether units are cut.  A block takes about 2 us for a round (a tile of each
+// wavefront; 1.5 us with short rows) and the join and its launch cost 11 us more; sequences are taken
+// to be a little over half of what the table holds.  Few units: cut where the
+// rounds that a unit takes one after the other are longer than that (1 x 4000
+// keys, 32/8 x 128 bf16: 40 us whole, 18 cut; 1 x 1000: 14.7 and 15.0; 8 x 4000:
+// 42 and 28; 16 x 2000: 25 and 27).  Units on every CU: cut where the longest
+// ones would keep some CUs alone (32 x 20000: 323 and 290; 64 x 12000: 370 and
+// 335; 64 x 1000: 32 and 45).  Many units even out by themselves.
+template <class F>
+bool worth_cutting(const CacheArgs &a, const AttendCut &c) {
+    int64_t span = (int64_t)a.max_pages * a.page;
+    if (a.window > 0) span = std::min(span, (int64_t)a.window + a.max_rows + 15);
+    const double units = (double)a.B * c.units, places = kCus * F::BLOCKS;
+    const int64_t tiles = (span + F::TILE - 1) / F::TILE + 1;
+    const double rounds = (double)tiles / kWaves, bytes = (double)kWaves * F::TILE * 2 * a.Dp * F::ES;
+    const double streaming = 0.6 * units * rounds * bytes / 5.2e6;      // us at 5.2 TB/s
+    if (units * tiles > INT32_MAX) return false;                        // a line of tiles is counted in 32 bits
+    return units < places ? (F::BLOCKS == 2 ? 1.5 : 2.0) * rounds > 11.0 + streaming || streaming > 80.0 : units < 4 * places && streaming > 80.0;
 }
 
-inline int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+inline size_t cuts_bytes(const AttendCut &c, int B) { return align256(sizeof(int2) * (size_t)B * c.units); }
 
 template <class F>
 sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t s) {
     using T = typename F::T;
-    const AttendCut c = cut_of(a.B, a.Hkv, (int64_t)a.max_rows * a.G, (int64_t)a.max_pages * a.page, F::TILE);
+    AttendCut c = cut_of(a.Hkv, rows_of(a.max_rows, a.G), F::NR);
+    if (worth_cutting<F>(a, c)) c.blocks = kCus * F::BLOCKS;
     Partials parts;
-    parts.ml = reinterpret_cast<float2 *>(ws + kWsBase);
-    parts.o = reinterpret_cast<float *>(ws + kWsBase + sizeof(float2) * 2 * kSharers * 16 * F::NR);
+    parts.cuts = reinterpret_cast<int2 *>(ws + kWsBase);
+    parts.ml = reinterpret_cast<float2 *>(ws + kWsBase + cuts_bytes(c, a.B));
+    parts.o = reinterpret_cast<float *>(parts.ml + 2 * kCus * F::BLOCKS * 16 * F::NR);
     ProfScope prof(K_CACHE_ATTEND, s);
     const int grid = xcd_grid(c.blocks ? c.blocks : a.B * c.units);
     attend_kernel<F><<<grid, kThreads, 0, s>>>(a, c, parts, static_cast<T *>(o), lse);
     SN_TRY(launch_status());
-    if (c.blocks) attend_join_kernel<F><<<a.B * c.units, kThreads, 0, s>>>(a, c, parts, static_cast<T *>(o), lse);
+    if (c.blocks) attend_join_kernel<F><<<a.B * c.units, kJoinThreads, 0, s>>>(a, c, parts, static_cast<T *>(o), lse);
     return launch_status();
 }
 template <typename T, int CODES, int DP>
 sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t s) {
-    return rows_per_tile(std::min<int64_t>((int64_t)a.max_rows * a.G, 64)) == 2 ? launch<Form<T, CODES, DP, 2>>(a, o, lse, ws, s)
-                                                                      : launch<Form<T, CODES, DP, 1>>(a, o, lse, ws, s);
+    constexpr int dtype = std::is_same<T, float>::value ? SN_F32 : SN_BF16;
+    if constexpr (DP == 64 || (DP == 128 && dtype == SN_BF16))
+        if (tiles_of_block(dtype, DP, a.B, a.Hkv, rows_of(a.max_rows, a.G)) == 2) return launch<Form<T, CODES, DP, 2>>(a, o, lse, ws, s);
+    return launch<Form<T, CODES, DP, 1>>(a, o, lse, ws, s);
 }
 template <typename T, int CODES>
 sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t s) {
@@ -909,12 +1019,15 @@ sn_status launch(const CacheArgs &a, int codes, void *o, float *lse, char *ws, h
 
 // Units are blocks of their own, or of the join.
 bool attend_fits(const sn_cache &op) {
-    return grid_fits((int64_t)op.n_sequences * cut_of(op).units + kXcds, kThreads);
+    const AttendCut c = cut_of(op.n_kv_heads, rows_of(op.max_rows, op.n_heads / op.n_kv_heads), 1);
+    return grid_fits((int64_t)op.n_sequences * c.units + kXcds, kThreads);
 }
 
 size_t attend_workspace(const sn_cache &op) {
-    const size_t rows = (size_t)2 * kSharers * 16 * rows_per_tile((int)std::min<int64_t>((int64_t)op.max_rows * (op.n_heads / op.n_kv_heads), 64));
-    return kWsBase + rows * (sizeof(float2) + padded(op.head_dim) * sizeof(float));
+    const int64_t rows = rows_of(op.max_rows, op.n_heads / op.n_kv_heads);
+    const int DP = padded(op.head_dim), nr = tiles_of_block(op.dtype, DP, op.n_sequences, op.n_kv_heads, rows);
+    const size_t held = (size_t)2 * kCus * (DP == 32 ? 2 : 1) * 16 * nr;
+    return kWsBase + cuts_bytes(cut_of(op.n_kv_heads, rows, nr), op.n_sequences) + held * (sizeof(float2) + DP * sizeof(float));
 }
 
 sn_status cache_attend(const CacheArgs &a, int dtype, int codes, void *o, float *lse, char *ws, hipStream_t s) {

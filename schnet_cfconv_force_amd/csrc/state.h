@@ -49,6 +49,7 @@ struct CacheArgs {
     int causal, window;
     const void *q;
     int64_t qs, qh;
+    int q_vec;                      // q's rows suit 16-byte reads
 };
 
 // Rows of sequence b in the call (r0, n) and its length, or n = 0 where the

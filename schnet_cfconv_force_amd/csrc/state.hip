@@ -107,6 +107,8 @@ CacheArgs cache_args(const sn_cache &op, void *ws) {
     a.H = op.n_heads; a.G = op.n_heads / op.n_kv_heads;
     a.scale = op.scale; a.causal = op.causal; a.window = op.window;
     a.q = op.q; a.qs = op.q_stride; a.qh = op.q_head_stride;
+    const int64_t per = op.dtype == SN_F32 ? 4 : 8;
+    a.q_vec = (reinterpret_cast<uintptr_t>(op.q) & 15) == 0 && a.qs % per == 0 && a.qh % per == 0 && a.D % 8 == 0;
     return a;
 }
 

@@ -264,3 +264,27 @@ def test_attend_long_and_many(sn, batch, longest, heads, kv, dim, dtype, codes):
     held[-1] = longest
     c = cache_case(sn, np.ones(batch, np.int64), held, kv, dim, 16, dtype, codes, 12, heads=heads)
     attend_check(sn, c)
+
+
+@pytest.mark.parametrize("dtype,codes", [("float32", None), ("bfloat16", "e4m3"), ("bfloat16", None)])
+@pytest.mark.parametrize("batch,causal", [(70, True), (70, False), (300, False)])
+def test_attend_sequences_that_share_blocks(sn, batch, causal, dtype, codes):
+    """A table with room for far more rows than there are: all sequences' keys are one line that the blocks share."""
+    print(f"[attend] shared {batch} {causal} {dtype} {codes}", flush=True)
+    rng = np.random.default_rng(batch)
+    held = rng.integers(1 if causal else 0, 900, batch)
+    held[rng.integers(batch)] = 3000
+    new = rng.integers(0, 3, batch)
+    new = np.minimum(new, held) if causal else new
+    c = cache_case(sn, new, held, 1, 32, 16, dtype, codes, 13, heads=3, spare=60000 // 16, causal=causal)
+    attend_check(sn, c)
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_many_rows_of_a_head(sn, dim, dtype, codes):
+    """More rows than a tile of 16, few and many blocks of them (one and two tiles a block)."""
+    print(f"[attend] rows {dim} {dtype} {codes}", flush=True)
+    attend_check(sn, cache_case(sn, [5, 17, 0], [70, 33, 9], 2, dim, 16, dtype, codes, 14, heads=16))
+    attend_check(sn, cache_case(sn, [5] * 70, list(range(5, 75)), 4, dim, 16, dtype, codes, 15, heads=32))
