@@ -11,6 +11,7 @@ namespace sn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRounds = 2;          // of four items of each group, in a block
 
 struct CacheRowsIO {
     const void *x[2];          // k, v given
@@ -19,119 +20,219 @@ struct CacheRowsIO {
     int vec;                   // rows given or returned suit 16-byte accesses
 };
 
-// Lanes of a row: a power of two that holds Dp / 8.
-inline int lanes_of(int Dp) {
-    int n = 2;
-    while (n * 8 < Dp) n *= 2;
-    return n;
-}
+// Rows beyond this are in no cache when they are read: they are stored past it
+// (48 x <= 4096 rows of 8 x 128, bf16, 500 MB: written and read back 405 us ->
+// 385; 8 x <= 2000, 42 MB: 35 -> 41).
+constexpr int64_t kPast = 128 << 20;
 
-template <typename T>
-__device__ inline void load_row8(const T *p, int d, int D, bool vec, float (&x)[8]) {
-    if (vec && d < D) {
-        typedef T vec_t __attribute__((ext_vector_type(16 / sizeof(T))));
-#pragma unroll
-        for (int i = 0; i < 8; i += 16 / sizeof(T)) {
-            const vec_t v = *reinterpret_cast<const vec_t *>(p + d + i);
-#pragma unroll
-            for (int j = 0; j < (int)(16 / sizeof(T)); ++j) x[i + j] = to_f32(v[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = d + j < D ? to_f32(p[d + j]) : 0.0f;
-    }
-}
-template <typename T>
-__device__ inline void store_row8(T *p, int d, int D, bool vec, const float (&x)[8]) {
-    if (vec && d < D) {
-        typedef T vec_t __attribute__((ext_vector_type(16 / sizeof(T))));
-#pragma unroll
-        for (int i = 0; i < 8; i += 16 / sizeof(T)) {
-            vec_t v;
-#pragma unroll
-            for (int j = 0; j < (int)(16 / sizeof(T)); ++j) v[j] = (T)x[i + j];
-            *reinterpret_cast<vec_t *>(p + d + i) = v;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (d + j < D) p[d + j] = (T)x[j];
-    }
-}
+// How rows are cut (host).  An item is a row of a head, of k or of v; a block
+// takes chunk_rows rows' items in order, its groups one each in turn.
+struct CacheCut {
+    int lane_bits;              // a group has 2^lane_bits lanes
+    int chunk_rows;
+    int step_row, step_head;    // from one item of a group to the next (heads of k, then of v)
+    bool past;                  // rows are stored past the caches
+};
 
-template <typename T, int CODES>
-__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheArgs a, CacheRowsIO io, int lanes, int chunk_rows) {
-    int r0, n, length;
-    sequence_rows(a, blockIdx.y, true, r0, n, length);
-    const int first = blockIdx.x * chunk_rows, rows = min(chunk_rows, n - first);
-    const int lane = threadIdx.x % lanes, d = lane * 8;
-    for (int i = threadIdx.x / lanes; i < rows * 2 * a.Hkv; i += kThreads / lanes) {
-        const int h = i % a.Hkv, n_ = i / a.Hkv & 1, row = first + i / a.Hkv / 2;
-        const T *src = static_cast<const T *>(io.x[n_]) + (r0 + row) * io.xs[n_] + h * io.xh[n_];
-        float x[8];
-        load_row8(src, d, a.D, io.vec, x);
-        const int at = length - n + row, page = page_of(a, blockIdx.y, at);
-        const int64_t place = (((int64_t)max(page, 0) * a.Hkv + h) << a.page_shift) + (at & (a.page - 1));
-        if constexpr (CODES == SN_CODES_NONE) {
-            if (page >= 0 && d < a.Dp) store_row8(static_cast<T *>(n_ ? a.v : a.k) + place * a.Dp, d, a.Dp, true, x);
+// A group's items in turn.
+struct Item {
+    int row, head;
+    __device__ inline void next(const CacheCut &c, int heads) {
+        row += c.step_row;
+        head += c.step_head;
+        if (head >= heads) {
+            head -= heads;
+            ++row;
+        }
+    }
+};
+
+constexpr int kItems = 4;       // items of a group on their way at once
+
+// Eight elements of a row as they lie in memory, zero from D on.
+template <typename T>
+struct Raw {
+    typedef uint32_t quad __attribute__((ext_vector_type(4)));
+    quad r[sizeof(T) / 2];
+    __device__ inline void load(const T *p, int d, int D, bool vec, bool has) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[i] = quad{0, 0, 0, 0};
+        if (!has || d >= D) return;
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[i] = *reinterpret_cast<const quad *>(p + d + i * 16 / sizeof(T));
         } else {
-            // magnitudes compared as bits: a NaN is above an infinity is above all else
-            uint32_t top = 0;
+            T x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-            for (int o = lanes >> 1; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-            constexpr float kTop = CODES == SN_CODES_INT8 ? 127.0f : 448.0f;
-            const float amax = __uint_as_float(top);
-            const bool bad = top >= 0x7f800000u, live = !bad && amax >= 0x1p-100f;
-            const float scale = bad ? __uint_as_float(0x7fc00000u) : live ? amax / kTop : 0.0f;
-            uint2 codes = {0, 0};
-            if (live) codes = encode8<CODES>(x, kTop / amax);
-            if (page >= 0 && d < a.Dp) {
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(n_ ? a.v : a.k) + place * a.Dp + d) = codes;
-                if (lane == 0) (n_ ? a.v_scale : a.k_scale)[place] = scale;
+            for (int j = 0; j < 8; ++j) x[j] = d + j < D ? p[d + j] : (T)0.0f;
+            __builtin_memcpy(r, x, sizeof(x));
+        }
+    }
+    __device__ inline void get(float (&x)[8]) const {
+        T y[8];
+        __builtin_memcpy(y, r, sizeof(y));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = to_f32(y[j]);
+    }
+    __device__ inline void set(const float (&x)[8]) {
+        T y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (T)x[j];
+        __builtin_memcpy(r, y, sizeof(y));
+    }
+    __device__ inline void store(T *p, int d, int D, bool vec, bool past) const {
+        if (d >= D) return;
+        if (vec) {
+            store_past<sizeof(T) / 2>(r, reinterpret_cast<quad *>(p + d), past);
+        } else {
+            T y[8];
+            __builtin_memcpy(y, r, sizeof(y));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (d + j < D) p[d + j] = y[j];
+        }
+    }
+};
+
+// Largest of the group's values, in every lane of it (at most sixteen lanes).
+template <int CTRL>
+__device__ inline uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, true));
+}
+__device__ inline uint32_t group_max(uint32_t v, int bits) {
+    v = dpp_max<0xb1>(v);                   // quad_perm 1 0 3 2
+    if (bits > 1) v = dpp_max<0x4e>(v);     // quad_perm 2 3 0 1
+    if (bits > 2) v = dpp_max<0x141>(v);    // row_half_mirror
+    if (bits > 3) v = dpp_max<0x140>(v);    // row_mirror
+    return v;
+}
+
+template <typename T, int CODES>
+__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheArgs a, CacheRowsIO io, CacheCut c) {
+    int r0, n, length;
+    sequence_rows(a, blockIdx.y, true, r0, n, length);
+    const int first = blockIdx.x * c.chunk_rows, rows = min(c.chunk_rows, n - first), heads = 2 * a.Hkv;
+    if (rows <= 0) return;
+    const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
+    Item at{group / heads, group % heads};
+    const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
+    while (at.row < rows) {
+        Item item[kItems];
+        Raw<T> raw[kItems];
+        int page[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            item[i] = at;
+            at.next(c, heads);
+            const bool has = item[i].row < rows, is_v = item[i].head >= a.Hkv;
+            const int h = item[i].head - (is_v ? a.Hkv : 0), row = first + item[i].row;
+            raw[i].load(static_cast<const T *>(io.x[is_v]) + (r0 + row) * io.xs[is_v] + h * io.xh[is_v], d, a.D, io.vec, has);
+            page[i] = has ? table[(length - n + row) >> a.page_shift] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const bool is_v = item[i].head >= a.Hkv;
+            const int h = item[i].head - (is_v ? a.Hkv : 0), pos = length - n + first + item[i].row;
+            if (item[i].row >= rows) break;
+            const bool ok = (uint32_t)page[i] < (uint32_t)a.n_pages;
+            if (!ok && lane == 0) flag_status(a.status, SN_ERR_INVALID);
+            const int64_t place = (((int64_t)page[i] * a.Hkv + h) << a.page_shift) + (pos & (a.page - 1));
+            if constexpr (CODES == SN_CODES_NONE) {
+                if (ok) raw[i].store(static_cast<T *>(is_v ? a.v : a.k) + place * a.Dp, d, a.Dp, true, c.past);
+            } else {
+                float x[8];
+                raw[i].get(x);
+                // magnitudes compared as bits: a NaN is above an infinity is above all else
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+                top = group_max(top, c.lane_bits);
+                constexpr float kTop = CODES == SN_CODES_INT8 ? 127.0f : 448.0f;
+                const float amax = __uint_as_float(top);
+                const bool bad = top >= 0x7f800000u, live = !bad && amax >= 0x1p-100f;
+                const float scale = bad ? __uint_as_float(0x7fc00000u) : live ? amax / kTop : 0.0f;
+                uint2 codes = {0, 0};
+                if (live) codes = encode8<CODES>(x, kTop / amax);
+                if (ok && d < a.Dp) {
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? a.v : a.k) + place * a.Dp + d) = codes;
+                    if (lane == 0) (is_v ? a.v_scale : a.k_scale)[place] = scale;
+                }
             }
         }
     }
 }
 
 template <typename T, int CODES>
-__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheArgs a, CacheRowsIO io, int lanes, int chunk_rows) {
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheArgs a, CacheRowsIO io, CacheCut c) {
     int r0, n, length;
     sequence_rows(a, blockIdx.y, true, r0, n, length);
-    const int first = blockIdx.x * chunk_rows, rows = min(chunk_rows, n - first);
-    const int lane = threadIdx.x % lanes, d = lane * 8;
-    for (int i = threadIdx.x / lanes; i < rows * 2 * a.Hkv; i += kThreads / lanes) {
-        const int h = i % a.Hkv, n_ = i / a.Hkv & 1, row = first + i / a.Hkv / 2;
-        const int at = length - n + row, page = page_of(a, blockIdx.y, at);
-        const int64_t place = (((int64_t)max(page, 0) * a.Hkv + h) << a.page_shift) + (at & (a.page - 1));
-        float x[8] = {};
-        if (page >= 0 && d < a.Dp) {
-            if constexpr (CODES == SN_CODES_NONE) {
-                load_row8(static_cast<const T *>(n_ ? a.v : a.k) + place * a.Dp, d, a.Dp, true, x);
-            } else {
-                decode8<CODES>(*reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(n_ ? a.v : a.k) + place * a.Dp + d), x);
-                const float scale = (n_ ? a.v_scale : a.k_scale)[place];
+    const int first = blockIdx.x * c.chunk_rows, rows = min(c.chunk_rows, n - first), heads = 2 * a.Hkv;
+    if (rows <= 0) return;
+    const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
+    Item at{group / heads, group % heads};
+    const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
+    while (at.row < rows) {
+        Item item[kItems];
+        int page[kItems];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= scale;
+        for (int i = 0; i < kItems; ++i) {
+            item[i] = at;
+            at.next(c, heads);
+            page[i] = item[i].row < rows ? table[(length - n + first + item[i].row) >> a.page_shift] : -1;
+        }
+        Raw<T> raw[kItems];
+        uint2 codes[kItems];
+        float scale[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const bool is_v = item[i].head >= a.Hkv, ok = (uint32_t)page[i] < (uint32_t)a.n_pages;
+            const int h = item[i].head - (is_v ? a.Hkv : 0), pos = length - n + first + item[i].row;
+            const int64_t place = (((int64_t)(ok ? page[i] : 0) * a.Hkv + h) << a.page_shift) + (pos & (a.page - 1));
+            if (!ok && item[i].row < rows && lane == 0) flag_status(a.status, SN_ERR_INVALID);
+            if constexpr (CODES == SN_CODES_NONE) {
+                raw[i].load(static_cast<const T *>(is_v ? a.v : a.k) + place * a.Dp, d, a.Dp, true, ok);
+            } else {
+                codes[i] = uint2{0, 0};
+                scale[i] = 0.0f;
+                if (ok && d < a.Dp) {
+                    codes[i] = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(is_v ? a.v : a.k) + place * a.Dp + d);
+                    scale[i] = (is_v ? a.v_scale : a.k_scale)[place];
+                }
             }
         }
-        T *dst = static_cast<T *>(io.out[n_]) + ((int64_t)(r0 + row) * a.Hkv + h) * a.D;
-        store_row8(dst, d, a.D, io.vec, x);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (item[i].row >= rows) break;
+            const bool is_v = item[i].head >= a.Hkv;
+            const int h = item[i].head - (is_v ? a.Hkv : 0);
+            if constexpr (CODES != SN_CODES_NONE) {
+                float x[8];
+                decode8<CODES>(codes[i], x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= scale[i];
+                raw[i].set(x);
+            }
+            raw[i].store(static_cast<T *>(io.out[is_v]) + ((int64_t)(r0 + first + item[i].row) * a.Hkv + h) * a.D, d, a.D, io.vec, c.past);
+        }
     }
 }
-
-// Rows of a block: about four rounds of its groups.
-int chunk_of(const CacheArgs &a, int lanes) { return std::max(1, 4 * (kThreads / lanes) / (2 * a.Hkv)); }
 
 template <typename T, int CODES>
 sn_status launch(const CacheArgs &a, const CacheRowsIO &io, bool write, hipStream_t s) {
-    const int lanes = lanes_of(a.Dp), rows = chunk_of(a, lanes);
-    const dim3 grid((a.max_rows + rows - 1) / rows, a.B);
+    CacheCut c;
+    c.lane_bits = 1;
+    while (8 << c.lane_bits < a.Dp) ++c.lane_bits;
+    const int groups = kThreads >> c.lane_bits, heads = 2 * a.Hkv;
+    c.step_row = groups / heads;
+    c.step_head = groups % heads;
+    c.chunk_rows = std::max(1, kRounds * kItems * groups / heads);
+    c.past = (int64_t)a.n_rows * heads * a.D * (int64_t)sizeof(T) > kPast;
+    const dim3 grid((a.max_rows + c.chunk_rows - 1) / c.chunk_rows, a.B);
     ProfScope prof(write ? K_CACHE_WRITE : K_CACHE_READ, s);
     if (write)
-        cache_write_kernel<T, CODES><<<grid, kThreads, 0, s>>>(a, io, lanes, rows);
+        cache_write_kernel<T, CODES><<<grid, kThreads, 0, s>>>(a, io, c);
     else
-        cache_read_kernel<T, CODES><<<grid, kThreads, 0, s>>>(a, io, lanes, rows);
+        cache_read_kernel<T, CODES><<<grid, kThreads, 0, s>>>(a, io, c);
     return launch_status();
 }
 template <typename T>

@@ -37,7 +37,7 @@ typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
 // How rows lie in the pages: in their own type, or as codes beside rows of T.
-template <typename T_, int CODES_, int DP_, int NR_>
+template <typename T_, int CODES_, int DP_, int NR_, bool PAST_ = false>
 struct Form {
     using T = T_;
     static constexpr int CODES = CODES_, DP = DP_, NR = NR_;
@@ -53,6 +53,7 @@ struct Form {
     // registers of a key block and of a value row
     static constexpr int KREGS = F32 ? DP / 4 : ES == 2 ? DP / 8 : DP / 16;
     static constexpr int VREGS = (W * ES + 3) / 4;
+    static constexpr int AUX = PAST_ ? 2 : 0;       // of a load: 2 goes past the caches
     // blocks that a CU holds: short rows of one tile fit 128 registers
     static constexpr int BLOCKS = DP == 32 && NR == 1 ? 2 : 1;
 };
@@ -234,21 +235,21 @@ constexpr uint32_t kNowhere = 0x80000000u;
 __device__ inline __amdgpu_buffer_rsrc_t block_at(const void *p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7fffffff, 0x00020000);
 }
-template <int BYTES>
+template <int BYTES, int AUX>
 __device__ inline void load_bytes(uint32_t *r, __amdgpu_buffer_rsrc_t block, uint32_t lane, int offset) {
     if constexpr (BYTES == 2) {
-        r[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(block, lane, offset, 0);
+        r[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(block, lane, offset, AUX);
     } else if constexpr (BYTES == 4) {
-        r[0] = __builtin_amdgcn_raw_buffer_load_b32(block, lane, offset, 0);
+        r[0] = __builtin_amdgcn_raw_buffer_load_b32(block, lane, offset, AUX);
     } else if constexpr (BYTES == 8) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(block, lane, offset, 0));
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(block, lane, offset, AUX));
         r[0] = v[0];
         r[1] = v[1];
     } else {
-        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(block, lane, offset, 0));
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(block, lane, offset, AUX));
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = v[i];
-        if constexpr (BYTES == 32) load_bytes<16>(r + 4, block, lane + 16, offset);
+        if constexpr (BYTES == 32) load_bytes<16, AUX>(r + 4, block, lane + 16, offset);
     }
 }
 
@@ -293,7 +294,7 @@ struct Walk {
             const int64_t at = place(tile, b, pg);
             const __amdgpu_buffer_rsrc_t block = block_at(static_cast<const char *>(a.k) + at * row);
 #pragma unroll
-            for (int c = 0; c < KLOADS; ++c) load_bytes<KBYTES>(&t.k[b][c * KBYTES / 4], block, ko[c], 0);
+            for (int c = 0; c < KLOADS; ++c) load_bytes<KBYTES, F::AUX>(&t.k[b][c * KBYTES / 4], block, ko[c], 0);
             if constexpr (F::CODES != SN_CODES_NONE)
                 t.ks[b] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(block_at(a.k_scale + at), 16 * g, 0, 0));
         }
@@ -304,7 +305,7 @@ struct Walk {
             const int64_t at = place(tile, b, pg);
             const __amdgpu_buffer_rsrc_t block = block_at(static_cast<const char *>(a.v) + at * row);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_bytes<F::W * F::ES>(t.v[b][i], block, vo, i * row);
+            for (int i = 0; i < 4; ++i) load_bytes<F::W * F::ES, F::AUX>(t.v[b][i], block, vo, i * row);
             if constexpr (F::CODES != SN_CODES_NONE)
                 t.vs[b] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(block_at(a.v_scale + at), 16 * g, 0, 0));
         }
@@ -957,9 +958,16 @@ AttendCut cut_of(int Hkv, int64_t rows, int nr) {
     return c;
 }
 
+// Keys that a row may see, and the bytes of all sequences' keys and values:
+// sequences are taken to be a little over half of what the table holds.
+inline int64_t span_of(const CacheArgs &a) {
+    const int64_t all = (int64_t)a.max_pages * a.page;
+    return a.window > 0 ? std::min(all, (int64_t)a.window + a.max_rows + 15) : all;
+}
+inline double bytes_of(const CacheArgs &a, int es) { return 0.6 * a.B * (double)span_of(a) * a.Hkv * 2 * a.Dp * es; }
+
 // Whether units are cut.  A block takes about 2 us for a round (a tile of each
-// wavefront; 1.5 us with short rows) and the join and its launch cost 11 us more; sequences are taken
-// to be a little over half of what the table holds.  Few units: cut where the
+// wavefront; 1.5 us with short rows) and the join and its launch cost 11 us more.  Few units: cut where the
 // rounds that a unit takes one after the other are longer than that (1 x 4000
 // keys, 32/8 x 128 bf16: 40 us whole, 18 cut; 1 x 1000: 14.7 and 15.0; 8 x 4000:
 // 42 and 28; 16 x 2000: 25 and 27).  Units on every CU: cut where the longest
@@ -967,12 +975,10 @@ AttendCut cut_of(int Hkv, int64_t rows, int nr) {
 // 335; 64 x 1000: 32 and 45).  Many units even out by themselves.
 template <class F>
 bool worth_cutting(const CacheArgs &a, const AttendCut &c) {
-    int64_t span = (int64_t)a.max_pages * a.page;
-    if (a.window > 0) span = std::min(span, (int64_t)a.window + a.max_rows + 15);
     const double units = (double)a.B * c.units, places = kCus * F::BLOCKS;
-    const int64_t tiles = (span + F::TILE - 1) / F::TILE + 1;
-    const double rounds = (double)tiles / kWaves, bytes = (double)kWaves * F::TILE * 2 * a.Dp * F::ES;
-    const double streaming = 0.6 * units * rounds * bytes / 5.2e6;      // us at 5.2 TB/s
+    const int64_t tiles = (span_of(a) + F::TILE - 1) / F::TILE + 1;
+    const double rounds = (double)tiles / kWaves;
+    const double streaming = bytes_of(a, F::ES) * c.row_tiles / 5.2e6;  // us at 5.2 TB/s
     if (units * tiles > INT32_MAX) return false;                        // a line of tiles is counted in 32 bits
     return units < places ? (F::BLOCKS == 2 ? 1.5 : 2.0) * rounds > 11.0 + streaming || streaming > 80.0 : units < 4 * places && streaming > 80.0;
 }
@@ -995,9 +1001,21 @@ sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t 
     if (c.blocks) attend_join_kernel<F><<<a.B * c.units, kJoinThreads, 0, s>>>(a, c, parts, static_cast<T *>(o), lse);
     return launch_status();
 }
+// Whether the rows are read past the caches: they are read once, and are more
+// than the caches hold (32 x <= 20000 keys, 32/8 x 128 bf16, 1.6 GB: 307 us and
+// 270 past them; 64 x 12000, 4 x 32 fp32, 480 MB: 100 and 92; 32 x 4000, 350 MB:
+// 72 and 70; 16 x 4000, 180 MB: 44 and 63).  8-bit rows gain nothing (330 MB: 80
+// and 82).
+bool reads_past(const CacheArgs &a, int es) {
+    const int64_t rows = rows_of(a.max_rows, a.G);
+    return cut_of(a.Hkv, rows, 1).row_tiles == 1 && bytes_of(a, es) > 3e8;
+}
+
 template <typename T, int CODES, int DP>
 sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t s) {
     constexpr int dtype = std::is_same<T, float>::value ? SN_F32 : SN_BF16;
+    if constexpr (CODES == SN_CODES_NONE)
+        if (reads_past(a, sizeof(T))) return launch<Form<T, CODES, DP, 1, true>>(a, o, lse, ws, s);
     if constexpr (DP == 64 || (DP == 128 && dtype == SN_BF16))
         if (tiles_of_block(dtype, DP, a.B, a.Hkv, rows_of(a.max_rows, a.G)) == 2) return launch<Form<T, CODES, DP, 2>>(a, o, lse, ws, s);
     return launch<Form<T, CODES, DP, 1>>(a, o, lse, ws, s);

@@ -7,6 +7,21 @@ namespace sn {
 
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// Stores of N values that go past the caches, or not.  (The empty statements
+// keep the compiler from merging the two kinds into one without the hint.)
+template <int N, typename V>
+__device__ inline void store_past(const V *v, V *p, bool past) {
+    if (past) {
+        asm volatile("");
+#pragma unroll
+        for (int i = 0; i < N; ++i) __builtin_nontemporal_store(v[i], p + i);
+        asm volatile("");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = v[i];
+    }
+}
+
 // --------------------------------------------------------------- rotation of heads
 
 constexpr int kMaxPairs = SN_MAX_HEAD_DIM / 2;
@@ -87,9 +102,12 @@ typedef float floatx2v __attribute__((ext_vector_type(2)));
 
 __device__ inline float e4m3_value(uint8_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
 
-// Eight codes of a row from its values x inv.
+// Eight codes of a row from its values x inv.  int8: adding 1.5 2^23 leaves the
+// nearest whole number (ties to even) in the lowest bits; the product is
+// rounded before, by itself.
 template <int CODES>
 __device__ inline uint2 encode8(const float (&x)[8], float inv) {
+#pragma clang fp contract(off)
     uint2 r;
     if constexpr (CODES == SN_CODES_E4M3) {
         int lo = 0, hi = 0;
@@ -102,9 +120,15 @@ __device__ inline uint2 encode8(const float (&x)[8], float inv) {
     } else {
         uint32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = (uint32_t)(int)rintf(x[j] * inv) & 0xff;
-        r.x = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-        r.y = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+        for (int j = 0; j < 8; ++j) {
+            const float y = x[j] * inv;
+            c[j] = __float_as_uint(y + 12582912.0f);
+        }
+        // byte 0 of each: pairs, then both pairs
+        const uint32_t p0 = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u), p1 = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
+        const uint32_t p2 = __builtin_amdgcn_perm(c[5], c[4], 0x0c0c0400u), p3 = __builtin_amdgcn_perm(c[7], c[6], 0x04000c0cu);
+        r.x = p0 | p1;
+        r.y = p2 | p3;
     }
     return r;
 }
