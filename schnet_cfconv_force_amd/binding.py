@@ -707,6 +707,11 @@ def group_norm_backward(plan: GroupNorm, x, gamma, beta, saved, dy, ws, stream=N
     return dx, dgamma, dbeta
 
 
+def _shaped(shape, dtype, device):
+    """A tensor of a shape without its memory, for torch.empty_like (three times as fast as torch.empty with a shape)."""
+    return _torch().empty((1,) * len(shape), dtype=dtype, device=device).expand(shape)
+
+
 # ------------------------------------------------------------------ rotation of heads
 #
 # The streams, workspaces and autograd conventions of the calls below are the context operators'.
@@ -763,6 +768,7 @@ class HeadRotary:
         self.current_stream, self.current_device = _current_getters()
         self.q_shape = torch.Size((self.n_rows, self.n_heads, self.head_dim))
         self.k_shape = torch.Size((self.n_rows, self.n_kv_heads, self.head_dim))
+        self.weight_like = _shaped((self.head_dim,), torch.float32, self.device)
 
     def _rows(self, q, k, names):
         """The strides of a query and a key tensor (k None where the plan has no key heads)."""
@@ -819,7 +825,7 @@ def head_rotary_backward(plan: HeadRotary, q, k, positions, d_q, d_k, ws, q_weig
     dk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     dqw = dkw = None
     if plan.norm:
-        dqw, dkw = torch.empty((2, plan.head_dim), dtype=torch.float32, device=plan.device).unbind(0)
+        dqw, dkw = (torch.empty_like(plan.weight_like, memory_format=torch.contiguous_format) for _ in range(2))
     _launch(plan, lib().sn_head_rotary_backward, stream, ws,
             (q, k, positions, d_q, d_k, q_weight, k_weight, dq, dk, dqw, dkw), op, d_q.data_ptr(), gs, gh, _ptr(d_k), ks, kh,
             dq.data_ptr(), _ptr(dk), _ptr(dqw), _ptr(dkw))
@@ -902,6 +908,7 @@ class CacheRows:
         self.current_stream, self.current_device = _current_getters()
         self.q_shape = torch.Size((self.n_rows, self.n_heads, cache.head_dim))
         self.k_shape = torch.Size((self.n_rows, cache.n_kv_heads, cache.head_dim))
+        self.k_like = _shaped(self.k_shape, self.dtype, self.device)
 
     def _bind(self, table, lengths, q=None) -> bytes:
         """The descriptor of one call (its own bytes: calls from several threads share nothing)."""
@@ -935,7 +942,8 @@ def cache_read(plan: CacheRows, table, lengths, ws, stream=None):
     """sn_cache_read -> (k, v) [n_rows, Hkv, D]: the plan's rows as the pages hold them."""
     torch = _torch()
     op = plan._bind(table, lengths)
-    k, v = torch.empty((2, *plan.k_shape), dtype=plan.dtype, device=plan.device).unbind(0)
+    k = torch.empty_like(plan.k_like, memory_format=torch.contiguous_format)
+    v = torch.empty_like(plan.k_like, memory_format=torch.contiguous_format)
     _launch(plan, lib().sn_cache_read, stream, ws, (k, v, table, lengths), op, k.data_ptr(), v.data_ptr())
     return k, v
 
