@@ -47,7 +47,7 @@ struct Form {
     // bf16 planes of the weights: 16 bits beside bf16 rows, 24 beside fp32 ones
     static constexpr int PP = std::is_same<T, float>::value ? 3 : 2;
     // 16-key blocks of a tile: about 8 KB of keys a wavefront where registers allow
-    static constexpr int NB = F32 ? (DP == 128 ? 1 : 2) : DP == 128 ? 2 : 4;
+    static constexpr int NB = F32 ? (DP == 128 ? 1 : 2) : DP == 128 || (ES == 1 && DP == 32) ? 2 : 4;
     static constexpr int TILE = 16 * NB;
     static constexpr int W = DP / 16;       // dims that a lane reads of a value row
     // registers of a key block and of a value row
@@ -258,7 +258,8 @@ template <class F>
 struct Walk {
     const CacheArgs &a;
     const __attribute__((address_space(4))) int32_t *table;     // the sequence's pages
-    int hk, key0, end;      // key/value head; first key of tile 0 (a multiple of 16), end of the keys
+    int hk, key0;           // key/value head; first key of tile 0 (a multiple of 16)
+    int from, end;          // keys that some row of the unit sees
     int row;                // bytes of a row
     static constexpr int KBYTES = F::KREGS == 2 ? 8 : 16, KLOADS = F::KREGS * 4 / KBYTES;
     uint32_t ko[KLOADS], vo;    // a lane's offsets in a block: its key row's dims, its value row's dims
@@ -433,17 +434,18 @@ __device__ inline void take(const Walk<F> &w, Tile<F> &t, int tile, const int (&
                             const Queries<F> &q, State<F> &st, float scale2, int all_first, int all_last) {
     constexpr int NB = F::NB, NR = F::NR;
     const int g = w.g, key = w.key_of(tile, 0);
-    int there[NB];      // keys of the block
+    int from[NB], there[NB];    // the block's keys that are there: [from, there)
     bool absent = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const bool ok = (uint32_t)pg[b] < (uint32_t)w.a.n_pages;
         there[b] = min(max(w.end - w.key_of(tile, b), 0), 16);
+        from[b] = max(w.from - w.key_of(tile, b), 0);
         if (!ok && there[b] > 0) {
             if (threadIdx.x % 64 == 0) flag_status(w.a.status, SN_ERR_INVALID);
             there[b] = 0;
         }
-        absent |= there[b] < 16;
+        absent |= there[b] < 16 || from[b] > 0;
     }
     floatx4 s[NR][NB];
 #pragma unroll
@@ -496,7 +498,7 @@ __device__ inline void take(const Walk<F> &w, Tile<F> &t, int tile, const int (&
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (4 * g + i >= there[b])
+                if (4 * g + i >= there[b] || 4 * g + i < from[b])
 #pragma unroll
                     for (int c = 0; c < F::VREGS; ++c) t.v[b][i][c] = 0;
     }
@@ -661,6 +663,7 @@ __device__ inline float plain_row(const CacheArgs &a, int b, int hk, int64_t q_a
         }
         if (pass == 0) l = block_join(sum, true, buf) + nan;
     }
+    if (m == INFINITY && nan == 0.0f) l = 1.0f;     // an infinite score: its log-sum is infinite, its row is not a number
     return o + nan;
 }
 
@@ -694,11 +697,13 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
     Walk<F> w(a);
     w.table = (const __attribute__((address_space(4))) int32_t *)(uintptr_t)(a.table + (int64_t)b * a.max_pages);
     w.hk = hk;
-    w.key0 = s.begin + t0 * F::TILE;
-    w.end = min(s.begin + t1 * F::TILE, s.length);
-    // positions that a row t sees
+    // positions that a row t sees, and those that some row of the unit does
     auto last_of = [&](int t) { return a.causal ? s.length - s.n + t + 1 : s.length; };
     auto first_of = [&](int t) { return a.window > 0 ? max(0, last_of(t) - a.window) : 0; };
+    const int t_first = tile * 16 * F::NR / a.G, t_last = (tile * 16 * F::NR + rows - 1) / a.G;
+    w.key0 = s.begin + t0 * F::TILE;
+    w.from = first_of(t_first);
+    w.end = min(s.begin + t1 * F::TILE, last_of(t_last));
     State<F> st;
 #pragma unroll
     for (int nr = 0; nr < F::NR; ++nr) {
@@ -710,18 +715,19 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
 #pragma unroll
         for (int j = 0; j < F::W; ++j) st.acc[nr][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const int all_first = first_of((tile * 16 * F::NR + rows - 1) / a.G), all_last = last_of(tile * 16 * F::NR / a.G);
+    const int all_first = first_of(t_last), all_last = last_of(t_first);
     const int tiles = w.end > w.key0 ? (w.end - w.key0 + F::TILE - 1) / F::TILE : 0;
-    if (wave < tiles) {
+    const int mine = max(w.from - w.key0, 0) / F::TILE + wave;      // the wavefront's first tile
+    if (mine < tiles) {
         Queries<F> q;
         Tile<F> tile_regs;
         int pg[F::NB], next_pg[F::NB];
-        w.pages(wave, pg);
+        w.pages(mine, pg);
         q.load(a, s, hk, tile);
-        w.load_keys(wave, pg, tile_regs);
-        w.load_values(wave, pg, tile_regs);
-        w.pages(min(wave + kWaves, tiles - 1), next_pg);
-        for (int i = wave; i < tiles; i += kWaves) {
+        w.load_keys(mine, pg, tile_regs);
+        w.load_values(mine, pg, tile_regs);
+        w.pages(min(mine + kWaves, tiles - 1), next_pg);
+        for (int i = mine; i < tiles; i += kWaves) {
             const int next = i + kWaves;
             int after[F::NB];       // pages are asked for two tiles ahead
             w.pages(min(next + kWaves, tiles - 1), after);
@@ -838,9 +844,9 @@ __global__ __launch_bounds__(kThreads, 2 * F::BLOCKS) void attend_kernel(CacheAr
             piece<F>(a, c, b, s, unit, at - u0, stop - u0, slot, parts, o, lse, x);
             at = stop;
         }
-        if (at >= end) return;
         first += s.tiles * c.units;
-        s = uniform_sequence(sequence_of<F>(a, ++b));
+        if (at >= end || ++b >= a.B) return;
+        s = uniform_sequence(sequence_of<F>(a, b));
     }
 }
 
@@ -869,7 +875,7 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(CacheArgs a, 
         const float base = top == -INFINITY ? 0.0f : top;
         for (int k = threadIdx.x % 16; k < n; k += 16) {
             const float2 ml = parts.ml[at_of(k, r)];
-            sum += ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+            sum += ml.y * (ml.x == top ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base));      // infinite ones too
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor(sum, o);
@@ -893,7 +899,8 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(CacheArgs a, 
                 if (i % R >= rows) continue;
                 const float2 ml = parts.ml[at_of(k0 + i / R, i % R)];
                 const float top = sums[i % R][0], sum = sums[i % R][1];
-                weights[i] = ml.y * __builtin_amdgcn_exp2f(ml.x - (top == -INFINITY ? 0.0f : top)) / (sum == 0.0f ? 1.0f : sum);
+                const float e = ml.x == top ? 1.0f : __builtin_amdgcn_exp2f(ml.x - (top == -INFINITY ? 0.0f : top));
+                weights[i] = ml.y * e / (sum == 0.0f ? 1.0f : sum);
             }
             __syncthreads();
             if (!has) continue;
