@@ -1011,18 +1011,19 @@ sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t 
 // Whether the rows are read past the caches: they are read once, and are more
 // than the caches hold (32 x <= 20000 keys, 32/8 x 128 bf16, 1.6 GB: 307 us and
 // 270 past them; 64 x 12000, 4 x 32 fp32, 480 MB: 100 and 92; 32 x 4000, 350 MB:
-// 72 and 70; 16 x 4000, 180 MB: 44 and 63).  8-bit rows gain nothing (330 MB: 80
-// and 82).
-bool reads_past(const CacheArgs &a, int es) {
-    const int64_t rows = rows_of(a.max_rows, a.G);
-    return cut_of(a.Hkv, rows, 1).row_tiles == 1 && bytes_of(a, es) > 3e8;
+// 72 and 70; 16 x 4000, 180 MB: 44 and 63).  8-bit rows gain only where units are
+// cut (32 x 20000, 875 MB: 170 and 159; 64 x 4000, not cut: 74 and 75).
+template <class F>
+bool reads_past(const CacheArgs &a) {
+    const AttendCut c = cut_of(a.Hkv, rows_of(a.max_rows, a.G), 1);
+    return c.row_tiles == 1 && bytes_of(a, F::ES) > 3e8 && (F::CODES == SN_CODES_NONE || worth_cutting<F>(a, c));
 }
 
 template <typename T, int CODES, int DP>
 sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t s) {
     constexpr int dtype = std::is_same<T, float>::value ? SN_F32 : SN_BF16;
-    if constexpr (CODES == SN_CODES_NONE)
-        if (reads_past(a, sizeof(T))) return launch<Form<T, CODES, DP, 1, true>>(a, o, lse, ws, s);
+    if constexpr (CODES == SN_CODES_NONE || DP == 128)
+        if (reads_past<Form<T, CODES, DP, 1>>(a)) return launch<Form<T, CODES, DP, 1, true>>(a, o, lse, ws, s);
     if constexpr (DP == 64 || (DP == 128 && dtype == SN_BF16))
         if (tiles_of_block(dtype, DP, a.B, a.Hkv, rows_of(a.max_rows, a.G)) == 2) return launch<Form<T, CODES, DP, 2>>(a, o, lse, ws, s);
     return launch<Form<T, CODES, DP, 1>>(a, o, lse, ws, s);

@@ -6,10 +6,13 @@
 //     y_a = z_a cos t - z_b sin t,  y_b = z_b cos t + z_a sin t
 //   g = dy turned back, dw = sum g xh, h = g w, dx = rstd (h - xh mean(h xh))
 //
-// A group of lanes owns a row's pairs, a lane V of them: its elements are two
-// vectors of V (a's and b's, or adjacent pairs), so a pair never leaves the
-// lane, and the sines and cosines are formed once for all heads of the row
-// that the lane walks.
+// What it costs is one read and one write of the rows (32768 rows of 32 + 8 heads
+// of 128, bf16, 671 MB: 133 us, 5.1 TB/s, a copy's rate).  A group of lanes owns a
+// head, a lane V of its pairs: its elements are two vectors of V (a's and b's,
+// or adjacent pairs), so a pair never leaves the lane.  A block's groups take
+// the heads of its rows in memory's order (lanes that walk the heads of a row of
+// their own spread a wavefront over eight rows: 153 us).  The block forms the
+// sines and cosines of its rows once, for all heads, in LDS.
 #include <algorithm>
 
 #include "state.h"
@@ -19,25 +22,26 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPartials = 1024;   // blocks of a backward pass, and with them partial weight gradients
-// Lanes that a pass keeps busy before a lane takes two heads or more: 17216 rows
-// of 4 + 4 heads of 32, fp32, a step: 26.6 us with 65536, 28.5 with twice as
-// many, 30.4 with four times; 4096 rows of 32 + 8 heads of 128, bf16: 21.0, 20.0
-// and 25.0; with half as many 25.7 there.
-constexpr int64_t kFill = 65536;
+constexpr int kHeads = 4;               // of a group, on their way at once
+// Blocks that a pass makes before a block takes more rows than one: 7001 rows of
+// 6 + 2 heads of 40, bf16, a step: 17 us with 512, 22 with 1024, 47 with 4096;
+// 17216 rows of 4 + 4 heads of 32, fp32: 25.7, 24.3 and 36; with 256: 17 and 26.
+constexpr int kBlocks = 512;
 // Outputs beyond this stay in no cache until they are read: they are stored past
-// it (32768 rows of 32 + 8 heads of 128, bf16: 159 us -> 144; 17216 rows of
-// 4 + 4 heads of 32, fp32, 18 MB: 9.3 -> 8.3; bf16, 9 MB: 9.4 -> 10.3).
+// it (32768 rows of 32 + 8 heads of 128, bf16: 143 us -> 135; 16384, a step: 181
+// -> 149; 17216 rows of 4 + 4 heads of 32, fp32, 18 MB: 9.9 -> 9.1; with smaller
+// ones, which the next kernel finds in the cache, there is nothing to gain).
 constexpr int64_t kStream = 16 << 20;
 
-// How rows and heads are cut (host).
+// How rows and heads are cut (host).  A block takes `rows` rows at a time; their
+// heads, in memory's order, go to its groups one each in turn.
 struct RotaryCut {
     int units;      // lanes of a group that have pairs
-    int lanes;      // lanes of a group, a power of two
-    int lane_bits;
-    // of q and of k, each with blocks of its own (grid y)
-    int slices[2];  // groups that share a row, each with a run of its heads
-    int heads[2];   // heads of a slice
-    int blocks[2];
+    int lane_bits;  // a group has 2^lane_bits lanes
+    int width;      // pairs of a row in the block's table of angles
+    int rows;
+    int step_row[2], step_head[2];      // of q and of k: from one head of a group to its next
+    int blocks[2];  // of q and of k (grid y)
     float inv_D;
     bool stream;    // stores go past the caches
 };
@@ -125,34 +129,35 @@ __device__ inline float group_sum(float v, int lanes) {
     return v;
 }
 
-// The pairs' frequencies and axes in LDS: lanes that index the arguments one by
-// one would wait for them again and again.
-struct Pairs {
-    double turns[kMaxPairs];
-    int axes[kMaxPairs];
-    __device__ inline void load(const RotaryArgs &a) {
-        if ((int)threadIdx.x < a.P) {
-            turns[threadIdx.x] = a.turns[threadIdx.x];
-            axes[threadIdx.x] = a.axes[threadIdx.x];
+// Sines and cosines of a block's rows, in LDS: once for all heads.  Angles in
+// full turns are reduced in fp64; what is left is at most half a turn.  Pairs
+// that do not turn have an angle of zero.
+constexpr int kTable = 1024;
+__device__ inline void fill_table(const RotaryArgs &a, const RotaryCut &k, int row0, int rows, float2 *table) {
+    for (int i = threadIdx.x; i < rows * k.width; i += kThreads) {
+        const int r = i / k.width, j = i - r * k.width;
+        float2 cs = make_float2(1.0f, 0.0f);
+        if (j < a.P) {
+            const double turn = (double)a.positions[(int64_t)a.axes[j] * a.n_rows + row0 + r] * a.turns[j];
+            sincospif(2.0f * (float)(turn - rint(turn)), &cs.y, &cs.x);
         }
-        __syncthreads();
+        table[i] = cs;
     }
-};
-
-// Angles in full turns are reduced in fp64; what is left is at most half a turn.
+}
 template <int V>
-__device__ inline void angles(const RotaryArgs &a, const Pairs &pairs, int row, const Place &p, float (&c)[V], float (&s)[V]) {
-    int at[V];
+__device__ inline void take_angles(const float2 *table, float (&c)[V], float (&s)[V]) {
+    if constexpr (V == 1) {
+        c[0] = table[0].x;
+        s[0] = table[0].y;
+    } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const int j = p.pair + e;
-        at[e] = j < a.P ? a.positions[(int64_t)pairs.axes[j] * a.n_rows + row] : 0;
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const int j = p.pair + e;
-        const double turn = j < a.P ? (double)at[e] * pairs.turns[j] : 0.0;
-        sincospif(2.0f * (float)(turn - rint(turn)), &s[e], &c[e]);
+        for (int e = 0; e < V; e += 2) {
+            const float4 x = *reinterpret_cast<const float4 *>(table + e);
+            c[e] = x.x;
+            s[e] = x.y;
+            c[e + 1] = x.z;
+            s[e + 1] = x.w;
+        }
     }
 }
 
@@ -176,112 +181,122 @@ __device__ inline void load_weights(const float *weights, const Place &p, float 
     }
 }
 
-// A group's row and run of heads.
-struct Part {
-    int row, h0, h1;
-    bool live;
+// A group's heads in turn.
+struct Head {
+    int row, head;      // row of the block's
+    __device__ inline void next(const RotaryCut &k, int n, int heads) {
+        row += k.step_row[n];
+        head += k.step_head[n];
+        if (head >= heads) {
+            head -= heads;
+            ++row;
+        }
+    }
 };
-__device__ inline Part part_of(const RotaryArgs &a, const RotaryCut &k, int n, uint32_t group) {
-    Part r;
-    const uint32_t row = group / (uint32_t)k.slices[n];
-    r.live = row < (uint32_t)a.n_rows;
-    r.row = r.live ? (int)row : 0;
-    r.h0 = (int)(group - row * k.slices[n]) * k.heads[n];
-    r.h1 = r.live ? min(r.h0 + k.heads[n], n ? a.Hkv : a.H) : r.h0;
-    return r;
-}
 
-// N heads are on their way at once.
+// N heads of a group are on their way at once.
 template <typename T, int V, bool IL, bool NORM, int N>
 __global__ __launch_bounds__(kThreads) void rotary_forward_kernel(RotaryArgs a, RotaryCut k) {
-    __shared__ Pairs pairs;
+    __shared__ alignas(16) float2 table[kTable];
     const int n = blockIdx.y;
     if ((int)blockIdx.x >= k.blocks[n]) return;
-    pairs.load(a);
     const RotaryTensor &t = a.t[n];
-    const Part part = part_of(a, k, n, (blockIdx.x * (uint32_t)kThreads + threadIdx.x) >> k.lane_bits);
-    Place p = place_of<V, IL>(threadIdx.x & (k.lanes - 1), k.units, a.D, a.P);
-    p.has_a &= part.live;
-    p.has_b &= part.live;
-    const T *x = static_cast<const T *>(t.x) + part.row * t.xs;
-    T *y = static_cast<T *>(t.out) + (int64_t)part.row * (n ? a.Hkv : a.H) * a.D;
-    float c[V], s[V], w[2 * V];
-    for (int hb = part.h0; hb < part.h1; hb += N) {
+    const int heads = n ? a.Hkv : a.H, lanes = 1 << k.lane_bits, u = threadIdx.x & (lanes - 1);
+    const int row0 = blockIdx.x * k.rows, rows = min(k.rows, a.n_rows - row0);
+    const Place p = place_of<V, IL>(u, k.units, a.D, a.P);
+    const int group = threadIdx.x >> k.lane_bits;
+    Head at{group / heads, group % heads};
+    float w[2 * V];
+    bool filled = false;
+    while (true) {
+        Head h[N];
         Run<T, V> ra[N], rb[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const T *from = x + (hb + i) * t.xh;
-            ra[i].load(from + p.a, p.has_a && hb + i < part.h1);
-            rb[i].load(from + p.b, p.has_b && hb + i < part.h1);
+            h[i] = at;
+            at.next(k, n, heads);
+            const bool has = h[i].row < rows;
+            const T *from = static_cast<const T *>(t.x) + (row0 + h[i].row) * t.xs + h[i].head * t.xh;
+            ra[i].load(from + p.a, p.has_a && has);
+            rb[i].load(from + p.b, p.has_b && has);
         }
-        if (hb == part.h0) {        // the first heads are on their way meanwhile
+        if (!filled) {      // the first heads are on their way meanwhile
             if (NORM) load_weights<V>(t.w, p, w);
-            angles<V>(a, pairs, part.row, p, c, s);
+            fill_table(a, k, row0, rows, table);
+            __syncthreads();
+            filled = true;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float v[2 * V];
+            if (h[i].row >= rows) return;
+            float v[2 * V], c[V], s[V];
             ra[i].get(v);
             rb[i].get(v + V);
+            take_angles<V>(table + h[i].row * k.width + min(p.pair, k.width - V), c, s);
             if (NORM) {
                 float sq = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) sq += v[e] * v[e];
-                const float r = __builtin_amdgcn_rsqf(group_sum(sq, k.lanes) * k.inv_D + a.eps);
+                const float r = __builtin_amdgcn_rsqf(group_sum(sq, lanes) * k.inv_D + a.eps);
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) v[e] *= r * w[e];
             }
             turn<V, IL>(v, c, s, 1.0f);
-            T *to = y + (int64_t)(hb + i) * a.D;
-            store_run<T, V>(to + p.a, p.has_a && hb + i < part.h1, v, k.stream);
-            store_run<T, V>(to + p.b, p.has_b && hb + i < part.h1, v + V, k.stream);
+            T *to = static_cast<T *>(t.out) + ((int64_t)(row0 + h[i].row) * heads + h[i].head) * a.D;
+            store_run<T, V>(to + p.a, p.has_a, v, k.stream);
+            store_run<T, V>(to + p.b, p.has_b, v + V, k.stream);
         }
     }
 }
 
-// Rows in turn by groups; a block leaves the weight gradients of its rows in
-// partials[q, k][block][D].
+// Runs of rows in turn by blocks; a block leaves the weight gradients of its
+// rows in partials[q, k][block][D].
 template <typename T, int V, bool IL, bool NORM, int N>
 __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a, RotaryCut k, float *partials) {
-    __shared__ Pairs pairs;
-    __shared__ float sums[kThreads * 2 * V];
+    __shared__ alignas(16) float2 table[kTable];
+    __shared__ float sums[NORM ? kThreads * 2 * V : 1];
     const int n = blockIdx.y;
     if ((int)blockIdx.x >= k.blocks[n]) return;
-    pairs.load(a);
     const RotaryTensor &t = a.t[n];
-    const int groups = kThreads >> k.lane_bits;
-    const Place p0 = place_of<V, IL>(threadIdx.x & (k.lanes - 1), k.units, a.D, a.P);
+    const int heads = n ? a.Hkv : a.H, lanes = 1 << k.lane_bits, u = threadIdx.x & (lanes - 1), groups = kThreads >> k.lane_bits;
+    const Place p = place_of<V, IL>(u, k.units, a.D, a.P);
+    const int group = threadIdx.x >> k.lane_bits;
     float dw[2 * V] = {}, w[2 * V];
-    if (NORM) load_weights<V>(t.w, p0, w);
-    const uint32_t all = (uint32_t)a.n_rows * k.slices[n];
-    for (uint32_t g0 = blockIdx.x * groups; g0 < all; g0 += k.blocks[n] * groups) {
-        const Part part = part_of(a, k, n, g0 + (threadIdx.x >> k.lane_bits));
-        Place p = p0;
-        p.has_a &= part.live;
-        p.has_b &= part.live;
-        const T *x = static_cast<const T *>(t.x) + part.row * t.xs, *dy = static_cast<const T *>(t.dy) + part.row * t.gs;
-        T *dx = static_cast<T *>(t.out) + (int64_t)part.row * (n ? a.Hkv : a.H) * a.D;
-        float c[V], s[V];
-        for (int hb = part.h0; hb < part.h1; hb += N) {
+    if (NORM) load_weights<V>(t.w, p, w);
+    for (int64_t row0 = (int64_t)blockIdx.x * k.rows; row0 < a.n_rows; row0 += (int64_t)k.blocks[n] * k.rows) {
+        const int rows = (int)min((int64_t)k.rows, a.n_rows - row0);
+        Head at{group / heads, group % heads};
+        bool filled = false;
+        while (at.row < rows || !filled) {
+            Head h[N];
             Run<T, V> xa[N], xb[N], ga[N], gb[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const bool has = hb + i < part.h1;
-                const T *from = dy + (hb + i) * t.gh;
+                h[i] = at;
+                at.next(k, n, heads);
+                const bool has = h[i].row < rows;
+                const T *from = static_cast<const T *>(t.dy) + (row0 + h[i].row) * t.gs + h[i].head * t.gh;
                 ga[i].load(from + p.a, p.has_a && has);
                 gb[i].load(from + p.b, p.has_b && has);
                 if (NORM) {
-                    const T *rows = x + (hb + i) * t.xh;
-                    xa[i].load(rows + p.a, p.has_a && has);
-                    xb[i].load(rows + p.b, p.has_b && has);
+                    const T *x = static_cast<const T *>(t.x) + (row0 + h[i].row) * t.xs + h[i].head * t.xh;
+                    xa[i].load(x + p.a, p.has_a && has);
+                    xb[i].load(x + p.b, p.has_b && has);
                 }
             }
-            if (hb == part.h0) angles<V>(a, pairs, part.row, p, c, s);
+            if (!filled) {
+                __syncthreads();        // the rows before are done with the table
+                fill_table(a, k, (int)row0, rows, table);
+                __syncthreads();
+                filled = true;
+            }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                float g[2 * V];
+                if (h[i].row >= rows) break;
+                float g[2 * V], c[V], s[V];
                 ga[i].get(g);
                 gb[i].get(g + V);
+                take_angles<V>(table + h[i].row * k.width + min(p.pair, k.width - V), c, s);
                 turn<V, IL>(g, c, s, -1.0f);
                 if (NORM) {
                     float v[2 * V];
@@ -293,17 +308,17 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
                         sq += v[e] * v[e];
                         dot += g[e] * w[e] * v[e];
                     }
-                    const float r = __builtin_amdgcn_rsqf(group_sum(sq, k.lanes) * k.inv_D + a.eps);
-                    const float m = group_sum(dot, k.lanes) * k.inv_D * r * r;
+                    const float r = __builtin_amdgcn_rsqf(group_sum(sq, lanes) * k.inv_D + a.eps);
+                    const float m = group_sum(dot, lanes) * k.inv_D * r * r;
 #pragma unroll
                     for (int e = 0; e < 2 * V; ++e) {
                         dw[e] += g[e] * (v[e] * r);
                         g[e] = r * (g[e] * w[e] - v[e] * m);
                     }
                 }
-                T *to = dx + (int64_t)(hb + i) * a.D;
-                store_run<T, V>(to + p.a, p.has_a && hb + i < part.h1, g, k.stream);
-                store_run<T, V>(to + p.b, p.has_b && hb + i < part.h1, g + V, k.stream);
+                T *to = static_cast<T *>(t.out) + ((row0 + h[i].row) * heads + h[i].head) * a.D;
+                store_run<T, V>(to + p.a, p.has_a, g, k.stream);
+                store_run<T, V>(to + p.b, p.has_b, g + V, k.stream);
             }
         }
     }
@@ -316,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
     for (int i = threadIdx.x; i < k.units * 2 * V; i += kThreads) {
         const int lane = i % k.units, e = i / k.units;
         float sum = 0.0f;
-        for (int g = 0; g < groups; ++g) sum += sums[e * kThreads + g * k.lanes + lane];
+        for (int g = 0; g < groups; ++g) sum += sums[e * kThreads + (g << k.lane_bits) + lane];
         const Place p = place_of<V, IL>(lane, k.units, a.D, a.P);
         const int d = e < V ? p.a + e : p.b + e - V;
         if (d < a.D) out[d] = sum;
@@ -358,21 +373,21 @@ bool runs_of(const RotaryArgs &a, int V, bool backward) {
 RotaryCut cut_of(const RotaryArgs &a, int V, int size, bool backward) {
     RotaryCut k;
     k.units = (a.D + 2 * V - 1) / (2 * V);
-    k.lanes = 1;
-    while (k.lanes < k.units) k.lanes *= 2;
-    k.lane_bits = __builtin_ctz(k.lanes);
+    k.lane_bits = 0;
+    while (1 << k.lane_bits < k.units) ++k.lane_bits;
+    k.width = k.units * V;
     k.inv_D = 1.0f / (float)a.D;
     k.stream = (int64_t)a.n_rows * (a.H + a.Hkv) * a.D * size > kStream;
-    const int64_t per = kThreads / k.lanes;
+    const int groups = kThreads >> k.lane_bits;
+    // four heads a group, and rows for kBlocks blocks
+    k.rows = std::min(std::max(1, kHeads * groups / a.H), kTable / k.width);
+    k.rows = std::max(1, std::min(k.rows, a.n_rows / kBlocks));
     for (int n = 0; n < 2; ++n) {
         const int heads = n ? a.Hkv : a.H;
-        int run = std::max(heads, 1);
-        // a head a group while that leaves SIMDs without a wavefront or two
-        while (run > 1 && (int64_t)a.n_rows * ((heads + run - 1) / run) * k.lanes < kFill) run = (run + 1) / 2;
-        k.heads[n] = run;
-        k.slices[n] = std::max(1, (heads + run - 1) / run);
-        const int64_t blocks = heads ? ((int64_t)a.n_rows * k.slices[n] + per - 1) / per : 0;
-        k.blocks[n] = (int)(backward ? std::min<int64_t>(blocks, kMaxPartials) : blocks);
+        k.step_row[n] = heads ? groups / heads : 0;
+        k.step_head[n] = heads ? groups % heads : 0;
+        const int blocks = heads ? (a.n_rows + k.rows - 1) / k.rows : 0;
+        k.blocks[n] = backward ? std::min(blocks, kMaxPartials) : blocks;
     }
     return k;
 }
@@ -382,11 +397,12 @@ sn_status launch(const RotaryArgs &a, float *partials, bool backward, float *dqw
     const RotaryCut k = cut_of(a, V, (int)sizeof(T), backward);
     ProfScope prof(backward ? K_ROTARY_BWD : K_ROTARY_FWD, s);
     const dim3 grid(std::max(k.blocks[0], k.blocks[1]), a.Hkv ? 2 : 1);
-    const bool many = std::max(k.heads[0], k.heads[1]) > 1;
+    // several heads of a group on their way where it has them
+    const bool many = (int64_t)k.rows * std::max(a.H, a.Hkv) > (kThreads >> k.lane_bits);
     if (grid.x > 0) {       // no rows: the weights' zeros alone
         if (!backward) {
             if (many)
-                rotary_forward_kernel<T, V, IL, NORM, 4><<<grid, kThreads, 0, s>>>(a, k);
+                rotary_forward_kernel<T, V, IL, NORM, kHeads><<<grid, kThreads, 0, s>>>(a, k);
             else
                 rotary_forward_kernel<T, V, IL, NORM, 1><<<grid, kThreads, 0, s>>>(a, k);
             return launch_status();
@@ -427,10 +443,8 @@ size_t rotary_workspace(const sn_head_rotary &op) {
     return kWsBase + (size_t)kMaxPartials * 2 * op.head_dim * sizeof(float);
 }
 
-// A forward pass has at most a group of 64 lanes for every head of every row.
-bool rotary_fits(const sn_head_rotary &op) {
-    return grid_fits((int64_t)op.n_rows * (op.n_heads + op.n_kv_heads) + 4, 64);
-}
+// A forward pass has at most a block for every row.
+bool rotary_fits(const sn_head_rotary &op) { return grid_fits(op.n_rows, kThreads); }
 
 sn_status rotary_forward(const RotaryArgs &a, int dtype, bool norm, hipStream_t s) {
     return launch(a, dtype, norm, nullptr, false, nullptr, nullptr, s);
