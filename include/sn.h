@@ -461,7 +461,7 @@ typedef struct sn_head_rotary {
     int32_t head_dim;            /* D, 1 .. SN_MAX_HEAD_DIM */
     int32_t dtype;               /* SN_F32 or SN_BF16: q, k and their gradients */
     int32_t norm;                /* 0 or 1 */
-    float eps;                   /* > 0 (with norm) */
+    float eps;                   /* > 0, a normal number (with norm) */
     int32_t n_pairs;             /* 0 .. D / 2 */
     int32_t n_axes;              /* 1 .. SN_MAX_AXES (with pairs) */
     int32_t interleaved;         /* 0 or 1 */
@@ -528,7 +528,10 @@ sn_status sn_head_rotary_backward(const sn_head_rotary *op, const void *d_q, int
  * whose length is negative, beyond its table, or below its count of rows (other
  * than in an attention that is not causal) is skipped; a place whose page is not
  * in [0, n_pages) is not written, reads back as zeros, and is an absent key.
- * Entries of the table behind a sequence's length are not read. */
+ * Entries of the table behind a sequence's length are not read.  What a call
+ * takes depends on max_pages page_size, the most that a sequence can hold, a
+ * little and on the lengths mostly: a table with room to spare costs nothing but
+ * a second launch of sn_cache_attend. */
 typedef struct sn_cache {
     int32_t n_pages;             /* >= 1 */
     int32_t page_size;           /* rows of a page: a power of two, 16 .. 1024 */
@@ -538,7 +541,7 @@ typedef struct sn_cache {
     int32_t codes;               /* SN_CODES_* */
     void *k, *v;                 /* device [n_pages][n_kv_heads][page_size][SN_CACHE_ROW(D)], 16-byte aligned */
     float *k_scale, *v_scale;    /* device [n_pages][n_kv_heads][page_size], 16-byte aligned (with codes) */
-    int32_t n_sequences;         /* B >= 1 */
+    int32_t n_sequences;         /* B, 1 .. 65535 */
     int32_t n_rows, max_rows;    /* the call's rows: of all sequences, of the one with the most */
     int32_t max_pages;           /* entries of a sequence in the table, >= 1 */
     const int32_t *row_ptr;      /* device [B+1] */
@@ -568,7 +571,8 @@ sn_status sn_cache_read(const sn_cache *op, void *k_out, void *v_out, void *ws, 
  * keys j that the row sees,
  *     s = scale q.k_j,  p = exp(s) / sum of exp(s),  o = sum of p v_j
  * with o [n_rows][H][D] and lse [n_rows][H] (may be NULL), the logarithm of the
- * sum of exp(s).  A row that sees no key gives o = 0 and lse = -inf.  Keys that
+ * sum of exp(s).  Scores have to stay within fp32: a row with an infinite one is
+ * not a number, as the formulas have it.  A row that sees no key gives o = 0 and lse = -inf.  Keys that
  * it does not see reach nothing, whatever they hold.  A long sequence is split
  * over its length and joined; scores, sums and joins are fp32.  With SN_BF16 p
  * enters its product in 16 bits. */

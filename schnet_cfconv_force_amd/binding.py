@@ -752,8 +752,8 @@ class HeadRotary:
         if self.n_pairs and (self.axes.min() < 0 or not np.isfinite(self.freqs).all()):
             raise ValueError("axes must not be negative, and frequencies have to be finite")
         self.norm = bool(norm)
-        if self.norm and not 0.0 < eps < np.inf:
-            raise ValueError(f"eps must be positive and finite, not {eps}")
+        if self.norm and not np.finfo(np.float32).tiny <= eps <= np.finfo(np.float32).max:
+            raise ValueError(f"eps must be a positive normal number of 32 bits, not {eps}")
         self.n_rows, self.n_heads, self.n_kv_heads = int(n_rows), int(n_heads), int(n_kv_heads)
         self.head_dim = int(head_dim)
         self.c = SnHeadRotary(self.n_rows, self.n_heads, self.n_kv_heads, self.head_dim, code, int(self.norm), float(eps),

@@ -490,7 +490,11 @@ __device__ inline void take(const Walk<F> &w, Tile<F> &t, int tile, const int (&
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = 4 * g + r, pos = key + 16 * b + at;
-                    if (at >= there[b] || pos < st.first[nr] || pos >= st.last[nr]) s[nr][b][r] = -INFINITY;
+                    if (at >= there[b] || pos < st.first[nr] || pos >= st.last[nr]) {
+                        s[nr][b][r] = -INFINITY;
+                        // its scale may be anything; with one tile of rows it is this row's alone
+                        if constexpr (F::CODES != SN_CODES_NONE && NR == 1) t.vs[b][r] = 0.0f;
+                    }
                 }
     }
     if (absent) {       // whatever lies in absent rows must not meet a weight of zero
@@ -528,8 +532,11 @@ __device__ inline void take(const Walk<F> &w, Tile<F> &t, int tile, const int (&
             for (int r = 0; r < 4; ++r) {
                 const float p = __builtin_amdgcn_exp2f(s[nr][b][r] - base);
                 sum += p;
-                s[nr][b][r] = p;
-                if constexpr (F::CODES != SN_CODES_NONE) s[nr][b][r] = p == 0.0f ? 0.0f : p * t.vs[b][r];
+                // a seen key's scale counts whatever its weight
+                if constexpr (F::CODES != SN_CODES_NONE)
+                    s[nr][b][r] = NR > 1 && s[nr][b][r] == -INFINITY ? 0.0f : p * t.vs[b][r];
+                else
+                    s[nr][b][r] = p;
             }
         st.l[nr] += sum;
     }

@@ -1,6 +1,7 @@
 // C-ABI entry points of the rotation of heads and of the state cache:
 // argument checks and argument packing.  The kernels are in rotary.hip,
 // cache.hip and cache_attend.hip.
+#include <cfloat>
 #include <cmath>
 
 #include "state.h"
@@ -32,7 +33,8 @@ sn_status check_rotary_sizes(const sn_head_rotary *op) {
 
 sn_status check_rotary(const sn_head_rotary *op) {
     SN_TRY(check_rotary_sizes(op));
-    if (op->norm && !(op->eps > 0.0f && std::isfinite(op->eps))) return SN_ERR_INVALID;
+    // a normal number: the reciprocal root of a smaller one is none
+    if (op->norm && !(op->eps >= FLT_MIN && std::isfinite(op->eps))) return SN_ERR_INVALID;
     if (!op->norm && (op->q_weight || op->k_weight)) return SN_ERR_INVALID;
     if (op->n_pairs > 0) {
         if (!op->freqs || !op->axes || (op->n_rows > 0 && !op->positions) || !aligned_for(op->positions, SN_F32))

@@ -113,6 +113,29 @@ def test_a_row_of_nan_written_reaches_the_rows_that_see_it(sn, codes):
     assert bool(torch.isfinite(got[0]).all()) and bool(torch.isnan(got[1]).all())
 
 
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_a_value_counts_whatever_its_weight(sn, what, dtype, codes):
+    """A seen key whose weight is below fp32 (its score is 200 under the others): its NaN or infinity reaches the row."""
+    import torch
+    if codes is not None and what == "inf":
+        what = "nan"        # such a row is kept as NaN
+    to = torch_type(dtype)
+    c = cache_case(sn, [1], [70], 1, 32, 16, dtype, codes, 38, heads=1)
+    rows = [x.clone() for x in c["rows"]]
+    q = c["q"]
+    q[0, 0] = 1.0
+    rows[0].zero_()
+    rows[0][40, 0] = -200 * 32 ** 0.5 / 32
+    rows[1][40, 0, 3] = float(what)
+    sn.cache_write(c["whole"], rows[0], rows[1], c["table"], c["lengths"], c["ws"])
+    got = sn.cache_attend(c["plan"], q, c["table"], c["lengths"], c["ws"])[0, 0]
+    assert sn.read_status(c["ws"]) == sn.SN_OK and got.dtype == to
+    hit = torch.isnan(got) if what == "nan" else torch.isinf(got)
+    assert bool(hit.all() if codes is not None else hit[3]) and bool(codes is not None or torch.isfinite(torch.cat([got[:3], got[4:]])).all())
+
+
 def test_rotary_nan_stays_in_its_head(sn):
     import torch
     plan, q, k, positions, w, g, freqs, axes = rotary_case(sn, 20, 4, 2, 32, [8, 8], False, True, "bfloat16", 26)

@@ -49,7 +49,7 @@ def test_rotary_plans_refuse():
         args = {"n_rows": 5, "n_heads": 4, "head_dim": 32, **change}
         with pytest.raises(sn.SnError):
             make(**args)
-    for change in ({"freqs": [1.0], "axes": [-1]}, {"freqs": [math.nan]}, {"freqs": [1.0, 2.0], "axes": [0]}, {"eps": 0.0},
+    for change in ({"freqs": [1.0], "axes": [-1]}, {"freqs": [math.nan]}, {"freqs": [1.0, 2.0], "axes": [0]}, {"eps": 0.0}, {"eps": 1e-40},
                    {"eps": math.inf}, {"dtype": torch.float16}):
         with pytest.raises(ValueError):
             make(5, 4, 32, **change)
@@ -155,7 +155,7 @@ def test_rotary_entry_points_refuse_before_any_gpu_work():
         assert lib.sn_head_rotary_workspace_bytes(ctypes.byref(d)) == 0, change
         assert forward(d) == sn.SN_ERR_INVALID and backward(d) == sn.SN_ERR_INVALID, change
     beyond, below, odd = np.array([0, 2, 1, 0], np.int32), np.array([0, -1, 1, 0], np.int32), np.array([1, math.inf, 1, 1.0])
-    for change in ({"eps": 0.0}, {"eps": math.nan}, {"norm": 0}, {"freqs": None}, {"axes": None}, {"positions": None}, {"positions": 258},
+    for change in ({"eps": 0.0}, {"eps": 1e-40}, {"eps": math.nan}, {"norm": 0}, {"freqs": None}, {"axes": None}, {"positions": None}, {"positions": 258},
                    {"q": None}, {"k": None}, {"q": 257}, {"k": 257}, {"q_weight": 258}, {"k_weight": 257}, {"axes": beyond.ctypes.data},
                    {"axes": below.ctypes.data}, {"freqs": odd.ctypes.data}):
         assert forward(desc(**change)) == sn.SN_ERR_INVALID and backward(desc(**change)) == sn.SN_ERR_INVALID, change
