@@ -47,7 +47,7 @@ struct Form {
     // bf16 planes of the weights: 16 bits beside bf16 rows, 24 beside fp32 ones
     static constexpr int PP = std::is_same<T, float>::value ? 3 : 2;
     // 16-key blocks of a tile: about 8 KB of keys a wavefront where registers allow
-    static constexpr int NB = F32 ? (DP == 128 ? 1 : 2) : DP == 128 || (ES == 1 && DP == 32) ? 2 : 4;
+    static constexpr int NB = F32 ? (DP == 128 ? 1 : DP == 16 ? 4 : 2) : DP == 128 || (ES == 1 && DP == 32) ? 2 : 4;
     static constexpr int TILE = 16 * NB;
     static constexpr int W = DP / 16;       // dims that a lane reads of a value row
     // registers of a key block and of a value row
@@ -55,7 +55,7 @@ struct Form {
     static constexpr int VREGS = (W * ES + 3) / 4;
     static constexpr int AUX = PAST_ ? 2 : 0;       // of a load: 2 goes past the caches
     // blocks that a CU holds: short rows of one tile fit 128 registers
-    static constexpr int BLOCKS = DP == 32 && NR == 1 ? 2 : 1;
+    static constexpr int BLOCKS = DP <= 32 && NR == 1 ? 2 : 1;
 };
 
 struct AttendCut {
@@ -1037,6 +1037,9 @@ sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t 
 }
 template <typename T, int CODES>
 sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t s) {
+    // fp32 products take heads of 16 as they are, bf16 ones 32 dims at a time
+    if constexpr (std::is_same<T, float>::value && CODES == SN_CODES_NONE)
+        if (a.Dp <= 16) return launch<T, CODES, 16>(a, o, lse, ws, s);
     if (a.Dp <= 32) return launch<T, CODES, 32>(a, o, lse, ws, s);
     if (a.Dp <= 64) return launch<T, CODES, 64>(a, o, lse, ws, s);
     return launch<T, CODES, 128>(a, o, lse, ws, s);
