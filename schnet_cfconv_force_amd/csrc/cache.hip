@@ -2,7 +2,9 @@
 //
 // A group of lanes holds a row of a head, a lane eight of its elements; the
 // largest magnitude is joined over the group, so a row is read once and its
-// codes and its scale are written once.
+// codes and its scale are written once.  What it costs is those bytes: 48 x
+// <= 4096 rows of 8 x 128, bf16 to int8, 790 MB a pass: written at 5.0 TB/s (the
+// vector units nine tenths busy with the codes), read back at 5.1.
 #include <algorithm>
 
 #include "state.h"
@@ -11,7 +13,7 @@ namespace sn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRounds = 2;          // of four items of each group, in a block
+
 
 struct CacheRowsIO {
     const void *x[2];          // k, v given
@@ -47,7 +49,10 @@ struct Item {
     }
 };
 
-constexpr int kItems = 4;       // items of a group on their way at once
+// Items of a group on their way at once, and of a block's groups: 48 x <= 4096
+// rows of 8 x 128, bf16 to int8 and back, 158 + 156 us; with two 167 + 166, with
+// eight 169 + 165; in blocks of eight items a group 163 + 167, of 32 182 + 191.
+constexpr int kItems = 4;
 
 // Eight elements of a row as they lie in memory, zero from D on.
 template <typename T>
@@ -225,7 +230,7 @@ sn_status launch(const CacheArgs &a, const CacheRowsIO &io, bool write, hipStrea
     const int groups = kThreads >> c.lane_bits, heads = 2 * a.Hkv;
     c.step_row = groups / heads;
     c.step_head = groups % heads;
-    c.chunk_rows = std::max(1, kRounds * kItems * groups / heads);
+    c.chunk_rows = std::max(1, kItems * groups / heads);
     c.past = (int64_t)a.n_rows * heads * a.D * (int64_t)sizeof(T) > kPast;
     const dim3 grid((a.max_rows + c.chunk_rows - 1) / c.chunk_rows, a.B);
     ProfScope prof(write ? K_CACHE_WRITE : K_CACHE_READ, s);
