@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-
 struct CacheRowsIO {
     const void *x[2];          // k, v given
     int64_t xs[2], xh[2];

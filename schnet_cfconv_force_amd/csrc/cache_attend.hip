@@ -20,6 +20,14 @@
 // and joins the others' at the end of the piece.  The tiles of all units form
 // one line that is cut evenly over the blocks, wherever sequences end; a unit
 // that is cut leaves partial rows (fp32), which a second launch joins.
+//
+// Measured (one new row a sequence): 32 x <= 20000 keys, 32/8 heads of 128, bf16,
+// 1.65 GB: 262 us, 6.3 TB/s, where a copy reaches 5.2; the same in e4m3, 0.85 GB:
+// 153 us, 5.5 TB/s (without the conversions it takes as long, without the scales
+// 155 of 162 then: the memory bounds it).  Short histories are bound by a chain
+// of dependent reads (lengths, pages, keys) and by the rounds a wavefront takes:
+// 271 keys, 4 x 32 fp32: 6.7 us; 64 x <= 1076 keys, 8 x 16 int8 beside fp32 rows:
+// 15 us, half of it vector instructions.
 #include <algorithm>
 #include <type_traits>
 
