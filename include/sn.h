@@ -543,11 +543,11 @@ typedef struct sn_cache {
     float *k_scale, *v_scale;    /* device [n_pages][n_kv_heads][page_size], 16-byte aligned (with codes) */
     int32_t n_sequences;         /* B, 1 .. 65535 */
     int32_t n_rows, max_rows;    /* the call's rows: of all sequences, of the one with the most */
-    int32_t max_pages;           /* entries of a sequence in the table, >= 1 */
+    int32_t max_pages;           /* entries of a sequence in the table, >= 1; times page_size at most 2^30 */
     const int32_t *row_ptr;      /* device [B+1] */
     const int32_t *table;        /* device [B][max_pages], contiguous */
     const int32_t *lengths;      /* device [B] */
-    /* read by sn_cache_attend alone */
+    /* read by sn_cache_workspace_bytes and sn_cache_attend alone */
     int32_t n_heads;             /* H, a multiple of n_kv_heads */
     float scale;                 /* finite */
     int32_t causal;              /* 1: a row sees the positions up to its own; 0: all of its sequence */

@@ -102,7 +102,7 @@ __device__ inline Sequence sequence_of(const CacheArgs &a, int b) {
         flag_status(a.status, SN_ERR_INVALID);
         s.n = 0;
     }
-    s.begin = a.window > 0 ? max(0, s.length - s.n + 1 - a.window) & ~15 : 0;
+    s.begin = s.n > 0 && a.window > 0 ? max(0, s.length - s.n + 1 - a.window) & ~15 : 0;
     // a row that sees nothing is written too: one tile at the least
     s.tiles = s.n > 0 ? max(1, (s.length - s.begin + F::TILE - 1) / F::TILE) : 0;
     return s;

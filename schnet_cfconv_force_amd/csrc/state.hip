@@ -74,8 +74,8 @@ sn_status check_cache_sizes(const sn_cache *op) {
     if (op->codes < SN_CODES_NONE || op->codes > SN_CODES_E4M3) return SN_ERR_INVALID;
     if (op->n_sequences < 1 || op->n_rows < 0 || op->max_rows < 0 || op->max_rows > op->n_rows) return SN_ERR_INVALID;
     if ((int64_t)op->max_rows * op->n_sequences < op->n_rows) return SN_ERR_INVALID;
-    // positions and rows with their heads are counted in 32 bits
-    if (op->max_pages < 1 || (int64_t)op->max_pages * op->page_size > INT32_MAX) return SN_ERR_INVALID;
+    // positions, with a tile behind the last, and rows with their heads are counted in 32 bits
+    if (op->max_pages < 1 || (int64_t)op->max_pages * op->page_size > (1 << 30)) return SN_ERR_INVALID;
     if ((int64_t)op->n_rows * op->n_kv_heads > INT32_MAX) return SN_ERR_INVALID;
     return cache_fits(*op) ? SN_OK : SN_ERR_INVALID;
 }

@@ -195,7 +195,7 @@ def test_cache_entry_points_refuse_before_any_gpu_work():
     assert all(f(None) == sn.SN_ERR_INVALID for f in calls)
     for change in ({"n_pages": 0}, {"page_size": 8}, {"page_size": 48}, {"page_size": 2048}, {"n_kv_heads": 0}, {"head_dim": 0},
                    {"head_dim": 129}, {"dtype": 2}, {"codes": 3}, {"codes": -1}, {"n_sequences": 0}, {"n_rows": -1}, {"max_rows": 7},
-                   {"max_rows": 1}, {"max_pages": 0}, {"max_pages": 2 ** 27}, {"n_rows": 2 ** 30, "max_rows": 2 ** 30},
+                   {"max_rows": 1}, {"max_pages": 0}, {"max_pages": 2 ** 27}, {"max_pages": 2 ** 26 + 1}, {"n_rows": 2 ** 30, "max_rows": 2 ** 30},
                    {"n_sequences": 65536, "n_rows": 65536}):
         d = desc(**change)
         assert lib.sn_cache_workspace_bytes(ctypes.byref(d)) == 0, change
@@ -206,7 +206,7 @@ def test_cache_entry_points_refuse_before_any_gpu_work():
     for change in ({"n_heads": 0}, {"n_heads": 3}, {"n_heads": 65536}, {"causal": 2}, {"window": -1}, {"window": 3, "causal": 0},
                    {"scale": math.nan}, {"scale": math.inf}, {"q": None}, {"q": 257}):
         assert attend(desc(**change)) == sn.SN_ERR_INVALID, change
-    d = desc()
+    d = desc(max_pages=2 ** 26)
     need = lib.sn_cache_workspace_bytes(ctypes.byref(d))
     assert need >= 256
     for f in calls:
