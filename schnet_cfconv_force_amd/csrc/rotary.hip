@@ -44,6 +44,7 @@ struct RotaryCut {
     int blocks[2];  // of q and of k (grid y)
     float inv_D;
     bool stream;    // stores go past the caches
+    bool single;    // one block of q and one of k (backward): no sums are left to join
 };
 
 template <typename T, int V>
@@ -250,9 +251,10 @@ __global__ __launch_bounds__(kThreads) void rotary_forward_kernel(RotaryArgs a, 
 }
 
 // Runs of rows in turn by blocks; a block leaves the weight gradients of its
-// rows in partials[q, k][block][D].
+// rows in partials[q, k][block][D], the only one in their place.
 template <typename T, int V, bool IL, bool NORM, int N>
-__global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a, RotaryCut k, float *partials) {
+__global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a, RotaryCut k, float *partials, float *dq_weight,
+                                                                   float *dk_weight) {
     __shared__ alignas(16) float2 table[kTable];
     __shared__ float sums[NORM ? kThreads * 2 * V : 1];
     const int n = blockIdx.y;
@@ -322,11 +324,12 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
             }
         }
     }
-    if (!NORM || !partials) return;
+    if (!NORM || !(n ? dk_weight : dq_weight)) return;
+    // the only block has the whole sums
+    float *out = k.single ? (n ? dk_weight : dq_weight) : partials + ((int64_t)n * kMaxPartials + blockIdx.x) * a.D;
 #pragma unroll
     for (int e = 0; e < 2 * V; ++e) sums[e * kThreads + threadIdx.x] = dw[e];
     __syncthreads();
-    float *out = partials + ((int64_t)n * kMaxPartials + blockIdx.x) * a.D;
     // element e of lane u, of all groups
     for (int i = threadIdx.x; i < k.units * 2 * V; i += kThreads) {
         const int lane = i % k.units, e = i / k.units;
@@ -344,6 +347,7 @@ __global__ __launch_bounds__(kThreads) void rotary_weights_kernel(const float *p
     __shared__ double sums[kThreads];
     const int n = blockIdx.y, d = blockIdx.x;
     float *out = n ? dk_weight : dq_weight;
+    if (!out) return;
     double sum = 0.0;
     for (int b = threadIdx.x; b < k.blocks[n]; b += kThreads) sum += partials[((int64_t)n * kMaxPartials + b) * D + d];
     sums[threadIdx.x] = sum;
@@ -351,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void rotary_weights_kernel(const float *p
         __syncthreads();
         if (threadIdx.x < o) sums[threadIdx.x] += sums[threadIdx.x + o];
     }
-    if (threadIdx.x == 0 && out) out[d] = (float)sums[0];
+    if (threadIdx.x == 0) out[d] = (float)sums[0];
 }
 
 // A lane's vector length: as long as every run of V elements lies whole in
@@ -382,6 +386,14 @@ RotaryCut cut_of(const RotaryArgs &a, int V, int size, bool backward) {
     // four heads a group, and rows for kBlocks blocks
     k.rows = std::min(std::max(1, kHeads * groups / a.H), kTable / k.width);
     k.rows = std::max(1, std::min(k.rows, a.n_rows / kBlocks));
+    // Four heads a group are one block's: a launch that joins the weights' sums costs
+    // more than more blocks give (forward and backward of 4 + 4 heads of 32, fp32,
+    // with the join and without: 1 row 24.2 and 21.8 us, 64 rows 24.3 and 22.2;
+    // replayed from a graph 9.5 and 7.0, 10.1 and 10.6: no longer than that). Keys
+    // there must be, for the join also writes the zeros of a weight without heads.
+    k.single = backward && a.n_rows > 0 && a.Hkv > 0 && a.n_rows <= kTable / k.width &&
+               (int64_t)a.n_rows * std::max(a.H, a.Hkv) <= kHeads * groups;
+    if (k.single) k.rows = a.n_rows;
     for (int n = 0; n < 2; ++n) {
         const int heads = n ? a.Hkv : a.H;
         k.step_row[n] = heads ? groups / heads : 0;
@@ -408,12 +420,12 @@ sn_status launch(const RotaryArgs &a, float *partials, bool backward, float *dqw
             return launch_status();
         }
         if (many)
-            rotary_backward_kernel<T, V, IL, NORM, 2><<<grid, kThreads, 0, s>>>(a, k, partials);
+            rotary_backward_kernel<T, V, IL, NORM, 2><<<grid, kThreads, 0, s>>>(a, k, partials, dqw, dkw);
         else
-            rotary_backward_kernel<T, V, IL, NORM, 1><<<grid, kThreads, 0, s>>>(a, k, partials);
+            rotary_backward_kernel<T, V, IL, NORM, 1><<<grid, kThreads, 0, s>>>(a, k, partials, dqw, dkw);
         SN_TRY(launch_status());
     }
-    if (NORM && (dqw || dkw)) rotary_weights_kernel<<<dim3(a.D, 2), kThreads, 0, s>>>(partials, k, a.D, dqw, dkw);
+    if (NORM && !k.single && (dqw || dkw)) rotary_weights_kernel<<<dim3(a.D, 2), kThreads, 0, s>>>(partials, k, a.D, dqw, dkw);
     return launch_status();
 }
 

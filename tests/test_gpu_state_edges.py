@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import state_ref as R
-from test_gpu_state import CODES, TYPES, attend_check, cache_case, kept_rows, normal, rotary_case, torch_type
+from test_gpu_state import CODES, TYPES, attend_check, cache_case, kept_rows, normal, rotary_case, rotary_check, torch_type
 
 pytestmark = pytest.mark.gpu
 
@@ -146,6 +146,39 @@ def test_rotary_nan_stays_in_its_head(sn):
     assert bool(torch.isnan(got[0][3, 2]).all()) and bool(torch.isnan(got[1][7, 1]).any())
     got[0][3, 2], got[1][7, 1] = want[0][3, 2], want[1][7, 1]
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,heads,kv,dim", [(1, 4, 4, 32), (64, 4, 4, 32), (65, 4, 4, 32), (64, 2, 4, 32), (9, 6, 1, 40), (4, 32, 8, 128),
+                                               (17, 8, 8, 128), (300, 1, 1, 7), (1, 300, 1, 16), (2000, 1, 1, 2), (3, 4, 0, 32)])
+def test_rotary_weight_sums_of_few_and_more_rows(sn, rows, heads, kv, dim, dtype):
+    """The weights' gradients on both sides of what one block sums alone, the same with either left out, in a workspace that
+    holds what was there before."""
+    import torch
+    case = rotary_case(sn, rows, heads, kv, dim, [dim // 2], False, True, dtype, 61)
+    rotary_check(sn, case, False, True, dtype)
+    plan, q, k, positions, w, g, _, _ = case
+    k, g[1] = (k, g[1]) if kv else (None, None)
+    ws = sn.head_rotary_workspace(plan)
+    want = sn.head_rotary_backward(plan, q, k, positions, *g, ws, *w)
+    ws[256:] = 255              # behind the status words
+    op = plan._bind(q, k, positions, *w)
+    gs, gh, ks, kh = plan._rows(*g, ("d_q", "d_k"))
+    pointer = lambda t: None if t is None else t.data_ptr()
+    for with_q, with_k in ((True, True), (True, False), (False, True), (False, False)):
+        dq, dk = torch.empty_like(want[0]), (torch.empty_like(want[1]) if kv else None)
+        sums = torch.full((2, 3 * dim), math.nan, device="cuda")
+        places = [sums[i, dim:2 * dim] if on else None for i, on in enumerate((with_q, with_k))]
+        st = sn.lib().sn_head_rotary_backward(op, g[0].data_ptr(), gs, gh, pointer(g[1]), ks, kh, dq.data_ptr(), pointer(dk),
+                                              pointer(places[0]), pointer(places[1]), ws.data_ptr(), ws.numel(),
+                                              torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == sn.SN_OK and torch.equal(dq, want[0]) and (not kv or torch.equal(dk, want[1]))
+        for i, place in enumerate(places):
+            if place is not None:
+                assert torch.equal(place, want[2 + i] if want[2 + i] is not None else torch.zeros_like(place))
+                place.fill_(math.nan)
+        assert bool(torch.isnan(sums).all())
 
 
 # ------------------------------------------------------------------ arrays that contradict the sizes
