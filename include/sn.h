@@ -307,7 +307,7 @@ sn_status sn_read_status(void *ws, void *stream);
  * repeated calls give identical bits.  No call synchronises. */
 
 /* Element type of the row tensors.  Sums, softmax statistics and norms are
- * fp32 or more whatever it is.  With SN_BF16 the attention's products take p in
+ * fp32 or more whatever it is.  With SN_BF16 the cross attention takes p in
  * 16 bits in the forward pass, and p and dS in 8 in the backward pass, where
  * each adds to a gradient about what rounding the gradient itself does (dbias,
  * which is fp32, is summed from unrounded dS); SN_F32 keeps 24 throughout. */
@@ -574,8 +574,7 @@ sn_status sn_cache_read(const sn_cache *op, void *k_out, void *v_out, void *ws, 
  * sum of exp(s).  Scores have to stay within fp32: a row with an infinite one is
  * not a number, as the formulas have it.  A row that sees no key gives o = 0 and lse = -inf.  Keys that
  * it does not see reach nothing, whatever they hold.  A long sequence is split
- * over its length and joined; scores, sums and joins are fp32.  With SN_BF16 p
- * enters its product in 16 bits. */
+ * over its length and joined; scores, weights, sums and joins are fp32. */
 sn_status sn_cache_attend(const sn_cache *op, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------- timing */

@@ -52,8 +52,7 @@ struct Form {
     static constexpr bool F32 = std::is_same<T, float>::value && CODES == SN_CODES_NONE;   // products in fp32
     static constexpr int ES = CODES != SN_CODES_NONE ? 1 : (int)sizeof(T);
     static constexpr int QP = std::is_same<T, float>::value ? 3 : 1;    // bf16 planes of q, exact to 2^-24
-    // bf16 planes of the weights: 16 bits beside bf16 rows, 24 beside fp32 ones
-    static constexpr int PP = std::is_same<T, float>::value ? 3 : 2;
+    static constexpr int PP = 3;        // of the weights, which keep their 24 bits
     // 16-key blocks of a tile: about 8 KB of keys a wavefront where registers allow
     static constexpr int NB = F32 ? (DP == 128 ? 1 : DP == 16 ? 4 : 2) : DP == 128 || (ES == 1 && DP == 32) ? 2 : 4;
     static constexpr int TILE = 16 * NB;

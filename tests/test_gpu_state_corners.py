@@ -1,0 +1,51 @@
+"""GPU: the rotation of heads and the state cache at values, sizes and layouts beyond the other tests' (state_ref.py states
+how the common tolerances are derived; a test with its own derives it beside it)."""
+import math
+
+import numpy as np
+import pytest
+
+import state_ref as R
+from test_gpu_state import CODES, TYPES, attend_check, cache_case, kept_rows, normal, torch_type
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sn():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import schnet_cfconv_force_amd as sn
+    sn.lib()
+    return sn
+
+
+# ------------------------------------------------------------------ bits of the weights
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dim,heads,kv", [(32, 64, 8), (64, 64, 8), (128, 64, 8), (64, 128, 4), (128, 128, 4)])
+def test_attend_weights_keep_their_bits(sn, dim, heads, kv, codes):
+    """bf16 rows, three keys a sequence, scores of one product within [-1, 1]: where values cancel, the output's own rounding
+    is small and an error of the weights shows.
+
+    In u = 2^-24 of the magnitudes.  A score is exact but for log2(e) in its scale, that product and the code's scale (3 of
+    the score) and the subtraction of the maximum: in powers of two at most (3 + 3) 1.45 + 2.9 = 11.6, 8.1 in p; the
+    exponential 2, the code's scale in p 1, so 11.1 above and, with two additions, 12.1 below; the quotient 5, the last
+    product 1, at most nine rounded additions in the matrix product: 38.2 in all.  (Weights of 16 bits are off by up to
+    128.)"""
+    import torch
+    print(f"[attend] bits {dim} {heads}/{kv} {codes}", flush=True)
+    B = 64
+    c = cache_case(sn, np.ones(B, np.int64), np.full(B, 3), kv, dim, 16, "bfloat16", codes, dim + heads, heads=heads, scale=1.0)
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    uniform = lambda *shape: (torch.rand(shape, generator=gen, device="cuda") * 2 - 1).bfloat16()     # noqa: E731
+    k = torch.zeros_like(c["rows"][0])
+    k[..., 0] = uniform(*k.shape[:2])
+    c["rows"] = [k, c["rows"][1]]
+    c["q"].zero_()
+    c["q"][..., 0] = uniform(*c["q"].shape[:2])
+    sn.cache_write(c["whole"], *c["rows"], c["table"], c["lengths"], c["ws"])
+    o = sn.cache_attend(c["plan"], c["q"], c["table"], c["lengths"], c["ws"])
+    assert sn.read_status(c["ws"]) == sn.SN_OK
+    ref, _ = R.attend(c["q"], *kept_rows(c), c["row_ptr"], c["held"], 1.0)
+    print(f"worst {R.check('o', o, ref['o'], 38.2 * R.U32, True):.3f} of the tolerance", flush=True)
