@@ -54,13 +54,14 @@ struct VecOf { typedef T type __attribute__((ext_vector_type(V))); };
 struct Place {
     int a, b;       // first elements
     int pair;       // the first pair
-    bool turned, has_a, has_b;
+    int turned;     // pairs that turn, the lane's first: of adjacent ones some, else all or none
+    bool has_a, has_b;
 };
 template <int V, bool IL>
 __device__ inline Place place_of(int u, int units, int D, int P) {
     Place p;
     p.pair = u * V;
-    p.turned = p.pair < P;      // of adjacent pairs the first: each is asked for on its own
+    p.turned = max(0, min(P - p.pair, V));
     if (IL) {
         p.a = 2 * V * u;
         p.b = p.a + V;
@@ -162,14 +163,16 @@ __device__ inline void take_angles(const float2 *table, float (&c)[V], float (&s
     }
 }
 
+// What does not turn is left alone: an infinity times a sine of zero would reach its neighbour.
 template <int V, bool IL>
-__device__ inline void turn(float (&x)[2 * V], const float (&c)[V], const float (&s)[V], float sign) {
+__device__ inline void turn(float (&x)[2 * V], const Place &p, const float (&c)[V], const float (&s)[V], float sign) {
+    if (p.turned == 0) return;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         float &a = x[IL ? 2 * e : e], &b = x[IL ? 2 * e + 1 : V + e];
         const float ta = a * c[e] - sign * b * s[e], tb = b * c[e] + sign * a * s[e];
-        a = ta;
-        b = tb;
+        a = !IL || e < p.turned ? ta : a;
+        b = !IL || e < p.turned ? tb : b;
     }
 }
 
@@ -242,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void rotary_forward_kernel(RotaryArgs a, 
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) v[e] *= r * w[e];
             }
-            turn<V, IL>(v, c, s, 1.0f);
+            turn<V, IL>(v, p, c, s, 1.0f);
             T *to = static_cast<T *>(t.out) + ((int64_t)(row0 + h[i].row) * heads + h[i].head) * a.D;
             store_run<T, V>(to + p.a, p.has_a, v, k.stream);
             store_run<T, V>(to + p.b, p.has_b, v + V, k.stream);
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
                 ga[i].get(g);
                 gb[i].get(g + V);
                 take_angles<V>(table + h[i].row * k.width + min(p.pair, k.width - V), c, s);
-                turn<V, IL>(g, c, s, -1.0f);
+                turn<V, IL>(g, p, c, s, -1.0f);
                 if (NORM) {
                     float v[2 * V];
                     xa[i].get(v);

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import state_ref as R
-from test_gpu_state import CODES, TYPES, attend_check, cache_case, kept_rows, normal, torch_type
+from test_gpu_state import CODES, TYPES, attend_check, cache_case, kept_rows, normal, rotary_case, rotary_check, torch_type
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,22 @@ def test_attend_weights_keep_their_bits(sn, dim, heads, kv, codes):
     assert sn.read_status(c["ws"]) == sn.SN_OK
     ref, _ = R.attend(c["q"], *kept_rows(c), c["row_ptr"], c["held"], 1.0)
     print(f"worst {R.check('o', o, ref['o'], 38.2 * R.U32, True):.3f} of the tolerance", flush=True)
+
+
+# ------------------------------------------------------------------ elements that do not turn
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,pairs", [(128, 32), (128, 37), (32, 4), (32, 0), (40, 12), (40, 3), (24, 8), (20, 3), (7, 2)])
+def test_rotary_elements_that_do_not_turn_keep_to_themselves(sn, dim, pairs, dtype, interleaved, norm):
+    """NaN and infinities in them, in the rows and in the gradients, do not reach their neighbours."""
+    import torch
+    print(f"[rotary] unturned {dim} {pairs} {dtype} {interleaved} {norm}", flush=True)
+    case = rotary_case(sn, 23, 3, 2, dim, [pairs] if pairs else [], interleaved, norm, dtype, 81)
+    plan, q, k, positions, w, g, _, _ = case
+    for i, t in enumerate((q, k, *g)):
+        for r, value in ((1, math.nan), (2, math.inf), (3, -math.inf)):
+            for h in range(t.shape[1]):
+                t[r + 4 * i, h, 2 * pairs + (3 * r + 5 * h) % (dim - 2 * pairs)] = value
+    rotary_check(sn, case, interleaved, norm, dtype)
