@@ -445,6 +445,23 @@ def _ragged(ptr, name: str):
     return ptr.astype(np.int32), int(np.diff(ptr).max())
 
 
+def _int32(value, name: str) -> int:
+    """A whole number that a descriptor holds in 32 bits (ctypes keeps the lowest 32 of a larger one, silently)."""
+    n = int(value)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must be within 32 bits, not {n}")
+    return n
+
+
+def _int32s(values, name: str):
+    """The same for an array: its own int32 copy, flat."""
+    wide = np.asarray(values, np.int64).ravel()
+    narrow = wide.astype(np.int32)
+    if not np.array_equal(wide, narrow):
+        raise ValueError(f"{name} must be within 32 bits")
+    return narrow
+
+
 def _rows(t, name: str, shape, dtype, device):
     """Check a row tensor (its last index contiguous); returns its strides."""
     strides = t.stride()
@@ -547,13 +564,14 @@ class CrossAttention:
         kp, max_k = _ragged(k_ptr, "k_ptr")
         if qp.size != kp.size:
             raise ValueError(f"q_ptr has {qp.size - 1} segments, k_ptr {kp.size - 1}")
-        self.thresholds = None if thresholds is None else np.ascontiguousarray(thresholds, np.int32).ravel()
+        self.thresholds = None if thresholds is None else _int32s(thresholds, "thresholds")
         self.n_buckets = 0 if self.thresholds is None else self.thresholds.size + 1
         self.q_ptr = torch.from_numpy(qp).to(device)
         self.k_ptr = torch.from_numpy(kp).to(device)
         self.device = self.q_ptr.device
         self.n_q, self.n_k = int(qp[-1]), int(kp[-1])
-        self.n_heads, self.n_kv_heads, self.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
+        self.n_heads, self.n_kv_heads = _int32(n_heads, "n_heads"), _int32(n_kv_heads, "n_kv_heads")
+        self.head_dim = _int32(head_dim, "head_dim")
         self.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
         # sizes are checked with the bias slot set, so that the bucket count is checked too
         self.c = SnCrossAttention(qp.size - 1, self.n_q, self.n_k, max_q, max_k, _ptr(self.q_ptr), _ptr(self.k_ptr),
@@ -650,7 +668,7 @@ class GroupNorm:
         self.row_ptr = torch.from_numpy(rp).to(device)
         self.device = self.row_ptr.device
         self.n_segments, self.n_rows = rp.size - 1, int(rp[-1])
-        self.n_channels, self.n_groups = int(n_channels), int(n_groups)
+        self.n_channels, self.n_groups = _int32(n_channels, "n_channels"), _int32(n_groups, "n_groups")
         self.c = SnGroupNorm(self.n_segments, self.n_rows, longest, _ptr(self.row_ptr), self.n_channels,
                              self.n_groups, _ACTIVATIONS[activation], code, float(eps))
         self.workspace_bytes = int(lib().sn_group_norm_workspace_bytes(ctypes.byref(self.c)))
@@ -723,7 +741,7 @@ def rotary_frequencies(sections, base: float = 10000.0, shared: bool = True):
     """sn_rotary_frequencies -> (freqs float64, axes int32), a value for each pair: sections[a] pairs turn by axis a.
 
     shared: one ladder base^(-j/n) falls over all n pairs; else every axis has a ladder of its own."""
-    sections = np.ascontiguousarray(sections, np.int32).ravel()
+    sections = _int32s(sections, "sections")
     n = max(int(np.clip(sections, 0, None).sum(dtype=np.int64)), 1)
     freqs, axes = np.zeros(min(n, SN_MAX_HEAD_DIM), np.float64), np.zeros(min(n, SN_MAX_HEAD_DIM), np.int32)
     _check(lib().sn_rotary_frequencies(sections.size, sections.ctypes.data, float(base), int(shared), freqs.ctypes.data,
@@ -745,7 +763,7 @@ class HeadRotary:
         code = _row_type(self.dtype)
         self.freqs = np.ascontiguousarray([] if freqs is None else freqs, np.float64).ravel().copy()
         self.n_pairs = self.freqs.size
-        self.axes = np.zeros(self.n_pairs, np.int32) if axes is None else np.ascontiguousarray(axes, np.int32).ravel().copy()
+        self.axes = np.zeros(self.n_pairs, np.int32) if axes is None else _int32s(axes, "axes")
         if self.axes.size != self.n_pairs:
             raise ValueError(f"{self.n_pairs} frequencies and {self.axes.size} axes")
         self.n_axes = int(self.axes.max()) + 1 if self.n_pairs else 0
@@ -754,8 +772,8 @@ class HeadRotary:
         self.norm = bool(norm)
         if self.norm and not np.finfo(np.float32).tiny <= eps <= np.finfo(np.float32).max:
             raise ValueError(f"eps must be a positive normal number of 32 bits, not {eps}")
-        self.n_rows, self.n_heads, self.n_kv_heads = int(n_rows), int(n_heads), int(n_kv_heads)
-        self.head_dim = int(head_dim)
+        self.n_rows, self.n_heads = _int32(n_rows, "n_rows"), _int32(n_heads, "n_heads")
+        self.n_kv_heads, self.head_dim = _int32(n_kv_heads, "n_kv_heads"), _int32(head_dim, "head_dim")
         self.c = SnHeadRotary(self.n_rows, self.n_heads, self.n_kv_heads, self.head_dim, code, int(self.norm), float(eps),
                               self.n_pairs, self.n_axes, int(bool(interleaved)), self.freqs.ctypes.data, self.axes.ctypes.data)
         self.workspace_bytes = int(lib().sn_head_rotary_workspace_bytes(ctypes.byref(self.c)))
@@ -853,8 +871,8 @@ class StateCache:
         if codes not in _CODES:
             raise ValueError(f"codes must be one of {tuple(_CODES)}, not {codes!r}")
         self.codes = codes
-        self.n_pages, self.page_size = int(n_pages), int(page_size)
-        self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        self.n_pages, self.page_size = _int32(n_pages, "n_pages"), _int32(page_size, "page_size")
+        self.n_kv_heads, self.head_dim = _int32(n_kv_heads, "n_kv_heads"), _int32(head_dim, "head_dim")
         self.c = SnCache(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, code, _CODES[codes])
         probe = SnCache.from_buffer_copy(self.c)
         probe.n_sequences = probe.max_pages = 1
@@ -889,15 +907,15 @@ class CacheRows:
         self.cache, self.dtype, self.device = cache, cache.dtype, cache.device
         rp, most = _ragged(row_ptr, "row_ptr")
         self.row_ptr = torch.from_numpy(rp).to(self.device)
-        self.n_sequences, self.n_rows, self.max_pages = rp.size - 1, int(rp[-1]), int(max_pages)
-        self.n_heads = cache.n_kv_heads if n_heads is None else int(n_heads)
+        self.n_sequences, self.n_rows, self.max_pages = rp.size - 1, int(rp[-1]), _int32(max_pages, "max_pages")
+        self.n_heads = cache.n_kv_heads if n_heads is None else _int32(n_heads, "n_heads")
         self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-        if not np.isfinite(self.scale):
-            raise ValueError(f"scale must be finite, not {scale}")
+        if not abs(self.scale) <= float(np.finfo(np.float32).max):
+            raise ValueError(f"scale must be finite in 32 bits, not {scale}")
         self.c = SnCache.from_buffer_copy(cache.c)
         self.c.n_sequences, self.c.n_rows, self.c.max_rows, self.c.max_pages = self.n_sequences, self.n_rows, most, self.max_pages
         self.c.row_ptr = _ptr(self.row_ptr)
-        self.c.n_heads, self.c.scale, self.c.causal, self.c.window = self.n_heads, self.scale, int(bool(causal)), int(window)
+        self.c.n_heads, self.c.scale, self.c.causal, self.c.window = self.n_heads, self.scale, int(bool(causal)), _int32(window, "window")
         self.workspace_bytes = int(lib().sn_cache_workspace_bytes(ctypes.byref(self.c)))
         if self.workspace_bytes == 0:
             raise SnError(SN_ERR_INVALID, "sn_cache")
