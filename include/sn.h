@@ -571,9 +571,11 @@ sn_status sn_cache_read(const sn_cache *op, void *k_out, void *v_out, void *ws, 
  * keys j that the row sees,
  *     s = scale q.k_j,  p = exp(s) / sum of exp(s),  o = sum of p v_j
  * with o [n_rows][H][D] and lse [n_rows][H] (may be NULL), the logarithm of the
- * sum of exp(s).  Scores have to stay within fp32: a row with an infinite one is
- * not a number, as the formulas have it.  A row that sees no key gives o = 0 and lse = -inf.  Keys that
- * it does not see reach nothing, whatever they hold.  A long sequence is split
+ * sum of exp(s).  Scores have to stay within fp32; infinite ones give what the
+ * formulas give: a row that has +inf or NaN is not a number, a key of -inf has no
+ * weight, and a row that sees no other is not a number with lse = -inf.  A row that
+ * sees no key gives o = 0 and lse = -inf.  Keys that it does not see reach nothing,
+ * whatever they hold.  A long sequence is split
  * over its length and joined; scores, weights, sums and joins are fp32. */
 sn_status sn_cache_attend(const sn_cache *op, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
 

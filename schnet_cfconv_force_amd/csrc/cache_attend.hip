@@ -800,7 +800,7 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
             parts.ml[(int64_t)slot * 16 * F::NR + r] = make_float2(m, l);
         } else if (lse) {
             const int row = tile * 16 * F::NR + r, t = row / a.G, h = hk * a.G + row % a.G;
-            lse[(int64_t)(s.r0 + t) * a.H + h] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+            lse[(int64_t)(s.r0 + t) * a.H + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;      // no key: -inf and the log of 0
         }
     };
     for (int i = threadIdx.x; i < rows * F::DP; i += kThreads) {
@@ -814,15 +814,28 @@ __device__ inline void piece(const CacheArgs &a, const AttendCut &c, int b, cons
         }
         if (d < a.D || slot >= 0) put(r, d, v);
     }
-    if ((int)threadIdx.x < rows) put_stats(threadIdx.x, x.stats[threadIdx.x][0], x.stats[threadIdx.x][1]);
+    if ((int)threadIdx.x < rows) {
+        const int r = threadIdx.x, t = (tile * 16 * F::NR + r) / a.G;
+        put_stats(r, x.stats[r][0], x.stats[r][1]);
+        // keys to see and no score above -inf
+        if (x.stats[r][0] == -INFINITY && max(first_of(t), w.key0) < min(last_of(t), w.end)) {
+            x.odd[r] = 1;
+            x.any = 1;
+        }
+    }
     __syncthreads();
     if (!x.any) return;
     for (int r = 0; r < rows; ++r) {
         if (!x.odd[r]) continue;
         const int row = tile * 16 * F::NR + r, t = row / a.G, h = hk * a.G + row % a.G;
         float m, l;
-        const float v = plain_row<F>(a, b, hk, (s.r0 + t) * a.qs + h * a.qh, max(first_of(t), w.key0), min(last_of(t), w.end),
-                                     scale2, x.plain, m, l);
+        float v = plain_row<F>(a, b, hk, (s.r0 + t) * a.qs + h * a.qh, max(first_of(t), w.key0), min(last_of(t), w.end),
+                               scale2, x.plain, m, l);
+        // every score of the piece is -inf: no weight beside other pieces; the join knows the row by its sum if there are none
+        if (slot >= 0 && m == -INFINITY && l == 0.0f && v != v) {
+            v = 0.0f;
+            l = 1.0f;
+        }
         if ((int)threadIdx.x < a.D) put(r, threadIdx.x, v);
         if (threadIdx.x == 0) put_stats(r, m, l);
         __syncthreads();
@@ -942,14 +955,14 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(CacheArgs a, 
         }
         if (!has || part > 0) continue;
         const int row = tile * R + r, t = row / a.G, h = hk * a.G + row % a.G;
+        if (sums[r][0] == -INFINITY && sums[r][1] > 0.0f) v = floatx4{NAN, NAN, NAN, NAN};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int d = quad * 4 % F::DP + e;
             if (d < a.D) o[((int64_t)(s.r0 + t) * a.H + h) * a.D + d] = (typename F::T)v[e];
         }
         if (lse && quad * 4 % F::DP == 0)
-            lse[(int64_t)(s.r0 + t) * a.H + h] =
-                sums[r][0] == -INFINITY ? -INFINITY : (sums[r][0] + __builtin_amdgcn_logf(sums[r][1])) * kLn2;
+            lse[(int64_t)(s.r0 + t) * a.H + h] = (sums[r][0] + __builtin_amdgcn_logf(sums[r][1])) * kLn2;
     }
 }
 

@@ -68,3 +68,41 @@ def test_rotary_elements_that_do_not_turn_keep_to_themselves(sn, dim, pairs, dty
             for h in range(t.shape[1]):
                 t[r + 4 * i, h, 2 * pairs + (3 * r + 5 * h) % (dim - 2 * pairs)] = value
     rotary_check(sn, case, interleaved, norm, dtype)
+
+
+# ------------------------------------------------------------------ scores that are not finite
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("dim,heads,spare", [(32, 6, 2), (32, 6, 4000), (128, 36, 2)])
+def test_attend_rows_of_infinite_scores(sn, dim, heads, spare, what, dtype, codes):
+    """Rows all of whose scores are NaN or one infinity: the row is not a number, and its lse is what the formula gives."""
+    print(f"[attend] scores {dim} {heads} {spare} {what} {dtype} {codes}", flush=True)
+    c = cache_case(sn, [2, 1, 3], [40, 300, 70], 2, dim, 16, dtype, codes, 91, heads=heads, spare=spare)
+    c["rows"] = [x.clone() for x in c["rows"]]
+    c["rows"][0][..., 5] = c["rows"][0][..., 5].abs() + 0.5
+    sn.cache_write(c["whole"], *c["rows"], c["table"], c["lengths"], c["ws"])
+    for row, head in ((0, 0), (1, heads - 1), (2, 3), (5, 1)):
+        c["q"][row, head, 5] = float(what)
+    attend_check(sn, c)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attend_keys_of_minus_infinity_have_no_weight(sn, dtype):
+    """Most of a long history scores -inf, whole pieces of it: the rest alone counts."""
+    import torch
+    c = cache_case(sn, [1, 2], [5000, 900], 1, 32, 16, dtype, None, 92, heads=3, spare=4000)
+    plain = c["q"].clone()
+    c["rows"] = [x.clone() for x in c["rows"]]
+    low = torch.cat([torch.arange(5000) < 4100, torch.arange(900) < 300]).cuda()
+    plain[..., 5], c["q"][..., 5] = 0.0, 1e30
+    c["rows"][0][..., 5] = 0.0
+    c["rows"][0][low, :, 5] = -1e30
+    sn.cache_write(c["whole"], *c["rows"], c["table"], c["lengths"], c["ws"])
+    o, lse = sn.cache_attend(c["plan"], c["q"], c["table"], c["lengths"], c["ws"], save=True)
+    assert sn.read_status(c["ws"]) == sn.SN_OK
+    absent = [low[:5000].cpu().numpy(), low[5000:].cpu().numpy()]
+    ref, factor = R.attend(plain, *kept_rows(c), c["row_ptr"], c["held"], c["plan"].scale, absent=absent)
+    R.check("o", o, ref["o"], factor, dtype == "bfloat16")
+    R.check("lse", lse, ref["lse"], 16 * R.U32)
