@@ -542,7 +542,7 @@ typedef struct sn_cache {
     void *k, *v;                 /* device [n_pages][n_kv_heads][page_size][SN_CACHE_ROW(D)], 16-byte aligned */
     float *k_scale, *v_scale;    /* device [n_pages][n_kv_heads][page_size], 16-byte aligned (with codes) */
     int32_t n_sequences;         /* B, 1 .. 65535 */
-    int32_t n_rows, max_rows;    /* the call's rows: of all sequences, of the one with the most */
+    int32_t n_rows, max_rows;    /* the call's rows: of all sequences (times n_kv_heads below 2^31), of the one with the most */
     int32_t max_pages;           /* entries of a sequence in the table, >= 1; times page_size at most 2^30 */
     const int32_t *row_ptr;      /* device [B+1] */
     const int32_t *table;        /* device [B][max_pages], contiguous */
@@ -556,7 +556,13 @@ typedef struct sn_cache {
     int64_t q_stride, q_head_stride;
 } sn_cache;
 
-/* Bytes of workspace of the calls below (host; sizes only). */
+/* Bytes of workspace of the calls below (host; sizes only); 0 for sizes that all
+ * would refuse.  Writes and reads take any sizes of the structure.  An attention's
+ * launch has a place for the rows of the sequence with the most in every sequence:
+ * it is refused (SN_ERR_INVALID) where n_rows n_heads is 2^31 or more or
+ *     n_sequences n_kv_heads ceil(max_rows n_heads / (16 n_kv_heads))
+ * is 2^23 - 8 or more (8192 rows of 32 heads beside 511 single ones); the bytes
+ * are those of writes and reads then, 256. */
 size_t sn_cache_workspace_bytes(const sn_cache *op);
 
 /* Writes the rows k and v [n_rows][n_kv_heads][D] (op->dtype, any strides) to

@@ -899,7 +899,8 @@ class CacheRows:
     row_ptr: host row offsets [B + 1]; the rows of sequence b are its last ones, at positions lengths[b] - count on.
     max_pages: entries of a sequence in the page table.  For cache_attend: n_heads (default: the cache's), scale
     (default 1 / sqrt(head_dim)), causal (a row sees the positions up to its own, else all) and window (> 0: only the
-    last `window` of them)."""
+    last `window` of them).  A plan of more rows than an attention's launch holds (sn_cache_workspace_bytes) writes and
+    reads alone."""
 
     def __init__(self, cache: StateCache, row_ptr, max_pages: int, n_heads=None, scale=None, causal: bool = True,
                  window: int = 0):

@@ -26,6 +26,10 @@ struct CacheRowsIO {
 // 385; 8 x <= 2000, 42 MB: 35 -> 41).
 constexpr int64_t kPast = 128 << 20;
 
+// A launch has a place for the longest sequence's rows in every sequence.  Beyond
+// this many blocks, most of them empty, a block takes several chunks in turn.
+constexpr int kBlocks = 1 << 22;
+
 // How rows are cut (host).  An item is a row of a head, of k or of v; a block
 // takes chunk_rows rows' items in order, its groups one each in turn.
 struct CacheCut {
@@ -115,51 +119,53 @@ template <typename T, int CODES>
 __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheArgs a, CacheRowsIO io, CacheCut c) {
     int r0, n, length;
     sequence_rows(a, blockIdx.y, true, r0, n, length);
-    const int first = blockIdx.x * c.chunk_rows, rows = min(c.chunk_rows, n - first), heads = 2 * a.Hkv;
-    if (rows <= 0) return;
+    const int heads = 2 * a.Hkv;
     const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
-    Item at{group / heads, group % heads};
     const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
-    while (at.row < rows) {
-        Item item[kItems];
-        Raw<T> raw[kItems];
-        int page[kItems];
+    for (int64_t chunk = (int64_t)blockIdx.x * c.chunk_rows; chunk < n; chunk += (int64_t)gridDim.x * c.chunk_rows) {
+        const int first = (int)chunk, rows = min(c.chunk_rows, n - first);
+        Item at{group / heads, group % heads};
+        while (at.row < rows) {
+            Item item[kItems];
+            Raw<T> raw[kItems];
+            int page[kItems];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            item[i] = at;
-            at.next(c, heads);
-            const bool has = item[i].row < rows, is_v = item[i].head >= a.Hkv;
-            const int h = item[i].head - (is_v ? a.Hkv : 0), row = first + item[i].row;
-            raw[i].load(static_cast<const T *>(io.x[is_v]) + (r0 + row) * io.xs[is_v] + h * io.xh[is_v], d, a.D, io.vec, has);
-            page[i] = has ? table[(length - n + row) >> a.page_shift] : 0;
-        }
+            for (int i = 0; i < kItems; ++i) {
+                item[i] = at;
+                at.next(c, heads);
+                const bool has = item[i].row < rows, is_v = item[i].head >= a.Hkv;
+                const int h = item[i].head - (is_v ? a.Hkv : 0), row = first + item[i].row;
+                raw[i].load(static_cast<const T *>(io.x[is_v]) + (r0 + row) * io.xs[is_v] + h * io.xh[is_v], d, a.D, io.vec, has);
+                page[i] = has ? table[(length - n + row) >> a.page_shift] : 0;
+            }
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const bool is_v = item[i].head >= a.Hkv;
-            const int h = item[i].head - (is_v ? a.Hkv : 0), pos = length - n + first + item[i].row;
-            if (item[i].row >= rows) break;
-            const bool ok = (uint32_t)page[i] < (uint32_t)a.n_pages;
-            if (!ok && lane == 0) flag_status(a.status, SN_ERR_INVALID);
-            const int64_t place = (((int64_t)page[i] * a.Hkv + h) << a.page_shift) + (pos & (a.page - 1));
-            if constexpr (CODES == SN_CODES_NONE) {
-                if (ok) raw[i].store(static_cast<T *>(is_v ? a.v : a.k) + place * a.Dp, d, a.Dp, true, c.past);
-            } else {
-                float x[8];
-                raw[i].get(x);
-                // magnitudes compared as bits: a NaN is above an infinity is above all else
-                uint32_t top = 0;
+            for (int i = 0; i < kItems; ++i) {
+                const bool is_v = item[i].head >= a.Hkv;
+                const int h = item[i].head - (is_v ? a.Hkv : 0), pos = length - n + first + item[i].row;
+                if (item[i].row >= rows) break;
+                const bool ok = (uint32_t)page[i] < (uint32_t)a.n_pages;
+                if (!ok && lane == 0) flag_status(a.status, SN_ERR_INVALID);
+                const int64_t place = (((int64_t)page[i] * a.Hkv + h) << a.page_shift) + (pos & (a.page - 1));
+                if constexpr (CODES == SN_CODES_NONE) {
+                    if (ok) raw[i].store(static_cast<T *>(is_v ? a.v : a.k) + place * a.Dp, d, a.Dp, true, c.past);
+                } else {
+                    float x[8];
+                    raw[i].get(x);
+                    // magnitudes compared as bits: a NaN is above an infinity is above all else
+                    uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-                top = group_max(top, c.lane_bits);
-                constexpr float kTop = CODES == SN_CODES_INT8 ? 127.0f : 448.0f;
-                const float amax = __uint_as_float(top);
-                const bool bad = top >= 0x7f800000u, live = !bad && amax >= 0x1p-100f;
-                const float scale = bad ? __uint_as_float(0x7fc00000u) : live ? amax / kTop : 0.0f;
-                uint2 codes = {0, 0};
-                if (live) codes = encode8<CODES>(x, kTop / amax);
-                if (ok && d < a.Dp) {
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? a.v : a.k) + place * a.Dp + d) = codes;
-                    if (lane == 0) (is_v ? a.v_scale : a.k_scale)[place] = scale;
+                    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+                    top = group_max(top, c.lane_bits);
+                    constexpr float kTop = CODES == SN_CODES_INT8 ? 127.0f : 448.0f;
+                    const float amax = __uint_as_float(top);
+                    const bool bad = top >= 0x7f800000u, live = !bad && amax >= 0x1p-100f;
+                    const float scale = bad ? __uint_as_float(0x7fc00000u) : live ? amax / kTop : 0.0f;
+                    uint2 codes = {0, 0};
+                    if (live) codes = encode8<CODES>(x, kTop / amax);
+                    if (ok && d < a.Dp) {
+                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? a.v : a.k) + place * a.Dp + d) = codes;
+                        if (lane == 0) (is_v ? a.v_scale : a.k_scale)[place] = scale;
+                    }
                 }
             }
         }
@@ -170,53 +176,55 @@ template <typename T, int CODES>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheArgs a, CacheRowsIO io, CacheCut c) {
     int r0, n, length;
     sequence_rows(a, blockIdx.y, true, r0, n, length);
-    const int first = blockIdx.x * c.chunk_rows, rows = min(c.chunk_rows, n - first), heads = 2 * a.Hkv;
-    if (rows <= 0) return;
+    const int heads = 2 * a.Hkv;
     const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
-    Item at{group / heads, group % heads};
     const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
-    while (at.row < rows) {
-        Item item[kItems];
-        int page[kItems];
+    for (int64_t chunk = (int64_t)blockIdx.x * c.chunk_rows; chunk < n; chunk += (int64_t)gridDim.x * c.chunk_rows) {
+        const int first = (int)chunk, rows = min(c.chunk_rows, n - first);
+        Item at{group / heads, group % heads};
+        while (at.row < rows) {
+            Item item[kItems];
+            int page[kItems];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            item[i] = at;
-            at.next(c, heads);
-            page[i] = item[i].row < rows ? table[(length - n + first + item[i].row) >> a.page_shift] : -1;
-        }
-        Raw<T> raw[kItems];
-        uint2 codes[kItems];
-        float scale[kItems];
+            for (int i = 0; i < kItems; ++i) {
+                item[i] = at;
+                at.next(c, heads);
+                page[i] = item[i].row < rows ? table[(length - n + first + item[i].row) >> a.page_shift] : -1;
+            }
+            Raw<T> raw[kItems];
+            uint2 codes[kItems];
+            float scale[kItems];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const bool is_v = item[i].head >= a.Hkv, ok = (uint32_t)page[i] < (uint32_t)a.n_pages;
-            const int h = item[i].head - (is_v ? a.Hkv : 0), pos = length - n + first + item[i].row;
-            const int64_t place = (((int64_t)(ok ? page[i] : 0) * a.Hkv + h) << a.page_shift) + (pos & (a.page - 1));
-            if (!ok && item[i].row < rows && lane == 0) flag_status(a.status, SN_ERR_INVALID);
-            if constexpr (CODES == SN_CODES_NONE) {
-                raw[i].load(static_cast<const T *>(is_v ? a.v : a.k) + place * a.Dp, d, a.Dp, true, ok);
-            } else {
-                codes[i] = uint2{0, 0};
-                scale[i] = 0.0f;
-                if (ok && d < a.Dp) {
-                    codes[i] = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(is_v ? a.v : a.k) + place * a.Dp + d);
-                    scale[i] = (is_v ? a.v_scale : a.k_scale)[place];
+            for (int i = 0; i < kItems; ++i) {
+                const bool is_v = item[i].head >= a.Hkv, ok = (uint32_t)page[i] < (uint32_t)a.n_pages;
+                const int h = item[i].head - (is_v ? a.Hkv : 0), pos = length - n + first + item[i].row;
+                const int64_t place = (((int64_t)(ok ? page[i] : 0) * a.Hkv + h) << a.page_shift) + (pos & (a.page - 1));
+                if (!ok && item[i].row < rows && lane == 0) flag_status(a.status, SN_ERR_INVALID);
+                if constexpr (CODES == SN_CODES_NONE) {
+                    raw[i].load(static_cast<const T *>(is_v ? a.v : a.k) + place * a.Dp, d, a.Dp, true, ok);
+                } else {
+                    codes[i] = uint2{0, 0};
+                    scale[i] = 0.0f;
+                    if (ok && d < a.Dp) {
+                        codes[i] = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(is_v ? a.v : a.k) + place * a.Dp + d);
+                        scale[i] = (is_v ? a.v_scale : a.k_scale)[place];
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            if (item[i].row >= rows) break;
-            const bool is_v = item[i].head >= a.Hkv;
-            const int h = item[i].head - (is_v ? a.Hkv : 0);
-            if constexpr (CODES != SN_CODES_NONE) {
-                float x[8];
-                decode8<CODES>(codes[i], x);
+            for (int i = 0; i < kItems; ++i) {
+                if (item[i].row >= rows) break;
+                const bool is_v = item[i].head >= a.Hkv;
+                const int h = item[i].head - (is_v ? a.Hkv : 0);
+                if constexpr (CODES != SN_CODES_NONE) {
+                    float x[8];
+                    decode8<CODES>(codes[i], x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= scale[i];
-                raw[i].set(x);
+                    for (int j = 0; j < 8; ++j) x[j] *= scale[i];
+                    raw[i].set(x);
+                }
+                raw[i].store(static_cast<T *>(io.out[is_v]) + ((int64_t)(r0 + first + item[i].row) * a.Hkv + h) * a.D, d, a.D, io.vec, c.past);
             }
-            raw[i].store(static_cast<T *>(io.out[is_v]) + ((int64_t)(r0 + first + item[i].row) * a.Hkv + h) * a.D, d, a.D, io.vec, c.past);
         }
     }
 }
@@ -231,7 +239,8 @@ sn_status launch(const CacheArgs &a, const CacheRowsIO &io, bool write, hipStrea
     c.step_head = groups % heads;
     c.chunk_rows = std::max(1, kItems * groups / heads);
     c.past = (int64_t)a.n_rows * heads * a.D * (int64_t)sizeof(T) > kPast;
-    const dim3 grid((a.max_rows + c.chunk_rows - 1) / c.chunk_rows, a.B);
+    const int chunks = (int)(((int64_t)a.max_rows + c.chunk_rows - 1) / c.chunk_rows);
+    const dim3 grid(std::min(chunks, kBlocks / a.B), a.B);
     ProfScope prof(write ? K_CACHE_WRITE : K_CACHE_READ, s);
     if (write)
         cache_write_kernel<T, CODES><<<grid, kThreads, 0, s>>>(a, io, c);
@@ -252,11 +261,6 @@ bool rows_vec(const CacheArgs &a, int dtype, const void *p, int64_t s, int64_t h
 }
 
 }  // namespace
-
-bool cache_fits(const sn_cache &op) {
-    // one row a block at the least
-    return op.n_sequences <= 65535 && grid_fits((int64_t)op.max_rows * op.n_sequences, kThreads);
-}
 
 sn_status cache_write(const CacheArgs &a, int dtype, int codes, const void *k, int64_t ks, int64_t kh, const void *v,
                       int64_t vs, int64_t vh, hipStream_t s) {

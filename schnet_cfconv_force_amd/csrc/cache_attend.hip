@@ -1073,8 +1073,9 @@ sn_status launch(const CacheArgs &a, int codes, void *o, float *lse, char *ws, h
 
 }  // namespace
 
-// Units are blocks of their own, or of the join.
+// Rows with their heads are counted in 32 bits; units are blocks of their own, or of the join.
 bool attend_fits(const sn_cache &op) {
+    if ((int64_t)op.n_rows * op.n_heads > INT32_MAX) return false;
     const AttendCut c = cut_of(op.n_kv_heads, rows_of(op.max_rows, op.n_heads / op.n_kv_heads), 1);
     return grid_fits((int64_t)op.n_sequences * c.units + kXcds, kThreads);
 }

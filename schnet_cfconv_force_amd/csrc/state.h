@@ -88,7 +88,6 @@ __device__ inline int page_of(const CacheArgs &a, int b, int p) {
     return -1;
 }
 
-bool cache_fits(const sn_cache &op);
 bool attend_fits(const sn_cache &op);
 size_t attend_workspace(const sn_cache &op);
 sn_status cache_write(const CacheArgs &a, int dtype, int codes, const void *k, int64_t ks, int64_t kh, const void *v,

@@ -72,19 +72,18 @@ sn_status check_cache_sizes(const sn_cache *op) {
     if (op->head_dim < 1 || op->head_dim > SN_MAX_HEAD_DIM) return SN_ERR_INVALID;
     if (op->dtype != SN_F32 && op->dtype != SN_BF16) return SN_ERR_INVALID;
     if (op->codes < SN_CODES_NONE || op->codes > SN_CODES_E4M3) return SN_ERR_INVALID;
-    if (op->n_sequences < 1 || op->n_rows < 0 || op->max_rows < 0 || op->max_rows > op->n_rows) return SN_ERR_INVALID;
+    if (op->n_sequences < 1 || op->n_sequences > 65535 || op->n_rows < 0 || op->max_rows < 0 || op->max_rows > op->n_rows) return SN_ERR_INVALID;
     if ((int64_t)op->max_rows * op->n_sequences < op->n_rows) return SN_ERR_INVALID;
     // positions, with a tile behind the last, and rows with their heads are counted in 32 bits
     if (op->max_pages < 1 || (int64_t)op->max_pages * op->page_size > (1 << 30)) return SN_ERR_INVALID;
-    if ((int64_t)op->n_rows * op->n_kv_heads > INT32_MAX) return SN_ERR_INVALID;
-    return cache_fits(*op) ? SN_OK : SN_ERR_INVALID;
+    return (int64_t)op->n_rows * op->n_kv_heads <= INT32_MAX ? SN_OK : SN_ERR_INVALID;
 }
 
-sn_status check_attend_sizes(const sn_cache *op) {
+// What an attention needs besides; whether its launch holds the rows is attend_fits.
+sn_status check_attend(const sn_cache *op) {
     if (op->n_heads < 1 || op->n_heads > 65535 || op->n_heads % op->n_kv_heads != 0) return SN_ERR_INVALID;
-    if ((int64_t)op->n_rows * op->n_heads > INT32_MAX) return SN_ERR_INVALID;
     if ((op->causal & ~1) != 0 || op->window < 0 || (op->window > 0 && !op->causal)) return SN_ERR_INVALID;
-    return attend_fits(*op) ? SN_OK : SN_ERR_INVALID;
+    return SN_OK;
 }
 
 sn_status check_cache(const sn_cache *op) {
@@ -172,8 +171,8 @@ sn_status sn_head_rotary_backward(const sn_head_rotary *op, const void *d_q, int
 }
 
 size_t sn_cache_workspace_bytes(const sn_cache *op) {
-    if (check_cache_sizes(op) != SN_OK || check_attend_sizes(op) != SN_OK) return 0;
-    return attend_workspace(*op);
+    if (check_cache_sizes(op) != SN_OK || check_attend(op) != SN_OK) return 0;
+    return attend_fits(*op) ? attend_workspace(*op) : kWsBase;
 }
 
 sn_status sn_cache_write(const sn_cache *op, const void *k, int64_t k_stride, int64_t k_head_stride, const void *v,
@@ -196,8 +195,8 @@ sn_status sn_cache_read(const sn_cache *op, void *k_out, void *v_out, void *ws, 
 
 sn_status sn_cache_attend(const sn_cache *op, void *o, float *lse, void *ws, size_t ws_bytes, void *stream) {
     SN_TRY(check_cache(op));
-    SN_TRY(check_attend_sizes(op));
-    if (!std::isfinite(op->scale)) return SN_ERR_INVALID;
+    SN_TRY(check_attend(op));
+    if (!attend_fits(*op) || !std::isfinite(op->scale)) return SN_ERR_INVALID;
     SN_TRY(check_ws(ws, ws_bytes, attend_workspace(*op)));
     if (op->n_rows == 0) return SN_OK;
     if (!op->q || !o || !aligned_for(op->q, op->dtype) || !aligned_for(o, op->dtype) || !aligned_for(lse, SN_F32))

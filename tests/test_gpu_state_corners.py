@@ -106,3 +106,29 @@ def test_attend_keys_of_minus_infinity_have_no_weight(sn, dtype):
     ref, factor = R.attend(plain, *kept_rows(c), c["row_ptr"], c["held"], c["plan"].scale, absent=absent)
     R.check("o", o, ref["o"], factor, dtype == "bfloat16")
     R.check("lse", lse, ref["lse"], 16 * R.U32)
+
+
+# ------------------------------------------------------------------ many rows beside few
+
+@pytest.mark.parametrize("codes", [None, "int8"])
+@pytest.mark.parametrize("batch,longest", [(256, 65600), (65535, 20011)])
+def test_rows_of_one_long_sequence_beside_many_short_ones(sn, batch, longest, codes):
+    """More places of rows than a launch has blocks, of which most hold nothing."""
+    import torch
+    print(f"[cache] ragged {batch} {longest} {codes}", flush=True)
+    counts = np.zeros(batch, np.int64)
+    counts[::7] = 1
+    counts[batch // 2], counts[-1] = longest, 300
+    need = -(-counts // 1024)
+    table = np.full((batch, int(need.max())), -1, np.int32)
+    table[np.arange(table.shape[1]) < need[:, None]] = np.random.default_rng(5).permutation(int(need.sum()))
+    cache = sn.StateCache(int(need.sum()), 1024, 1, 16, codes=codes)
+    plan = sn.CacheRows(cache, np.concatenate([[0], np.cumsum(counts)]), table.shape[1])
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    rows = [normal(gen, int(counts.sum()), 1, 16, to=torch.float32) for _ in range(2)]
+    table, lengths, ws = torch.from_numpy(table).cuda(), torch.from_numpy(counts.astype(np.int32)).cuda(), sn.cache_workspace(plan)
+    sn.cache_write(plan, *rows, table, lengths, ws)
+    back = sn.cache_read(plan, table, lengths, ws)
+    assert sn.read_status(ws) == sn.SN_OK
+    for x, got in zip(rows, back):
+        assert torch.equal(got.cpu(), R.held(x, codes).float())

@@ -1,4 +1,5 @@
 """CPU: sizes at the ends of what the plans of the rotation, the state cache and the context operators hold."""
+import ctypes
 import math
 import os
 
@@ -52,3 +53,31 @@ def test_windows_and_scales_at_the_ends_of_32_bits():
     for scale in (1e39, -1e39, math.nan):
         with pytest.raises(ValueError):
             sn.CacheRows(cache, [0, 1], 4, scale=scale)
+
+
+# ------------------------------------------------------------------ many rows
+
+def test_plans_of_more_rows_than_an_attention_holds_write_and_read():
+    """Their workspace is the status words alone, and an attention is refused before any GPU work."""
+    sn = _sn()
+    lib, S = sn.lib(), sn.binding.SnCache
+
+    def desc(B, n_rows, max_rows, max_pages, n_heads=4):
+        return S(9, 1024, 2, 32, sn.SN_BF16, sn.SN_CODES_INT8, 256, 256, 256, 256, B, n_rows, max_rows, max_pages, 256, 256, 256, n_heads,
+                 0.5, 1, 0, 256, 128, 32)
+
+    for d in (desc(32, 32 * 65536, 65536, 64, 64), desc(256, 65536 + 255, 65536, 64, 512), desc(65535, 65536, 65536, 64),
+              desc(1, 2 ** 29, 2 ** 29, 2 ** 19), desc(1, 2 ** 28, 2 ** 28, 2 ** 18, 8)):
+        assert lib.sn_cache_workspace_bytes(ctypes.byref(d)) == 256
+        assert lib.sn_cache_attend(ctypes.byref(d), 256, None, 256, 1 << 40, None) == sn.SN_ERR_INVALID
+        # past the sizes, to the rows' addresses
+        assert lib.sn_cache_write(ctypes.byref(d), None, 64, 32, 256, 64, 32, 256, 256, None) == sn.SN_ERR_INVALID
+        assert lib.sn_cache_read(ctypes.byref(d), None, 256, 256, 255, None) == sn.SN_ERR_WORKSPACE
+    # the largest that an attention's launch holds, and the next
+    assert lib.sn_cache_workspace_bytes(ctypes.byref(desc(2, 8 * 2 ** 18, 8 * 2 ** 18 - 16, 2 ** 11))) > 256
+    for B, max_rows, held in ((1, 2 ** 25 - 40, True), (1, 2 ** 25 - 24, False)):
+        d = desc(B, max_rows, max_rows, 2 ** 15)
+        assert (lib.sn_cache_workspace_bytes(ctypes.byref(d)) > 256) == held
+    cache = sn.StateCache(4, 1024, 2, 32, device="cpu")
+    plan = sn.CacheRows(cache, np.concatenate([[0], np.full(256, 65536)]).cumsum()[:33], 64, n_heads=64)
+    assert plan.workspace_bytes == 256
