@@ -118,7 +118,7 @@ __device__ inline uint32_t group_max(uint32_t v, int bits) {
 template <typename T, int CODES>
 __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheArgs a, CacheRowsIO io, CacheCut c) {
     int r0, n, length;
-    sequence_rows(a, blockIdx.y, true, r0, n, length);
+    sequence_rows(a, blockIdx.y, r0, n, length);
     const int heads = 2 * a.Hkv;
     const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
     const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheArgs a, Cach
 template <typename T, int CODES>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheArgs a, CacheRowsIO io, CacheCut c) {
     int r0, n, length;
-    sequence_rows(a, blockIdx.y, true, r0, n, length);
+    sequence_rows(a, blockIdx.y, r0, n, length);
     const int heads = 2 * a.Hkv;
     const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
     const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;

@@ -68,24 +68,16 @@ struct CacheArgs {
 };
 
 // Rows of sequence b in the call (r0, n) and its length, or n = 0 where the
-// device arrays contradict the sizes.  same: every row has a place of its own.
-__device__ inline void sequence_rows(const CacheArgs &a, int b, bool same, int &r0, int &n, int &length) {
+// device arrays contradict the sizes: every row has a place of its own.
+__device__ inline void sequence_rows(const CacheArgs &a, int b, int &r0, int &n, int &length) {
     segment_rows(a.row_ptr, b, a.B, a.n_rows, a.max_rows, a.status, r0, n);
     const auto lengths = (const __attribute__((address_space(4))) int32_t *)(uintptr_t)a.lengths;
     length = lengths[b];
-    if (length < 0 || length > (int64_t)a.max_pages * a.page || (same && length < n)) {
+    if (length < 0 || length > (int64_t)a.max_pages * a.page || length < n) {
         if (n > 0 && threadIdx.x == 0) flag_status(a.status, SN_ERR_INVALID);
         n = 0;
         length = 0;
     }
-}
-
-// The page of position p of sequence b, or -1 (flagged) where there is none.
-__device__ inline int page_of(const CacheArgs &a, int b, int p) {
-    const int page = a.table[(int64_t)b * a.max_pages + (p >> a.page_shift)];
-    if (page >= 0 && page < a.n_pages) return page;
-    flag_status(a.status, SN_ERR_INVALID);
-    return -1;
 }
 
 bool attend_fits(const sn_cache &op);
@@ -96,8 +88,6 @@ sn_status cache_read(const CacheArgs &a, int dtype, int codes, void *k, void *v,
 sn_status cache_attend(const CacheArgs &a, int dtype, int codes, void *o, float *lse, char *ws, hipStream_t s);
 
 // --------------------------------------------------------------- codes
-
-typedef float floatx2v __attribute__((ext_vector_type(2)));
 
 __device__ inline float e4m3_value(uint8_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
 
