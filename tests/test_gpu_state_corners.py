@@ -132,3 +132,56 @@ def test_rows_of_one_long_sequence_beside_many_short_ones(sn, batch, longest, co
     assert sn.read_status(ws) == sn.SN_OK
     for x, got in zip(rows, back):
         assert torch.equal(got.cpu(), R.held(x, codes).float())
+
+
+# ------------------------------------------------------------------ cut histories of several row tiles
+
+def poisoned(sn, c, b, at):
+    """Values and keys of sequence b near its end that are no numbers: v NaN, k NaN and v infinite (codes hold rows of
+    those as NaN)."""
+    c["rows"] = [x.clone() for x in c["rows"]]
+    first = int(c["ptr"][b])
+    c["rows"][1][first + at[0], 0, 3] = math.nan
+    c["rows"][0][first + at[1], -1, 7] = math.nan
+    c["rows"][1][first + at[2], -1, 5] = math.inf
+    sn.cache_write(c["whole"], *c["rows"], c["table"], c["lengths"], c["ws"])
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("causal,odd", [(True, False), (True, True), (False, False)])
+def test_attend_ragged_prompts_over_shared_blocks(sn, causal, odd, dim, dtype, codes):
+    """A prompt of many row tiles (two a block, or one) beside single rows and none, in a table with room: sequences that
+    have fewer row tiles than the longest, on one line of tiles; also with values that some rows of a tile do not see."""
+    print(f"[attend] prompts {causal} {odd} {dim} {dtype} {codes}", flush=True)
+    new, held = [64, 1, 0, 5], [700, 300, 33, 70] if causal else [700, 0, 33, 3]
+    c = cache_case(sn, new, held, 2, dim, 16, dtype, codes, 101, heads=32, spare=4000, causal=causal)
+    if odd:
+        poisoned(sn, c, 0, (690, 696, 680))
+    attend_check(sn, c)
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("window,odd", [(0, False), (8000, False), (8000, True)])
+def test_attend_ragged_rows_over_long_histories(sn, window, odd, dim, dtype, codes):
+    """A few rows of shared heads, three row tiles of the longest: units cut anywhere, with a window and without."""
+    print(f"[attend] ragged {window} {odd} {dim} {dtype} {codes}", flush=True)
+    c = cache_case(sn, [5, 1, 0, 3], [9000, 100, 50, 8500], 2, dim, 16, dtype, codes, 102, heads=16, spare=40, window=window)
+    if odd:
+        poisoned(sn, c, 0, (8997, 8998, 8996))
+    attend_check(sn, c)
+
+
+@pytest.mark.parametrize("batch,longest,heads,dim,dtype,codes", [(1, 150000, 3, 32, "float32", None), (1, 150000, 2, 32, "float32", "int8"),
+                                                                 (1, 290000, 1, 32, "bfloat16", None), (256, 120000, 32, 64, "bfloat16", None),
+                                                                 (256, 120000, 32, 64, "bfloat16", "e4m3")])
+def test_attend_one_history_over_all_blocks(sn, batch, longest, heads, dim, dtype, codes):
+    """More pieces of a unit than the join takes at a time."""
+    print(f"[attend] pieces {batch} {longest} {heads} {dim} {dtype} {codes}", flush=True)
+    held = np.random.default_rng(103).integers(1, 40, batch)
+    held[batch // 3] = longest
+    c = cache_case(sn, np.ones(batch, np.int64), held, 1, dim, 16, dtype, codes, 103, heads=heads)
+    attend_check(sn, c)
