@@ -465,7 +465,7 @@ typedef struct sn_head_rotary {
     int32_t n_pairs;             /* 0 .. D / 2 */
     int32_t n_axes;              /* 1 .. SN_MAX_AXES (with pairs) */
     int32_t interleaved;         /* 0 or 1 */
-    const double *freqs;         /* host [n_pairs], finite: radians a position */
+    const double *freqs;         /* host [n_pairs], within +-2^52: radians a position */
     const int32_t *axes;         /* host [n_pairs], each in [0, n_axes) */
     const int32_t *positions;    /* device [n_axes][n_rows], contiguous (with pairs) */
     const void *q;               /* device [n_rows][n_heads][D] */
@@ -480,8 +480,8 @@ typedef struct sn_head_rotary {
  * Pairs are given to the axes in runs, sections[a] of them to axis a.  shared:
  * one ladder base^(-j/n) falls over all pairs; else every axis has its own,
  * base^(-j/sections[a]).  Writes n values each.  SN_ERR_INVALID unless
- * 1 <= n_axes <= SN_MAX_AXES, every section >= 1, n <= SN_MAX_HEAD_DIM / 2 and
- * base > 0 is finite. */
+ * 1 <= n_axes <= SN_MAX_AXES, every section >= 1, n <= SN_MAX_HEAD_DIM / 2,
+ * base > 0 is finite and every frequency is below 2^52. */
 sn_status sn_rotary_frequencies(int32_t n_axes, const int32_t *sections, double base, int32_t shared, double *freqs,
                                 int32_t *axes);
 

@@ -767,8 +767,8 @@ class HeadRotary:
         if self.axes.size != self.n_pairs:
             raise ValueError(f"{self.n_pairs} frequencies and {self.axes.size} axes")
         self.n_axes = int(self.axes.max()) + 1 if self.n_pairs else 0
-        if self.n_pairs and (self.axes.min() < 0 or not np.isfinite(self.freqs).all()):
-            raise ValueError("axes must not be negative, and frequencies have to be finite")
+        if self.n_pairs and (self.axes.min() < 0 or not (np.abs(self.freqs) < 2.0 ** 52).all()):
+            raise ValueError("axes must not be negative, and frequencies have to be within +-2^52")
         self.norm = bool(norm)
         if self.norm and not np.finfo(np.float32).tiny <= eps <= np.finfo(np.float32).max:
             raise ValueError(f"eps must be a positive normal number of 32 bits, not {eps}")

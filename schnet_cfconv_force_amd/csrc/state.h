@@ -25,6 +25,7 @@ __device__ inline void store_past(const V *v, V *p, bool past) {
 // --------------------------------------------------------------- rotation of heads
 
 constexpr int kMaxPairs = SN_MAX_HEAD_DIM / 2;
+constexpr double kMaxFrequency = 0x1p52;    // from here on fp64 holds no angle of any position
 
 struct RotaryTensor {
     const void *x, *dy;             // rows; gradients of the turned rows (backward)

@@ -40,7 +40,7 @@ sn_status check_rotary(const sn_head_rotary *op) {
         if (!op->freqs || !op->axes || (op->n_rows > 0 && !op->positions) || !aligned_for(op->positions, SN_F32))
             return SN_ERR_INVALID;
         for (int j = 0; j < op->n_pairs; ++j)
-            if (!std::isfinite(op->freqs[j]) || op->axes[j] < 0 || op->axes[j] >= op->n_axes) return SN_ERR_INVALID;
+            if (!(std::fabs(op->freqs[j]) < kMaxFrequency) || op->axes[j] < 0 || op->axes[j] >= op->n_axes) return SN_ERR_INVALID;
     }
     if (op->n_rows > 0 && (!op->q || (op->n_kv_heads > 0 && !op->k))) return SN_ERR_INVALID;
     if (!aligned_for(op->q, op->dtype) || !aligned_for(op->k, op->dtype) || !aligned_for(op->q_weight, SN_F32) ||
@@ -130,11 +130,18 @@ sn_status sn_rotary_frequencies(int32_t n_axes, const int32_t *sections, double 
         n += sections[a];
     }
     if (n > kMaxPairs) return SN_ERR_INVALID;
+    auto frequency = [&](int a, int i, int j) {
+        return shared ? std::pow(base, -(double)j / (double)n) : std::pow(base, -(double)i / sections[a]);
+    };
     int j = 0;
+    for (int a = 0; a < n_axes; ++a)        // a base far below 1 gives a rising ladder
+        for (int i = 0; i < sections[a]; ++i, ++j)
+            if (!(frequency(a, i, j) < kMaxFrequency)) return SN_ERR_INVALID;
+    j = 0;
     for (int a = 0; a < n_axes; ++a)
         for (int i = 0; i < sections[a]; ++i, ++j) {
             axes[j] = a;
-            freqs[j] = shared ? std::pow(base, -(double)j / (double)n) : std::pow(base, -(double)i / sections[a]);
+            freqs[j] = frequency(a, i, j);
         }
     return SN_OK;
 }

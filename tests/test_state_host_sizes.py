@@ -81,3 +81,26 @@ def test_plans_of_more_rows_than_an_attention_holds_write_and_read():
     cache = sn.StateCache(4, 1024, 2, 32, device="cpu")
     plan = sn.CacheRows(cache, np.concatenate([[0], np.full(256, 65536)]).cumsum()[:33], 64, n_heads=64)
     assert plan.workspace_bytes == 256
+
+
+# ------------------------------------------------------------------ frequencies
+
+def test_frequencies_whose_angles_fp64_does_not_hold_are_refused():
+    """A position times the largest finite numbers is infinite, and its sine not a number."""
+    sn = _sn()
+    lib, S = sn.lib(), sn.binding.SnHeadRotary
+    axes = np.zeros(1, np.int32)
+    for freq, fine in ((1e308, False), (-1e308, False), (2.0 ** 52, False), (2.0 ** 51, True)):
+        freqs = np.array([freq])
+        d = S(6, 4, 2, 32, sn.SN_BF16, 0, 1e-6, 1, 1, 0, freqs.ctypes.data, axes.ctypes.data, 256, 256, 256, 128, 32, 64, 32, None, None)
+        # behind the descriptor comes the workspace
+        assert lib.sn_head_rotary_forward(ctypes.byref(d), None, 256, 256, 0, None) == (sn.SN_ERR_WORKSPACE if fine else sn.SN_ERR_INVALID)
+        if fine:
+            sn.HeadRotary(6, 4, 32, freqs=freqs, device="cpu")
+        else:
+            with pytest.raises(ValueError):
+                sn.HeadRotary(6, 4, 32, freqs=freqs, device="cpu")
+    for base in (5e-324, 1e-300, 1e-20):
+        with pytest.raises(sn.SnError):
+            sn.rotary_frequencies([40], base)
+    assert np.allclose(sn.rotary_frequencies([4], 2.0 ** -8)[0], [1, 4, 16, 64])
