@@ -132,16 +132,19 @@ __device__ inline float group_sum(float v, int lanes) {
 }
 
 // Sines and cosines of a block's rows, in LDS: once for all heads.  Angles in
-// full turns are reduced in fp64; what is left is at most half a turn.  Pairs
-// that do not turn have an angle of zero.
+// full turns are reduced in fp64; what is left is at most half a turn, in fp32 with
+// its rounding as a small second turn.  Pairs that do not turn have an angle of zero.
 constexpr int kTable = 1024;
 __device__ inline void fill_table(const RotaryArgs &a, const RotaryCut &k, int row0, int rows, float2 *table) {
     for (int i = threadIdx.x; i < rows * k.width; i += kThreads) {
         const int r = i / k.width, j = i - r * k.width;
         float2 cs = make_float2(1.0f, 0.0f);
         if (j < a.P) {
-            const double turn = (double)a.positions[(int64_t)a.axes[j] * a.n_rows + row0 + r] * a.turns[j];
-            sincospif(2.0f * (float)(turn - rint(turn)), &cs.y, &cs.x);
+            const double turn = (double)a.positions[(int64_t)a.axes[j] * a.n_rows + row0 + r] * a.turns[j], part = turn - rint(turn);
+            const float near = (float)part, rest = (float)(2.0 * M_PI) * (float)(part - (double)near);
+            float sine, cosine;
+            sincospif(2.0f * near, &sine, &cosine);
+            cs = make_float2(fmaf(-sine, rest, cosine), fmaf(cosine, rest, sine));
         }
         table[i] = cs;
     }

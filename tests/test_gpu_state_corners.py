@@ -185,3 +185,26 @@ def test_attend_one_history_over_all_blocks(sn, batch, longest, heads, dim, dtyp
     held[batch // 3] = longest
     c = cache_case(sn, np.ones(batch, np.int64), held, 1, dim, 16, dtype, codes, 103, heads=heads)
     attend_check(sn, c)
+
+
+# ------------------------------------------------------------------ angles
+
+def test_rotary_sines_near_half_turns(sn):
+    """Rows (1, 0) turn to (cos t, sin t), t = -3000 .. 3000 radians: 355 and its multiples lie close to half turns, where a
+    sine is small and the angle's rounding to fp32 would show.
+
+    In u = 2^-24: sine and cosine 8 of their own value, the second turn's addition 1, and its part of the other one at most
+    2 of 2^-26 turns, 1e-14; the angle itself, in fp64, 2 roundings of 478 turns, 7e-13 radians."""
+    import torch
+    n = 6001
+    q = torch.zeros(n, 1, 2, device="cuda")
+    q[..., 0] = 1.0
+    at = torch.arange(-3000, 3001, dtype=torch.int32, device="cuda")
+    plan = sn.HeadRotary(n, 1, 2, freqs=[1.0], norm=False)
+    y, _ = sn.head_rotary_forward(plan, q, None, at[None], sn.head_rotary_workspace(plan))
+    t = at.cpu().double()
+    want = torch.stack([torch.cos(t), torch.sin(t)], -1)[:, None]
+    bound = 9 * R.U32 * want.abs() + 1e-12
+    worst = float(((y.cpu().double() - want).abs() / bound).max())
+    print(f"worst {worst:.3f} of the tolerance", flush=True)
+    assert worst <= 1
