@@ -35,6 +35,7 @@ constexpr int kBlocks = 1 << 22;
 struct CacheCut {
     int lane_bits;              // a group has 2^lane_bits lanes
     int chunk_rows;
+    uint32_t next_chunk;        // rows from a block's chunk to its next (a length is at most 2^30)
     int step_row, step_head;    // from one item of a group to the next (heads of k, then of v)
     bool past;                  // rows are stored past the caches
 };
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheArgs a, Cach
     const int heads = 2 * a.Hkv;
     const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
     const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
-    for (int64_t chunk = (int64_t)blockIdx.x * c.chunk_rows; chunk < n; chunk += (int64_t)gridDim.x * c.chunk_rows) {
+    for (uint32_t chunk = blockIdx.x * c.chunk_rows; chunk < (uint32_t)n; chunk += c.next_chunk) {
         const int first = (int)chunk, rows = min(c.chunk_rows, n - first);
         Item at{group / heads, group % heads};
         while (at.row < rows) {
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheArgs a, Cache
     const int heads = 2 * a.Hkv;
     const int lane = threadIdx.x & ((1 << c.lane_bits) - 1), d = lane * 8, group = threadIdx.x >> c.lane_bits;
     const int32_t *table = a.table + (int64_t)blockIdx.y * a.max_pages;
-    for (int64_t chunk = (int64_t)blockIdx.x * c.chunk_rows; chunk < n; chunk += (int64_t)gridDim.x * c.chunk_rows) {
+    for (uint32_t chunk = blockIdx.x * c.chunk_rows; chunk < (uint32_t)n; chunk += c.next_chunk) {
         const int first = (int)chunk, rows = min(c.chunk_rows, n - first);
         Item at{group / heads, group % heads};
         while (at.row < rows) {
@@ -241,6 +242,7 @@ sn_status launch(const CacheArgs &a, const CacheRowsIO &io, bool write, hipStrea
     c.past = (int64_t)a.n_rows * heads * a.D * (int64_t)sizeof(T) > kPast;
     const int chunks = (int)(((int64_t)a.max_rows + c.chunk_rows - 1) / c.chunk_rows);
     const dim3 grid(std::min(chunks, kBlocks / a.B), a.B);
+    c.next_chunk = grid.x * (uint32_t)c.chunk_rows;
     ProfScope prof(write ? K_CACHE_WRITE : K_CACHE_READ, s);
     if (write)
         cache_write_kernel<T, CODES><<<grid, kThreads, 0, s>>>(a, io, c);
