@@ -529,9 +529,11 @@ sn_status sn_head_rotary_backward(const sn_head_rotary *op, const void *d_q, int
  * than in an attention that is not causal) is skipped; a place whose page is not
  * in [0, n_pages) is not written, reads back as zeros, and is an absent key.
  * Entries of the table behind a sequence's length are not read.  What a call
- * takes depends on max_pages page_size, the most that a sequence can hold, a
- * little and on the lengths mostly: a table with room to spare costs nothing but
- * a second launch of sn_cache_attend. */
+ * takes goes by the lengths, and in sn_cache_attend by max_pages page_size, the
+ * most that a sequence can hold: from that it chooses whether histories are split
+ * (a second launch, some 4 us) and read past the caches.  Lengths far below it
+ * cost a little for that (16 x 4000 keys of 8 x 128, bf16: 47 us in a table for
+ * 4000, 67 in one for 8000, 52 in one for 32000), long ones nothing. */
 typedef struct sn_cache {
     int32_t n_pages;             /* >= 1 */
     int32_t page_size;           /* rows of a page: a power of two, 16 .. 1024 */

@@ -19,15 +19,17 @@
 // Every wavefront walks its own tiles with its own running maximum and sum
 // and joins the others' at the end of the piece.  The tiles of all units form
 // one line that is cut evenly over the blocks, wherever sequences end; a unit
-// that is cut leaves partial rows (fp32), which a second launch joins.
+// that is cut leaves partial rows (fp32), which a second launch joins.  (Every
+// sequence has as many units as the one with the most rows: those without rows
+// end at once, but their tiles are on the line.  8 x 20000 keys, 32/8 heads of
+// 128, bf16: 112 us for single rows, 272 where one sequence has 32.)
 //
 // Measured (one new row a sequence): 32 x <= 20000 keys, 32/8 heads of 128, bf16,
 // 1.65 GB: 262 us, 6.3 TB/s, where a copy reaches 5.2; the same in e4m3, 0.85 GB:
-// 153 us, 5.5 TB/s (without the conversions it takes as long, without the scales
-// 155 of 162 then: the memory bounds it).  Short histories are bound by a chain
-// of dependent reads (lengths, pages, keys) and by the rounds a wavefront takes:
-// 271 keys, 4 x 32 fp32: 6.7 us; 64 x <= 1076 keys, 8 x 16 int8 beside fp32 rows:
-// 15 us, half of it vector instructions.
+// 154 us, 5.5 TB/s.  Short histories are bound by a chain of dependent reads
+// (lengths, pages, keys) and by the rounds a wavefront takes: 271 keys, 4 x 32
+// fp32: 6.7 us; 64 x <= 1076 keys, 8 x 16 int8 beside fp32 rows: 15 us, half of it
+// vector instructions.
 #include <algorithm>
 #include <type_traits>
 
@@ -975,10 +977,10 @@ inline int64_t rows_of(int max_rows, int G) { return (int64_t)max_rows * G; }
 
 // Tiles of 16 rows for which a block reads the keys once.  Two halve what is
 // read, but their blocks are half as many and take a CU alone: 64 x 8 rows of
-// 32/8 heads over 1000 keys, bf16, 64: 39 us with one, 30 with two; 128: 56 and
-// 42; 8 x 16 rows over 500 keys, 128: 11.5 and 16.  Heads of 32 gain nothing
-// (19 and 20), and fp32 rows of 128 do not fit the registers twice (114 and
-// 132, 8-bit rows 55 and 63).
+// 32/8 heads over 1000 keys, bf16, 64: 45 us with one, 35 with two; 128: 67 and
+// 55, e4m3 56 and 43; 8 x 16 rows over 500 keys, 128: 11.5 and 16.  Heads of 32
+// gain nothing (19 and 20), and fp32 rows of 128 do not fit the registers twice
+// (114 and 132, 8-bit rows 55 and 63).
 inline int tiles_of_block(int dtype, int DP, int64_t sequences, int Hkv, int64_t rows) {
     if (rows <= 16 || DP == 32 || (DP == 128 && dtype == SN_F32)) return 1;
     return sequences * Hkv * ((rows + 15) / 16) >= 2 * kCus ? 2 : 1;
@@ -1001,12 +1003,15 @@ inline int64_t span_of(const CacheArgs &a) {
 inline double bytes_of(const CacheArgs &a, int es) { return 0.6 * a.B * (double)span_of(a) * a.Hkv * 2 * a.Dp * es; }
 
 // Whether units are cut.  A block takes about 2 us for a round (a tile of each
-// wavefront; 1.5 us with short rows) and the join and its launch cost 11 us more.  Few units: cut where the
-// rounds that a unit takes one after the other are longer than that (1 x 4000
-// keys, 32/8 x 128 bf16: 40 us whole, 18 cut; 1 x 1000: 14.7 and 15.0; 8 x 4000:
-// 42 and 28; 16 x 2000: 25 and 27).  Units on every CU: cut where the longest
-// ones would keep some CUs alone (32 x 20000: 323 and 290; 64 x 12000: 370 and
-// 335; 64 x 1000: 32 and 45).  Many units even out by themselves.
+// wavefront; 1.5 us with short rows).  Few units: cut where the rounds that a unit
+// takes one after the other are 11 us longer than the bytes (the join, its launch
+// and the shorter pieces cost 4 to 6, and what is left has to be gained; 1 x 4000
+// keys, 32/8 x 128 bf16: 40 us whole, 19 cut; 1 x 1000: 14.9 and 14.8; 8 x 4000:
+// 43 and 33; 16 x 2000: 27 and 32).  Units on every CU: cut where the longest
+// ones would keep some CUs alone (32 x <= 20000: 331 and 262; 64 x <= 12000: 385
+// and 304; 64 x 1000: 46 and 50).  Many units even out by themselves.  The host
+// knows what the table holds, not the lengths: short ones in a table with room
+// are cut where that does not pay (271 keys, 4 x 32 fp32: 6.7 and 10.4).
 template <class F>
 bool worth_cutting(const CacheArgs &a, const AttendCut &c) {
     const double units = (double)a.B * c.units, places = kCus * F::BLOCKS;
@@ -1036,10 +1041,11 @@ sn_status launch(const CacheArgs &a, void *o, float *lse, char *ws, hipStream_t 
     return launch_status();
 }
 // Whether the rows are read past the caches: they are read once, and are more
-// than the caches hold (32 x <= 20000 keys, 32/8 x 128 bf16, 1.6 GB: 307 us and
-// 270 past them; 64 x 12000, 4 x 32 fp32, 480 MB: 100 and 92; 32 x 4000, 350 MB:
-// 72 and 70; 16 x 4000, 180 MB: 44 and 63).  8-bit rows gain only where units are
-// cut (32 x 20000, 875 MB: 170 and 159; 64 x 4000, not cut: 74 and 75).
+// than the caches hold (32 x <= 20000 keys, 32/8 x 128 bf16, 1.6 GB: 295 us and
+// 262 past them; 64 x <= 12000, 4 x 32 fp32, 480 MB: 98 and 88; 32 x 4000, 520 MB:
+// 94 and 83; 16 x 4000, 260 MB: 46 and 67).  8-bit rows gain where units are cut
+// (32 x <= 20000, 875 MB: 166 and 157) and little elsewhere (64 x 4000: 104 and 98).
+// By the table, too: 16 x 4000 in one for 8000 takes 67, in one for 32000 (cut) 52.
 template <class F>
 bool reads_past(const CacheArgs &a) {
     const AttendCut c = cut_of(a.Hkv, rows_of(a.max_rows, a.G), 1);

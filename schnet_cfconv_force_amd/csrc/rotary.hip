@@ -12,7 +12,8 @@
 // or adjacent pairs), so a pair never leaves the lane.  A block's groups take
 // the heads of its rows in memory's order (lanes that walk the heads of a row of
 // their own spread a wavefront over eight rows: 153 us).  The block forms the
-// sines and cosines of its rows once, for all heads, in LDS.
+// sines and cosines of its rows once, for all heads, in LDS.  Where pairs do not
+// come in fours a lane takes single elements, at 2 to 4 TB/s (runs_of).
 #include <algorithm>
 
 #include "state.h"
@@ -23,9 +24,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxPartials = 1024;   // blocks of a backward pass, and with them partial weight gradients
 constexpr int kHeads = 4;               // of a group, on their way at once
-// Blocks that a pass makes before a block takes more rows than one: 7001 rows of
-// 6 + 2 heads of 40, bf16, a step: 17 us with 512, 22 with 1024, 47 with 4096;
-// 17216 rows of 4 + 4 heads of 32, fp32: 25.7, 24.3 and 36; with 256: 17 and 26.
+// Blocks that a pass makes before a block takes more rows than one.  Forward and
+// backward replayed from a graph (called, the host adds to the shorter ones): 7001
+// rows of 6 + 2 heads of 40, bf16, 17.2 us with 512, 21.9 with 1024, 48 with 4096,
+// 17.5 with 256; 17216 rows of 4 + 4 heads of 32, fp32, 25.9, 24.0, 35 and 26.0.
 constexpr int kBlocks = 512;
 // Outputs beyond this stay in no cache until they are read: they are stored past
 // it (32768 rows of 32 + 8 heads of 128, bf16: 143 us -> 135; 16384, a step: 181
@@ -365,7 +367,9 @@ __global__ __launch_bounds__(kThreads) void rotary_weights_kernel(const float *p
 }
 
 // A lane's vector length: as long as every run of V elements lies whole in
-// one aligned place of every tensor, else 1.
+// one aligned place of every tensor, else 1 (32768 rows of 32 + 8 heads of 128,
+// bf16, 64 pairs in halves 132 us, 37 pairs 212, a step 322 and 559; of 80, 10
+// pairs in halves 205, adjacent 110; 8 + 8 heads of 20, fp32, 84 MB: 24).
 template <typename T>
 bool runs_of(const RotaryArgs &a, int V, bool backward) {
     if (a.D % (2 * V) != 0 || (!a.interleaved && a.P % V != 0)) return false;
