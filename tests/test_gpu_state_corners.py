@@ -208,3 +208,90 @@ def test_rotary_sines_near_half_turns(sn):
     worst = float(((y.cpu().double() - want).abs() / bound).max())
     print(f"worst {worst:.3f} of the tolerance", flush=True)
     assert worst <= 1
+
+
+# ------------------------------------------------------------------ layouts and sizes
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("layout", ["joined", "odd"])
+@pytest.mark.parametrize("dim,spare", [(16, 2), (32, 4000), (40, 2), (128, 2)])
+def test_attend_strided_queries(sn, dim, spare, layout, dtype, codes):
+    """Queries that are a part of wider rows, or begin at odd elements; one row of NaN among them, which is formed apart."""
+    import torch
+    print(f"[attend] strides {dim} {spare} {layout} {dtype} {codes}", flush=True)
+    c = cache_case(sn, [3, 1, 0, 2], [150, 40, 9, 700], 2, dim, 16, dtype, codes, 111, heads=6, spare=spare)
+    n, to = c["q"].shape[0], c["q"].dtype
+    if layout == "joined":
+        wide = torch.zeros(n, 6 + 4, dim, dtype=to, device="cuda")[:, :6]
+    else:
+        wide = torch.zeros(n * 6 * (dim + 1) + 1, dtype=to, device="cuda")[1:].view(n, 6, dim + 1)[..., :dim]
+    wide.copy_(c["q"])
+    wide[3, 2, dim - 1] = math.nan
+    c["q"] = wide
+    attend_check(sn, c)
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kv,dim", [(300, 16), (70, 128), (33, 40)])
+def test_many_heads(sn, kv, dim, dtype, codes):
+    """More heads than a block has groups of lanes: written, read back and attended to."""
+    import torch
+    print(f"[cache] heads {kv} {dim} {dtype} {codes}", flush=True)
+    c = cache_case(sn, [2, 1], [20, 37], kv, dim, 16, dtype, codes, 112)
+    k, v = sn.cache_read(c["whole"], c["table"], c["lengths"], c["ws"])
+    for x, got in zip(c["rows"], (k, v)):
+        assert torch.equal(got.cpu(), R.held(x, codes).to(torch.float32).to(x.dtype))
+    attend_check(sn, c)
+
+
+@pytest.mark.parametrize("heads,kv", [(2, 300), (300, 2), (1, 65)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rotary_many_heads(sn, heads, kv, dtype):
+    print(f"[rotary] heads {heads} {kv} {dtype}", flush=True)
+    rotary_check(sn, rotary_case(sn, 600, heads, kv, 32, [8, 4], False, True, dtype, 113), False, True, dtype)
+
+
+def test_rows_beyond_31_bits(sn):
+    """Row tensors of more than 2^31 elements: turned, with their weights' gradients, written and read back."""
+    import torch
+    rows, heads, dim = 2 ** 21 + 5, 8, 128
+    gen = torch.Generator(device="cuda").manual_seed(114)
+    x = torch.empty(rows, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    freqs, axes = sn.rotary_frequencies([32])
+    plan = sn.HeadRotary(rows, heads, dim, freqs=freqs, axes=axes, dtype=torch.bfloat16)
+    at = torch.arange(rows, dtype=torch.int32, device="cuda")[None]
+    ws = sn.head_rotary_workspace(plan)
+    y, _ = sn.head_rotary_forward(plan, x, None, at, ws)
+    dx, _, dw, _ = sn.head_rotary_backward(plan, x, None, at, y, None, ws)
+    for part in (slice(0, 40), slice(rows - 40, rows)):
+        ref, factor = R.rotary(x[part], None, at[:, part], freqs, axes, False, True, 1e-6, y[part])
+        R.check("y", y[part], ref["y"], factor, True)
+        R.check("dx", dx[part], ref["dx"], factor, True)
+    # turned back, y is its own rows but for its rounding: dw is close to sum xh^2, all positive
+    want = torch.zeros(dim, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, 1 << 16):
+        p = slice(i, min(i + (1 << 16), rows))
+        xd, g = x[p].double(), y[p].double()
+        t = at[0, p, None].double() * torch.from_numpy(freqs).cuda()
+        c, s = torch.cos(t)[:, None], torch.sin(t)[:, None]
+        a, b = g[..., :32].clone(), g[..., 32:64].clone()
+        g[..., :32], g[..., 32:64] = a * c + b * s, b * c - a * s
+        want += (g * xd / torch.sqrt((xd * xd).mean(-1, keepdim=True) + 1e-6)).sum((0, 1))
+    R.check("dw", dw, (want.cpu(), 2 * want.abs().cpu()), 64 * R.U32)
+    del dx, y
+    page = 1024
+    cache = sn.StateCache(-(-rows // page), page, heads, dim, dtype=torch.bfloat16)
+    keep = sn.CacheRows(cache, [0, rows], cache.n_pages)
+    table = torch.randperm(cache.n_pages, generator=gen, device="cuda").to(torch.int32)[None]
+    lengths, ws = torch.tensor([rows], dtype=torch.int32, device="cuda"), sn.cache_workspace(keep)
+    sn.cache_write(keep, x, x, table, lengths, ws)
+    k, v = sn.cache_read(keep, table, lengths, ws)
+    assert sn.read_status(ws) == sn.SN_OK and torch.equal(k, x) and torch.equal(v, x)
+    q = normal(gen, 1, heads, dim, to=torch.bfloat16)
+    one = sn.CacheRows(cache, [0, 1], cache.n_pages, window=100)
+    o = sn.cache_attend(one, q, table, lengths, sn.cache_workspace(one))
+    last = x[-100:].double().cpu()
+    ref, factor = R.attend(q, [last], [last], [0, 1], [100], one.scale)
+    R.check("o", o, ref["o"], factor, True)
