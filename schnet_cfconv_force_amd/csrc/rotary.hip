@@ -341,8 +341,12 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
     // element e of lane u, of all groups
     for (int i = threadIdx.x; i < k.units * 2 * V; i += kThreads) {
         const int lane = i % k.units, e = i / k.units;
-        float sum = 0.0f;
-        for (int g = 0; g < groups; ++g) sum += sums[e * kThreads + (g << k.lane_bits) + lane];
+        const float *of = sums + e * kThreads + lane;
+        double part[4] = {};        // up to 256 groups' sums: one after the other in fp32 they lost some digits
+        for (int g = 0; g < groups; g += 4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[j] += of[(g + j) << k.lane_bits];
+        const float sum = (float)((part[0] + part[1]) + (part[2] + part[3]));
         const Place p = place_of<V, IL>(lane, k.units, a.D, a.P);
         const int d = e < V ? p.a + e : p.b + e - V;
         if (d < a.D) out[d] = sum;

@@ -295,3 +295,24 @@ def test_rows_beyond_31_bits(sn):
     last = x[-100:].double().cpu()
     ref, factor = R.attend(q, [last], [last], [0, 1], [100], one.scale)
     R.check("o", o, ref["o"], factor, True)
+
+
+# ------------------------------------------------------------------ long sums
+
+@pytest.mark.parametrize("rows", [64, 5000])
+def test_rotary_weight_sums_keep_their_digits(sn, rows):
+    """Heads of +-1 have a norm of 1, so that a weight's gradient is the sum of exact numbers: each a little above 1, by half
+    of what one step of an fp32 sum near 200 is.  A few terms of a thread, a block's sum rounded once, the sum of all: at most
+    4 u of the whole."""
+    import torch
+    plan = sn.HeadRotary(rows, 4, 8, n_kv_heads=4, eps=1e-30)
+    x = torch.ones(rows, 4, 8, device="cuda")
+    x[..., ::2] = -1.0
+    dy = x * (1 + 0.49 * 2.0 ** -16)
+    ws = sn.head_rotary_workspace(plan)
+    _, _, dqw, dkw = sn.head_rotary_backward(plan, x, x, None, dy, dy, ws)
+    want = (dy.double() * x.double()).sum((0, 1)).cpu()
+    for got in (dqw, dkw):
+        worst = float(((got.cpu().double() - want).abs() / want).max()) / R.U32
+        print(f"off by {worst:.2f} u", flush=True)
+        assert worst <= 4
