@@ -26,8 +26,8 @@ constexpr int kMaxPartials = 1024;   // blocks of a backward pass, and with them
 constexpr int kHeads = 4;               // of a group, on their way at once
 // Blocks that a pass makes before a block takes more rows than one.  Forward and
 // backward replayed from a graph (called, the host adds to the shorter ones): 7001
-// rows of 6 + 2 heads of 40, bf16, 17.2 us with 512, 21.9 with 1024, 48 with 4096,
-// 17.5 with 256; 17216 rows of 4 + 4 heads of 32, fp32, 25.9, 24.0, 35 and 26.0.
+// rows of 6 + 2 heads of 40, bf16, 17.4 us with 512, 21.9 with 1024, 48 with 4096,
+// 17.5 with 256; 17216 rows of 4 + 4 heads of 32, fp32, 26.0, 24.0, 35 and 26.0.
 constexpr int kBlocks = 512;
 // Outputs beyond this stay in no cache until they are read: they are stored past
 // it (32768 rows of 32 + 8 heads of 128, bf16: 143 us -> 135; 16384, a step: 181
@@ -402,8 +402,8 @@ RotaryCut cut_of(const RotaryArgs &a, int V, int size, bool backward) {
     k.rows = std::max(1, std::min(k.rows, a.n_rows / kBlocks));
     // Four heads a group are one block's: a launch that joins the weights' sums costs
     // more than more blocks give (forward and backward of 4 + 4 heads of 32, fp32,
-    // with the join and without: 1 row 24.2 and 21.8 us, 64 rows 24.3 and 22.2;
-    // replayed from a graph 9.5 and 7.0, 10.1 and 10.6: no longer than that). Keys
+    // with the join and without: 1 row 23.6 and 21.4 us, 64 rows 23.5 and 20.8;
+    // replayed from a graph 9.9 and 7.5, 10.6 and 11.1: no longer than that). Keys
     // there must be, for the join also writes the zeros of a weight without heads.
     k.single = backward && a.n_rows > 0 && a.Hkv > 0 && a.n_rows <= kTable / k.width &&
                (int64_t)a.n_rows * std::max(a.H, a.Hkv) <= kHeads * groups;
